@@ -30,6 +30,8 @@ FLAG_SLOT_RANGE = 0x1
 FLAG_POS_RANGE = 0x2
 FLAG_TIMEOUT = 0x4
 FLAG_COUNTER = 0x8
+FLAG_BLOCK_RANGE = 0x10
+FLAG_LENGTH = 0x20
 
 # every function the header declares
 EXPORTS = (
@@ -41,7 +43,9 @@ EXPORTS = (
     "dspark_ctx_kv_project", "dspark_ctx_kv_project_write", "dspark_gemma_rms_norm",
     "dspark_ctx_kv_write_layer_slots", "dspark_ctx_kv_tables_update_slots", "dspark_ctx_kv_tables_layer_slots",
     "dspark_ctx_kv_write_general", "dspark_ctx_kv_general_supported", "dspark_ctx_kv_validate_layers_general",
-    "dspark_ctx_kv_write_sched", "dspark_ctx_kv_write_noalloc",
+    "dspark_ctx_kv_write_sched", "dspark_ctx_kv_write_noalloc", "dspark_rope_table", "dspark_rope_kv_insert",
+    "dspark_tree_attention", "dspark_tree_attention_workspace", "dspark_attention_weight_accumulate",
+    "dspark_kv_evict", "dspark_kv_evict_workspace",
 )
 
 
@@ -134,6 +138,24 @@ def lib() -> ctypes.CDLL:
         L.dspark_ctx_kv_general_supported.restype = I
         L.dspark_ctx_kv_validate_layers_general.argtypes = [I, ctypes.POINTER(CacheDesc)]
         L.dspark_ctx_kv_validate_layers_general.restype = I
+        # include/dspark_draft_attn.h
+        F, D = ctypes.c_float, ctypes.c_double
+        L.dspark_rope_table.argtypes = [P, I64, I64, I, ctypes.POINTER(D), D, I, P]
+        L.dspark_rope_kv_insert.argtypes = [P, I64, I64] * 5 + [P, I, I64, P, I64, I, I, I, I, I, I, P, P, I64, I, I,
+                                                                P, P, P, P]
+        queries = [P, I64, I64, I64, I, I, I, P, I64, I, I]
+        table = [P, I64, I64, P, P, I]
+        L.dspark_tree_attention.argtypes = queries + [P, P] + table + [I, P, I, F, P, P, P, I64, P, P]
+        L.dspark_tree_attention_workspace.argtypes = [I64, I, I, I, I, I]
+        L.dspark_attention_weight_accumulate.argtypes = queries + [P] + table + [P, F, F, P, I64, P, P]
+        L.dspark_kv_evict.argtypes = [P, I64, I, I, I, I, P, I64, I64, P, I, P, P, P, P, I64, P, I64, I64, I64, P, P,
+                                      I64, P, P]
+        L.dspark_kv_evict_workspace.argtypes = [I, I, I64, I64]
+        for n in ("dspark_rope_table", "dspark_rope_kv_insert", "dspark_tree_attention",
+                  "dspark_attention_weight_accumulate", "dspark_kv_evict"):
+            getattr(L, n).restype = I
+        for n in ("dspark_tree_attention_workspace", "dspark_kv_evict_workspace"):
+            getattr(L, n).restype = I64
         _lib = L
         return L
 

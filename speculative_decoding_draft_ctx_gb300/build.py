@@ -28,11 +28,18 @@ NORM_SRC = os.path.join(CSRC, "hidden_norm.cu")
 GENERAL_SRC = os.path.join(CSRC, "ctx_kv_general.cu")
 WARP_SRC = os.path.join(CSRC, "ctx_kv_warp.cu")
 NOALLOC_SRC = os.path.join(CSRC, "ctx_kv_noalloc.cu")
-CU_SRCS = (KERNEL_SRC, TMA_SRC, QK_SRC, PROJ_SRC, NORM_SRC, GENERAL_SRC, WARP_SRC, NOALLOC_SRC)
+ROPE_SRC = os.path.join(CSRC, "rope.cu")
+EVICT_SRC = os.path.join(CSRC, "kv_evict.cu")
+ATTN_SRCS = tuple(os.path.join(CSRC, f) for f in ("tree_attn.cu", "tree_attn_d64.cu", "tree_attn_d128.cu", "tree_attn_d256.cu"))
+CU_SRCS = (KERNEL_SRC, TMA_SRC, QK_SRC, PROJ_SRC, NORM_SRC, GENERAL_SRC, WARP_SRC, NOALLOC_SRC, ROPE_SRC, EVICT_SRC,
+           *ATTN_SRCS)
 API_SRC = os.path.join(CSRC, "ctx_kv_api.cpp")
+DRAFT_API_SRC = os.path.join(CSRC, "draft_attn_api.cpp")
+API_SRCS = (API_SRC, DRAFT_API_SRC)
 HEADERS = [os.path.join(CSRC, "ctx_kv_internal.h"), os.path.join(CSRC, "ctx_kv_device.cuh"),
-           os.path.join(CSRC, "ctx_kv_pipe.cuh"),
-           os.path.join(INCLUDE, "dspark_ctx_kv.h")]
+           os.path.join(CSRC, "ctx_kv_pipe.cuh"), os.path.join(CSRC, "draft_attn_internal.h"),
+           os.path.join(CSRC, "tree_attn_mma.cuh"),
+           os.path.join(INCLUDE, "dspark_ctx_kv.h"), os.path.join(INCLUDE, "dspark_draft_attn.h")]
 
 _lock = threading.Lock()
 
@@ -51,7 +58,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(s) > t for s in [*CU_SRCS, API_SRC, *HEADERS])
+    return any(os.path.getmtime(s) > t for s in [*CU_SRCS, *API_SRCS, *HEADERS])
 
 
 def _run(cmd):
@@ -78,10 +85,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
                 cmd.insert(1, "-Xptxas=-v")
             objs.append(obj)
             cmds.append(cmd)
-        aobj = os.path.join(BUILD_DIR, "ctx_kv_api.o")
-        cmds.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(home, "include"),
-                     "-I", INCLUDE, "-c", API_SRC, "-o", aobj])
-        objs.append(aobj)
+        for src in API_SRCS:
+            aobj = os.path.join(BUILD_DIR, os.path.basename(src)[:-4] + ".o")
+            cmds.append(["g++", "-O2", "-std=c++17", "-fPIC", "-Wall", "-I", os.path.join(home, "include"),
+                         "-I", INCLUDE, "-c", src, "-o", aobj])
+            objs.append(aobj)
         with ThreadPoolExecutor(len(cmds)) as ex:
             outs = list(ex.map(_run, cmds))
         if verbose:

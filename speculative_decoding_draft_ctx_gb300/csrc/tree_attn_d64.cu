@@ -1,0 +1,9 @@
+// The drafted tokens' attention and the weight accumulation for head dim 64
+// (one translation unit per head dim, so that they compile side by side).
+#include "tree_attn_mma.cuh"
+
+namespace dspark {
+namespace attn {
+DSPARK_ATTN_DEFINE(64)
+}
+}  // namespace dspark
