@@ -166,29 +166,30 @@ __device__ __forceinline__ Request request(const AttnParams &p, int b, int mask_
 }
 
 // Block-wide search of the request that holds unit `target`, and the sum of
-// all units (kThreads threads, scratch of kWarps + 4 words): `units(b)` is
-// evaluated once per request and pass by one thread.
+// all units (THREADS threads, scratch of THREADS / 32 + 4 words): `units(b)`
+// is evaluated once per request and pass by one thread.
 struct Find {
     int64_t total, before;  // all units; those of the requests before `b`
     int b;
 };
 
-template <typename F>
-__device__ Find find_request(int requests, int64_t *scratch, F units, int64_t (*share)(int64_t, void *), void *arg)
+template <int THREADS, typename F, typename S>
+__device__ Find find_request(int requests, int64_t *scratch, F units, S share)
 {
+    constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Find f{0, 0, -1};
     int64_t mine = 0;
     for (int pass = 0; pass < 2; pass++) {
         int64_t base = 0, target = 0;
         if (pass == 1) {
-            target = share(f.total, arg);
+            target = share(f.total);
             if (target < 0 || target >= f.total)
                 return f;
         }
-        for (int b0 = 0; b0 < requests; b0 += kThreads) {
+        for (int b0 = 0; b0 < requests; b0 += THREADS) {
             const int b = b0 + tid;
-            if (pass == 0 || requests > kThreads)
+            if (pass == 0 || requests > THREADS)
                 mine = b < requests ? units(b) : 0;
             int64_t x = mine;
 #pragma unroll
@@ -203,14 +204,14 @@ __device__ Find find_request(int requests, int64_t *scratch, F units, int64_t (*
             __syncthreads();
             int64_t below = 0, all = 0;
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) {
+            for (int w = 0; w < W; w++) {
                 below += w < warp ? scratch[w] : 0;
                 all += scratch[w];
             }
             const int64_t end = base + below + x;
             if (pass == 1 && target >= end - mine && target < end) {
-                scratch[kWarps] = b;
-                scratch[kWarps + 1] = end - mine;
+                scratch[W] = b;
+                scratch[W + 1] = end - mine;
             }
             base += all;
         }
@@ -218,8 +219,8 @@ __device__ Find find_request(int requests, int64_t *scratch, F units, int64_t (*
             f.total = base;
     }
     __syncthreads();
-    f.b = (int)scratch[kWarps];
-    f.before = scratch[kWarps + 1];
+    f.b = (int)scratch[W];
+    f.before = scratch[W + 1];
     return f;
 }
 
@@ -497,16 +498,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
         return items * ((r.ctx + r.nq + kTile - 1) / kTile);
     };
     // shares start at total * c / n for c < n = the CTAs that get one
-    struct Share {
-        int cta, ctas;
-    } sh{cta, ctas};
-    const Find f = find_request(p.num_requests, scratch, units_of,
-                                [](int64_t total, void *arg) -> int64_t {
-                                    const Share *s = static_cast<const Share *>(arg);
-                                    const int64_t n = total < s->ctas ? total : s->ctas;
-                                    return s->cta < n ? (int64_t)((unsigned long long)total * s->cta / (unsigned long long)(n ? n : 1)) : -1;
-                                },
-                                &sh);
+    const Find f = find_request<kThreads>(p.num_requests, scratch, units_of, [&](int64_t total) -> int64_t {
+        const int64_t n = total < ctas ? total : ctas;
+        return cta < n ? (int64_t)((unsigned long long)total * cta / (unsigned long long)n) : -1;
+    });
     const int64_t total = f.total;
     const int64_t n_cta = total < ctas ? total : ctas;
     PartDesc *descs = reinterpret_cast<PartDesc *>(p.parts);
@@ -648,7 +643,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
             const bool masked = drafted || (lv[0] & lv[1] & lv[2] & lv[3]) != 0xffffu;
 #pragma unroll
             for (int n = 0; n < NS; n++) {
-                s[n][0] *= c0, s[n][1] *= c0, s[n][2] *= c1, s[n][3] *= c1;
+                s[n][0] = __fmul_rn(s[n][0], c0), s[n][1] = __fmul_rn(s[n][1], c0);  // rounded apart from the
+                s[n][2] = __fmul_rn(s[n][2], c1), s[n][3] = __fmul_rn(s[n][3], c1);  // subtraction of m: exactly 0 at the maximum
                 if (masked) {
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
@@ -958,15 +954,9 @@ __global__ void __launch_bounds__(kThreads, (WeightCfg<D, FP8>::kCtas)) weight_k
     auto units_of = [&](int b) -> int64_t {
         return (int64_t)p.num_kv_heads * ((checked(b, flags).ctx + kTile - 1) / kTile);
     };
-    struct Share {
-        int cta, ctas;
-    } sh{cta, ctas};
-    const Find f = find_request(p.num_requests, scratch, units_of,
-                                [](int64_t total, void *arg) -> int64_t {
-                                    const Share *s = static_cast<const Share *>(arg);
-                                    return (int64_t)((unsigned long long)total * s->cta / (unsigned long long)s->ctas);
-                                },
-                                &sh);
+    const Find f = find_request<kThreads>(p.num_requests, scratch, units_of, [&](int64_t total) {
+        return (int64_t)((unsigned long long)total * cta / (unsigned long long)ctas);
+    });
     const int64_t total = f.total;
     const int64_t lo = (int64_t)((unsigned long long)total * cta / (unsigned long long)ctas);
     const int64_t hi = (int64_t)((unsigned long long)total * (cta + 1) / (unsigned long long)ctas);

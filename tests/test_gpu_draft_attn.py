@@ -174,6 +174,15 @@ def test_rope_gradient(layout):
 
 # ------------------------------------------------------------------ attention
 
+
+@pytest.fixture(params=["rule", "mma", "tc"])
+def kernel(request, monkeypatch):
+    """Each test runs with the kernel the call's sizes choose and with each one pinned."""
+    if request.param != "rule":
+        monkeypatch.setenv("DSPARK_TREE_ATTN_KERNEL", request.param)
+    return request.param
+
+
 ATTN = [  # ctx, nq, Hq, Hkv, D, bs, fp8, mask
     ((1,), (1,), 1, 1, 64, 1, False, "dense"),
     ((0,), (1,), 8, 8, 128, 16, False, "causal"),
@@ -189,6 +198,10 @@ ATTN = [  # ctx, nq, Hq, Hkv, D, bs, fp8, mask
     ((31, 500), (3, 1), 16, 1, 64, 16, True, "dense"),
     ((2000,), (130,), 4, 4, 128, 16, False, "tree"),
     ((0, 0), (0, 0), 4, 4, 128, 16, False, "dense"),
+    ((4000, 300), (64, 33), 32, 4, 128, 16, False, "tree"),
+    ((3000, 0, 700), (64, 5, 20), 40, 8, 128, 64, True, "tree"),
+    ((2500, 129), (30, 70), 20, 4, 64, 100, False, "causal"),
+    ((2500, 127), (17, 70), 40, 4, 64, 16, True, "tree"),
     (tuple(range(0, 300)), tuple(i % 3 for i in range(300)), 2, 2, 64, 16, False, "causal"),
 ]
 
@@ -199,7 +212,7 @@ def run_attention(p, kind, mask, **kw):
 
 
 @pytest.mark.parametrize("ctx,nq,Hq,Hkv,D,bs,fp8,kind", ATTN)
-def test_attention(ctx, nq, Hq, Hkv, D, bs, fp8, kind):
+def test_attention(ctx, nq, Hq, Hkv, D, bs, fp8, kind, kernel):
     p = Problem(len(ctx) + D + bs, ctx, nq, Hq, Hkv, D, bs, fp8, packed=True).cuda()
     mask = tree_mask(nq, max(1, -(-max(nq) // 64)), D, empty=(0,) if sum(nq) else ())
     out, lse = run_attention(p, kind, mask)
@@ -209,7 +222,7 @@ def test_attention(ctx, nq, Hq, Hkv, D, bs, fp8, kind):
     assert int(p.d_flags) == 0
 
 
-def test_attention_rows_without_anything_and_rows_behind():
+def test_attention_rows_without_anything_and_rows_behind(kernel):
     """A row that sees nothing: zeros and -inf.  Rows of no request and outputs behind them stay."""
     p = Problem(3, (0, 4), (3, 2), 4, 2, 128, 16, False, pad_rows=3).cuda()
     mask = torch.tensor([[0], [2], [0], [0], [3], [-1], [-1], [-1]])
@@ -232,7 +245,7 @@ def test_attention_rows_without_anything_and_rows_behind():
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("ctx", [3, 700])
-def test_attention_keeps_what_is_masked_out(fp8, D, ctx):
+def test_attention_keeps_what_is_masked_out(fp8, D, ctx, kernel):
     """NaN and infinities in drafted tokens reach the rows that see them and no others."""
     nq = (6, 40)
     p = Problem(D + ctx, (ctx, 70), nq, 4, 2, D, 16, fp8)
@@ -256,7 +269,7 @@ def test_attention_keeps_what_is_masked_out(fp8, D, ctx):
     assert torch.isfinite(out[6:45]).all()
 
 
-def test_attention_infinite_context_value_and_large_scores():
+def test_attention_infinite_context_value_and_large_scores(kernel):
     p = Problem(8, (90,), (2,), 2, 1, 128, 16, False, q_std=300.0)
     p.cache[int(p.table[0, 1]), 0, 3, 130] = math.inf
     p.cuda()
@@ -270,7 +283,7 @@ def test_attention_infinite_context_value_and_large_scores():
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1.7])
-def test_attention_any_scale(scale):
+def test_attention_any_scale(scale, kernel):
     p = Problem(4, (70, 5), (3, 9), 8, 2, 64, 16, True).cuda()
     out, lse = run_attention(p, "causal", None, scale=scale)
     want, z, to, tl = attention(p, "causal", None, scale=scale)
@@ -278,7 +291,7 @@ def test_attention_any_scale(scale):
     close(out, want, to)
 
 
-def test_attention_queries_of_any_magnitude_over_fp8():
+def test_attention_queries_of_any_magnitude_over_fp8(kernel):
     """Rows far above and below fp16's range: each row is scaled on its own."""
     p = Problem(6, (50,), (4,), 2, 1, 128, 16, True)
     p.qkv = (p.qkv.float() * torch.tensor([2.0 ** -130, 1e-12, 1.0, 1e30]).view(4, 1, 1)).to(torch.bfloat16)
@@ -292,7 +305,7 @@ def test_attention_queries_of_any_magnitude_over_fp8():
     close(out[3], v, 1.01 * 2.0 ** -8 * v.abs())
 
 
-def test_attention_out_of_range_lengths_and_blocks():
+def test_attention_out_of_range_lengths_and_blocks(kernel):
     """Bad lengths leave the request out, bad blocks their tokens; nothing else changes."""
     def problem():
         return Problem(7, (40, 33, 50, 21), (3, 2, 4, 2), 4, 2, 128, 16, False, table_cols=5)
@@ -346,7 +359,7 @@ def test_attention_out_of_range_lengths_and_blocks():
         close(out[5:9], want, to)
 
 
-def test_attention_far_offsets_in_a_large_cache():
+def test_attention_far_offsets_in_a_large_cache(kernel):
     """Rows beyond 2^31 elements of the cache."""
     D, bs, H = 128, 16, 8
     blocks = (1 << 31) // (H * bs * 2 * D) * 5 // 4
@@ -367,7 +380,7 @@ def test_attention_far_offsets_in_a_large_cache():
     close(w, *weight(p, lse, torch.zeros((2, H, 100)), 1.0))
 
 
-def test_attention_same_bits_again_and_on_another_stream_and_in_graphs():
+def test_attention_same_bits_again_and_on_another_stream_and_in_graphs(kernel):
     p = Problem(12, (900, 20, 3000), (7, 7, 7), 16, 2, 128, 16, False).cuda()
     a = run_attention(p, "dense", None)
     b = run_attention(p, "dense", None)
