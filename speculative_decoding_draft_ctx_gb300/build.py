@@ -31,7 +31,7 @@ NOALLOC_SRC = os.path.join(CSRC, "ctx_kv_noalloc.cu")
 ROPE_SRC = os.path.join(CSRC, "rope.cu")
 EVICT_SRC = os.path.join(CSRC, "kv_evict.cu")
 ATTN_SRCS = tuple(os.path.join(CSRC, f) for f in ("tree_attn.cu", "tree_attn_d64.cu", "tree_attn_d128.cu", "tree_attn_d256.cu",
-                                                     "tree_attn_tc.cu"))
+                                                     "tree_attn_tc_d64.cu", "tree_attn_tc_d128.cu"))
 CU_SRCS = (KERNEL_SRC, TMA_SRC, QK_SRC, PROJ_SRC, NORM_SRC, GENERAL_SRC, WARP_SRC, NOALLOC_SRC, ROPE_SRC, EVICT_SRC,
            *ATTN_SRCS)
 API_SRC = os.path.join(CSRC, "ctx_kv_api.cpp")

@@ -46,6 +46,8 @@ int check_cache(const void *cache, int64_t num_blocks, int nkv, int block_size, 
         return fail(DSPARK_ERR_DTYPE, "kv dtype %d unknown", kv_dtype);
     if (num_blocks < 1 || num_blocks > ((INT64_MAX / nkv) / block_size) / (4 * head_dim))
         return fail(DSPARK_ERR_INVALID_ARG, "cache of %lld blocks invalid", (long long)num_blocks);
+    if (num_blocks * nkv * block_size >= (int64_t)UINT32_MAX)  // more rows than 32 bits number: beyond any device's memory
+        return fail(DSPARK_ERR_INVALID_ARG, "cache of %lld blocks invalid", (long long)num_blocks);
     if (!cache)
         return fail(DSPARK_ERR_INVALID_ARG, "null kv_cache");
     if (!aligned(cache, 16))
@@ -120,6 +122,7 @@ int check_attention(AttnParams &p, const void *q, int64_t q_ts, int64_t q_hs, in
     p.num_kv_heads = nkv;
     p.group = heads / nkv;
     p.block_size = block_size;
+    p.block_magic = block_size > 1 ? UINT64_MAX / (uint64_t)block_size + 1 : 0;
     p.num_requests = requests;
     p.scale = scale;
     return DSPARK_OK;

@@ -61,6 +61,7 @@ struct AttnParams {
     int64_t num_blocks;
     int32_t num_heads, num_kv_heads, group;  // group = num_heads / num_kv_heads
     int32_t block_size, num_requests;
+    uint64_t block_magic;  // floor(2^64 / block_size) + 1; 0 for size 1
     int32_t mask_kind, mask_words;
     float scale;        // softmax scale
     // attention

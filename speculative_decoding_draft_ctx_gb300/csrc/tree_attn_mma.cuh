@@ -63,6 +63,7 @@ namespace dspark {
 namespace attn {
 
 constexpr int kThreads = 128, kWarps = 4, kTile = 64;
+constexpr int kItemCost = 4;  // of an item besides its tiles, in tiles of kTile keys (see Walk)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -80,7 +81,7 @@ __device__ __forceinline__ int swz(int x)
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
 {
     const int n = live ? 16 : 0;  // the rest of the 16 bytes is filled with zeros
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n));
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -146,6 +147,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 }
 
 // ------------------------------------------------------------------ requests, items, units
+
+// j / block_size by a multiply (p.block_magic = floor(2^64 / block_size) + 1, exact while j * block_size < 2^64; 0 for size 1)
+__device__ __forceinline__ int block_of(const AttnParams &p, int j)
+{
+    return p.block_magic ? (int)__umul64hi((unsigned long long)j, p.block_magic) : j;
+}
 
 struct Request {
     int q0, nq, ctx;  // first row of q, drafted tokens, context tokens (nq = 0: nothing to do)
@@ -224,6 +231,89 @@ __device__ Find find_request(int requests, int64_t *scratch, F units, S share)
     return f;
 }
 
+// The flattened sequence of work: for every request, for every item (a row
+// group of ROWS of one KV head), EXTRA units for what an item costs besides its
+// tiles (queries in, results out, an empty pipeline: without them a CTA that
+// got two dozen requests of a few tokens took as long as all others together),
+// then a unit per tile.  A CTA's share [lo, hi) of it gives it the tiles of an
+// item whose units lie inside.
+template <int ROWS, int KEYS, int EXTRA>
+struct Walk {
+    int64_t lo, hi, at;  // the share; where the current item begins
+    int b, item, items, tiles, t0, t1, groups;  // t0 .. t1: this CTA's tiles of the item
+    int mask_limit;
+    Request rq;
+
+    __device__ __forceinline__ static int64_t units(const AttnParams &p, const Request &r)
+    {
+        if (r.nq == 0)
+            return 0;
+        const int64_t items = (int64_t)p.num_kv_heads * (((int64_t)r.nq * p.group + ROWS - 1) / ROWS);
+        return items * ((r.ctx + r.nq + KEYS - 1) / KEYS + EXTRA);
+    }
+    __device__ __forceinline__ void enter(const AttnParams &p)
+    {
+        unsigned ignore = 0;
+        rq = request(p, b, mask_limit, ignore);
+        groups = (rq.nq * p.group + ROWS - 1) / ROWS;
+        items = rq.nq ? p.num_kv_heads * groups : 0;
+        tiles = (rq.ctx + rq.nq + KEYS - 1) / KEYS;
+    }
+    __device__ __forceinline__ void clip()
+    {
+        const int64_t first = at + EXTRA;
+        t0 = (int)max((int64_t)0, min((int64_t)tiles, lo - first));
+        t1 = (int)max((int64_t)0, min((int64_t)tiles, hi - first));
+    }
+    __device__ __forceinline__ bool more() const { return at < hi; }
+    // to the next item with tiles of this CTA; at >= hi when there is none
+    __device__ __forceinline__ void next(const AttnParams &p)
+    {
+        do {
+            at += tiles + EXTRA;
+            if (at >= hi)
+                return;
+            if (++item >= items) {
+                item = 0;
+                do {
+                    b++;
+                    enter(p);
+                } while (items == 0);  // at < hi: there is one
+            }
+            clip();
+        } while (t0 >= t1);
+    }
+    // the first item of the share of request `first`, whose units begin at `before`
+    __device__ __forceinline__ void start(const AttnParams &p, int64_t lo_, int64_t hi_, int first, int64_t before, int limit)
+    {
+        lo = lo_, hi = hi_, at = lo_, b = first, mask_limit = limit;
+        item = t0 = t1 = 0;
+        if (lo >= hi)
+            return;
+        enter(p);
+        item = (int)((lo - before) / (tiles + EXTRA));
+        at = before + (int64_t)item * (tiles + EXTRA);
+        clip();
+        if (t0 >= t1)
+            next(p);
+    }
+    __device__ __forceinline__ int head() const { return item / groups; }
+    __device__ __forceinline__ int row0() const { return (item % groups) * ROWS; }
+    __device__ __forceinline__ bool begun() const { return t0 == 0; }
+    __device__ __forceinline__ bool finished() const { return t1 == tiles; }
+    // the CTA that has the item's last tile, of n that share `total` units: the largest c with floor(total c / n) <= its unit
+    __device__ __forceinline__ int last_cta(int64_t total, int64_t n) const
+    {
+        return (int)(((unsigned long long)(at + EXTRA + tiles) * n - 1) / (unsigned long long)total);
+    }
+};
+
+// Share c of n of `total` units.
+__device__ __forceinline__ int64_t share_start(int64_t total, int64_t c, int64_t n)
+{
+    return (int64_t)((unsigned long long)total * (unsigned long long)c / (unsigned long long)n);
+}
+
 // ------------------------------------------------------------------ the cached tiles
 
 // Copies kTile rows of `ROW` bytes (the first COPY of them wanted) of one
@@ -244,7 +334,7 @@ struct Loader {
         phys = 0;
         off = 0;
         if (live) {
-            const int blk = j / p.block_size;
+            const int blk = block_of(p, j);
             off = j - blk * p.block_size;
             phys = __ldg(p.table + b * p.table_stride + blk);
         }
@@ -263,14 +353,20 @@ struct Loader {
             mask[warp] = bits;
         const unsigned char *row =
             p.cache + (live ? ((phys * p.num_kv_heads + h) * p.block_size + off) * (int64_t)ROW : 0);
+        constexpr int kIt = 16 * kWords / 32, kBatch = kIt < 8 ? kIt : 8;
 #pragma unroll
-        for (int i = 0; i < 16 * kWords / 32; i++) {
-            const int idx = i * 32 + lane;
-            const int x = idx / kWords, c = idx % kWords;
-            const unsigned long long src = __shfl_sync(0xffffffffu, (unsigned long long)row, x);
-            const int y = warp * 16 + x;
-            cp16(stage + y * COPY + ((c ^ swz<COPY>(y)) << 4), reinterpret_cast<const unsigned char *>(src) + 16 * c,
-                 (bits >> x) & 1u);
+        for (int i0 = 0; i0 < kIt; i0 += kBatch) {  // the addresses, then the copies: the shuffles' latency once
+            unsigned long long src[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; i++)
+                src[i] = __shfl_sync(0xffffffffu, (unsigned long long)row, ((i0 + i) * 32 + lane) / kWords);
+#pragma unroll
+            for (int i = 0; i < kBatch; i++) {
+                const int idx = (i0 + i) * 32 + lane;
+                const int x = idx / kWords, c = idx % kWords, y = warp * 16 + x;
+                cp16(stage + y * COPY + ((c ^ swz<COPY>(y)) << 4), reinterpret_cast<const unsigned char *>(src[i]) + 16 * c,
+                     (bits >> x) & 1u);
+            }
         }
     }
 };
@@ -446,28 +542,23 @@ __device__ __forceinline__ float drafted_v(const AttnParams &p, int b, int ctx, 
     return __uint_as_float((uint32_t) reinterpret_cast<const uint16_t *>(p.cache)[at] << 16);
 }
 
-// What row i's result in dim d must have added for the infinities and NaN
-// among the drafted V it sees (their tile entries were zeroed).
+// Adds to dims [d0, d1) of row i's result `dst` what the infinities and NaN
+// among the drafted V it sees make of the sum (their tile entries were zeroed).
 template <int D, bool FP8>
-__device__ __noinline__ float nonfinite_sum(const AttnParams &p, int b, Request rq, int h, int i, int d)
+__device__ __noinline__ void add_nonfinite(const AttnParams &p, int b, Request rq, int h, int i, uint16_t *dst, int d0, int d1)
 {
-    float x = 0.0f;
-    for (int a = 0; a < rq.nq; a++) {
-        if (!sees(p, rq, i, a))
-            continue;
-        const float v = drafted_v<D, FP8>(p, b, rq.ctx, h, a, d);
-        if (!(fabsf(v) <= 3.4028235e38f))
-            x += v;
+    for (int d = d0; d < d1; d++) {
+        float x = 0.0f;
+        for (int a = 0; a < rq.nq; a++) {
+            if (!sees(p, rq, i, a))
+                continue;
+            const float v = drafted_v<D, FP8>(p, b, rq.ctx, h, a, d);
+            if (!(fabsf(v) <= 3.4028235e38f))
+                x += v;
+        }
+        if (x != 0.0f)  // NaN too
+            dst[d] = (uint16_t)pack_bf16x2(__uint_as_float((uint32_t)dst[d] << 16) + x, 0.0f);
     }
-    return x;
-}
-
-// The dims of n-tile n that a lane's accumulators c and c + 1 hold (c even).
-template <bool FP8>
-__device__ __forceinline__ int out_dim(int n, int lane, int c)
-{
-    const int t = lane & 3;
-    return FP8 ? 16 * (n >> 1) + 4 * t + 2 * (c & 1) + (n & 1) : 8 * n + 2 * t + (c & 1);
 }
 
 template <int D, bool FP8, int WR>
@@ -490,18 +581,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
 
     // ---- this CTA's share of the units
     const int ctas = gridDim.x, cta = blockIdx.x;
-    auto units_of = [&](int b) -> int64_t {
-        const Request r = request(p, b, mask_limit, flags);
-        if (r.nq == 0)
-            return 0;
-        const int64_t items = (int64_t)p.num_kv_heads * (((int64_t)r.nq * p.group + C::kRows - 1) / C::kRows);
-        return items * ((r.ctx + r.nq + kTile - 1) / kTile);
-    };
-    // shares start at total * c / n for c < n = the CTAs that get one
-    const Find f = find_request<kThreads>(p.num_requests, scratch, units_of, [&](int64_t total) -> int64_t {
-        const int64_t n = total < ctas ? total : ctas;
-        return cta < n ? (int64_t)((unsigned long long)total * cta / (unsigned long long)n) : -1;
-    });
+    using W = Walk<C::kRows, kTile, kItemCost>;
+    const Find f = find_request<kThreads>(
+        p.num_requests, scratch, [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); },
+        [&](int64_t total) {
+            const int64_t n = min(total, (int64_t)ctas);
+            return cta < n ? share_start(total, cta, n) : (int64_t)-1;
+        });
     const int64_t total = f.total;
     const int64_t n_cta = total < ctas ? total : ctas;
     PartDesc *descs = reinterpret_cast<PartDesc *>(p.parts);
@@ -514,57 +600,27 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
             atomicOr(p.error_flags, flags);
         return;
     }
-    const int64_t lo = (int64_t)((unsigned long long)total * cta / (unsigned long long)n_cta);
-    const int64_t hi = (int64_t)((unsigned long long)total * (cta + 1) / (unsigned long long)n_cta);
-
     const float ks = FP8 && p.k_scale ? __ldg(p.k_scale) : 1.0f, vs = FP8 && p.v_scale ? __ldg(p.v_scale) : 1.0f;
     const float base_scale = p.scale * kLog2e * ks;
 
-    // ---- a walk over (request, item, tile): one for the copies, one for the products
-    struct Walk {
-        int64_t u;   // unit
-        int b, item, items, tile, tiles, rts;
-        Request rq;
-    };
-    auto enter = [&](Walk &w) {  // request w.b: its sizes
-        unsigned ignore = 0;
-        w.rq = request(p, w.b, mask_limit, ignore);
-        w.rts = (w.rq.nq * p.group + C::kRows - 1) / C::kRows;
-        w.items = w.rq.nq ? p.num_kv_heads * w.rts : 0;
-        w.tiles = (w.rq.ctx + w.rq.nq + kTile - 1) / kTile;
-    };
-    auto step = [&](Walk &w) {
-        w.u++;
-        if (++w.tile < w.tiles)
-            return;
-        w.tile = 0;
-        if (++w.item < w.items || w.u >= hi)
-            return;
-        w.item = 0;
-        do {
-            w.b++;
-            enter(w);
-        } while (w.items == 0);  // w.u < hi: there is one
-    };
-    Walk cp;
-    cp.u = lo;
-    cp.b = f.b;
-    enter(cp);
-    {
-        const int64_t in = lo - f.before;
-        cp.item = (int)(in / cp.tiles);
-        cp.tile = (int)(in - (int64_t)cp.item * cp.tiles);
-    }
-    Walk w = cp;
+    // ---- two walks over the share: one for the copies, one for the products
+    W w;
+    w.start(p, share_start(total, cta, n_cta), share_start(total, cta + 1, n_cta), f.b, f.before, mask_limit);
+    W cp = w;
+    int cp_tile = cp.t0;
 
     Loader<C::kRow, C::kRow> ld;
-    ld.fetch(p, cp.b, cp.tile, cp.rq.ctx + cp.rq.nq, flags);
+    if (cp.more())
+        ld.fetch(p, cp.b, cp_tile, cp.rq.ctx + cp.rq.nq, flags);
     auto issue = [&](int stage) {
-        if (cp.u < hi) {
-            ld.load(p, cp.item / cp.rts, stages + stage * C::kStage, live[stage], flags);
-            step(cp);
-            if (cp.u < hi)
-                ld.fetch(p, cp.b, cp.tile, cp.rq.ctx + cp.rq.nq, flags);
+        if (cp.more()) {
+            ld.load(p, cp.head(), stages + stage * C::kStage, live[stage], flags);
+            if (++cp_tile >= cp.t1) {
+                cp.next(p);
+                cp_tile = cp.t0;
+            }
+            if (cp.more())
+                ld.fetch(p, cp.b, cp_tile, cp.rq.ctx + cp.rq.nq, flags);
         }
         cp_commit();
     };
@@ -573,10 +629,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
         issue(s);
     int stage = 0;
 
-    while (w.u < hi) {
+    while (w.more()) {
         // ---------------------------------------------------------------- one item, as far as it is this CTA's
-        const int h = w.item / w.rts, row0 = (w.item - h * w.rts) * C::kRows;
-        const int64_t item_start = w.u - w.tile, item_end = item_start + w.tiles;
+        const int h = w.head(), row0 = w.row0();
         const int len = w.rq.ctx + w.rq.nq, rows = w.rq.nq * p.group;
         const Request rq = w.rq;
         const int b = w.b;
@@ -593,13 +648,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
         if (tid == 0)
             any_bad = 0;
 
-        const int64_t stop = item_end < hi ? item_end : hi;
-        for (; w.u < stop; w.u++, w.tile++) {
+        for (int tile = w.t0; tile < w.t1; tile++) {
             cp_wait<C::kStages - 2>();
             __syncthreads();  // the tile has landed for all; every warp is done with the stage that is filled next
             issue((stage + C::kStages - 1) % C::kStages);
             const uint32_t st = stages + stage * C::kStage;
-            const int key0 = w.tile * kTile;
+            const int key0 = tile * kTile;
             const bool drafted = key0 + kTile > rq.ctx;  // the tile holds drafted tokens or ends beyond them
             if (drafted) {
                 // infinities and NaN among the drafted V: zeroed here, accounted for at the end
@@ -760,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
                 }
             }
         }
-        const bool begun = item_start >= lo, done = item_end <= hi;
+        const bool begun = w.begun(), done = w.finished();
         const int bad = any_bad;
         if (wk == 0) {
             if (begun && done) {
@@ -779,12 +833,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
                     }
 #pragma unroll
                     for (int n = 0; n < C::kNT; n += 2) {
-                        float x[4] = {o[n][2 * sx] * inv, o[n][2 * sx + 1] * inv, o[n + 1][2 * sx] * inv, o[n + 1][2 * sx + 1] * inv};
-                        if (bad) {
-#pragma unroll
-                            for (int k = 0; k < 4; k++)
-                                x[k] += nonfinite_sum<D, FP8>(p, b, rq, h, i, out_dim<FP8>(n + (k >> 1), lane, k & 1));
-                        }
+                        const float x[4] = {o[n][2 * sx] * inv, o[n][2 * sx + 1] * inv, o[n + 1][2 * sx] * inv, o[n + 1][2 * sx + 1] * inv};
                         if constexpr (FP8) {
                             // dims 16 (n / 2) + 4 t ...: even tile, odd tile, even, odd
                             *reinterpret_cast<uint2 *>(dst + 8 * n + 4 * (lane & 3)) = make_uint2(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[1], x[3]));
@@ -793,6 +842,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
                             *reinterpret_cast<uint32_t *>(dst + 8 * n + 8 + 2 * (lane & 3)) = pack_bf16x2(x[2], x[3]);
                         }
                     }
+                }
+                if (bad) {
+                    __syncwarp();  // the rows are written: one lane of each four adds to them
+                    if ((lane & 3) == 0) {
+                        if (r0 < rows)
+                            add_nonfinite<D, FP8>(p, b, rq, h, i0, p.out + ((int64_t)(rq.q0 + i0) * p.num_heads + h * p.group + (r0 - i0 * p.group)) * D, 0, D);
+                        if (r0 + 8 < rows)
+                            add_nonfinite<D, FP8>(p, b, rq, h, i1, p.out + ((int64_t)(rq.q0 + i1) * p.num_heads + h * p.group + (r0 + 8 - i1 * p.group)) * D, 0, D);
+                    }
+                    __syncwarp();
                 }
             } else {
                 float *part = parts + ((int64_t)cta * 2 + (begun ? 1 : 0)) * C::kPart + wr * (C::kNT * 128 + 32);
@@ -810,23 +869,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
         if (begun && !done && tid == 0) {
             PartDesc &d = descs[cta];
             d.q0 = rq.q0, d.rows = rows, d.row0 = row0, d.h = h, d.nq = rq.nq, d.ctx = rq.ctx, d.b = b;
-            // the CTA whose share holds the item's last unit: the largest c with total c / n < item_end
-            d.last = (int32_t)(((unsigned long long)item_end * n_cta - 1) / (unsigned long long)total);
+            d.last = w.last_cta(total, n_cta);
         }
         if (bad && !(begun && done) && tid == 0)
             descs[cta].bad[begun ? 1 : 0] = 1;
         __syncthreads();  // any_bad and the join buffer are free again
-        // the next item
-        w.tile = 0;
-        if (w.u < hi) {
-            if (++w.item >= w.items) {
-                w.item = 0;
-                do {
-                    w.b++;
-                    enter(w);
-                } while (w.items == 0);
-            }
-        }
+        w.next(p);
     }
     cp_wait<0>();
     flags = __reduce_or_sync(0xffffffffu, flags);
@@ -880,7 +928,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
         }
     }
     const float vs = FP8 && p.v_scale ? __ldg(p.v_scale) : 1.0f;
-    const Request rq{d.q0, d.nq, d.ctx};
 #pragma unroll
     for (int s = 0; s < 2; s++) {
         const int r = row0 + g + 8 * s;
@@ -896,12 +943,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 #pragma unroll
         for (int k = 0; k < NW; k += 2) {
             const int n = warp * NW + k;
-            float x[4] = {o[k][2 * s] * inv, o[k][2 * s + 1] * inv, o[k + 1][2 * s] * inv, o[k + 1][2 * s + 1] * inv};
-            if (bad) {
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    x[e] += nonfinite_sum<D, FP8>(p, d.b, rq, d.h, i, out_dim<FP8>(n + (e >> 1), lane, e & 1));
-            }
+            const float x[4] = {o[k][2 * s] * inv, o[k][2 * s + 1] * inv, o[k + 1][2 * s] * inv, o[k + 1][2 * s + 1] * inv};
             if constexpr (FP8) {
                 *reinterpret_cast<uint2 *>(dst + 8 * n + 4 * (lane & 3)) = make_uint2(pack_bf16x2(x[0], x[2]), pack_bf16x2(x[1], x[3]));
             } else {
@@ -909,6 +951,17 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
                 *reinterpret_cast<uint32_t *>(dst + 8 * n + 8 + 2 * (lane & 3)) = pack_bf16x2(x[2], x[3]);
             }
         }
+    }
+    if (bad) {
+        __syncwarp();  // the warp's quarter of each row is written: one lane of each four adds to it
+        if ((lane & 3) == 0)
+            for (int s = 0; s < 2; s++) {
+                const int r = row0 + g + 8 * s, i = r / p.group;
+                if (r < d.rows)
+                    add_nonfinite<D, FP8>(p, d.b, Request{d.q0, d.nq, d.ctx}, d.h, i,
+                                          p.out + ((int64_t)(d.q0 + i) * p.num_heads + d.h * p.group + (r - i * p.group)) * D,
+                                          warp * (D / 4), (warp + 1) * (D / 4));
+            }
     }
 }
 

@@ -16,7 +16,7 @@
 // each, overwritten by the weights P, two 16-bit values a column, which feed
 // the second product from there) and both outputs (D columns each).
 //
-//  - producer warps (4): gather the tile's K and V through the block table
+//  - producer warps (2 for K, 2 for V): gather the tiles through the block table
 //    into separate rings, bf16 with 16-byte asynchronous copies straight into
 //    the operands' 128-byte swizzle, fp8 through registers, converted to
 //    fp16 once per tile instead of once per row tile;
@@ -45,43 +45,58 @@ namespace dspark {
 namespace attn {
 
 constexpr int kTcThreads = 416, kKeysTc = 128;  // 8 softmax warps, 4 producers, 1 that issues the products
+constexpr int kProducers = 4, kItemCostTc = 3;   // EXTRA of Walk, in tiles of kKeysTc keys
 constexpr float kLazy = 8.0f;  // growth of a maximum (log2) that waits for a rescale
 
-template <int D, bool FP8>
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// RT: row tiles of 128 rows an item has at most (1 or 2).
+template <int D, bool FP8, int RT>
 struct TcCfg {
-    static constexpr int kStages = D == 64 ? 4 : 2;       // of the K ring and of the V ring
+    // K is done with after the first product, V only after the softmax
+    static constexpr int kStagesK = D == 64 ? 4 : 2, kStagesV = D == 64 ? 4 : RT == 1 ? 3 : 2;
     static constexpr int kTileBytes = kKeysTc * D * 2;    // one K or V tile, 16-bit
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kRow = 2 * D * (FP8 ? 1 : 2);    // bytes of a cached token
-    static constexpr int kSmem = 1024 + 2 * kQBytes + 2 * kStages * kTileBytes;
+    static constexpr int kSmem = 1024 + RT * kQBytes + (kStagesK + kStagesV) * kTileBytes;
     static constexpr int kRowPart = (D + 2) * 128;        // floats of one row tile's part
-    static constexpr int kPart = 2 * kRowPart;
+    static constexpr int kPart = RT * kRowPart;
+    static_assert(kSmem + 6 * 1024 <= 227 * 1024, "shared memory");
 };
 
-template <int D, bool FP8>
+template <int D, bool FP8, int RT>
 __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __grid_constant__ AttnParams p)
 {
-    using C = TcCfg<D, FP8>;
+    using C = TcCfg<D, FP8, RT>;
     using namespace tc;
-    constexpr int NS = C::kStages;
+    constexpr int NK = C::kStagesK, NV = C::kStagesV;
     constexpr uint32_t kS[2] = {0, 128}, kO[2] = {256, 256 + 128};  // tensor-memory columns
     constexpr uint32_t kIdQK = idesc(FP8, false, 128, kKeysTc), kIdPV = idesc(FP8, true, 128, D);
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (tc::saddr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *sq = smem, *sk = smem + 2 * C::kQBytes, *sv = sk + NS * C::kTileBytes;
-    __shared__ uint64_t kfull[NS], kempty[NS], vfull[NS], vempty[NS], qfull[2], sfull[2], pfull[2], ofull[2], jfull, jempty, done;
+    unsigned char *sq = smem, *sk = smem + RT * C::kQBytes, *sv = sk + NK * C::kTileBytes;
+    __shared__ uint64_t kfull[NK], kempty[NK], vfull[NV], vempty[NV], qfull[2], sfull[2], pfull[2], ofull[2], jfull, jempty, done;
     __shared__ uint32_t tmem_slot, live[8][4];
-    __shared__ int abort_flag, bad[16];
+    __shared__ uint32_t rows[kProducers][2][128];  // cache rows of each producer's job and its next; ~0: not there
+    __shared__ int abort_flag;
+    __shared__ int bad[16];  // item number + 1 where infinities or NaN came up among an item's drafted V
     __shared__ float join_ml[256];
     __shared__ int64_t scratch[kTcThreads / 32 + 4];
     volatile int *abort = &abort_flag;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        for (int s = 0; s < NS; s++) {
-            bar_init(kfull + s, 128 + 4);  // the producers' copies, and their live masks
-            bar_init(vfull + s, 128);
+        for (int s = 0; s < NK; s++) {
+            bar_init(kfull + s, 32 + 1);  // a producer warp's copies, and its live masks
             bar_init(kempty + s, 1);
+        }
+        for (int s = 0; s < NV; s++) {
+            bar_init(vfull + s, 32);
             bar_init(vempty + s, 1);
         }
         for (int s = 0; s < 2; s++) {
@@ -94,6 +109,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         bar_init(&jempty, 128);
         bar_init(&done, 1);
         abort_flag = 0;
+        for (int i = 0; i < 16; i++)
+            bad[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 12) {
@@ -106,18 +123,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
 
     // ---- this CTA's share of the units
     const int ctas = gridDim.x, cta = blockIdx.x;
+    using W = Walk<128 * RT, kKeysTc, kItemCostTc>;
     const Find f = find_request<kTcThreads>(
-        p.num_requests, scratch,
-        [&](int b) -> int64_t {
-            const Request r = request(p, b, mask_limit, flags);
-            if (r.nq == 0)
-                return 0;
-            const int64_t items = (int64_t)p.num_kv_heads * (((int64_t)r.nq * p.group + 255) / 256);
-            return items * ((r.ctx + r.nq + kKeysTc - 1) / kKeysTc);
-        },
-        [&](int64_t total) -> int64_t {
-            const int64_t n = total < ctas ? total : ctas;
-            return cta < n ? (int64_t)((unsigned long long)total * cta / (unsigned long long)n) : -1;
+        p.num_requests, scratch, [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); },
+        [&](int64_t total) {
+            const int64_t n = min(total, (int64_t)ctas);
+            return cta < n ? share_start(total, cta, n) : (int64_t)-1;
         });
     const int64_t total = f.total, n_cta = total < ctas ? total : ctas;
     PartDesc *descs = reinterpret_cast<PartDesc *>(p.parts);
@@ -128,68 +139,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
-    int64_t lo = 0, hi = 0;
-    if (f.b >= 0) {
-        lo = (int64_t)((unsigned long long)total * cta / (unsigned long long)n_cta);
-        hi = (int64_t)((unsigned long long)total * (cta + 1) / (unsigned long long)n_cta);
-    }
+    // every role walks the CTA's share on its own, item by item
+    W w;
+    w.start(p, f.b >= 0 ? share_start(total, cta, n_cta) : 0, f.b >= 0 ? share_start(total, cta + 1, n_cta) : 0, f.b, f.before,
+            mask_limit);
 
-    // every role walks the CTA's units on its own, item by item
-    struct Walk {
-        int64_t u;
-        int b, item, items, tile, tiles, rgs;
-        Request rq;
-    };
-    auto enter = [&](Walk &w) {
-        unsigned ignore = 0;
-        w.rq = request(p, w.b, mask_limit, ignore);
-        w.rgs = (w.rq.nq * p.group + 255) / 256;
-        w.items = w.rq.nq ? p.num_kv_heads * w.rgs : 0;
-        w.tiles = (w.rq.ctx + w.rq.nq + kKeysTc - 1) / kKeysTc;
-    };
-    auto start = [&]() {
-        Walk w;
-        w.u = lo;
-        w.b = f.b;
-        w.item = w.tile = 0;
-        w.tiles = 1;
-        if (lo < hi) {
-            enter(w);
-            const int64_t in = lo - f.before;
-            w.item = (int)(in / w.tiles);
-            w.tile = (int)(in - (int64_t)w.item * w.tiles);
-        }
-        return w;
-    };
-    // the tiles of the item at w that are this CTA's
-    auto share = [&](const Walk &w) { return (int)min((int64_t)(w.tiles - w.tile), hi - w.u); };
-    auto next = [&](Walk &w, int n) {  // past those tiles
-        w.u += n;
-        w.tile = 0;
-        if (w.u < hi && ++w.item >= w.items) {
-            w.item = 0;
-            do {
-                w.b++;
-                enter(w);
-            } while (w.items == 0);
-        }
-    };
-
-    if (warp >= 12) {
+    if (warp == 12) {
         // ------------------------------------------------------------ the issuing thread
-        if (tid == 12 * 32) {
-            Walk w = start();
+        if (lane == 0) {
             int base = 0;            // tiles consumed before this item
             int nq[2] = {0, 0};      // Q tiles used
             int np[2] = {0, 0};      // P tiles used
             bool ok = true;
-            while (w.u < hi && ok) {
-                const int n = share(w);
-                const int row0 = (w.item % w.rgs) * 256;
-                const bool two = w.rq.nq * p.group - row0 > 128;
+            while (w.more() && ok) {
+                const int n = w.t1 - w.t0;
+                const bool two = RT == 2 && w.rq.nq * p.group - w.row0() > 128;
                 auto qk = [&](int s, int j, bool last) {
-                    const int x = base + j, st = x % NS;
-                    if (!ok || !bar_wait(kfull + st, (uint32_t)(x / NS) & 1u, abort)) {
+                    const int x = base + j, st = x % NK;
+                    if (!ok || !bar_wait(kfull + st, (uint32_t)(x / NK) & 1u, abort)) {
                         ok = false;
                         return;
                     }
@@ -205,8 +172,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                         mma_commit(kempty + st);
                 };
                 auto pv = [&](int s, int j, bool first, bool last) {
-                    const int x = base + j, st = x % NS;
-                    if (!ok || !bar_wait(vfull + st, (uint32_t)(x / NS) & 1u, abort) ||
+                    const int x = base + j, st = x % NV;
+                    if (!ok || !bar_wait(vfull + st, (uint32_t)(x / NV) & 1u, abort) ||
                         !bar_wait(pfull + s, (uint32_t)np[s] & 1u, abort)) {
                         ok = false;
                         return;
@@ -244,166 +211,221 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     }
                 }
                 base += n;
-                next(w, n);
+                w.next(p);
             }
             mma_commit(&done);
         }
         __syncwarp();
     } else if (warp >= 8) {
-        // ------------------------------------------------------------ producers: a thread per tile row for the addresses
+        // ------------------------------------------------------------ producers
+        // Two warps copy K tiles and two V tiles.  A stage of a ring belongs to
+        // one warp (an even or an odd one), so that a warp is never more than
+        // one use of a stage ahead of its barrier, whose parity it waits for.
+        // A warp looks the block numbers of its next tile but one up while it
+        // copies, and has the rows of its next tile fetched into L2, so that
+        // what is in flight is not bounded by the rings.
         const int pw = warp - 8;
-        Walk w = start();
-        int base = 0, item_no = 0;
-        bool ok = true;
-        int64_t phys = 0;
-        int off = 0;
-        bool in = false;
-        auto fetch = [&](int b, int tile, int len) {
-            const int j = tile * kKeysTc + pw * 32 + lane;
-            in = j < len;
-            phys = 0, off = 0;
-            if (in) {
-                const int blk = j / p.block_size;
-                off = j - blk * p.block_size;
-                phys = __ldg(p.table + b * p.table_stride + blk);
+        struct Job {
+            int tile, x, item, ctx, h;  // tile of the request; number of the tile and of the item in this CTA's share
+            int slot;                   // of rows[pw]
+            bool valid;
+        };
+        int phys[4], off[4];  // of the job looked up last: rows lane, lane + 32, ...; off < 0: past the end
+        const int half = pw >> 1;                       // 0: the warp copies K, 1: V
+        int gen_x = 0, gen_tile = w.t0, gen_item = 0;  // the next tile of the share
+        auto step = [&]() {
+            gen_x++;
+            if (++gen_tile >= w.t1) {
+                w.next(p);
+                gen_tile = w.t0;
+                gen_item++;
             }
         };
-        if (w.u < hi)
-            fetch(w.b, w.tile, w.rq.ctx + w.rq.nq);
-        while (w.u < hi && ok) {
-            const int n = share(w), len = w.rq.ctx + w.rq.nq, ctx = w.rq.ctx, tile0 = w.tile;
-            const int h = w.item / w.rgs;
-            Walk after = w;
-            next(after, n);
-            if (tid == 8 * 32)
-                bad[item_no & 15] = 0;
-            for (int j = 0; j < n; j++) {
-                const int x = base + j, st = x % NS;
-                const uint32_t parity = ((uint32_t)(x / NS) & 1u) ^ 1u;
-                bool here = in;
-                if (here && (phys < 0 || phys >= p.num_blocks)) {
-                    flags |= kFlagBlockRange;
-                    here = false;
+        auto look = [&](Job &jb, int slot) {
+            while (w.more() && ((gen_x % (half ? NV : NK)) & 1) != (pw & 1))
+                step();
+            jb.valid = w.more();
+            if (!jb.valid)
+                return;
+            jb.tile = gen_tile, jb.x = gen_x, jb.item = gen_item, jb.ctx = w.rq.ctx, jb.h = w.head(), jb.slot = slot;
+            const int len = w.rq.ctx + w.rq.nq;
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                const int j = gen_tile * kKeysTc + 32 * g + lane, blk = block_of(p, j);
+                off[g] = j < len ? j - blk * p.block_size : -1;
+                phys[g] = 0;
+                if (j < len)
+                    phys[g] = __ldg(p.table + w.b * p.table_stride + blk);
+            }
+            step();
+        };
+        // the addresses, once the block numbers have come, and the rows into L2
+        auto resolve = [&](const Job &jb) {
+            if (jb.valid) {
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    uint32_t at = ~0u;
+                    if (off[g] >= 0) {
+                        if (phys[g] < 0 || phys[g] >= p.num_blocks) {
+                            flags |= kFlagBlockRange;
+                        } else {
+                            at = (uint32_t)(((int64_t)phys[g] * p.num_kv_heads + jb.h) * p.block_size + off[g]);
+                            const unsigned char *row = p.cache + (int64_t)at * C::kRow + half * (C::kRow / 2);
+#pragma unroll
+                            for (int y = 0; y < C::kRow / 2; y += 128)
+                                asm volatile("prefetch.global.L2 [%0];" ::"l"(row + y));
+                        }
+                    }
+                    rows[pw][jb.slot][32 * g + lane] = at;
                 }
-                const unsigned bits = __ballot_sync(0xffffffffu, here);
-                const unsigned long long row = reinterpret_cast<unsigned long long>(
-                    p.cache + (here ? ((phys * p.num_kv_heads + h) * p.block_size + off) * (int64_t)C::kRow : 0));
-                // the next tile's blocks
-                if (j + 1 < n)
-                    fetch(w.b, tile0 + j + 1, len);
-                else if (after.u < hi)
-                    fetch(after.b, after.tile, after.rq.ctx + after.rq.nq);
-                const int key0 = (tile0 + j) * kKeysTc;
-                const bool drafted = key0 + kKeysTc > ctx;
+            }
+            __syncwarp();
+        };
+        Job cur, nx1, nx2;
+        look(cur, 0);
+        resolve(cur);
+        look(nx1, 1);
+        bool ok = true;
+        while (cur.valid && ok) {
+            resolve(nx1);
+            look(nx2, cur.slot);
+            const bool is_v = half != 0;
+            const int st = is_v ? cur.x % NV : cur.x % NK, key0 = cur.tile * kKeysTc;
+            const uint32_t parity = ((uint32_t)(is_v ? cur.x / NV : cur.x / NK) & 1u) ^ 1u;
+            const bool drafted = is_v && key0 + kKeysTc > cur.ctx;
+            uint64_t *full = is_v ? vfull + st : kfull + st, *empty = is_v ? vempty + st : kempty + st;
+            unsigned char *tile = (is_v ? sv : sk) + st * C::kTileBytes;
+            const uint32_t dst0 = tc::saddr(tile);
+            const uint32_t *from = rows[pw][cur.slot];
+            const unsigned char *cache = p.cache + half * (C::kRow / 2);
+            // short rolled loops: the roles' straight-line code would not stay
+            // in the instruction caches side by side
+            if constexpr (FP8) {
+                constexpr int kW = D / 16, kR = 32 / kW;  // 16-byte words of a row's half; rows a warp takes at once
+                constexpr int kB = 4, kN = 128 / (kR * kB);
+                const int c = lane % kW, r = lane / kW;
+                uint4 v[kB], nv[kB];
+                auto load = [&](int bt, uint4 (&to)[kB]) {
+                    uint32_t src[kB];
 #pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    uint64_t *full = half ? vfull + st : kfull + st, *empty = half ? vempty + st : kempty + st;
-                    const uint32_t dst0 = tc::saddr((half ? sv : sk) + st * C::kTileBytes);
-                    if constexpr (FP8) {
-                        constexpr int kW = D / 16, kIt = kW;  // 16-byte words of a row's half; 32 rows x kW words / 32 lanes
-                        uint4 v[kIt];
+                    for (int i = 0; i < kB; i++)
+                        src[i] = from[(bt * kB + i) * kR + r];
 #pragma unroll
-                        for (int i = 0; i < kIt; i++) {
-                            const int idx = i * 32 + lane, y = idx / kW, c = idx % kW;
-                            const unsigned long long src = __shfl_sync(0xffffffffu, row, y);
-                            v[i] = make_uint4(0, 0, 0, 0);
-                            if ((bits >> y) & 1u)
-                                v[i] = __ldg(reinterpret_cast<const uint4 *>(src + half * D + 16 * c));
-                        }
-                        ok = ok && bar_wait(empty, parity, abort);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok)
-                            break;
+                    for (int i = 0; i < kB; i++) {
+                        to[i] = make_uint4(0, 0, 0, 0);
+                        if (src[i] != ~0u)
+                            to[i] = __ldg(reinterpret_cast<const uint4 *>(cache + (int64_t)src[i] * C::kRow + 16 * c));
+                    }
+                };
+                load(0, v);
+                ok = bar_wait(empty, parity, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+#pragma unroll 1
+                for (int bt = 0; bt < kN; bt++) {
+                    if (bt + 1 < kN)
+                        load(bt + 1, nv);
 #pragma unroll
-                        for (int i = 0; i < kIt; i++) {
-                            const int idx = i * 32 + lane, y = idx / kW, c = idx % kW, yy = pw * 32 + y;
-                            uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                            if (half && drafted && key0 + yy >= ctx) {
-#pragma unroll
-                                for (int k = 0; k < 4; k++)
-                                    if (nonfinite_word(q[k], true)) {
-#pragma unroll
-                                        for (int e = 0; e < 4; e++)
-                                            if (((q[k] >> (8 * e)) & 0x7fu) == 0x7fu)
-                                                q[k] &= ~(0xffu << (8 * e));
-                                        bad[item_no & 15] = 1;
-                                    }
-                            }
-                            uint32_t o[8];
-#pragma unroll
-                            for (int k = 0; k < 4; k++)
-                                o[2 * k] = e4m3_to_half2((uint16_t)q[k]), o[2 * k + 1] = e4m3_to_half2((uint16_t)(q[k] >> 16));
-#pragma unroll
-                            for (int k = 0; k < 2; k++) {
-                                const int cc = 2 * c + k;  // 16-byte word of the fp16 row
-                                const uint32_t at = dst0 + (cc >> 3) * 16384 + yy * 128 + (((cc & 7) ^ (yy & 7)) << 4);
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(o[4 * k]), "r"(o[4 * k + 1]),
-                                             "r"(o[4 * k + 2]), "r"(o[4 * k + 3])
-                                             : "memory");
-                            }
-                        }
-                        if (half == 0 && lane == 0)
-                            live[x & 7][pw] = bits;
-                        fence_async();
-                        bar_arrive(full);
-                        if (half == 0 && lane == 0)
-                            bar_arrive(full);
-                    } else {
-                        constexpr int kW = D / 8, kIt = kW;
-                        ok = ok && bar_wait(empty, parity, abort);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok)
-                            break;
-#pragma unroll
-                        for (int i = 0; i < kIt; i++) {
-                            const int idx = i * 32 + lane, y = idx / kW, c = idx % kW, yy = pw * 32 + y;
-                            const unsigned long long src = __shfl_sync(0xffffffffu, row, y);
-                            cp16(dst0 + (c >> 3) * 16384 + yy * 128 + (((c & 7) ^ (yy & 7)) << 4),
-                                 reinterpret_cast<const unsigned char *>(src) + half * 2 * D + 16 * c, (bits >> y) & 1u);
-                        }
-                        if (half == 0 && lane == 0) {
-                            live[x & 7][pw] = bits;
-                            bar_arrive(full);
-                        }
-                        if (half && drafted) {
-                            // infinities and NaN among the drafted V: zeroed here, accounted for at the end
-                            asm volatile("cp.async.wait_all;" ::: "memory");
-                            for (int i = 0; i < kIt; i++) {
-                                const int idx = i * 32 + lane, y = idx / kW, c = idx % kW, yy = pw * 32 + y;
-                                if (key0 + yy < ctx)
-                                    continue;
-                                uint4 *at = reinterpret_cast<uint4 *>(sv + st * C::kTileBytes + (c >> 3) * 16384 + yy * 128 +
-                                                                      (((c & 7) ^ (yy & 7)) << 4));
-                                const uint4 v = *at;
-                                uint32_t q[4] = {v.x, v.y, v.z, v.w};
-                                bool hit = false;
-#pragma unroll
-                                for (int k = 0; k < 4; k++)
-                                    if (nonfinite_word(q[k], false)) {
-                                        hit = true;
-                                        if ((q[k] & 0x7f80u) == 0x7f80u)
-                                            q[k] &= 0xffff0000u;
-                                        if ((q[k] & 0x7f800000u) == 0x7f800000u)
-                                            q[k] &= 0xffffu;
-                                    }
-                                if (hit) {
-                                    *at = make_uint4(q[0], q[1], q[2], q[3]);
-                                    bad[item_no & 15] = 1;
+                    for (int i = 0; i < kB; i++) {
+                        const int y = (bt * kB + i) * kR + r;
+                        uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                        if (drafted && key0 + y >= cur.ctx) {
+#pragma unroll 1
+                            for (int k = 0; k < 16; k++) {
+                                const uint32_t wd = k < 4 ? q[0] : k < 8 ? q[1] : k < 12 ? q[2] : q[3];
+                                if (((wd >> (8 * (k & 3))) & 0x7fu) == 0x7fu) {
+                                    const uint32_t keep = ~(0xffu << (8 * (k & 3)));
+                                    q[0] &= k < 4 ? keep : 0xffffffffu, q[1] &= k >= 4 && k < 8 ? keep : 0xffffffffu;
+                                    q[2] &= k >= 8 && k < 12 ? keep : 0xffffffffu, q[3] &= k >= 12 ? keep : 0xffffffffu;
+                                    bad[cur.item & 15] = cur.item + 1;
                                 }
                             }
-                            fence_async();
-                            bar_arrive(full);
-                        } else {
-                            bar_arrive_copies(full);
+                        }
+                        uint32_t o[8];
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            o[2 * k] = e4m3_to_half2((uint16_t)q[k]), o[2 * k + 1] = e4m3_to_half2((uint16_t)(q[k] >> 16));
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            // 16-byte words 2 c and 2 c + 1 of the fp16 row, odd lanes the other way round (bank conflicts)
+                            const int kk = k ^ (c & 1), cc = 2 * c + kk;
+                            const uint32_t at = dst0 + (cc >> 3) * 16384 + y * 128 + (((cc & 7) ^ (y & 7)) << 4);
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(kk ? o[4] : o[0]), "r"(kk ? o[5] : o[1]),
+                                         "r"(kk ? o[6] : o[2]), "r"(kk ? o[7] : o[3])
+                                         : "memory");
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kB; i++)
+                        v[i] = nv[i];
+                }
+            } else {
+                constexpr int kW = D / 8, kR = 32 / kW, kB = 8;
+                const int c = lane % kW, r = lane / kW;
+                const uint32_t dc = dst0 + (c >> 3) * 16384;
+                ok = bar_wait(empty, parity, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+#pragma unroll 1
+                for (int y0 = 0; y0 < 128; y0 += kR * kB) {
+                    uint32_t src[kB];
+#pragma unroll
+                    for (int i = 0; i < kB; i++)
+                        src[i] = from[y0 + i * kR + r];
+#pragma unroll
+                    for (int i = 0; i < kB; i++) {
+                        const int y = y0 + i * kR + r;
+                        cp16(dc + y * 128 + (((c & 7) ^ (y & 7)) << 4),
+                             src[i] != ~0u ? cache + (int64_t)src[i] * C::kRow + 16 * c : p.cache, src[i] != ~0u);
+                    }
+                }
+                if (drafted) {
+                    // infinities and NaN among the drafted V: zeroed here, accounted for at the end
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+                    for (int y = r; y < 128; y += kR) {
+                        if (key0 + y < cur.ctx)
+                            continue;
+                        uint4 *at = reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4));
+                        const uint4 v = *at;
+                        uint32_t q[4] = {v.x, v.y, v.z, v.w};
+                        bool hit = false;
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            if (nonfinite_word(q[k], false)) {
+                                hit = true;
+                                if ((q[k] & 0x7f80u) == 0x7f80u)
+                                    q[k] &= 0xffff0000u;
+                                if ((q[k] & 0x7f800000u) == 0x7f800000u)
+                                    q[k] &= 0xffffu;
+                            }
+                        if (hit) {
+                            *at = make_uint4(q[0], q[1], q[2], q[3]);
+                            bad[cur.item & 15] = cur.item + 1;
                         }
                     }
                 }
-                if (!ok)
-                    break;
             }
-            base += n;
-            item_no++;
-            w = after;
+            if (!is_v) {
+#pragma unroll
+                for (int g = 0; g < 4; g++) {
+                    const unsigned bits = __ballot_sync(0xffffffffu, from[32 * g + lane] != ~0u);
+                    if (lane == 0)
+                        live[cur.x & 7][g] = bits;
+                }
+                if (lane == 0)
+                    bar_arrive(full);
+            }
+            if (FP8 || drafted) {
+                fence_async();
+                bar_arrive(full);
+            } else {
+                bar_arrive_copies(full);
+            }
+            cur = nx1;
+            nx1 = nx2;
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
@@ -412,17 +434,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const float ks = FP8 && p.k_scale ? __ldg(p.k_scale) : 1.0f, vs = FP8 && p.v_scale ? __ldg(p.v_scale) : 1.0f;
         const float base_scale = p.scale * kLog2e * ks;
-        Walk w = start();
         int base = 0, item_no = 0;
         int nS = 0, nO = 0;  // S tiles read, PV products issued (of this stream)
         int nJ = 0;          // items whose rows the streams shared
         bool ok = true;
-        while (w.u < hi && ok) {
-            const int n = share(w), rows = w.rq.nq * p.group;
-            const int h = w.item / w.rgs, row0 = (w.item - h * w.rgs) * 256;
-            const bool two = rows - row0 > 128;
-            const int64_t item_start = w.u - w.tile;
-            const bool begun = item_start >= lo, finished = item_start + w.tiles <= hi;
+        while (w.more() && ok) {
+            const int n = w.t1 - w.t0, rows = w.rq.nq * p.group;
+            const int h = w.head(), row0 = w.row0();
+            const bool two = RT == 2 && rows - row0 > 128;
+            const bool begun = w.begun(), finished = w.finished();
             const int rt = two ? s : 0, my = row0 + rt * 128 + r;
             const bool mine = my < rows, warp_live = row0 + rt * 128 + q4 * 32 < rows;
             const int i = mine ? my / p.group : 0, hq = h * p.group + (mine ? my - i * p.group : 0);
@@ -439,7 +459,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 if constexpr (FP8) {
                     float top = 0.0f;
                     if (!zero)
-#pragma unroll
+#pragma unroll 4
                         for (int k = 0; k < D / 8; k++) {
                             const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + k);
                             const uint32_t q[4] = {v.x, v.y, v.z, v.w};
@@ -455,7 +475,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     fix = e > 126 ? 0.5f : 1.0f;
                 }
                 if (two || s == 0) {
-#pragma unroll
+#pragma unroll 4
                     for (int k = 0; k < D / 8; k++) {
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (!zero)
@@ -480,7 +500,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
 
             for (int k = 0; k < steps; k++) {
                 const int j = two ? k : 2 * k + s;
-                const int key0 = (w.tile + j) * kKeysTc;
+                const int key0 = (w.t0 + j) * kKeysTc;
                 ok = ok && bar_wait(sfull + s, (uint32_t)nS & 1u, abort);
                 nS++;
                 ok = __all_sync(0xffffffffu, ok);
@@ -489,58 +509,55 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 fence_after();
                 if (warp_live) {
                     const int lx = (base + j) & 7;
-                    uint32_t vis[4] = {live[lx][0], live[lx][1], live[lx][2], live[lx][3]};  // bit b of vis[g]: key key0 + 32 g + b is seen
-                    const bool drafted = key0 + kKeysTc > w.rq.ctx;
-                    const bool masked = drafted || (vis[0] & vis[1] & vis[2] & vis[3]) != 0xffffffffu;
-                    if (masked) {
-                        const uint64_t *words = p.tree_mask + (int64_t)(w.rq.q0 + i) * p.mask_words;
-                        const int limit = p.mask_kind == 1 ? min(w.rq.nq, i + 1) : w.rq.nq;
-#pragma unroll
-                        for (int g = 0; g < 4; g++) {
-                            const int a0 = key0 + 32 * g - w.rq.ctx;  // the drafted token of bit 0; below 0: context
-                            if (a0 > -32) {
-                                const int sh = a0 < 0 ? -a0 : 0, a = a0 < 0 ? 0 : a0;  // bits below sh are context
-                                uint32_t t = 0xffffffffu;
-                                if (p.mask_kind == 2) {
-                                    const int wd = a >> 6, bt = a & 63;
-                                    uint64_t y = wd < p.mask_words ? __ldg(words + wd) >> bt : 0ull;
-                                    if (bt > 32 && wd + 1 < p.mask_words)
-                                        y |= __ldg(words + wd + 1) << (64 - bt);
-                                    t = (uint32_t)y;
-                                }
-                                const int room = limit - a;
-                                t = room <= 0 ? 0u : room < 32 ? t & ((1u << room) - 1u) : t;
-                                vis[g] &= sh ? (t << sh) | ((1u << sh) - 1u) : t;
+                    const uint32_t all = live[lx][0] & live[lx][1] & live[lx][2] & live[lx][3];
+                    const bool masked = key0 + kKeysTc > w.rq.ctx || all != 0xffffffffu;
+                    // bit b of visible(g): key key0 + 32 g + b is seen
+                    auto visible = [&](int g) {
+                        uint32_t vis = mine ? live[lx][g] : 0u;
+                        const int a0 = key0 + 32 * g - w.rq.ctx;  // the drafted token of bit 0; below 0: context
+                        if (a0 > -32) {
+                            const int sh = a0 < 0 ? -a0 : 0, a = a0 < 0 ? 0 : a0;  // bits below sh are context
+                            uint32_t t = 0xffffffffu;
+                            if (p.mask_kind == 2) {
+                                const uint64_t *words = p.tree_mask + (int64_t)(w.rq.q0 + i) * p.mask_words;
+                                const int wd = a >> 6, bt = a & 63;
+                                uint64_t y = wd < p.mask_words ? __ldg(words + wd) >> bt : 0ull;
+                                if (bt > 32 && wd + 1 < p.mask_words)
+                                    y |= __ldg(words + wd + 1) << (64 - bt);
+                                t = (uint32_t)y;
                             }
-                            if (!mine)
-                                vis[g] = 0;
+                            const int room = (p.mask_kind == 1 ? min(w.rq.nq, i + 1) : w.rq.nq) - a;
+                            t = room <= 0 ? 0u : room < 32 ? t & ((1u << room) - 1u) : t;
+                            vis &= sh ? (t << sh) | ((1u << sh) - 1u) : t;
                         }
-                    }
-                    // scores of half of the keys, -inf where not seen
-                    auto load_half = [&](int half, uint32_t (&x)[64]) {
-                        tmem_ld64(tmem + lanes + kS[s] + 64 * half, x);
+                        return vis;
+                    };
+                    // 32 scores, -inf where not seen
+                    auto load32 = [&](int g, uint32_t (&x)[32]) {
+                        tmem_ld32(tmem + lanes + kS[s] + 32 * g, x);
                         if (masked) {
+                            const uint32_t vis = visible(g);
 #pragma unroll
-                            for (int e = 0; e < 64; e++)
-                                if (!((vis[2 * half + (e >> 5)] >> (e & 31)) & 1u))
+                            for (int e = 0; e < 32; e++)
+                                if (!((vis >> e) & 1u))
                                     x[e] = 0xff800000u;
                         }
                     };
-                    // ---- maximum
-                    float top = -INFINITY;
+                    // ---- maximum.  Rolled loops over 32 scores, read again below:
+                    // all 128 at once took the registers and, unrolled, more time
+                    // in instruction fetches than this takes in all
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int g = 0; g < 4; g++) {
+                        uint32_t x[32];
+                        load32(g, x);
 #pragma unroll
-                    for (int half = 0; half < 2; half++) {
-                        uint32_t x[64];
-                        load_half(half, x);
-                        float t0 = __uint_as_float(x[0]), t1 = __uint_as_float(x[1]), t2 = __uint_as_float(x[2]), t3 = __uint_as_float(x[3]);
+                        for (int e = 0; e < 32; e += 8)
 #pragma unroll
-                        for (int e = 4; e < 64; e += 4) {
-                            t0 = fmaxf(t0, __uint_as_float(x[e])), t1 = fmaxf(t1, __uint_as_float(x[e + 1]));
-                            t2 = fmaxf(t2, __uint_as_float(x[e + 2])), t3 = fmaxf(t3, __uint_as_float(x[e + 3]));
-                        }
-                        top = fmaxf(top, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)));
+                            for (int k2 = 0; k2 < 4; k2++)
+                                top[k2] = max3(top[k2], __uint_as_float(x[e + 2 * k2]), __uint_as_float(x[e + 2 * k2 + 1]));
                     }
-                    const float t = top * c;
+                    const float t = max3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
                     const bool grow = t > m + kLazy || (m == -INFINITY && t > m);
                     if (__any_sync(0xffffffffu, grow)) {
                         const float old = m;
@@ -554,7 +571,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                             if (!ok)
                                 break;
                             fence_after();
-#pragma unroll
+#pragma unroll 1
                             for (int d = 0; d < D; d += 32) {
                                 uint32_t o[32];
                                 tmem_ld32(tmem + lanes + kO[s] + d, o);
@@ -567,40 +584,38 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     }
                     const float mu = m == -INFINITY ? 0.0f : m;
                     const uint64_t m2 = pr(-mu, -mu);
+                    // s c - m in one rounding shows m's own where that is large
+                    // (scores beyond 2^24): the product is rounded first there
+                    const bool apart = __any_sync(0xffffffffu, fabsf(mu) > 16777216.0f);
                     uint64_t sum0 = 0, sum1 = 0;
-                    // s c - m in one rounding; where m is so large that its own rounding
-                    // shows in that (scores beyond 2^24), the product is rounded first
-                    auto weights = [&](auto apart) {
+#pragma unroll 1
+                    for (int g = 0; g < 4; g++) {
+                        uint32_t x[32], pk[16];
+                        load32(g, x);
+                        if (apart) {
 #pragma unroll
-                        for (int half = 0; half < 2; half++) {
-                            uint32_t x[64], pk[32];
-                            load_half(half, x);
+                            for (int e = 0; e < 32; e++)
+                                x[e] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x[e]), c), mu));
+                        } else {
 #pragma unroll
-                            for (int e = 0; e < 64; e += 4) {
-                                const uint64_t x0 = pr(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                                const uint64_t x1 = pr(__uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-                                float a0, a1, a2, a3;
-                                if constexpr (decltype(apart)::value) {
-                                    a0 = __fsub_rn(__fmul_rn(__uint_as_float(x[e]), c), mu), a1 = __fsub_rn(__fmul_rn(__uint_as_float(x[e + 1]), c), mu);
-                                    a2 = __fsub_rn(__fmul_rn(__uint_as_float(x[e + 2]), c), mu), a3 = __fsub_rn(__fmul_rn(__uint_as_float(x[e + 3]), c), mu);
-                                } else {
-                                    unpr(fma2(x0, c2, m2), a0, a1);
-                                    unpr(fma2(x1, c2, m2), a2, a3);
-                                }
-                                a0 = ex2(a0), a1 = ex2(a1), a2 = ex2(a2), a3 = ex2(a3);
-                                sum0 = add2(sum0, pr(a0, a1));
-                                sum1 = add2(sum1, pr(a2, a3));
-                                pk[e / 2] = pack2<FP8>(a0, a1);
-                                pk[e / 2 + 1] = pack2<FP8>(a2, a3);
+                            for (int e = 0; e < 32; e += 2) {
+                                float a0, a1;
+                                unpr(fma2(pr(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, m2), a0, a1);
+                                x[e] = __float_as_uint(a0), x[e + 1] = __float_as_uint(a1);
                             }
-                            // columns 32 half .. of P lie over scores that are used up
-                            tmem_st32(tmem + lanes + kS[s] + 32 * half, pk);
                         }
-                    };
-                    if (__any_sync(0xffffffffu, fabsf(mu) > 16777216.0f))
-                        weights(std::true_type{});
-                    else
-                        weights(std::false_type{});
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const float a0 = ex2(__uint_as_float(x[e])), a1 = ex2(__uint_as_float(x[e + 1]));
+                            const float a2 = ex2(__uint_as_float(x[e + 2])), a3 = ex2(__uint_as_float(x[e + 3]));
+                            sum0 = add2(sum0, pr(a0, a1));
+                            sum1 = add2(sum1, pr(a2, a3));
+                            pk[e / 2] = pack2<FP8>(a0, a1);
+                            pk[e / 2 + 1] = pack2<FP8>(a2, a3);
+                        }
+                        // columns 16 g .. of P lie over scores that are used up
+                        tmem_st16(tmem + lanes + kS[s] + 16 * g, pk);
+                    }
                     float a0, a1;
                     unpr(add2(sum0, sum1), a0, a1);
                     l += a0 + a1;
@@ -641,7 +656,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             }
             if (!ok)
                 break;
-            const int is_bad = bad[item_no & 15];
+            const bool is_bad = bad[item_no & 15] == item_no + 1;
             if ((two || s == 0) && warp_live) {
                 const bool other = !two && n > 1;
                 float *part = parts + ((int64_t)cta * 2 + (begun ? 1 : 0)) * C::kPart + rt * C::kRowPart + r;
@@ -649,7 +664,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 const float inv = l > 0.0f ? vs / l : l == 0.0f ? 0.0f : l;
                 const int64_t at = (int64_t)(w.rq.q0 + i) * p.num_heads + hq;
                 uint16_t *dst = p.out + at * D;
-#pragma unroll
+#pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
                     uint32_t o[32];
                     tmem_ld32(tmem + lanes + kO[0 + (two ? s : 0)] + d, o);
@@ -669,18 +684,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
 #pragma unroll
                         for (int e = 0; e < 32; e++)
                             v[e] = __uint_as_float(o[e]) * inv;
-                        if (is_bad) {
-                            for (int a = 0; a < w.rq.nq; a++) {
-                                if (!sees(p, w.rq, i, a))
-                                    continue;
-#pragma unroll
-                                for (int e = 0; e < 32; e++) {
-                                    const float z = drafted_v<D, FP8>(p, w.b, w.rq.ctx, h, a, d + e);
-                                    if (!(fabsf(z) <= 3.4028235e38f))
-                                        v[e] += z;
-                                }
-                            }
-                        }
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
                             *reinterpret_cast<uint4 *>(dst + d + e) =
@@ -690,8 +693,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 }
                 if (!direct)
                     part[D * 128] = m, part[(D + 1) * 128] = l;
-                else if (mine)
+                else if (mine) {
+                    if (is_bad)
+                        add_nonfinite<D, FP8>(p, w.b, w.rq, h, i, dst, 0, D);
                     p.lse[at] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+                }
             }
             fence_before();
             if (!two && s == 0)
@@ -700,14 +706,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 if (begun && !finished) {
                     PartDesc &d = descs[cta];
                     d.q0 = w.rq.q0, d.rows = rows, d.row0 = row0, d.h = h, d.nq = w.rq.nq, d.ctx = w.rq.ctx, d.b = w.b;
-                    d.last = (int32_t)(((unsigned long long)(item_start + w.tiles) * n_cta - 1) / (unsigned long long)total);
+                    d.last = w.last_cta(total, n_cta);
                 }
                 if (is_bad && !(begun && finished))
                     descs[cta].bad[begun ? 1 : 0] = 1;
             }
             base += n;
             item_no++;
-            next(w, n);
+            w.next(p);
         }
     }
     __syncthreads();
@@ -730,10 +736,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
 
 // Joins the parts of the item that CTA blockIdx.x began and did not finish:
 // block y takes 32 dims (y % (D / 32)) of row tile y / (D / 32), a thread per row.
-template <int D, bool FP8>
+template <int D, bool FP8, int RT>
 __global__ void __launch_bounds__(128) join_tc_kernel(const __grid_constant__ AttnParams p, int ctas)
 {
-    using C = TcCfg<D, FP8>;
+    using C = TcCfg<D, FP8, RT>;
     pdl_enter();
     const int r = threadIdx.x, rt = blockIdx.y / (D / 32), d0 = (blockIdx.y % (D / 32)) * 32;
     const PartDesc *descs = reinterpret_cast<const PartDesc *>(p.parts);
@@ -771,23 +777,21 @@ __global__ void __launch_bounds__(128) join_tc_kernel(const __grid_constant__ At
     const int64_t at = (int64_t)(d.q0 + i) * p.num_heads + hq;
     if (d0 == 0)
         p.lse[at] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
-    const Request rq{d.q0, d.nq, d.ctx};
 #pragma unroll
-    for (int e = 0; e < 32; e++) {
+    for (int e = 0; e < 32; e++)
         o[e] *= inv;
-        if (bad)
-            o[e] += nonfinite_sum<D, FP8>(p, d.b, rq, d.h, i, d0 + e);
-    }
 #pragma unroll
     for (int e = 0; e < 32; e += 8)
         *reinterpret_cast<uint4 *>(p.out + at * D + d0 + e) =
             make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
                        pack_bf16x2(o[e + 6], o[e + 7]));
+    if (bad)
+        add_nonfinite<D, FP8>(p, d.b, Request{d.q0, d.nq, d.ctx}, d.h, i, p.out + at * D, d0, d0 + 32);
 }
 
 // ------------------------------------------------------------------ launches
 
-template <int D, bool FP8>
+template <int D, bool FP8, int RT>
 cudaError_t attention_tc_ctas(int &ctas)
 {
     static int cached[64];
@@ -801,7 +805,8 @@ cudaError_t attention_tc_ctas(int &ctas)
     if (have == 0) {
         e = cudaDeviceGetAttribute(&have, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(attention_tc_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, TcCfg<D, FP8>::kSmem);
+            e = cudaFuncSetAttribute(attention_tc_kernel<D, FP8, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     TcCfg<D, FP8, RT>::kSmem);
         if (e != cudaSuccess)
             return e;
         __atomic_store_n(&cached[dev], have, __ATOMIC_RELEASE);
@@ -810,26 +815,26 @@ cudaError_t attention_tc_ctas(int &ctas)
     return cudaSuccess;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int RT>
 int64_t attention_tc_bytes(cudaError_t &e)
 {
     int ctas = 0;
-    e = attention_tc_ctas<D, FP8>(ctas);
-    return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * (int64_t)TcCfg<D, FP8>::kPart * 4) : 0;
+    e = attention_tc_ctas<D, FP8, RT>(ctas);
+    return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * (int64_t)TcCfg<D, FP8, RT>::kPart * 4) : 0;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, int RT>
 cudaError_t attention_tc(const AttnParams &p, cudaStream_t stream)
 {
-    using C = TcCfg<D, FP8>;
+    using C = TcCfg<D, FP8, RT>;
     int ctas = 0;
-    cudaError_t e = attention_tc_ctas<D, FP8>(ctas);
+    cudaError_t e = attention_tc_ctas<D, FP8, RT>(ctas);
     if (e == cudaSuccess)
-        e = launch_pdl(attention_tc_kernel<D, FP8>, ctas, kTcThreads, C::kSmem, stream, p);
+        e = launch_pdl(attention_tc_kernel<D, FP8, RT>, ctas, kTcThreads, C::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(2 * (D / 32)));
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(RT * (D / 32)));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -837,27 +842,31 @@ cudaError_t attention_tc(const AttnParams &p, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_tc_kernel<D, FP8>, p, ctas);
+    return cudaLaunchKernelEx(&cfg, join_tc_kernel<D, FP8, RT>, p, ctas);
 }
 
 template <int D>
-int64_t workspace_tc(bool fp8, cudaError_t &e)
+int64_t workspace_tc(int rt, bool fp8, cudaError_t &e)
 {
-    return fp8 ? attention_tc_bytes<D, true>(e) : attention_tc_bytes<D, false>(e);
+    if (rt == 1)
+        return fp8 ? attention_tc_bytes<D, true, 1>(e) : attention_tc_bytes<D, false, 1>(e);
+    return fp8 ? attention_tc_bytes<D, true, 2>(e) : attention_tc_bytes<D, false, 2>(e);
 }
 
 template <int D>
-cudaError_t attention_tc_d(const AttnParams &p, bool fp8, cudaStream_t stream)
+cudaError_t attention_tc_d(const AttnParams &p, int rt, bool fp8, cudaStream_t stream)
 {
-    return fp8 ? attention_tc<D, true>(p, stream) : attention_tc<D, false>(p, stream);
+    if (rt == 1)
+        return fp8 ? attention_tc<D, true, 1>(p, stream) : attention_tc<D, false, 1>(p, stream);
+    return fp8 ? attention_tc<D, true, 2>(p, stream) : attention_tc<D, false, 2>(p, stream);
 }
 
-#define DSPARK_ATTN_TC_DECLARE(D)                                 \
-    extern template int64_t workspace_tc<D>(bool, cudaError_t &); \
-    extern template cudaError_t attention_tc_d<D>(const AttnParams &, bool, cudaStream_t);
-#define DSPARK_ATTN_TC_DEFINE(D)                           \
-    template int64_t workspace_tc<D>(bool, cudaError_t &); \
-    template cudaError_t attention_tc_d<D>(const AttnParams &, bool, cudaStream_t);
+#define DSPARK_ATTN_TC_DECLARE(D)                                      \
+    extern template int64_t workspace_tc<D>(int, bool, cudaError_t &); \
+    extern template cudaError_t attention_tc_d<D>(const AttnParams &, int, bool, cudaStream_t);
+#define DSPARK_ATTN_TC_DEFINE(D)                                \
+    template int64_t workspace_tc<D>(int, bool, cudaError_t &); \
+    template cudaError_t attention_tc_d<D>(const AttnParams &, int, bool, cudaStream_t);
 
 }  // namespace attn
 }  // namespace dspark
