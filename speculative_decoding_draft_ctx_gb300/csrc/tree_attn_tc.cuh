@@ -12,25 +12,28 @@
 // row, no shuffles) keep the tensor cores busy: with more than 128 rows a
 // stream is a half of the rows and every tile serves both; with up to 128
 // the streams share the rows and take every other tile, their results joined
-// in the end.  Tensor memory: scores S of both streams (128 fp32 columns
-// each, overwritten by the weights P, two 16-bit values a column, which feed
-// the second product from there) and both outputs (D columns each).
+// in the end.  Tensor memory: per stream two buffers of scores S (64 keys,
+// fp32 columns; overwritten by the weights P, two 16-bit values a column,
+// which feed the second product from there) and the output (D columns).
 //
-//  - producer warps (2 for K, 2 for V): gather the tiles through the block table
-//    into separate rings, bf16 with 16-byte asynchronous copies straight into
-//    the operands' 128-byte swizzle, fp8 through registers, converted to
+//  - producer warps (2 for K, 2 for V): gather the tiles through the block
+//    table into separate rings, bf16 with 16-byte asynchronous copies straight
+//    into the operands' 128-byte swizzle, fp8 through registers, converted to
 //    fp16 once per tile instead of once per row tile;
 //  - one thread issues S = Q K^T (depth D) and O += P V (V as the cache holds
-//    it: its N direction contiguous), in the order S0 S1 | PV0 S0' PV1 S1' |
-//    so that one stream's products run under the other's softmax;
-//  - softmax warps (8): 64 scores of a row at a time in registers, maximum,
+//    it: its N direction contiguous) for half tiles of 64 keys.  With a buffer
+//    of S per half, the scores of the next half are ready while a half is in
+//    the softmax: with one of 128 keys a stream waited for PV and the next QK
+//    of its own, and 4 in 9 cycles of every softmax warp were that wait;
+//  - softmax warps (8): 32 scores of a row at a time in registers, maximum,
 //    base-2 exponentials with paired fp32 instructions, P back to tensor
 //    memory.  The output is rescaled only when a row's maximum has grown by
 //    more than 2^8 since the value in use: until then the weights exceed 1,
 //    which costs neither range nor precision.
 //
-// 13 warps leave 128 registers a thread, so a row's 128 scores are read twice
-// (for the maximum and for the weights), 64 at a time.
+// Loops are rolled where a role's straight-line code would not stay in the
+// instruction caches beside the others' (unrolled, a warp's instruction took
+// about ten cycles).  13 warps leave 128 registers a thread.
 // Every wait is bounded; on expiry the CTA raises DSPARK_FLAG_TIMEOUT, stops
 // issuing, waits for its copies and products in flight, frees its tensor
 // memory and returns.
@@ -69,20 +72,29 @@ struct TcCfg {
     static_assert(kSmem + 6 * 1024 <= 227 * 1024, "shared memory");
 };
 
+// 64-key halves of the n tiles at w: the second half of a request's last tile
+// is left out where no token lies in it.
+template <typename W>
+__device__ __forceinline__ int tile_halves(const W &w, int n)
+{
+    return 2 * n - (w.finished() && w.rq.ctx + w.rq.nq <= (w.t1 - 1) * kKeysTc + kKeysTc / 2 ? 1 : 0);
+}
+
 template <int D, bool FP8, int RT>
 __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __grid_constant__ AttnParams p)
 {
     using C = TcCfg<D, FP8, RT>;
     using namespace tc;
     constexpr int NK = C::kStagesK, NV = C::kStagesV;
-    constexpr uint32_t kS[2] = {0, 128}, kO[2] = {256, 256 + 128};  // tensor-memory columns
-    constexpr uint32_t kIdQK = idesc(FP8, false, 128, kKeysTc), kIdPV = idesc(FP8, true, 128, D);
+    // tensor-memory columns: scores of stream s, half h at 128 s + 64 h; outputs at 256 + 128 s
+    constexpr uint32_t kO[2] = {256, 256 + 128};
+    constexpr uint32_t kIdQK = idesc(FP8, false, 128, kKeysTc / 2), kIdPV = idesc(FP8, true, 128, D);
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (tc::saddr(smem_raw) & 1023u)) & 1023u);
     unsigned char *sq = smem, *sk = smem + RT * C::kQBytes, *sv = sk + NK * C::kTileBytes;
-    __shared__ uint64_t kfull[NK], kempty[NK], vfull[NV], vempty[NV], qfull[2], sfull[2], pfull[2], ofull[2], jfull, jempty, done;
+    __shared__ uint64_t kfull[NK], kempty[NK], vfull[NV], vempty[NV], qfull[2], sfull[4], pfull[4], ofull[2], jfull, jempty, done;
     __shared__ uint32_t tmem_slot, live[8][4];
-    __shared__ uint32_t rows[kProducers][2][128];  // cache rows of each producer's job and its next; ~0: not there
+    __shared__ uint32_t rows[kProducers][2][64];  // cache rows of each producer's tile and its next; ~0: not there
     __shared__ int abort_flag;
     __shared__ int bad[16];  // item number + 1 where infinities or NaN came up among an item's drafted V
     __shared__ float join_ml[256];
@@ -92,18 +104,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int s = 0; s < NK; s++) {
-            bar_init(kfull + s, 32 + 1);  // a producer warp's copies, and its live masks
+            bar_init(kfull + s, 64 + 2);  // two producer warps' copies, and their live masks
             bar_init(kempty + s, 1);
         }
         for (int s = 0; s < NV; s++) {
-            bar_init(vfull + s, 32);
+            bar_init(vfull + s, 64);
             bar_init(vempty + s, 1);
         }
         for (int s = 0; s < 2; s++) {
             bar_init(qfull + s, 128);
-            bar_init(pfull + s, 4);
-            bar_init(sfull + s, 1);
             bar_init(ofull + s, 1);
+            for (int h = 0; h < 2; h++) {
+                bar_init(pfull + 2 * s + h, 4);
+                bar_init(sfull + 2 * s + h, 1);
+            }
         }
         bar_init(&jfull, 128);
         bar_init(&jempty, 128);
@@ -147,67 +161,79 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     if (warp == 12) {
         // ------------------------------------------------------------ the issuing thread
         if (lane == 0) {
-            int base = 0;            // tiles consumed before this item
-            int nq[2] = {0, 0};      // Q tiles used
-            int np[2] = {0, 0};      // P tiles used
+            int base = 0;                // tiles consumed before this item
+            int nq[2] = {0, 0};          // Q tiles used
+            uint32_t par = 0;            // parities of pfull
             bool ok = true;
             while (w.more() && ok) {
                 const int n = w.t1 - w.t0;
                 const bool two = RT == 2 && w.rq.nq * p.group - w.row0() > 128;
-                auto qk = [&](int s, int j, bool last) {
-                    const int x = base + j, st = x % NK;
+                const int halves = tile_halves(w, n);
+                // element e of stream s: half e & 1 of the stream's tile e / 2
+                auto tile_of = [&](int s, int e) { return two ? e >> 1 : 2 * (e >> 1) + s; };
+                auto count = [&](int s) {  // halves of the stream
+                    if (two)
+                        return halves;
+                    const int tiles = s == 0 ? (n + 1) >> 1 : n >> 1;
+                    return 2 * tiles - (((n - 1) & 1) == s && (halves & 1) ? 1 : 0);
+                };
+                auto last_half = [&](int j, int h) { return h == 1 || 2 * j + 1 == halves; };
+                auto qk = [&](int s, int e) {
+                    const int j = tile_of(s, e), h = e & 1, x = base + j, st = x % NK;
                     if (!ok || !bar_wait(kfull + st, (uint32_t)(x / NK) & 1u, abort)) {
                         ok = false;
                         return;
                     }
                     fence_async();
                     fence_after();
-                    const uint32_t a = tc::saddr(sq + (two ? s : 0) * C::kQBytes), b = tc::saddr(sk + st * C::kTileBytes);
+                    const uint32_t a = tc::saddr(sq + (two ? s : 0) * C::kQBytes);
+                    const uint32_t b = tc::saddr(sk + st * C::kTileBytes) + h * 8192;  // 64 keys of 128 bytes
+                    const uint32_t d = tmem + 128 * s + 64 * h;
 #pragma unroll
                     for (int k = 0; k < D / 16; k++)
-                        mma_ss(tmem + kS[s], desc128(a + (k / 4) * 16384 + (k % 4) * 32, 16),
-                               desc128(b + (k / 4) * 16384 + (k % 4) * 32, 16), kIdQK, k != 0);
-                    mma_commit(sfull + s);
-                    if (last)
+                        mma_ss(d, desc128(a + (k / 4) * 16384 + (k % 4) * 32, 16), desc128(b + (k / 4) * 16384 + (k % 4) * 32, 16),
+                               kIdQK, k != 0);
+                    mma_commit(sfull + 2 * s + h);
+                    if ((!two || s == 1) && last_half(j, h))
                         mma_commit(kempty + st);
                 };
-                auto pv = [&](int s, int j, bool first, bool last) {
-                    const int x = base + j, st = x % NV;
-                    if (!ok || !bar_wait(vfull + st, (uint32_t)(x / NV) & 1u, abort) ||
-                        !bar_wait(pfull + s, (uint32_t)np[s] & 1u, abort)) {
+                auto pv = [&](int s, int e) {
+                    const int j = tile_of(s, e), h = e & 1, x = base + j, st = x % NV, pb = 2 * s + h;
+                    if (!ok || !bar_wait(vfull + st, (uint32_t)(x / NV) & 1u, abort) || !bar_wait(pfull + pb, (par >> pb) & 1u, abort)) {
                         ok = false;
                         return;
                     }
-                    np[s]++;
+                    par ^= 1u << pb;
                     fence_async();
                     fence_after();
-                    const uint32_t b = tc::saddr(sv + st * C::kTileBytes);
+                    const uint32_t a = tmem + 128 * s + 64 * h;
+                    const uint32_t b = tc::saddr(sv + st * C::kTileBytes) + h * 8192;
 #pragma unroll
-                    for (int k = 0; k < kKeysTc / 16; k++)
-                        mma_ts(tmem + kO[s], tmem + kS[s] + 8 * k, desc128(b + k * 2048, 16384), kIdPV, !(first && k == 0));
+                    for (int k = 0; k < 4; k++)
+                        mma_ts(tmem + kO[s], a + 8 * k, desc128(b + k * 2048, 16384), kIdPV, !(e == 0 && k == 0));
                     mma_commit(ofull + s);
-                    if (last)
+                    if ((!two || s == 1) && last_half(j, h))
                         mma_commit(vempty + st);
                 };
                 for (int s = 0; s < (two ? 2 : 1) && ok; s++)
                     ok = bar_wait(qfull + s, (uint32_t)(nq[s]++) & 1u, abort);
-                qk(0, 0, !two);
-                if (two)
-                    qk(1, 0, true);
-                else if (n > 1)
-                    qk(1, 1, true);
-                for (int j = 0; j < n && ok; j++) {
-                    if (two) {
-                        pv(0, j, j == 0, false);
-                        if (j + 1 < n)
-                            qk(0, j + 1, false);
-                        pv(1, j, j == 0, true);
-                        if (j + 1 < n)
-                            qk(1, j + 1, true);
-                    } else {
-                        pv(j & 1, j, j < 2, true);
-                        if (j + 2 < n)
-                            qk(j & 1, j + 2, true);
+                const int c0 = count(0), c1 = count(1);
+#pragma unroll 1
+                for (int e = 0; e < 2; e++) {
+                    if (e < c0)
+                        qk(0, e);
+                    if (e < c1)
+                        qk(1, e);
+                }
+#pragma unroll 1
+                for (int e = 0; e < c0 && ok; e++) {  // c1 <= c0
+#pragma unroll 1
+                    for (int s = 0; s < 2; s++) {
+                        const int c = s ? c1 : c0;
+                        if (e < c)
+                            pv(s, e);
+                        if (e + 2 < c)
+                            qk(s, e + 2);
                     }
                 }
                 base += n;
@@ -218,128 +244,116 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         __syncwarp();
     } else if (warp >= 8) {
         // ------------------------------------------------------------ producers
-        // Two warps copy K tiles and two V tiles.  A stage of a ring belongs to
-        // one warp (an even or an odd one), so that a warp is never more than
-        // one use of a stage ahead of its barrier, whose parity it waits for.
-        // A warp looks the block numbers of its next tile but one up while it
-        // copies, and has the rows of its next tile fetched into L2, so that
-        // what is in flight is not bounded by the rings.
-        const int pw = warp - 8;
-        struct Job {
-            int tile, x, item, ctx, h;  // tile of the request; number of the tile and of the item in this CTA's share
-            int slot;                   // of rows[pw]
-            bool valid;
-        };
-        int phys[4], off[4];  // of the job looked up last: rows lane, lane + 32, ...; off < 0: past the end
-        const int half = pw >> 1;                       // 0: the warp copies K, 1: V
-        int gen_x = 0, gen_tile = w.t0, gen_item = 0;  // the next tile of the share
-        auto step = [&]() {
-            gen_x++;
-            if (++gen_tile >= w.t1) {
-                w.next(p);
-                gen_tile = w.t0;
-                gen_item++;
-            }
-        };
-        auto look = [&](Job &jb, int slot) {
-            while (w.more() && ((gen_x % (half ? NV : NK)) & 1) != (pw & 1))
-                step();
-            jb.valid = w.more();
-            if (!jb.valid)
+        // Two warps copy K, two V, each 64 rows of every tile.  While a warp
+        // copies a tile it has the next one's rows fetched into L2, so that what
+        // is in flight is not bounded by the rings, and looks up the blocks of
+        // the one after.
+        const int pw = warp - 8, half = pw >> 1, sub = pw & 1;  // half 0: K, 1: V
+        const bool is_v = half != 0;
+        const unsigned char *cache = p.cache + half * (C::kRow / 2);
+        unsigned char *ring = is_v ? sv : sk;
+        const int ns = is_v ? NV : NK;
+        int phys[2], off[2];  // of the tile looked up last: rows lane and lane + 32 of the warp's; off < 0: past the end
+        int look_tile = w.t0, look_head = w.more() ? w.head() : 0;
+        W lw = w;  // the walk of the look-ups; w is the walk of the copies
+        auto look = [&]() {
+            off[0] = off[1] = -1;
+            if (!lw.more())
                 return;
-            jb.tile = gen_tile, jb.x = gen_x, jb.item = gen_item, jb.ctx = w.rq.ctx, jb.h = w.head(), jb.slot = slot;
-            const int len = w.rq.ctx + w.rq.nq;
+            const int len = lw.rq.ctx + lw.rq.nq;
+            look_head = lw.head();
 #pragma unroll
-            for (int g = 0; g < 4; g++) {
-                const int j = gen_tile * kKeysTc + 32 * g + lane, blk = block_of(p, j);
-                off[g] = j < len ? j - blk * p.block_size : -1;
+            for (int g = 0; g < 2; g++) {
+                const int j = look_tile * kKeysTc + 64 * sub + 32 * g + lane, blk = block_of(p, j);
                 phys[g] = 0;
-                if (j < len)
-                    phys[g] = __ldg(p.table + w.b * p.table_stride + blk);
-            }
-            step();
-        };
-        // the addresses, once the block numbers have come, and the rows into L2
-        auto resolve = [&](const Job &jb) {
-            if (jb.valid) {
-#pragma unroll
-                for (int g = 0; g < 4; g++) {
-                    uint32_t at = ~0u;
-                    if (off[g] >= 0) {
-                        if (phys[g] < 0 || phys[g] >= p.num_blocks) {
-                            flags |= kFlagBlockRange;
-                        } else {
-                            at = (uint32_t)(((int64_t)phys[g] * p.num_kv_heads + jb.h) * p.block_size + off[g]);
-                            const unsigned char *row = p.cache + (int64_t)at * C::kRow + half * (C::kRow / 2);
-#pragma unroll
-                            for (int y = 0; y < C::kRow / 2; y += 128)
-                                asm volatile("prefetch.global.L2 [%0];" ::"l"(row + y));
-                        }
-                    }
-                    rows[pw][jb.slot][32 * g + lane] = at;
+                if (j < len) {
+                    off[g] = j - blk * p.block_size;
+                    phys[g] = __ldg(p.table + lw.b * p.table_stride + blk);
                 }
+            }
+            if (++look_tile >= lw.t1) {
+                lw.next(p);
+                look_tile = lw.t0;
+            }
+        };
+        // the rows' numbers, once the block numbers have come, and the rows into L2
+        auto resolve = [&](int slot) {
+#pragma unroll
+            for (int g = 0; g < 2; g++) {
+                uint32_t at = ~0u;
+                if (off[g] >= 0) {
+                    if (phys[g] < 0 || phys[g] >= p.num_blocks) {
+                        flags |= kFlagBlockRange;
+                    } else {
+                        at = (uint32_t)(((int64_t)phys[g] * p.num_kv_heads + look_head) * p.block_size + off[g]);
+                        const unsigned char *row = cache + (int64_t)at * C::kRow;
+#pragma unroll
+                        for (int y = 0; y < C::kRow / 2; y += 128)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(row + y));
+                    }
+                }
+                rows[pw][slot][32 * g + lane] = at;
             }
             __syncwarp();
         };
-        Job cur, nx1, nx2;
-        look(cur, 0);
-        resolve(cur);
-        look(nx1, 1);
-        bool ok = true;
-        while (cur.valid && ok) {
-            resolve(nx1);
-            look(nx2, cur.slot);
-            const bool is_v = half != 0;
-            const int st = is_v ? cur.x % NV : cur.x % NK, key0 = cur.tile * kKeysTc;
-            const uint32_t parity = ((uint32_t)(is_v ? cur.x / NV : cur.x / NK) & 1u) ^ 1u;
-            const bool drafted = is_v && key0 + kKeysTc > cur.ctx;
-            uint64_t *full = is_v ? vfull + st : kfull + st, *empty = is_v ? vempty + st : kempty + st;
-            unsigned char *tile = (is_v ? sv : sk) + st * C::kTileBytes;
-            const uint32_t dst0 = tc::saddr(tile);
-            const uint32_t *from = rows[pw][cur.slot];
-            const unsigned char *cache = p.cache + half * (C::kRow / 2);
-            // short rolled loops: the roles' straight-line code would not stay
-            // in the instruction caches side by side
+        constexpr int kW = D * (FP8 ? 1 : 2) / 16, kR = 32 / kW;  // 16-byte words of a row's half; rows a warp takes at once
+        const int c = lane % kW, r = lane / kW;
+        // fp8: half of the warp's rows at a time in registers, loaded a tile ahead
+        constexpr int kB = FP8 ? 32 / kR : 8;
+        uint4 va[FP8 ? kB : 1], vb[FP8 ? kB : 1];
+        auto load = [&](const uint32_t *from, uint4 *to) {
             if constexpr (FP8) {
-                constexpr int kW = D / 16, kR = 32 / kW;  // 16-byte words of a row's half; rows a warp takes at once
-                constexpr int kB = 4, kN = 128 / (kR * kB);
-                const int c = lane % kW, r = lane / kW;
-                uint4 v[kB], nv[kB];
-                auto load = [&](int bt, uint4 (&to)[kB]) {
-                    uint32_t src[kB];
+                uint32_t src[kB];
 #pragma unroll
-                    for (int i = 0; i < kB; i++)
-                        src[i] = from[(bt * kB + i) * kR + r];
+                for (int i = 0; i < kB; i++)
+                    src[i] = from[i * kR + r];
+#pragma unroll
+                for (int i = 0; i < kB; i++) {
+                    to[i] = make_uint4(0, 0, 0, 0);
+                    if (src[i] != ~0u)
+                        to[i] = __ldg(reinterpret_cast<const uint4 *>(cache + (int64_t)src[i] * C::kRow + 16 * c));
+                }
+            }
+        };
+        bool ok = true;
+        int x = 0, item = 0, tile = w.t0;  // tile and item number of the share; the request's tile
+        look();
+        resolve(0);
+        if (FP8 && w.more()) {
+            load(rows[pw][0], va);
+            load(rows[pw][0] + 32, vb);
+        }
+        look();
+        while (w.more() && ok) {
+            const int st = x % ns, key0 = tile * kKeysTc + 64 * sub, slot = x & 1;
+            const uint32_t parity = ((uint32_t)(x / ns) & 1u) ^ 1u;
+            const bool drafted = is_v && key0 + 64 > w.rq.ctx;
+            uint64_t *full = (is_v ? vfull : kfull) + st, *empty = (is_v ? vempty : kempty) + st;
+            unsigned char *dst = ring + st * C::kTileBytes;
+            const uint32_t dst0 = tc::saddr(dst);
+            const uint32_t *from = rows[pw][slot];
+            resolve(slot ^ 1);  // the next tile
+            look();
+            ok = bar_wait(empty, parity, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+            if constexpr (FP8) {
+                auto store = [&](const uint4 *v, int row0) {
 #pragma unroll
                     for (int i = 0; i < kB; i++) {
-                        to[i] = make_uint4(0, 0, 0, 0);
-                        if (src[i] != ~0u)
-                            to[i] = __ldg(reinterpret_cast<const uint4 *>(cache + (int64_t)src[i] * C::kRow + 16 * c));
-                    }
-                };
-                load(0, v);
-                ok = bar_wait(empty, parity, abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
-#pragma unroll 1
-                for (int bt = 0; bt < kN; bt++) {
-                    if (bt + 1 < kN)
-                        load(bt + 1, nv);
-#pragma unroll
-                    for (int i = 0; i < kB; i++) {
-                        const int y = (bt * kB + i) * kR + r;
+                        const int y = 64 * sub + row0 + i * kR + r;
                         uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        if (drafted && key0 + y >= cur.ctx) {
+                        if (drafted && tile * kKeysTc + y >= w.rq.ctx) {
+                            // NaN among the drafted V: zeroed here, accounted for at the end
+                            if (nonfinite_word(q[0], true) || nonfinite_word(q[1], true) || nonfinite_word(q[2], true) || nonfinite_word(q[3], true)) {
+                                bad[item & 15] = item + 1;
+#pragma unroll
+                                for (int k = 0; k < 4; k++)
 #pragma unroll 1
-                            for (int k = 0; k < 16; k++) {
-                                const uint32_t wd = k < 4 ? q[0] : k < 8 ? q[1] : k < 12 ? q[2] : q[3];
-                                if (((wd >> (8 * (k & 3))) & 0x7fu) == 0x7fu) {
-                                    const uint32_t keep = ~(0xffu << (8 * (k & 3)));
-                                    q[0] &= k < 4 ? keep : 0xffffffffu, q[1] &= k >= 4 && k < 8 ? keep : 0xffffffffu;
-                                    q[2] &= k >= 8 && k < 12 ? keep : 0xffffffffu, q[3] &= k >= 12 ? keep : 0xffffffffu;
-                                    bad[cur.item & 15] = cur.item + 1;
-                                }
+                                    for (int e = 0; e < 32; e += 8)
+                                        if (((q[k] >> e) & 0x7fu) == 0x7fu)
+                                            q[k] &= ~(0xffu << e);
                             }
                         }
                         uint32_t o[8];
@@ -356,39 +370,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                                          : "memory");
                         }
                     }
-#pragma unroll
-                    for (int i = 0; i < kB; i++)
-                        v[i] = nv[i];
-                }
+                };
+                store(va, 0);
+                load(rows[pw][slot ^ 1], va);
+                store(vb, 32);
+                load(rows[pw][slot ^ 1] + 32, vb);
             } else {
-                constexpr int kW = D / 8, kR = 32 / kW, kB = 8;
-                const int c = lane % kW, r = lane / kW;
                 const uint32_t dc = dst0 + (c >> 3) * 16384;
-                ok = bar_wait(empty, parity, abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
 #pragma unroll 1
-                for (int y0 = 0; y0 < 128; y0 += kR * kB) {
+                for (int y0 = 0; y0 < 64; y0 += kR * kB) {
                     uint32_t src[kB];
 #pragma unroll
                     for (int i = 0; i < kB; i++)
                         src[i] = from[y0 + i * kR + r];
 #pragma unroll
                     for (int i = 0; i < kB; i++) {
-                        const int y = y0 + i * kR + r;
-                        cp16(dc + y * 128 + (((c & 7) ^ (y & 7)) << 4),
-                             src[i] != ~0u ? cache + (int64_t)src[i] * C::kRow + 16 * c : p.cache, src[i] != ~0u);
+                        const int y = 64 * sub + y0 + i * kR + r;
+                        cp16(dc + y * 128 + (((c & 7) ^ (y & 7)) << 4), src[i] != ~0u ? cache + (int64_t)src[i] * C::kRow + 16 * c : p.cache,
+                             src[i] != ~0u);
                     }
                 }
                 if (drafted) {
                     // infinities and NaN among the drafted V: zeroed here, accounted for at the end
                     asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll 1
-                    for (int y = r; y < 128; y += kR) {
-                        if (key0 + y < cur.ctx)
+                    for (int y = 64 * sub + r; y < 64 * sub + 64; y += kR) {
+                        if (tile * kKeysTc + y < w.rq.ctx)
                             continue;
-                        uint4 *at = reinterpret_cast<uint4 *>(tile + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4));
+                        uint4 *at = reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4));
                         const uint4 v = *at;
                         uint32_t q[4] = {v.x, v.y, v.z, v.w};
                         bool hit = false;
@@ -403,17 +412,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                             }
                         if (hit) {
                             *at = make_uint4(q[0], q[1], q[2], q[3]);
-                            bad[cur.item & 15] = cur.item + 1;
+                            bad[item & 15] = item + 1;
                         }
                     }
                 }
             }
             if (!is_v) {
 #pragma unroll
-                for (int g = 0; g < 4; g++) {
+                for (int g = 0; g < 2; g++) {
                     const unsigned bits = __ballot_sync(0xffffffffu, from[32 * g + lane] != ~0u);
                     if (lane == 0)
-                        live[cur.x & 7][g] = bits;
+                        live[x & 7][2 * sub + g] = bits;
                 }
                 if (lane == 0)
                     bar_arrive(full);
@@ -424,8 +433,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             } else {
                 bar_arrive_copies(full);
             }
-            cur = nx1;
-            nx1 = nx2;
+            __syncwarp();  // every lane is done with this tile's row numbers
+            x++;
+            if (++tile >= w.t1) {
+                w.next(p);
+                tile = w.t0;
+                item++;
+            }
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
@@ -435,7 +449,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         const float ks = FP8 && p.k_scale ? __ldg(p.k_scale) : 1.0f, vs = FP8 && p.v_scale ? __ldg(p.v_scale) : 1.0f;
         const float base_scale = p.scale * kLog2e * ks;
         int base = 0, item_no = 0;
-        int nS = 0, nO = 0;  // S tiles read, PV products issued (of this stream)
+        uint32_t spar = 0;   // parities of the stream's two sfull
+        int nO = 0;          // halves whose weights are out (of this stream)
         int nJ = 0;          // items whose rows the streams shared
         bool ok = true;
         while (w.more() && ok) {
@@ -446,7 +461,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             const int rt = two ? s : 0, my = row0 + rt * 128 + r;
             const bool mine = my < rows, warp_live = row0 + rt * 128 + q4 * 32 < rows;
             const int i = mine ? my / p.group : 0, hq = h * p.group + (mine ? my - i * p.group : 0);
-            const int steps = two ? n : s == 0 ? (n + 1) / 2 : n / 2;
+            const int halves = tile_halves(w, n);
+            const int mine_tiles = s == 0 ? (n + 1) / 2 : n / 2;
+            const int steps = two ? halves : 2 * mine_tiles - (((n - 1) & 1) == s && (halves & 1) ? 1 : 0);  // halves of the stream
             // ---- the query row.  A negative scale turns its sign, a zero one
             // zeroes it, so that the factor c of the scores is positive.
             float c = base_scale;
@@ -499,21 +516,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             float m = -INFINITY, l = 0.0f;  // the maximum in use (scaled, base 2), the sum of weights
 
             for (int k = 0; k < steps; k++) {
-                const int j = two ? k : 2 * k + s;
-                const int key0 = (w.t0 + j) * kKeysTc;
-                ok = ok && bar_wait(sfull + s, (uint32_t)nS & 1u, abort);
-                nS++;
+                const int j = two ? k >> 1 : 2 * (k >> 1) + s, hb = k & 1;
+                const int key0 = (w.t0 + j) * kKeysTc + 64 * hb;
+                const uint32_t ts = tmem + lanes + 128 * s + 64 * hb;
+                ok = ok && bar_wait(sfull + 2 * s + hb, (spar >> hb) & 1u, abort);
+                spar ^= 1u << hb;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
                 fence_after();
                 if (warp_live) {
                     const int lx = (base + j) & 7;
-                    const uint32_t all = live[lx][0] & live[lx][1] & live[lx][2] & live[lx][3];
-                    const bool masked = key0 + kKeysTc > w.rq.ctx || all != 0xffffffffu;
+                    const bool masked = key0 + 64 > w.rq.ctx || (live[lx][2 * hb] & live[lx][2 * hb + 1]) != 0xffffffffu;
                     // bit b of visible(g): key key0 + 32 g + b is seen
                     auto visible = [&](int g) {
-                        uint32_t vis = mine ? live[lx][g] : 0u;
+                        uint32_t vis = mine ? live[lx][2 * hb + g] : 0u;
                         const int a0 = key0 + 32 * g - w.rq.ctx;  // the drafted token of bit 0; below 0: context
                         if (a0 > -32) {
                             const int sh = a0 < 0 ? -a0 : 0, a = a0 < 0 ? 0 : a0;  // bits below sh are context
@@ -534,7 +551,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     };
                     // 32 scores, -inf where not seen
                     auto load32 = [&](int g, uint32_t (&x)[32]) {
-                        tmem_ld32(tmem + lanes + kS[s] + 32 * g, x);
+                        tmem_ld32(ts + 32 * g, x);
                         if (masked) {
                             const uint32_t vis = visible(g);
 #pragma unroll
@@ -543,12 +560,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                                     x[e] = 0xff800000u;
                         }
                     };
-                    // ---- maximum.  Rolled loops over 32 scores, read again below:
-                    // all 128 at once took the registers and, unrolled, more time
-                    // in instruction fetches than this takes in all
+                    // ---- maximum (the scores are read again below)
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int g = 0; g < 4; g++) {
+                    for (int g = 0; g < 2; g++) {
                         uint32_t x[32];
                         load32(g, x);
 #pragma unroll
@@ -566,6 +581,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                         l *= fr;
                         if (k > 0) {
                             // the products so far have to be in before they are rescaled
+                            // (S of this half came after the last but one)
                             ok = ok && bar_wait(ofull + s, (uint32_t)(nO - 1) & 1u, abort);
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok)
@@ -589,7 +605,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     const bool apart = __any_sync(0xffffffffu, fabsf(mu) > 16777216.0f);
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll 1
-                    for (int g = 0; g < 4; g++) {
+                    for (int g = 0; g < 2; g++) {
                         uint32_t x[32], pk[16];
                         load32(g, x);
                         if (apart) {
@@ -614,7 +630,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                             pk[e / 2 + 1] = pack2<FP8>(a2, a3);
                         }
                         // columns 16 g .. of P lie over scores that are used up
-                        tmem_st16(tmem + lanes + kS[s] + 16 * g, pk);
+                        tmem_st16(ts + 16 * g, pk);
                     }
                     float a0, a1;
                     unpr(add2(sum0, sum1), a0, a1);
@@ -624,16 +640,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(pfull + s);
+                    bar_arrive(pfull + 2 * s + hb);
                 nO++;
             }
             if (!ok)
                 break;
             // ---- the item ends here, or the CTA's share of it does
-            if (steps > 0) {
-                ok = bar_wait(ofull + s, (uint32_t)(nO - 1) & 1u, abort);
-                ok = __all_sync(0xffffffffu, ok);
-            }
+            // the last product is in; a parity tells neighbouring phases apart only,
+            // and the last S tells of the last product but two
+            for (int k = steps > 1 ? 2 : steps; k >= 1; k--)
+                ok = ok && bar_wait(ofull + s, (uint32_t)(nO - k) & 1u, abort);
+            ok = __all_sync(0xffffffffu, ok);
             fence_after();
             float y0 = 1.0f, y1 = 0.0f;  // factors of the two streams' sums
             if (!two) {
@@ -664,6 +681,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 const float inv = l > 0.0f ? vs / l : l == 0.0f ? 0.0f : l;
                 const int64_t at = (int64_t)(w.rq.q0 + i) * p.num_heads + hq;
                 uint16_t *dst = p.out + at * D;
+                // results go through this warp's own rows of the Q tile, which no
+                // product reads any more, so that rows are written whole
+                auto stage = [&](int y, int word) {
+                    return reinterpret_cast<uint4 *>(sq + rt * C::kQBytes + (word >> 3) * 16384 + (q4 * 32 + y) * 128 + (((word & 7) ^ (y & 7)) << 4));
+                };
 #pragma unroll 1
                 for (int d = 0; d < D; d += 32) {
                     uint32_t o[32];
@@ -686,10 +708,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                             v[e] = __uint_as_float(o[e]) * inv;
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4 *>(dst + d + e) =
+                            *stage(lane, (d + e) / 8) =
                                 make_uint4(pack_bf16x2(v[e], v[e + 1]), pack_bf16x2(v[e + 2], v[e + 3]), pack_bf16x2(v[e + 4], v[e + 5]),
                                            pack_bf16x2(v[e + 6], v[e + 7]));
                     }
+                }
+                if (direct) {
+                    __syncwarp();
+                    constexpr int kOW = D / 8, kOR = 32 / kOW;  // 16-byte words of a row, rows at once
+                    const int oc = lane % kOW;
+#pragma unroll 1
+                    for (int y = lane / kOW; y < 32; y += kOR) {
+                        const int my2 = row0 + rt * 128 + q4 * 32 + y;
+                        if (my2 >= rows)
+                            break;
+                        const int i2 = my2 / p.group;
+                        *reinterpret_cast<uint4 *>(p.out + ((int64_t)(w.rq.q0 + i2) * p.num_heads + h * p.group + (my2 - i2 * p.group)) * D + 8 * oc) =
+                            *stage(y, oc);
+                    }
+                    __syncwarp();
                 }
                 if (!direct)
                     part[D * 128] = m, part[(D + 1) * 128] = l;
