@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 namespace dspark {
 namespace tc {
 
@@ -114,6 +116,29 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 __device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+}
+
+// true in one lane of the (converged) warp, always the same
+__device__ __forceinline__ bool elect()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// f(integral_constant<int, v>) for 0 <= v < N: descriptors made of constants
+// stay in uniform registers, which is where tcgen05.mma takes them from
+template <int N, typename F>
+__device__ __forceinline__ void pick(int v, F f)
+{
+    if constexpr (N > 1) {
+        if (v == N - 1)
+            f(std::integral_constant<int, N - 1>{});
+        else
+            pick<N - 1>(v, f);
+    } else {
+        f(std::integral_constant<int, 0>{});
+    }
 }
 
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }

@@ -34,23 +34,13 @@ bool use_tc(int64_t rows, int group, int requests, int head_dim)
     return rows * group > kTcRows * requests;
 }
 
-// Row tiles of an item: one while the mean request's rows fit it (three
-// stages of each ring instead of two), else two (K|V read once for 256 rows).
-int row_tiles(int64_t rows, int group, int requests) { return rows * group > 128 * (int64_t)requests ? 2 : 1; }
-
-int64_t workspace_tc(int64_t rows, int group, int requests, int head_dim, bool fp8, cudaError_t &e)
-{
-    const int rt = row_tiles(rows, group, requests);
-    return head_dim == 64 ? attn::workspace_tc<64>(rt, fp8, e) : attn::workspace_tc<128>(rt, fp8, e);
-}
-
 }  // namespace
 
 int64_t tree_attention_workspace(int64_t rows, int num_heads, int num_kv_heads, int head_dim, int requests, bool fp8,
                                  cudaError_t &e)
 {
     if (use_tc(rows, num_heads / num_kv_heads, requests, head_dim))
-        return workspace_tc(rows, num_heads / num_kv_heads, requests, head_dim, fp8, e);
+        return head_dim == 64 ? attn::workspace_tc<64>(fp8, e) : attn::workspace_tc<128>(fp8, e);
     const int wr = attn::row_warps(rows, num_heads / num_kv_heads, requests);
     switch (head_dim) {
     case 64: return attn::workspace_d<64>(wr, fp8, e);
@@ -62,10 +52,7 @@ int64_t tree_attention_workspace(int64_t rows, int num_heads, int num_kv_heads, 
 cudaError_t launch_tree_attention(const AttnParams &p, int head_dim, bool fp8, cudaStream_t stream)
 {
     if (use_tc(p.num_rows, p.group, p.num_requests, head_dim))
-        {
-        const int rt = row_tiles(p.num_rows, p.group, p.num_requests);
-        return head_dim == 64 ? attn::attention_tc_d<64>(p, rt, fp8, stream) : attn::attention_tc_d<128>(p, rt, fp8, stream);
-    }
+        return head_dim == 64 ? attn::attention_tc_d<64>(p, fp8, stream) : attn::attention_tc_d<128>(p, fp8, stream);
     const int wr = attn::row_warps(p.num_rows, p.group, p.num_requests);
     switch (head_dim) {
     case 64: return attn::attention_d<64>(p, wr, fp8, stream);

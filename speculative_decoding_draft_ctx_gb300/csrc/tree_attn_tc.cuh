@@ -12,19 +12,20 @@
 // row, no shuffles) keep the tensor cores busy: with more than 128 rows a
 // stream is a half of the rows and every tile serves both; with up to 128
 // the streams share the rows and take every other tile, their results joined
-// in the end.  Tensor memory: per stream two buffers of scores S (64 keys,
-// fp32 columns; overwritten by the weights P, two 16-bit values a column,
-// which feed the second product from there) and the output (D columns).
+// in the end.  Tensor memory: scores S of both streams (128 fp32 columns
+// each, overwritten by the weights P, two 16-bit values a column, which feed
+// the second product from there) and both outputs (D columns each).
 //
 //  - producer warps (2 for K, 2 for V): gather the tiles through the block
 //    table into separate rings, bf16 with 16-byte asynchronous copies straight
 //    into the operands' 128-byte swizzle, fp8 through registers, converted to
 //    fp16 once per tile instead of once per row tile;
-//  - one thread issues S = Q K^T (depth D) and O += P V (V as the cache holds
-//    it: its N direction contiguous) for half tiles of 64 keys.  With a buffer
-//    of S per half, the scores of the next half are ready while a half is in
-//    the softmax: with one of 128 keys a stream waited for PV and the next QK
-//    of its own, and 4 in 9 cycles of every softmax warp were that wait;
+//  - a warp per stream issues S = Q K^T (depth D) and O += P V (V as the cache
+//    holds it: its N direction contiguous).  An MMA of 128 rows takes 64 cycles
+//    for any width up to 128, so scores come 128 keys at a time (half tiles
+//    with two buffers took the wait out of the softmax but doubled the first
+//    product: 395 against 293 us on two 131k contexts), while the weights of
+//    the first 64 keys go into the second product as soon as they are there;
 //  - softmax warps (8): 32 scores of a row at a time in registers, maximum,
 //    base-2 exponentials with paired fp32 instructions, P back to tensor
 //    memory.  The output is rescaled only when a row's maximum has grown by
@@ -33,13 +34,11 @@
 //
 // Loops are rolled where a role's straight-line code would not stay in the
 // instruction caches beside the others' (unrolled, a warp's instruction took
-// about ten cycles).  13 warps leave 128 registers a thread.
+// about ten cycles).  14 warps leave 128 registers a thread.
 // Every wait is bounded; on expiry the CTA raises DSPARK_FLAG_TIMEOUT, stops
 // issuing, waits for its copies and products in flight, frees its tensor
 // memory and returns.
 #pragma once
-
-#include <type_traits>
 
 #include "tc_ptx.cuh"
 #include "tree_attn_mma.cuh"
@@ -47,7 +46,7 @@
 namespace dspark {
 namespace attn {
 
-constexpr int kTcThreads = 416, kKeysTc = 128;  // 8 softmax warps, 4 producers, 1 that issues the products
+constexpr int kTcThreads = 448, kKeysTc = 128;  // 8 softmax warps, 4 producers, 2 that issue the products
 constexpr int kProducers = 4, kItemCostTc = 3;   // EXTRA of Walk, in tiles of kKeysTc keys
 constexpr float kLazy = 8.0f;  // growth of a maximum (log2) that waits for a rescale
 
@@ -58,17 +57,17 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-// RT: row tiles of 128 rows an item has at most (1 or 2).
-template <int D, bool FP8, int RT>
+template <int D, bool FP8>
 struct TcCfg {
-    // K is done with after the first product, V only after the softmax
-    static constexpr int kStagesK = D == 64 ? 4 : 2, kStagesV = D == 64 ? 4 : RT == 1 ? 3 : 2;
+    // Even: where the streams take turns, a stage belongs to one of them within
+    // an item, so that neither is ever two phases off a stage's barrier.
+    static constexpr int kStagesK = D == 64 ? 4 : 2, kStagesV = D == 64 ? 4 : 2;
     static constexpr int kTileBytes = kKeysTc * D * 2;    // one K or V tile, 16-bit
     static constexpr int kQBytes = 128 * D * 2;
     static constexpr int kRow = 2 * D * (FP8 ? 1 : 2);    // bytes of a cached token
-    static constexpr int kSmem = 1024 + RT * kQBytes + (kStagesK + kStagesV) * kTileBytes;
+    static constexpr int kSmem = 1024 + 2 * kQBytes + (kStagesK + kStagesV) * kTileBytes;
     static constexpr int kRowPart = (D + 2) * 128;        // floats of one row tile's part
-    static constexpr int kPart = RT * kRowPart;
+    static constexpr int kPart = 2 * kRowPart;
     static_assert(kSmem + 6 * 1024 <= 227 * 1024, "shared memory");
 };
 
@@ -80,19 +79,19 @@ __device__ __forceinline__ int tile_halves(const W &w, int n)
     return 2 * n - (w.finished() && w.rq.ctx + w.rq.nq <= (w.t1 - 1) * kKeysTc + kKeysTc / 2 ? 1 : 0);
 }
 
-template <int D, bool FP8, int RT>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __grid_constant__ AttnParams p)
 {
-    using C = TcCfg<D, FP8, RT>;
+    using C = TcCfg<D, FP8>;
     using namespace tc;
     constexpr int NK = C::kStagesK, NV = C::kStagesV;
-    // tensor-memory columns: scores of stream s, half h at 128 s + 64 h; outputs at 256 + 128 s
+    // tensor-memory columns: scores of stream s at 128 s, output at 256 + 128 s
     constexpr uint32_t kO[2] = {256, 256 + 128};
-    constexpr uint32_t kIdQK = idesc(FP8, false, 128, kKeysTc / 2), kIdPV = idesc(FP8, true, 128, D);
+    constexpr uint32_t kIdQK = idesc(FP8, false, 128, kKeysTc), kIdPV = idesc(FP8, true, 128, D);
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (tc::saddr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *sq = smem, *sk = smem + RT * C::kQBytes, *sv = sk + NK * C::kTileBytes;
-    __shared__ uint64_t kfull[NK], kempty[NK], vfull[NV], vempty[NV], qfull[2], sfull[4], pfull[4], ofull[2], jfull, jempty, done;
+    unsigned char *sq = smem, *sk = smem + 2 * C::kQBytes, *sv = sk + NK * C::kTileBytes;
+    __shared__ uint64_t kfull[NK], kempty[NK], vfull[NV], vempty[NV], qfull[2], sfull[2], pfull[4], ofull[2], jfull, jempty, go1, done[2];
     __shared__ uint32_t tmem_slot, live[8][4];
     __shared__ uint32_t rows[kProducers][2][64];  // cache rows of each producer's tile and its next; ~0: not there
     __shared__ int abort_flag;
@@ -105,23 +104,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     if (tid == 0) {
         for (int s = 0; s < NK; s++) {
             bar_init(kfull + s, 64 + 2);  // two producer warps' copies, and their live masks
-            bar_init(kempty + s, 1);
+            bar_init(kempty + s, 2);  // both streams
         }
         for (int s = 0; s < NV; s++) {
             bar_init(vfull + s, 64);
-            bar_init(vempty + s, 1);
+            bar_init(vempty + s, 2);
         }
         for (int s = 0; s < 2; s++) {
             bar_init(qfull + s, 128);
             bar_init(ofull + s, 1);
-            for (int h = 0; h < 2; h++) {
-                bar_init(pfull + 2 * s + h, 4);
-                bar_init(sfull + 2 * s + h, 1);
-            }
+            bar_init(sfull + s, 1);
+            bar_init(pfull + 2 * s, 4);
+            bar_init(pfull + 2 * s + 1, 4);
+            bar_init(done + s, 1);
         }
         bar_init(&jfull, 128);
         bar_init(&jempty, 128);
-        bar_init(&done, 1);
+        bar_init(&go1, 4);
         abort_flag = 0;
         for (int i = 0; i < 16; i++)
             bad[i] = 0;
@@ -137,7 +136,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
 
     // ---- this CTA's share of the units
     const int ctas = gridDim.x, cta = blockIdx.x;
-    using W = Walk<128 * RT, kKeysTc, kItemCostTc>;
+    using W = Walk<256, kKeysTc, kItemCostTc>;
     const Find f = find_request<kTcThreads>(
         p.num_requests, scratch, [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); },
         [&](int64_t total) {
@@ -158,90 +157,132 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     w.start(p, f.b >= 0 ? share_start(total, cta, n_cta) : 0, f.b >= 0 ? share_start(total, cta + 1, n_cta) : 0, f.b, f.before,
             mask_limit);
 
-    if (warp == 12) {
-        // ------------------------------------------------------------ the issuing thread
-        if (lane == 0) {
+    if (warp >= 12) {
+        // ------------------------------------------------------------ the issuing warps, one per stream
+        // The whole warp walks and waits, one lane issues: in a branch of one
+        // lane the descriptors went through vector registers and an MMA took
+        // 106 cycles to issue, of any size.
+        const bool leader = elect();
+        auto stream = [&](auto sc) {
+            constexpr int s = decltype(sc)::value;
             int base = 0;                // tiles consumed before this item
-            int nq[2] = {0, 0};          // Q tiles used
-            uint32_t par = 0;            // parities of pfull
+            int nq0 = 0, nq1 = 0, ngo = 0;  // uses of qfull[0], qfull[1] and go1
+            uint32_t par = 0;            // parities of the stream's two pfull
             bool ok = true;
             while (w.more() && ok) {
                 const int n = w.t1 - w.t0;
-                const bool two = RT == 2 && w.rq.nq * p.group - w.row0() > 128;
+                const bool two = w.rq.nq * p.group - w.row0() > 128;
                 const int halves = tile_halves(w, n);
-                // element e of stream s: half e & 1 of the stream's tile e / 2
-                auto tile_of = [&](int s, int e) { return two ? e >> 1 : 2 * (e >> 1) + s; };
-                auto count = [&](int s) {  // halves of the stream
-                    if (two)
-                        return halves;
-                    const int tiles = s == 0 ? (n + 1) >> 1 : n >> 1;
-                    return 2 * tiles - (((n - 1) & 1) == s && (halves & 1) ? 1 : 0);
+                const int steps = two ? n : s == 0 ? (n + 1) >> 1 : n >> 1;
+                auto tile_of = [&](int k) { return two ? k : 2 * k + s; };
+                auto wait = [&](uint64_t *bar, uint32_t parity) {
+                    ok = ok && bar_wait(bar, parity, abort);
+                    ok = __all_sync(0xffffffffu, ok);
                 };
-                auto last_half = [&](int j, int h) { return h == 1 || 2 * j + 1 == halves; };
-                auto qk = [&](int s, int e) {
-                    const int j = tile_of(s, e), h = e & 1, x = base + j, st = x % NK;
-                    if (!ok || !bar_wait(kfull + st, (uint32_t)(x / NK) & 1u, abort)) {
-                        ok = false;
-                        return;
-                    }
+                // a stage is free when both streams are done with it; where the
+                // streams take turns, the other one's word is given with this one's
+                auto release = [&](uint64_t *bar) {
+                    mma_commit(bar);
+                    if (!two)
+                        bar_arrive(bar);
+                };
+                auto qk = [&](int k) {
+                    const int st = (base + tile_of(k)) % NK;
                     fence_async();
                     fence_after();
-                    const uint32_t a = tc::saddr(sq + (two ? s : 0) * C::kQBytes);
-                    const uint32_t b = tc::saddr(sk + st * C::kTileBytes) + h * 8192;  // 64 keys of 128 bytes
-                    const uint32_t d = tmem + 128 * s + 64 * h;
+                    if (leader) {
+                        pick<NK>(st, [&](auto stc) {
+                            constexpr int S = decltype(stc)::value;
+                            const uint32_t b = tc::saddr(sk) + S * C::kTileBytes;
+                            auto issue = [&](uint32_t a) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; k++)
-                        mma_ss(d, desc128(a + (k / 4) * 16384 + (k % 4) * 32, 16), desc128(b + (k / 4) * 16384 + (k % 4) * 32, 16),
-                               kIdQK, k != 0);
-                    mma_commit(sfull + 2 * s + h);
-                    if ((!two || s == 1) && last_half(j, h))
-                        mma_commit(kempty + st);
-                };
-                auto pv = [&](int s, int e) {
-                    const int j = tile_of(s, e), h = e & 1, x = base + j, st = x % NV, pb = 2 * s + h;
-                    if (!ok || !bar_wait(vfull + st, (uint32_t)(x / NV) & 1u, abort) || !bar_wait(pfull + pb, (par >> pb) & 1u, abort)) {
-                        ok = false;
-                        return;
+                                for (int k = 0; k < D / 16; k++)
+                                    mma_ss(tmem + 128 * s, desc128(a + (k / 4) * 16384 + (k % 4) * 32, 16),
+                                           desc128(b + (k / 4) * 16384 + (k % 4) * 32, 16), kIdQK, k != 0);
+                            };
+                            if (s == 1 && two)
+                                issue(tc::saddr(sq) + C::kQBytes);
+                            else
+                                issue(tc::saddr(sq));
+                            mma_commit(sfull + s);
+                            release(kempty + S);
+                        });
                     }
-                    par ^= 1u << pb;
+                    __syncwarp();
+                };
+                auto pv = [&](int k, int h, bool last) {
+                    const int st = (base + tile_of(k)) % NV;
                     fence_async();
                     fence_after();
-                    const uint32_t a = tmem + 128 * s + 64 * h;
-                    const uint32_t b = tc::saddr(sv + st * C::kTileBytes) + h * 8192;
+                    if (leader) {
+                        pick<NV>(st, [&](auto stc) {
+                            pick<2>(h, [&](auto hc) {
+                                constexpr int S = decltype(stc)::value, H = decltype(hc)::value;
+                                const uint32_t b = tc::saddr(sv) + S * C::kTileBytes + H * 8192;  // 64 keys of 128 bytes
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        mma_ts(tmem + kO[s], a + 8 * k, desc128(b + k * 2048, 16384), kIdPV, !(e == 0 && k == 0));
+                                for (int i = 0; i < 4; i++)
+                                    mma_ts(tmem + kO[s], tmem + 128 * s + 32 * H + 8 * i, desc128(b + i * 2048, 16384), kIdPV,
+                                           i != 0 || H != 0 || k != 0);
+                                if (last)
+                                    release(vempty + S);
+                            });
+                        });
+                    }
+                    __syncwarp();
+                };
+                auto kwait = [&](int k) {
+                    const int x = base + tile_of(k);
+                    wait(kfull + x % NK, (uint32_t)(x / NK) & 1u);
+                };
+                // Where the streams share the rows, stream 1 waits for its own
+                // softmax to be here first: then everything before this item is
+                // done, and the phases below are the next ones of their barriers.
+                if (steps > 0) {
+                    if (s == 1 && !two)
+                        wait(&go1, (uint32_t)(ngo++) & 1u);
+                    wait(qfull + (two ? s : 0), (uint32_t)(two && s == 1 ? nq1 : nq0) & 1u);
+                }
+                nq0++;
+                nq1 += two;
+                if (steps > 0 && ok) {
+                    kwait(0);
+                    if (ok)
+                        qk(0);
+                }
+#pragma unroll 1
+                for (int k = 0; k < steps && ok; k++) {
+                    const int x = base + tile_of(k);
+                    const bool both = 2 * tile_of(k) + 1 != halves;
+                    wait(vfull + x % NV, (uint32_t)(x / NV) & 1u);
+                    if (k + 1 < steps)
+                        kwait(k + 1);
+                    wait(pfull + 2 * s, par & 1u);
+                    par ^= 1u;
+                    if (ok)
+                        pv(k, 0, !both);
+                    if (both && ok) {
+                        wait(pfull + 2 * s + 1, (par >> 1) & 1u);
+                        par ^= 2u;
+                        if (ok)
+                            pv(k, 1, true);
+                    }
+                    if (k + 1 < steps && ok)
+                        qk(k + 1);
+                }
+                if (steps > 0 && leader)
                     mma_commit(ofull + s);
-                    if ((!two || s == 1) && last_half(j, h))
-                        mma_commit(vempty + st);
-                };
-                for (int s = 0; s < (two ? 2 : 1) && ok; s++)
-                    ok = bar_wait(qfull + s, (uint32_t)(nq[s]++) & 1u, abort);
-                const int c0 = count(0), c1 = count(1);
-#pragma unroll 1
-                for (int e = 0; e < 2; e++) {
-                    if (e < c0)
-                        qk(0, e);
-                    if (e < c1)
-                        qk(1, e);
-                }
-#pragma unroll 1
-                for (int e = 0; e < c0 && ok; e++) {  // c1 <= c0
-#pragma unroll 1
-                    for (int s = 0; s < 2; s++) {
-                        const int c = s ? c1 : c0;
-                        if (e < c)
-                            pv(s, e);
-                        if (e + 2 < c)
-                            qk(s, e + 2);
-                    }
-                }
+                __syncwarp();
                 base += n;
                 w.next(p);
             }
-            mma_commit(&done);
-        }
-        __syncwarp();
+            if (leader)
+                mma_commit(done + s);
+            __syncwarp();
+        };
+        if (warp == 12)
+            stream(std::integral_constant<int, 0>{});
+        else
+            stream(std::integral_constant<int, 1>{});
     } else if (warp >= 8) {
         // ------------------------------------------------------------ producers
         // Two warps copy K, two V, each 64 rows of every tile.  While a warp
@@ -449,21 +490,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         const float ks = FP8 && p.k_scale ? __ldg(p.k_scale) : 1.0f, vs = FP8 && p.v_scale ? __ldg(p.v_scale) : 1.0f;
         const float base_scale = p.scale * kLog2e * ks;
         int base = 0, item_no = 0;
-        uint32_t spar = 0;   // parities of the stream's two sfull
-        int nO = 0;          // halves whose weights are out (of this stream)
+        int nS = 0, nO = 0;  // S tiles read, items whose output is done (of this stream)
         int nJ = 0;          // items whose rows the streams shared
         bool ok = true;
         while (w.more() && ok) {
             const int n = w.t1 - w.t0, rows = w.rq.nq * p.group;
             const int h = w.head(), row0 = w.row0();
-            const bool two = RT == 2 && rows - row0 > 128;
+            const bool two = rows - row0 > 128;
             const bool begun = w.begun(), finished = w.finished();
             const int rt = two ? s : 0, my = row0 + rt * 128 + r;
             const bool mine = my < rows, warp_live = row0 + rt * 128 + q4 * 32 < rows;
             const int i = mine ? my / p.group : 0, hq = h * p.group + (mine ? my - i * p.group : 0);
             const int halves = tile_halves(w, n);
-            const int mine_tiles = s == 0 ? (n + 1) / 2 : n / 2;
-            const int steps = two ? halves : 2 * mine_tiles - (((n - 1) & 1) == s && (halves & 1) ? 1 : 0);  // halves of the stream
+            const int steps = two ? n : s == 0 ? (n + 1) / 2 : n / 2;  // tiles of the stream
+            if (!two && s == 1 && steps > 0 && lane == 0)
+                bar_arrive(&go1);
             // ---- the query row.  A negative scale turns its sign, a zero one
             // zeroes it, so that the factor c of the scores is positive.
             float c = base_scale;
@@ -516,21 +557,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             float m = -INFINITY, l = 0.0f;  // the maximum in use (scaled, base 2), the sum of weights
 
             for (int k = 0; k < steps; k++) {
-                const int j = two ? k >> 1 : 2 * (k >> 1) + s, hb = k & 1;
-                const int key0 = (w.t0 + j) * kKeysTc + 64 * hb;
-                const uint32_t ts = tmem + lanes + 128 * s + 64 * hb;
-                ok = ok && bar_wait(sfull + 2 * s + hb, (spar >> hb) & 1u, abort);
-                spar ^= 1u << hb;
+                const int j = two ? k : 2 * k + s;
+                const int key0 = (w.t0 + j) * kKeysTc;
+                const int nh = 2 * j + 1 == halves ? 1 : 2;  // 64-key halves that hold tokens
+                const uint32_t ts = tmem + lanes + 128 * s;
+                ok = ok && bar_wait(sfull + s, (uint32_t)nS & 1u, abort);
+                nS++;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
                 fence_after();
                 if (warp_live) {
                     const int lx = (base + j) & 7;
-                    const bool masked = key0 + 64 > w.rq.ctx || (live[lx][2 * hb] & live[lx][2 * hb + 1]) != 0xffffffffu;
+                    const bool masked = key0 + kKeysTc > w.rq.ctx || (live[lx][0] & live[lx][1] & live[lx][2] & live[lx][3]) != 0xffffffffu;
                     // bit b of visible(g): key key0 + 32 g + b is seen
                     auto visible = [&](int g) {
-                        uint32_t vis = mine ? live[lx][2 * hb + g] : 0u;
+                        uint32_t vis = mine ? live[lx][g] : 0u;
                         const int a0 = key0 + 32 * g - w.rq.ctx;  // the drafted token of bit 0; below 0: context
                         if (a0 > -32) {
                             const int sh = a0 < 0 ? -a0 : 0, a = a0 < 0 ? 0 : a0;  // bits below sh are context
@@ -563,7 +605,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     // ---- maximum (the scores are read again below)
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int g = 0; g < 2; g++) {
+                    for (int g = 0; g < 2 * nh; g++) {
                         uint32_t x[32];
                         load32(g, x);
 #pragma unroll
@@ -580,13 +622,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                         const float fr = old == m ? 1.0f : ex2(old - m);  // 0 from -inf
                         l *= fr;
                         if (k > 0) {
-                            // the products so far have to be in before they are rescaled
-                            // (S of this half came after the last but one)
-                            ok = ok && bar_wait(ofull + s, (uint32_t)(nO - 1) & 1u, abort);
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok)
-                                break;
-                            fence_after();
+                            // the products so far are in: S of this tile came after them
 #pragma unroll 1
                             for (int d = 0; d < D; d += 32) {
                                 uint32_t o[32];
@@ -605,7 +641,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     const bool apart = __any_sync(0xffffffffu, fabsf(mu) > 16777216.0f);
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll 1
-                    for (int g = 0; g < 2; g++) {
+                    for (int g = 0; g < 2 * nh; g++) {
                         uint32_t x[32], pk[16];
                         load32(g, x);
                         if (apart) {
@@ -631,26 +667,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                         }
                         // columns 16 g .. of P lie over scores that are used up
                         tmem_st16(ts + 16 * g, pk);
+                        if (g & 1) {  // a half's weights are out: its product may begin
+                            tmem_wait_st();
+                            fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                bar_arrive(pfull + 2 * s + (g >> 1));
+                        }
                     }
                     float a0, a1;
                     unpr(add2(sum0, sum1), a0, a1);
                     l += a0 + a1;
-                    tmem_wait_st();
+                } else {
+                    fence_before();
+                    if (lane < nh)
+                        bar_arrive(pfull + 2 * s + lane);
+                    __syncwarp();
                 }
-                fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    bar_arrive(pfull + 2 * s + hb);
-                nO++;
             }
             if (!ok)
                 break;
             // ---- the item ends here, or the CTA's share of it does
-            // the last product is in; a parity tells neighbouring phases apart only,
-            // and the last S tells of the last product but two
-            for (int k = steps > 1 ? 2 : steps; k >= 1; k--)
-                ok = ok && bar_wait(ofull + s, (uint32_t)(nO - k) & 1u, abort);
-            ok = __all_sync(0xffffffffu, ok);
+            if (steps > 0) {
+                ok = bar_wait(ofull + s, (uint32_t)nO & 1u, abort);
+                ok = __all_sync(0xffffffffu, ok);
+                nO++;
+            }
             fence_after();
             float y0 = 1.0f, y1 = 0.0f;  // factors of the two streams' sums
             if (!two) {
@@ -758,8 +800,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         // every product has completed before the tensor memory is freed
         if (lane == 0) {
             const unsigned long long t0 = gtimer();
-            while (!bar_try(&done, 0) && gtimer() - t0 < kTimeoutNs) {
-            }
+            for (int s = 0; s < 2; s++)
+                while (!bar_try(done + s, 0) && gtimer() - t0 < kTimeoutNs) {
+                }
         }
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
@@ -773,10 +816,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
 
 // Joins the parts of the item that CTA blockIdx.x began and did not finish:
 // block y takes 32 dims (y % (D / 32)) of row tile y / (D / 32), a thread per row.
-template <int D, bool FP8, int RT>
+template <int D, bool FP8>
 __global__ void __launch_bounds__(128) join_tc_kernel(const __grid_constant__ AttnParams p, int ctas)
 {
-    using C = TcCfg<D, FP8, RT>;
+    using C = TcCfg<D, FP8>;
     pdl_enter();
     const int r = threadIdx.x, rt = blockIdx.y / (D / 32), d0 = (blockIdx.y % (D / 32)) * 32;
     const PartDesc *descs = reinterpret_cast<const PartDesc *>(p.parts);
@@ -828,7 +871,7 @@ __global__ void __launch_bounds__(128) join_tc_kernel(const __grid_constant__ At
 
 // ------------------------------------------------------------------ launches
 
-template <int D, bool FP8, int RT>
+template <int D, bool FP8>
 cudaError_t attention_tc_ctas(int &ctas)
 {
     static int cached[64];
@@ -842,8 +885,8 @@ cudaError_t attention_tc_ctas(int &ctas)
     if (have == 0) {
         e = cudaDeviceGetAttribute(&have, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(attention_tc_kernel<D, FP8, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     TcCfg<D, FP8, RT>::kSmem);
+            e = cudaFuncSetAttribute(attention_tc_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     TcCfg<D, FP8>::kSmem);
         if (e != cudaSuccess)
             return e;
         __atomic_store_n(&cached[dev], have, __ATOMIC_RELEASE);
@@ -852,26 +895,26 @@ cudaError_t attention_tc_ctas(int &ctas)
     return cudaSuccess;
 }
 
-template <int D, bool FP8, int RT>
+template <int D, bool FP8>
 int64_t attention_tc_bytes(cudaError_t &e)
 {
     int ctas = 0;
-    e = attention_tc_ctas<D, FP8, RT>(ctas);
-    return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * (int64_t)TcCfg<D, FP8, RT>::kPart * 4) : 0;
+    e = attention_tc_ctas<D, FP8>(ctas);
+    return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * (int64_t)TcCfg<D, FP8>::kPart * 4) : 0;
 }
 
-template <int D, bool FP8, int RT>
+template <int D, bool FP8>
 cudaError_t attention_tc(const AttnParams &p, cudaStream_t stream)
 {
-    using C = TcCfg<D, FP8, RT>;
+    using C = TcCfg<D, FP8>;
     int ctas = 0;
-    cudaError_t e = attention_tc_ctas<D, FP8, RT>(ctas);
+    cudaError_t e = attention_tc_ctas<D, FP8>(ctas);
     if (e == cudaSuccess)
-        e = launch_pdl(attention_tc_kernel<D, FP8, RT>, ctas, kTcThreads, C::kSmem, stream, p);
+        e = launch_pdl(attention_tc_kernel<D, FP8>, ctas, kTcThreads, C::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(RT * (D / 32)));
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(2 * (D / 32)));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -879,31 +922,27 @@ cudaError_t attention_tc(const AttnParams &p, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_tc_kernel<D, FP8, RT>, p, ctas);
+    return cudaLaunchKernelEx(&cfg, join_tc_kernel<D, FP8>, p, ctas);
 }
 
 template <int D>
-int64_t workspace_tc(int rt, bool fp8, cudaError_t &e)
+int64_t workspace_tc(bool fp8, cudaError_t &e)
 {
-    if (rt == 1)
-        return fp8 ? attention_tc_bytes<D, true, 1>(e) : attention_tc_bytes<D, false, 1>(e);
-    return fp8 ? attention_tc_bytes<D, true, 2>(e) : attention_tc_bytes<D, false, 2>(e);
+    return fp8 ? attention_tc_bytes<D, true>(e) : attention_tc_bytes<D, false>(e);
 }
 
 template <int D>
-cudaError_t attention_tc_d(const AttnParams &p, int rt, bool fp8, cudaStream_t stream)
+cudaError_t attention_tc_d(const AttnParams &p, bool fp8, cudaStream_t stream)
 {
-    if (rt == 1)
-        return fp8 ? attention_tc<D, true, 1>(p, stream) : attention_tc<D, false, 1>(p, stream);
-    return fp8 ? attention_tc<D, true, 2>(p, stream) : attention_tc<D, false, 2>(p, stream);
+    return fp8 ? attention_tc<D, true>(p, stream) : attention_tc<D, false>(p, stream);
 }
 
-#define DSPARK_ATTN_TC_DECLARE(D)                                      \
-    extern template int64_t workspace_tc<D>(int, bool, cudaError_t &); \
-    extern template cudaError_t attention_tc_d<D>(const AttnParams &, int, bool, cudaStream_t);
-#define DSPARK_ATTN_TC_DEFINE(D)                                \
-    template int64_t workspace_tc<D>(int, bool, cudaError_t &); \
-    template cudaError_t attention_tc_d<D>(const AttnParams &, int, bool, cudaStream_t);
+#define DSPARK_ATTN_TC_DECLARE(D)                                 \
+    extern template int64_t workspace_tc<D>(bool, cudaError_t &); \
+    extern template cudaError_t attention_tc_d<D>(const AttnParams &, bool, cudaStream_t);
+#define DSPARK_ATTN_TC_DEFINE(D)                           \
+    template int64_t workspace_tc<D>(bool, cudaError_t &); \
+    template cudaError_t attention_tc_d<D>(const AttnParams &, bool, cudaStream_t);
 
 }  // namespace attn
 }  // namespace dspark
