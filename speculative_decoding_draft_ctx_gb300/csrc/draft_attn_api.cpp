@@ -352,9 +352,10 @@ int64_t dspark_kv_evict_workspace(int num_requests, int num_kv_heads, int64_t st
         fail(DSPARK_ERR_INVALID_ARG, "evict workspace: invalid sizes");
         return -1;
     }
-    // the list of places given up and the list of tokens that move, per pair
+    // per pair the number of moves, the list of places given up and the list
+    // of tokens that move
     const int64_t len = std::max<int64_t>(0, std::min(budget, stride - budget));
-    return (int64_t)num_requests * num_kv_heads * 2 * len * 4;
+    return (int64_t)num_requests * num_kv_heads * (1 + 2 * len) * 4;
 }
 
 int dspark_kv_evict(void *kv_cache, int64_t num_blocks, int num_kv_heads, int block_size, int head_dim, int kv_dtype,
@@ -399,7 +400,8 @@ int dspark_kv_evict(void *kv_cache, int64_t num_blocks, int num_kv_heads, int bl
     p.weights_out = weights_out;
     p.positions_out = positions_out;
     p.new_lens = new_lens;
-    p.lists = static_cast<int32_t *>(workspace);
+    p.counts = static_cast<int32_t *>(workspace);
+    p.lists = p.counts + (int64_t)num_requests * num_kv_heads;
     p.error_flags = error_flags;
     p.num_blocks = num_blocks;
     p.stride = stride;

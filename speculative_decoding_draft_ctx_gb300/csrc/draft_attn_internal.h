@@ -89,7 +89,8 @@ struct EvictParams {
     const int32_t *positions;
     float *weights_out;
     int32_t *positions_out, *new_lens;
-    int32_t *lists;    // workspace: [B * H][2][list_len]
+    int32_t *counts;   // workspace: [B * H] moves, then
+    int32_t *lists;    // [B * H][2][list_len]: places, then cache rows, given up and moved from
     unsigned int *error_flags;
     int64_t num_blocks, stride, list_len;
     int64_t budget, sinks, recent;

@@ -16,13 +16,20 @@
 // every row behind the first hole.
 //
 // One cluster of NC CTAs per (request, KV head): each CTA ranks a slice of
-// the places (its keys stay in shared memory where the slice fits), the
-// histograms and counts are summed over distributed shared memory, the two
-// lists go to the workspace, and after a cluster barrier the pairs are copied
-// by all warps of the cluster, four rows in flight per warp.  NC is the
-// smallest power of two that gives every SM two CTAs, at most 16, and at
-// least 512 places per CTA: a serving batch has enough (request, head) pairs,
-// a single long request does not.  Bound: the weights' and positions' read
+// the places, its warps consecutive segments of it (ballots give the ranks in
+// place order, whole lines are read and written), its keys in shared memory
+// where the slice fits; the histograms and counts are summed over distributed
+// shared memory, the two lists go to the workspace, and after a cluster
+// barrier all threads move the pairs' weights and positions and turn the
+// places into cache rows.  NC is the smallest power of two that gives every SM
+// two CTAs, at most 16, and at least 512 places per CTA: a serving batch has
+// enough (request, head) pairs, a single long request does not.
+//
+// The rows are copied by a second kernel, launched with programmatic overlap:
+// it needs no cluster, so every SM takes part (in the first kernel two 131k
+// contexts halved took 137 us: eight clusters of 16 CTAs do not spread over
+// all SMs, nor do their registers allow 4 KB in flight per warp), and a warp
+// needs nothing but the two lists.  Bound: the weights' and positions' read
 // and write, and the rows that move; on small n the barriers between passes.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
@@ -37,15 +44,14 @@ namespace cg = cooperative_groups;
 namespace dspark {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kKeysMax = 16384;  // keys of a slice kept in shared memory (64 KB)
 
 struct Shared {
-    unsigned hist[256];   // this CTA's histogram, read by the others
-    unsigned warp_sum[kWarps];
-    unsigned total;       // block scan
-    unsigned counts[2];   // this CTA's {equal} then {holes, movers}, read by the others
-    unsigned bin, above;  // the pass's result
+    unsigned hist[256];        // this CTA's histogram, read by the others
+    unsigned total[256];       // the cluster's
+    unsigned warp_sum[32];
+    unsigned counts[2];        // this CTA's {equal} then {holes, movers}, read by the others
+    unsigned bin, above, same; // a pass's result: the cut's digit, keys above it, keys with it
 };
 
 __device__ __forceinline__ uint32_t sort_key(float w, bool keep_always)
@@ -58,51 +64,40 @@ __device__ __forceinline__ uint32_t sort_key(float w, bool keep_always)
     return u & 0x80000000u ? ~u : u | 0x80000000u;  // in [0x007fffff, 0xff800000]
 }
 
-// Exclusive prefix sum over the block; every thread also gets the total.
-__device__ __forceinline__ unsigned block_scan(unsigned v, Shared &sh, unsigned &total)
+// Sum over the warps before this one of their (warp-uniform) v, and over all.
+template <int kWarps>
+__device__ __forceinline__ unsigned warps_before(unsigned v, Shared &sh, unsigned &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    unsigned x = v;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const unsigned y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d)
-            x += y;
-    }
-    if (lane == 31)
-        sh.warp_sum[warp] = x;
+    if (lane == 0)
+        sh.warp_sum[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        unsigned s = lane < kWarps ? sh.warp_sum[lane] : 0u, z = s;
-#pragma unroll
-        for (int d = 1; d < kWarps; d <<= 1) {
-            const unsigned y = __shfl_up_sync(0xffffffffu, z, d);
-            if (lane >= d)
-                z += y;
-        }
-        if (lane < kWarps)
-            sh.warp_sum[lane] = z - s;
-        if (lane == kWarps - 1)
-            sh.total = z;
-    }
+    const unsigned x = lane < kWarps ? sh.warp_sum[lane] : 0u;
+    total = __reduce_add_sync(0xffffffffu, x);
+    const unsigned before = __reduce_add_sync(0xffffffffu, lane < warp ? x : 0u);
     __syncthreads();
-    const unsigned base = sh.warp_sum[warp];
-    total = sh.total;
-    __syncthreads();
-    return base + x - v;
+    return before;
 }
 
-__global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, int cluster_size)
+template <int kThreads, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const EvictParams p, int NC)
 {
+    constexpr int kWarps = kThreads / 32;
     pdl_enter();
     extern __shared__ uint32_t keys[];
     __shared__ Shared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank();
-    const int NC = cluster_size;
     const int64_t bh = blockIdx.x / NC;
     const int b = (int)(bh / p.num_kv_heads), h = (int)(bh - (int64_t)b * p.num_kv_heads);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const unsigned below = (1u << lane) - 1u;  // the lanes before this one
+    auto barrier = [&] {
+        if (NC > 1)
+            cluster.sync();
+        else
+            __syncthreads();
+    };
 
     const int n = __ldg(p.context_lens + b);
     const bool bad = n < 0 || n > p.stride || n > p.table_blocks * p.block_size;
@@ -127,203 +122,264 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictParams p, in
                 po[j] = pos[j];
         }
     }
-    if (!cut)
-        return;  // the same for every CTA of the cluster
+    if (!cut) {  // the same for every CTA of the cluster
+        if (rank == 0 && tid == 0)
+            p.counts[bh] = 0;
+        return;
+    }
     const int budget = (int)p.budget;
     const int64_t first_recent = (int64_t)__ldg(p.seq_lens + b) - p.recent;
     const int per = (n + NC - 1) / NC;
     const int lo = min(n, rank * per), hi = min(n, lo + per);
     const bool in_smem = per <= kKeysMax;
-    auto key_of = [&](int j) {
-        const int at = pos[j];
-        return sort_key(w[j], at < p.sinks || at >= first_recent);
+    // the warp's segment: whole groups of 32 places
+    const int seg = ((per + kWarps - 1) / kWarps + 31) & ~31;
+    const int s0 = min(hi, lo + warp * seg), s1 = min(hi, s0 + seg);
+    for (int i = tid; i < 256; i += kThreads)
+        sh.hist[i] = 0;
+    __syncthreads();
+    // ---- the keys, the first digit's histogram, and (not in place) the places
+    // that no move will write: a hole is written again by its mover below
+#pragma unroll 4
+    for (int j = s0 + lane; j < s1; j += 32) {
+        const float wv = w[j];
+        const int32_t pv = pos[j];
+        const uint32_t k = sort_key(wv, pv < p.sinks || pv >= first_recent);
+        if (in_smem)
+            keys[j - lo] = k;
+        atomicAdd(&sh.hist[k >> 24], 1u);
+        if (copies)
+            wo[j] = j < budget ? wv : 0.0f;
+        if (copies_pos)
+            po[j] = j < budget ? pv : -1;
+    }
+    auto key = [&](int j) {
+        if (in_smem)
+            return keys[j - lo];
+        const int32_t pv = pos[j];
+        return sort_key(w[j], pv < p.sinks || pv >= first_recent);
     };
-    if (in_smem)
-        for (int j = lo + tid; j < hi; j += kThreads)
-            keys[j - lo] = key_of(j);
-    auto key = [&](int j) { return in_smem ? keys[j - lo] : key_of(j); };
 
     // ---- the budget-th largest key
     uint32_t prefix = 0;
     unsigned need = (unsigned)budget;  // still to take among the keys that agree with the prefix
     for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kThreads)
-            sh.hist[i] = 0;
+        if (shift < 24) {
+            for (int i = tid; i < 256; i += kThreads)
+                sh.hist[i] = 0;
+            __syncthreads();
+            const uint32_t mask = 0xffffffffu << (shift + 8);
+            for (int j = s0 + lane; j < s1; j += 32) {
+                const uint32_t k = key(j);
+                if ((k & mask) == prefix)
+                    atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
+            }
+        }
+        barrier();
+        if (tid < 256) {  // one bin per thread: the cluster's loads go out together
+            unsigned v = sh.hist[tid];
+            if (NC > 1) {
+                v = 0;
+#pragma unroll 8
+                for (int c = 0; c < NC; c++)
+                    v += cluster.map_shared_rank(&sh, c)->hist[tid];
+            }
+            sh.total[tid] = v;
+        }
         __syncthreads();
-        const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-        for (int j = lo + tid; j < hi; j += kThreads) {
-            const uint32_t k = key(j);
-            if ((k & mask) == prefix)
-                atomicAdd(&sh.hist[(k >> shift) & 255u], 1u);
+        // lane l of warp 0 takes bins 255 - 8 l ... 248 - 8 l: counts from the top
+        if (warp == 0) {
+            unsigned v[8], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                v[i] = sh.total[255 - 8 * lane - i];
+                sum += v[i];
+            }
+            unsigned x = sum;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const unsigned y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d)
+                    x += y;
+            }
+            unsigned before = x - sum;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                if (before < need && before + v[i] >= need) {
+                    sh.bin = 255u - 8 * lane - i;
+                    sh.above = before;
+                    sh.same = v[i];
+                }
+                before += v[i];
+            }
         }
-        cluster.sync();
-        // thread i < 256 sums bin 255 - i over the cluster; the scan then counts from the top
-        unsigned v = 0;
-        if (tid < 256)
-            for (int c = 0; c < NC; c++)
-                v += cluster.map_shared_rank(&sh, c)->hist[255 - tid];
-        unsigned total;
-        const unsigned before = block_scan(v, sh, total);
-        if (tid < 256 && before < need && before + v >= need) {
-            sh.bin = 255u - (unsigned)tid;
-            sh.above = before;
-        }
-        cluster.sync();  // the result is there, and every CTA has read the histograms
+        barrier();  // the result is there, and every CTA has read the histograms
         prefix |= sh.bin << shift;
         need -= sh.above;
     }
-    // keys > prefix are kept, and the first `need` of those equal to it
+    // keys > prefix are kept, and the first `need` of the `same` equal to it
+    const bool ties = need < sh.same;
 
-    // ---- how many equal keys lie in the slices before this one
-    const int chunk = (hi - lo + kThreads - 1) / kThreads;  // consecutive places per thread
-    const int j0 = min(hi, lo + tid * chunk), j1 = min(hi, j0 + chunk);
-    unsigned eq = 0;
-    for (int j = j0; j < j1; j++)
-        eq += key(j) == prefix;
-    unsigned total;
-    unsigned eq_before = block_scan(eq, sh, total);
-    if (tid == 0)
-        sh.counts[0] = total;
-    cluster.sync();
-    for (int c = 0; c < rank; c++)
-        eq_before += cluster.map_shared_rank(&sh, c)->counts[0];
-    cluster.sync();
+    // ---- equal keys before this warp's segment, where only some of them are kept
+    unsigned eq_before = 0;
+    if (ties) {
+        unsigned eq = 0, total;
+        for (int j = s0 + lane; j - lane < s1; j += 32)
+            eq += __popc(__ballot_sync(0xffffffffu, j < s1 && key(j) == prefix));
+        eq_before = warps_before<kWarps>(eq, sh, total);
+        if (tid == 0)
+            sh.counts[0] = total;
+        barrier();
+        for (int c = 0; c < rank; c++)
+            eq_before += cluster.map_shared_rank(&sh, c)->counts[0];
+        barrier();
+    }
+    // whether place j (one per lane) stays; e: equal keys before the group of 32
+    auto stays = [&](int j, unsigned &e) {
+        const uint32_t k = j < s1 ? key(j) : 0u;
+        bool keep = k >= prefix;
+        if (ties) {
+            const unsigned same = __ballot_sync(0xffffffffu, j < s1 && k == prefix);
+            keep = k > prefix || (k == prefix && e + __popc(same & below) < need);
+            e += __popc(same);
+        }
+        return keep && j < s1;
+    };
 
     // ---- holes (given up, below budget) and movers (kept, at or above it)
     unsigned holes = 0, movers = 0, e = eq_before;
-    for (int j = j0; j < j1; j++) {
-        const uint32_t k = key(j);
-        const bool keep = k > prefix || (k == prefix && e++ < need);
-        holes += !keep && j < budget;
-        movers += keep && j >= budget;
+    for (int j = s0 + lane; j - lane < s1; j += 32) {
+        const bool keep = stays(j, e);
+        holes += __popc(__ballot_sync(0xffffffffu, j < s1 && !keep && j < budget));
+        movers += __popc(__ballot_sync(0xffffffffu, keep && j >= budget));
     }
     unsigned nh, nm;
-    unsigned hole_at = block_scan(holes, sh, nh), mover_at = block_scan(movers, sh, nm);
+    unsigned hole_at = warps_before<kWarps>(holes, sh, nh), mover_at = warps_before<kWarps>(movers, sh, nm);
     if (tid == 0)
         sh.counts[0] = nh, sh.counts[1] = nm;
-    cluster.sync();
+    barrier();
     unsigned moves = 0;
     for (int c = 0; c < NC; c++) {
-        const Shared *o = cluster.map_shared_rank(&sh, c);
+        const Shared *o = NC > 1 ? cluster.map_shared_rank(&sh, c) : &sh;
         if (c < rank)
             hole_at += o->counts[0], mover_at += o->counts[1];
         moves += o->counts[0];
     }
     int32_t *hole_list = p.lists + bh * 2 * p.list_len, *mover_list = hole_list + p.list_len;
     e = eq_before;
-    for (int j = j0; j < j1; j++) {
-        const uint32_t k = key(j);
-        const bool keep = k > prefix || (k == prefix && e++ < need);
-        if (j < budget) {
-            if (!keep)
-                hole_list[hole_at++] = j;
-            else {
-                if (copies)
-                    wo[j] = w[j];
-                if (copies_pos)
-                    po[j] = pos[j];
-            }
-        } else if (keep) {
-            mover_list[mover_at++] = j;
-            if (copies)
+    for (int j = s0 + lane; j - lane < s1; j += 32) {
+        const bool keep = stays(j, e);
+        const bool hole = j < s1 && !keep && j < budget, mover = keep && j >= budget;
+        const unsigned hb = __ballot_sync(0xffffffffu, hole), mb = __ballot_sync(0xffffffffu, mover);
+        if (hole)
+            hole_list[hole_at + __popc(hb & below)] = j;
+        if (mover)
+            mover_list[mover_at + __popc(mb & below)] = j;
+        hole_at += __popc(hb), mover_at += __popc(mb);
+        if (j < s1 && j >= budget && !keep) {  // in place: given up beyond the budget
+            if (!copies)
                 wo[j] = 0.0f;
-            if (copies_pos)
+            if (!copies_pos)
                 po[j] = -1;
-        } else {
-            wo[j] = 0.0f;
-            po[j] = -1;
         }
     }
-    cluster.sync();  // the lists are complete (and no CTA's shared memory is read any more)
+    if (rank == 0 && tid == 0)
+        p.counts[bh] = (int32_t)moves;
+    barrier();  // the lists are complete (and no CTA's shared memory is read any more)
 
-    // ---- the moves
-    const int warps = NC * kWarps, gw = rank * kWarps + warp;
+    // ---- the weights and positions move, a pair per thread; its places become rows of the cache
     const int32_t *table = p.table + b * p.table_stride;
-    const int clog = __ffs(p.row_bytes >> 4) - 1, chunks = 1 << clog;  // 16-byte words of a row: 8, 16, 32 or 64
     bool bad_block = false;
-    auto row_of = [&](int j) -> unsigned char * {
+    auto row_of = [&](int j) -> uint32_t {
         const int blk = j / p.block_size;
         const int64_t phys = __ldg(table + blk);
         if (phys < 0 || phys >= p.num_blocks) {
             bad_block = true;
-            return nullptr;
+            return ~0u;
         }
-        return p.cache + ((phys * p.num_kv_heads + h) * p.block_size + (j - blk * p.block_size)) * (int64_t)p.row_bytes;
+        return (uint32_t)((phys * p.num_kv_heads + h) * p.block_size + (j - blk * p.block_size));
     };
-    // each lane looks one pair up, then the warp copies the 32 rows
-    for (unsigned base = gw * 32u; base < moves; base += warps * 32u) {
-        const unsigned i = base + lane;
-        unsigned char *from = nullptr, *to = nullptr;
-        if (i < moves) {
-            const int d = hole_list[i], s = mover_list[i];
-            from = row_of(s), to = row_of(d);
-            const float ws = w[s];
-            const int32_t ps = pos[s];
-            wo[d] = ws;
-            po[d] = ps;
-            if (!copies)
-                wo[s] = 0.0f;
-            if (!copies_pos)
-                po[s] = -1;
-            if (!to)
-                from = nullptr;
-        }
-        const int count = (int)min(32u, moves - base);
-        const int words = count * chunks;  // 16-byte words of these rows, lane-strided
-        for (int x0 = 0; x0 < words; x0 += 32 * 4) {
-            uint4 v[4];
-            unsigned char *dst[4];
-#pragma unroll
-            for (int k = 0; k < 4; k++) {
-                const int x = x0 + k * 32 + lane;
-                const int row = min(x >> clog, 31), c = x & (chunks - 1);
-                const unsigned long long f = __shfl_sync(0xffffffffu, (unsigned long long)from, row);
-                const unsigned long long t = __shfl_sync(0xffffffffu, (unsigned long long)to, row);
-                dst[k] = nullptr;
-                if (x < words && f != 0) {
-                    v[k] = *reinterpret_cast<const uint4 *>(f + 16 * c);
-                    dst[k] = reinterpret_cast<unsigned char *>(t + 16 * c);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                if (dst[k])
-                    *reinterpret_cast<uint4 *>(dst[k]) = v[k];
-        }
+#pragma unroll 2
+    for (unsigned i = (unsigned)(rank * kThreads + tid); i < moves; i += (unsigned)(NC * kThreads)) {
+        const int d = hole_list[i], s = mover_list[i];
+        const float wv = w[s];
+        const int32_t pv = pos[s];
+        const uint32_t to = row_of(d), from = row_of(s);
+        wo[d] = wv;
+        po[d] = pv;
+        if (!copies)
+            wo[s] = 0.0f;
+        if (!copies_pos)
+            po[s] = -1;
+        hole_list[i] = (int32_t)to;
+        mover_list[i] = (int32_t)(to == ~0u ? ~0u : from);
     }
     if (bad_block && p.error_flags)
         atomicOr(p.error_flags, kFlagBlockRange);
 }
 
+// Copies the rows of the lists: blockIdx.x is the (request, KV head) pair,
+// blockIdx.y its share of the moves.
+__global__ void __launch_bounds__(256, 3) move_kernel(const EvictParams p)
+{
+    pdl_enter();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned moves = (unsigned)p.counts[blockIdx.x];
+    const int32_t *holes = p.lists + (int64_t)blockIdx.x * 2 * p.list_len, *movers = holes + p.list_len;
+    const int clog = __ffs(p.row_bytes >> 4) - 1, chunks = 1 << clog;  // 16-byte words of a row: 8, 16, 32 or 64
+    const unsigned pairs = min(32u, 256u >> clog);                     // rows a warp copies at once: 8 words per lane
+    const unsigned step = gridDim.y * 8u * pairs;
+    // lane i < pairs holds the rows of pair base + i
+    auto look = [&](unsigned base, uint32_t &from, uint32_t &to) {
+        from = to = ~0u;
+        if (lane < pairs && base + lane < moves)
+            from = (uint32_t)movers[base + lane], to = (uint32_t)holes[base + lane];
+    };
+    uint32_t from, to;
+    unsigned base = (blockIdx.y * 8u + warp) * pairs;
+    look(base, from, to);
+    for (; base < moves; base += step) {
+        uint4 v[8];
+        uint32_t next_from, next_to;
+        look(base + step, next_from, next_to);
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int x = k * 32 + lane, row = x >> clog;
+            const uint32_t f = __shfl_sync(0xffffffffu, from, row & 31);
+            if (row < pairs && f != ~0u)
+                v[k] = *reinterpret_cast<const uint4 *>(p.cache + (int64_t)f * p.row_bytes + 16 * (x & (chunks - 1)));
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int x = k * 32 + lane, row = x >> clog;
+            const uint32_t f = __shfl_sync(0xffffffffu, from, row & 31), t = __shfl_sync(0xffffffffu, to, row & 31);
+            if (row < pairs && f != ~0u)
+                *reinterpret_cast<uint4 *>(p.cache + (int64_t)t * p.row_bytes + 16 * (x & (chunks - 1))) = v[k];
+        }
+        from = next_from, to = next_to;
+    }
+}
+
 }  // namespace
 
-cudaError_t launch_kv_evict(const EvictParams &p, cudaStream_t stream)
+namespace {
+
+template <int kThreads, int kBlocks>
+cudaError_t launch(const EvictParams &p, int64_t pairs, int nc, int dev, cudaStream_t stream)
 {
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess)
-        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess)
-        return e;
-    if (dev < 0 || dev >= 64)
-        return cudaErrorInvalidDevice;
     static std::mutex mu;
     static bool attr_set[64];
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!attr_set[dev]) {
-            e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            cudaError_t e = cudaFuncSetAttribute(evict_kernel<kThreads, kBlocks>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
             if (e == cudaSuccess)
-                e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
+                e = cudaFuncSetAttribute(evict_kernel<kThreads, kBlocks>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeysMax * 4);
             if (e != cudaSuccess)
                 return e;
             attr_set[dev] = true;
         }
     }
-    const int64_t pairs = (int64_t)p.num_requests * p.num_kv_heads;
-    int nc = 1;
-    while (nc < 16 && pairs * nc < 2 * sms && p.stride > 512 * nc)
-        nc *= 2;
     const int64_t per = (p.stride + nc - 1) / nc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * nc));
@@ -339,7 +395,44 @@ cudaError_t launch_kv_evict(const EvictParams &p, cudaStream_t stream)
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, evict_kernel, p, nc);
+    return cudaLaunchKernelEx(&cfg, evict_kernel<kThreads, kBlocks>, p, nc);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_evict(const EvictParams &p, cudaStream_t stream)
+{
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev < 0 || dev >= 64)
+        return cudaErrorInvalidDevice;
+    const int64_t pairs = (int64_t)p.num_requests * p.num_kv_heads;
+    int nc = 1;
+    while (nc < 16 && pairs * nc < 2 * sms && p.stride > 512 * nc)
+        nc *= 2;
+    // pairs enough for every SM: 256 threads, so that all are there at once
+    e = pairs * nc > sms ? launch<256, 4>(p, pairs, nc, dev, stream) : launch<512, 2>(p, pairs, nc, dev, stream);
+    if (e != cudaSuccess || p.list_len == 0)
+        return e;
+    // the moves: three CTAs per SM over all pairs, none of them with less than
+    // 8 rows a warp to copy where the lists are full
+    const int64_t most = (p.list_len + 63) / 64;
+    int64_t shares = (3 * (int64_t)sms + pairs - 1) / pairs;
+    shares = shares < most ? shares : most;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)pairs, (unsigned)shares);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, move_kernel, p);
 }
 
 }  // namespace dspark

@@ -11,21 +11,25 @@
 // Here the frequency is a 64-bit fixed-point fraction F = f / 2 pi * 2^64 of a
 // turn, so p F mod 2^64 is the angle's fraction of a turn, exact but for F's
 // own rounding (p 2^-65 turns): the wrap of the integer product is the range
-// reduction.  The top bits give the nearest quarter turn, the signed rest (at
-// most 1/8 turn) goes to fp32 with a relative rounding and through
-// sincospif.  Bound: the store of 2 or 4 bytes per entry; a thread makes 4
+// reduction.  The top bits give the nearest quarter turn, the signed rest
+// x (|x| <= pi/4) goes to fp32 with a relative rounding and into the Taylor
+// series of sine (to x^9: the next term is below 2^-29 x) and cosine (to x^8:
+// below 2^-25).  Bound: the store of 2 or 4 bytes per entry; a thread makes 4
 // neighbouring angles, so it stores 8 or 16 bytes of cos and of sin.
 //
 // Rotation.  A head row of D dims is held by D / 8 lanes, 8 dims (16 bytes)
-// each, so a warp takes 256 / D rows per step.  Half layout: the partner of
+// each, so a warp takes 256 / D rows at once.  Half layout: the partner of
 // dim i < r/2 is i + r/2, r/16 lanes away: one shuffle per word.
 // Interleaved: both dims of a pair are in one lane.  Where a row is not
 // 16-byte aligned, or r/2 is no whole number of lanes, the same code loads
 // its elements and partners one by one (before any store of the warp, so in
 // place is safe).  Per element the arithmetic is x1 c - x2 s in fp32 (the
 // product of two bf16 values is exact there), rounded once to bf16.  Bound:
-// the read and write of q and k.  A CTA walks (token, group of head rows)
-// units; every lane issues kBatch rows' loads before it computes.
+// the read and write of q and k.  A warp's unit is kBatch row groups of one
+// token: their loads go out before the position is waited for and the cos|sin
+// words (whole 8- or 16-byte loads) after it, so a unit waits twice; four
+// CTAs per SM keep 32 warps' units in flight (with a CTA per token, 104
+// registers and a scalar load per cos and sin, a prefill batch took 97 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -45,9 +49,10 @@ __device__ __forceinline__ void turn_cos_sin(uint64_t u, float &c, float &s)
 {
     const uint64_t quarter = (u + (1ull << 61)) >> 62;  // nearest quarter turn, 0..3 (4 wraps to 0)
     const int64_t rest = (int64_t)(u - (quarter << 62));  // in [-2^61, 2^61)
-    // |rest| <= 1/8 turn; half turns = rest 2^-63
-    float sn, cs;
-    sincospif((float)rest * 0x1p-63f, &sn, &cs);
+    const float x = (float)rest * 3.40612158e-19f;  // 2 pi 2^-64: radians, at most pi/4
+    const float x2 = x * x;
+    const float sn = fmaf(x * x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 362880.0f, -1.0f / 5040.0f), 1.0f / 120.0f), -1.0f / 6.0f), x);
+    const float cs = fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, 1.0f / 40320.0f, -1.0f / 720.0f), 1.0f / 24.0f), -0.5f), 1.0f);
     const int n = (int)quarter & 3;
     const float a = (n & 1) ? sn : cs, b = (n & 1) ? cs : sn;
     c = (n == 1 || n == 2) ? -a : a;
@@ -115,12 +120,34 @@ __device__ __forceinline__ uint4 gather8(const uint16_t *p)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// 4 table entries from entry `at` (a multiple of 4; rows start at multiples of 8 entries)
+template <bool TF32>
+__device__ __forceinline__ void table4(const void *table, int64_t at, float (&o)[4])
+{
+    if constexpr (TF32) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(table) + at));
+        o[0] = v.x, o[1] = v.y, o[2] = v.z, o[3] = v.w;
+    } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(table) + at));
+        o[0] = bfl(v.x), o[1] = bfh(v.x), o[2] = bfl(v.y), o[3] = bfh(v.y);
+    }
+}
+
+template <bool TF32>
+__device__ __forceinline__ float table1(const void *table, int64_t at)
+{
+    if constexpr (TF32)
+        return __ldg(static_cast<const float *>(table) + at);
+    else
+        return __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(table) + at) << 16);
+}
+
 // VEC: rows are 16-byte aligned and a lane's 8 dims rotate together (half
 // layout: r % 16 == 0; interleaved: r % 8 == 0).
 template <int D, bool VEC, bool TF32>
-__global__ void __launch_bounds__(kThreads) rope_insert_kernel(const __grid_constant__ RopeInsertParams p)
+__global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) rope_insert_kernel(const __grid_constant__ RopeInsertParams p)
 {
-    constexpr int L = D / 8, RPW = 32 / L;  // lanes per row, rows per warp step
+    constexpr int L = D / 8, RPW = 32 / L;  // lanes per row, rows per warp and step
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int q = lane % L, sub = lane / L;
@@ -128,21 +155,49 @@ __global__ void __launch_bounds__(kThreads) rope_insert_kernel(const __grid_cons
     const int Hq = p.num_heads, Hkv = p.num_kv_heads;
     const bool insert = p.slot_mapping != nullptr;
     const int rows = Hq + Hkv + (insert ? Hkv : 0);  // head rows of a token: q, k and (insert) v
-    const int step = RPW * kWarps * gridDim.y;       // rows between two of a warp's row groups
-    // the lane's first dim; the dims its rotation pairs with
-    const int d0 = 8 * q;
+    const int groups = (rows + RPW * kBatch - 1) / (RPW * kBatch);
+    const int d0 = 8 * q;                            // the lane's first dim
+    const bool turns = d0 < r;                       // VEC: all of its dims turn, or none
     const int lanes_half = r >> 4;                   // VEC, half layout: lanes of one half
-    Fp8Scale kq, vq;
-    if (insert && p.fp8) {
-        kq = fp8_scale(p.k_scale ? __ldg(p.k_scale) : 1.0f);
-        vq = fp8_scale(p.v_scale ? __ldg(p.v_scale) : 1.0f);
-    }
+    const int partner_lane = q < lanes_half ? lane + lanes_half : q < 2 * lanes_half ? lane - lanes_half : lane;
     const float sign = p.inverse ? -1.0f : 1.0f;
     unsigned flags = 0;
 
-    for (int64_t t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
+    const int64_t units = p.num_tokens * groups, stride = (int64_t)gridDim.x * kWarps;
+    for (int64_t u = (int64_t)blockIdx.x * kWarps + warp; u < units; u += stride) {
+        const int64_t t = u <= 0x7fffffff ? (int64_t)((uint32_t)u / (uint32_t)groups) : u / groups;
+        const int g = (int)(u - t * groups) * RPW * kBatch + sub;  // the lane's first row
         int64_t pos = __ldg(p.positions + t);
         int64_t slot = insert ? __ldg(p.slot_mapping + t) : -1;
+        uint4 x[kBatch];
+        uint32_t partner[VEC ? 1 : kBatch][4];
+#pragma unroll
+        for (int b = 0; b < kBatch; b++) {
+            const int hh = g + b * RPW;
+            x[b] = make_uint4(0, 0, 0, 0);
+            if (hh < rows) {
+                const uint16_t *src = hh < Hq         ? p.q + t * p.q_ts + hh * p.q_hs
+                                      : hh < Hq + Hkv ? p.k + t * p.k_ts + (hh - Hq) * p.k_hs
+                                                      : p.v + t * p.v_ts + (hh - Hq - Hkv) * p.v_hs;
+                if constexpr (VEC) {
+                    x[b] = *reinterpret_cast<const uint4 *>(src + d0);
+                } else {
+                    x[b] = gather8(src + d0);
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        uint32_t w = 0;
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const int d = d0 + 2 * j + e;
+                            int m = p.interleaved ? d ^ 1 : (d < half ? d + half : d - half);
+                            m = d < r ? m : d;
+                            w |= (uint32_t)src[m] << (16 * e);
+                        }
+                        partner[b][j] = w;
+                    }
+                }
+            }
+        }
         const bool turn = pos >= 0 && pos < p.max_pos;
         if (!turn) {
             flags |= kFlagPos;
@@ -155,121 +210,91 @@ __global__ void __launch_bounds__(kThreads) rope_insert_kernel(const __grid_cons
         }
         // cos and signed sin of the lane's dims: out = x c + partner s
         float c[8], s[8];
+        if (VEC && turns && turn) {
+            const int64_t row = pos * r;
+            if (p.interleaved) {
+                float cv[4], sv[4];
+                table4<TF32>(p.cos_sin, row + (d0 >> 1), cv);
+                table4<TF32>(p.cos_sin, row + half + (d0 >> 1), sv);
 #pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const int d = d0 + e;
-            c[e] = 1.0f, s[e] = 0.0f;
-            if (turn && d < r) {
-                const int i = p.interleaved ? d >> 1 : (d < half ? d : d - half);
-                const bool upper = p.interleaved ? (d & 1) : d >= half;
-                float sv;
-                if constexpr (TF32) {
-                    const float *cs = static_cast<const float *>(p.cos_sin) + pos * r;
-                    c[e] = __ldg(cs + i), sv = __ldg(cs + half + i);
-                } else {
-                    const uint16_t *cs = static_cast<const uint16_t *>(p.cos_sin) + pos * r;
-                    c[e] = __uint_as_float((uint32_t)__ldg(cs + i) << 16);
-                    sv = __uint_as_float((uint32_t)__ldg(cs + half + i) << 16);
+                for (int e = 0; e < 4; e++) {
+                    c[2 * e] = c[2 * e + 1] = cv[e];
+                    s[2 * e] = -sign * sv[e], s[2 * e + 1] = sign * sv[e];
                 }
-                s[e] = (upper ? sv : -sv) * sign;
+            } else {
+                const int i = d0 < half ? d0 : d0 - half;
+                const float sg = d0 < half ? -sign : sign;
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    float cv[4], sv[4];
+                    table4<TF32>(p.cos_sin, row + i + e, cv);
+                    table4<TF32>(p.cos_sin, row + half + i + e, sv);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        c[e + k] = cv[k], s[e + k] = sg * sv[k];
+                }
             }
+        } else if (!VEC) {
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const int d = d0 + e;
+                c[e] = 1.0f, s[e] = 0.0f;
+                if (turn && d < r) {
+                    const int i = p.interleaved ? d >> 1 : (d < half ? d : d - half);
+                    const bool upper = p.interleaved ? (d & 1) : d >= half;
+                    c[e] = table1<TF32>(p.cos_sin, pos * r + i);
+                    s[e] = (upper ? sign : -sign) * table1<TF32>(p.cos_sin, pos * r + half + i);
+                }
+            }
+            __syncwarp();  // in place: every partner is read before any row of the unit is written
         }
         const int64_t blk = slot >= 0 ? slot / p.block_size : 0;
         const int64_t row0 = slot >= 0 ? (blk * Hkv * p.block_size + (slot - blk * p.block_size)) * (2 * D) : 0;
         const int64_t hstride = (int64_t)p.block_size * (2 * D);
-
-        for (int g = (blockIdx.y * kWarps + warp) * RPW; g < rows; g += step * kBatch) {
-            uint4 x[kBatch];
-            uint32_t partner[kBatch][VEC ? 1 : 4];
 #pragma unroll
-            for (int b = 0; b < kBatch; b++) {
-                const int hh = g + b * step + sub;
-                x[b] = make_uint4(0, 0, 0, 0);
-                if (hh < rows) {
-                    const uint16_t *src = hh < Hq         ? p.q + t * p.q_ts + hh * p.q_hs
-                                          : hh < Hq + Hkv ? p.k + t * p.k_ts + (hh - Hq) * p.k_hs
-                                                          : p.v + t * p.v_ts + (hh - Hq - Hkv) * p.v_hs;
-                    if constexpr (VEC) {
-                        x[b] = *reinterpret_cast<const uint4 *>(src + d0);
-                    } else {
-                        x[b] = gather8(src + d0);
-                        if (hh < Hq + Hkv) {
+        for (int b = 0; b < kBatch; b++) {
+            const int hh = g + b * RPW;
+            if (g - sub + b * RPW >= rows)
+                break;  // uniform over the warp
+            const uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
+            uint32_t y[4], pw[4];
 #pragma unroll
-                            for (int j = 0; j < 4; j++) {
-                                uint32_t w = 0;
+            for (int j = 0; j < 4; j++) {
+                if constexpr (!VEC)
+                    pw[j] = partner[b][j];
+                else
+                    pw[j] = p.interleaved ? (w[j] >> 16) | (w[j] << 16) : __shfl_sync(0xffffffffu, w[j], partner_lane);
+            }
 #pragma unroll
-                                for (int e = 0; e < 2; e++) {
-                                    const int d = d0 + 2 * j + e;
-                                    int m = p.interleaved ? d ^ 1 : (d < half ? d + half : d - half);
-                                    m = d < r ? m : d;
-                                    w |= (uint32_t)src[m] << (16 * e);
-                                }
-                                partner[b][j] = w;
-                            }
-                        }
+            for (int j = 0; j < 4; j++) {
+                y[j] = w[j];
+                if (turn && d0 + 2 * j < r)
+                    y[j] = pack_bf16x2(fmaf(bfl(w[j]), c[2 * j], bfl(pw[j]) * s[2 * j]),
+                                       fmaf(bfh(w[j]), c[2 * j + 1], bfh(pw[j]) * s[2 * j + 1]));
+            }
+            if (hh >= rows)
+                continue;
+            if (hh < Hq + Hkv) {
+                uint16_t *dst = hh < Hq ? p.q_out + t * p.qo_ts + hh * p.qo_hs : p.k_out + t * p.ko_ts + (hh - Hq) * p.ko_hs;
+                if constexpr (VEC) {
+                    *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(y[0], y[1], y[2], y[3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        dst[d0 + 2 * j] = (uint16_t)y[j];
+                        dst[d0 + 2 * j + 1] = (uint16_t)(y[j] >> 16);
                     }
                 }
             }
-            if constexpr (!VEC)
-                __syncwarp();  // in place: every partner is read before any row of the batch is written
-#pragma unroll
-            for (int b = 0; b < kBatch; b++) {
-                const int hh = g + b * step + sub;
-                if (g + b * step >= rows)
-                    break;  // uniform over the warp
-                uint32_t w[4] = {x[b].x, x[b].y, x[b].z, x[b].w};
-                uint32_t y[4];
-                if (hh < Hq + Hkv || VEC) {  // VEC: every lane takes part in the shuffles
-                    uint32_t pw[4];
-                    if constexpr (VEC) {
-                        if (p.interleaved) {
-#pragma unroll
-                            for (int j = 0; j < 4; j++)
-                                pw[j] = (w[j] >> 16) | (w[j] << 16);
-                        } else {
-                            const int pl = q < lanes_half ? lane + lanes_half : q < 2 * lanes_half ? lane - lanes_half : lane;
-#pragma unroll
-                            for (int j = 0; j < 4; j++)
-                                pw[j] = __shfl_sync(0xffffffffu, w[j], pl);
-                        }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; j++)
-                            pw[j] = partner[b][j];
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        float lo = bfl(w[j]), hi = bfh(w[j]);
-                        if (d0 + 2 * j < r) {
-                            lo = fmaf(lo, c[2 * j], bfl(pw[j]) * s[2 * j]);
-                            hi = fmaf(hi, c[2 * j + 1], bfh(pw[j]) * s[2 * j + 1]);
-                        }
-                        y[j] = d0 + 2 * j < r && turn ? pack_bf16x2(lo, hi) : w[j];
-                    }
-                }
-                if (hh >= rows)
-                    continue;
-                if (hh < Hq + Hkv) {
-                    uint16_t *dst = hh < Hq ? p.q_out + t * p.qo_ts + hh * p.qo_hs
-                                            : p.k_out + t * p.ko_ts + (hh - Hq) * p.ko_hs;
-                    if constexpr (VEC) {
-                        *reinterpret_cast<uint4 *>(dst + d0) = make_uint4(y[0], y[1], y[2], y[3]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; j++) {
-                            dst[d0 + 2 * j] = (uint16_t)y[j];
-                            dst[d0 + 2 * j + 1] = (uint16_t)(y[j] >> 16);
-                        }
-                    }
-                }
-                if (slot >= 0 && hh >= Hq) {
-                    const bool is_k = hh < Hq + Hkv;
-                    const uint4 o = is_k ? make_uint4(y[0], y[1], y[2], y[3]) : x[b];
-                    const int64_t at = row0 + (is_k ? hh - Hq : hh - Hq - Hkv) * hstride + (is_k ? 0 : D) + d0;
-                    if (p.fp8)
-                        *reinterpret_cast<uint2 *>(p.cache + at) = quantise8(o, is_k ? kq : vq);
-                    else
-                        *reinterpret_cast<uint4 *>(p.cache + 2 * at) = o;
+            if (slot >= 0 && hh >= Hq) {
+                const bool is_k = hh < Hq + Hkv;
+                const uint4 o = is_k ? make_uint4(y[0], y[1], y[2], y[3]) : x[b];
+                const int64_t at = row0 + (is_k ? hh - Hq : hh - Hq - Hkv) * hstride + (is_k ? 0 : D) + d0;
+                if (p.fp8) {
+                    const float *sc = is_k ? p.k_scale : p.v_scale;
+                    *reinterpret_cast<uint2 *>(p.cache + at) = quantise8(o, fp8_scale(sc ? __ldg(sc) : 1.0f));
+                } else {
+                    *reinterpret_cast<uint4 *>(p.cache + 2 * at) = o;
                 }
             }
         }
@@ -288,21 +313,6 @@ int sm_count(cudaError_t &e)
     return sms;
 }
 
-cudaError_t launch_grid(void (*kernel)(RopeInsertParams), const RopeInsertParams &p, int blocks, int splits,
-                        cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks, (unsigned)splits);
-    cfg.blockDim = dim3((unsigned)kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 template <int D>
 cudaError_t launch_rope_d(const RopeInsertParams &p, cudaStream_t stream)
 {
@@ -310,22 +320,15 @@ cudaError_t launch_rope_d(const RopeInsertParams &p, cudaStream_t stream)
     const int sms = sm_count(e);
     if (e != cudaSuccess)
         return e;
-    // One CTA per token while tokens last for four CTAs per SM; fewer tokens
-    // split their head rows over blockIdx.y so that the small calls of a draft
-    // step have one batch of loads per warp.
     const int rows = p.num_heads + p.num_kv_heads * (p.slot_mapping ? 2 : 1);
-    const int groups = (rows + 256 / D * kWarps - 1) / (256 / D * kWarps);
-    const int most = 4 * sms;
-    const int blocks = (int)(p.num_tokens < most ? p.num_tokens : most);
-    int splits = most / (blocks > 0 ? blocks : 1);
-    splits = splits < 1 ? 1 : splits > groups ? groups : splits;
-    if (splits > 64)
-        splits = 64;
+    const int per = 256 / D * kBatch;  // rows of a unit
+    const int64_t want = (p.num_tokens * ((rows + per - 1) / per) + kWarps - 1) / kWarps, most = (p.vec ? 4 : 2) * (int64_t)sms;
+    const int blocks = (int)(want < most ? want : most);
     if (p.vec)
-        return launch_grid(p.table_fp32 ? rope_insert_kernel<D, true, true> : rope_insert_kernel<D, true, false>, p,
-                           blocks, splits, stream);
-    return launch_grid(p.table_fp32 ? rope_insert_kernel<D, false, true> : rope_insert_kernel<D, false, false>, p,
-                       blocks, splits, stream);
+        return launch_pdl(p.table_fp32 ? rope_insert_kernel<D, true, true> : rope_insert_kernel<D, true, false>, blocks,
+                          kThreads, 0, stream, p);
+    return launch_pdl(p.table_fp32 ? rope_insert_kernel<D, false, true> : rope_insert_kernel<D, false, false>, blocks,
+                      kThreads, 0, stream, p);
 }
 
 }  // namespace

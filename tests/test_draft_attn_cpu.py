@@ -128,9 +128,9 @@ def test_evict_status(L, over, want):
 
 
 def test_workspaces(L):
-    # two lists of at most min(budget, places - budget) entries of 4 bytes per request and head
-    assert L.dspark_kv_evict_workspace(3, 2, 100, 60) == 3 * 2 * 2 * 40 * 4
-    assert L.dspark_kv_evict_workspace(3, 2, 100, 100) == 0 and L.dspark_kv_evict_workspace(3, 2, 10, 100) == 0
+    # a count and two lists of at most min(budget, places - budget) entries of 4 bytes per request and head
+    assert L.dspark_kv_evict_workspace(3, 2, 100, 60) == 3 * 2 * (1 + 2 * 40) * 4
+    assert L.dspark_kv_evict_workspace(3, 2, 100, 100) == 24 and L.dspark_kv_evict_workspace(3, 2, 10, 100) == 24
     assert L.dspark_kv_evict_workspace(3, 2, 100, 0) == -1
     assert L.dspark_tree_attention_workspace(0, 8, 2, 128, 4, 0) == 0 and L.dspark_tree_attention_workspace(5, 8, 2, 128, 0, 0) == 0
     assert L.dspark_tree_attention_workspace(5, 8, 3, 128, 4, 0) == -1 and L.dspark_tree_attention_workspace(5, 8, 2, 80, 4, 0) == -1
