@@ -1,5 +1,4 @@
-// Which kernel serves a call of the drafted tokens' attention and of the
-// weight accumulation.
+// Which kernel serves a call of the drafted tokens' attention.
 #include <cstdlib>
 #include <cstring>
 
@@ -58,15 +57,6 @@ cudaError_t launch_tree_attention(const AttnParams &p, int head_dim, bool fp8, c
     case 64: return attn::attention_d<64>(p, wr, fp8, stream);
     case 128: return attn::attention_d<128>(p, wr, fp8, stream);
     default: return attn::attention_d<256>(p, wr, fp8, stream);
-    }
-}
-
-cudaError_t launch_attention_weight(const AttnParams &p, int head_dim, bool fp8, cudaStream_t stream)
-{
-    switch (head_dim) {
-    case 64: return attn::weight_d<64>(p, fp8, stream);
-    case 128: return attn::weight_d<128>(p, fp8, stream);
-    default: return attn::weight_d<256>(p, fp8, stream);
     }
 }
 

@@ -1,4 +1,4 @@
-// The drafted tokens' attention and the weight accumulation for head dim 256
+// The drafted tokens' attention (mma.sync) for head dim 256
 // (one translation unit per head dim, so that they compile side by side).
 #include "tree_attn_mma.cuh"
 

@@ -1,6 +1,6 @@
-// Drafted tokens' attention over the paged cache, and the attention weight
-// the cached tokens received: the pieces both kernels share and the
-// attention kernel for up to 64 query rows at a time (mma.sync, sm_103a).
+// Drafted tokens' attention over the paged cache: the pieces that its kernels
+// and the weight accumulation share, and the attention kernel for up to 64
+// query rows at a time (mma.sync, sm_103a).
 //
 // Mathematics.  For a query row q and the keys j it sees, with s_j = scale
 // q.k_j:  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  lse = m +
@@ -965,176 +965,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     }
 }
 
-// ------------------------------------------------------------------ the weight kernel
-
-// Units are (request, KV head, tile); a CTA takes an equal share of them and
-// for each tile all rows of its head, four warps of 16 rows at a time, so
-// every weight has one owner and one order of summation.  Only K is read.
-template <int D, bool FP8>
-struct WeightCfg {
-    static constexpr int kRow = 2 * D * (FP8 ? 1 : 2), kCopy = kRow / 2;
-    static constexpr int kStage = kTile * kCopy;
-    static constexpr int kStages = kStage <= 8192 ? 4 : kStage <= 16384 ? 3 : 2;
-    static constexpr int kSmem = kStages * kStage;
-    static constexpr int kCtas = D == 256 ? 2 : 3;
-};
-
-template <int D, bool FP8>
-__global__ void __launch_bounds__(kThreads, (WeightCfg<D, FP8>::kCtas)) weight_kernel(const __grid_constant__ AttnParams p)
-{
-    using C = WeightCfg<D, FP8>;
-    extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int64_t scratch[kWarps + 4];
-    __shared__ uint32_t live[C::kStages][kWarps];
-    __shared__ float sums[2][kWarps][kTile];
-    pdl_enter();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2;
-    const uint32_t stages = saddr(smem);
-    unsigned flags = 0;
-    const int ctas = gridDim.x, cta = blockIdx.x;
-    // a request without drafted tokens still decays
-    auto checked = [&](int b, unsigned &fl) {
-        Request r = request(p, b, 0x7fffffff, fl);
-        if (r.ctx > p.weight_stride || (r.nq == 0 && (r.ctx < 0 || r.ctx > p.table_blocks * p.block_size))) {
-            fl |= kFlagLength;
-            r.ctx = 0;
-        }
-        const int q1 = __ldg(p.query_start + b + 1);
-        if (r.nq == 0 && !(q1 == r.q0 && r.q0 >= 0 && q1 <= p.num_rows))
-            r.ctx = 0;  // left out
-        return r;
-    };
-    auto units_of = [&](int b) -> int64_t {
-        return (int64_t)p.num_kv_heads * ((checked(b, flags).ctx + kTile - 1) / kTile);
-    };
-    const Find f = find_request<kThreads>(p.num_requests, scratch, units_of, [&](int64_t total) {
-        return (int64_t)((unsigned long long)total * cta / (unsigned long long)ctas);
-    });
-    const int64_t total = f.total;
-    const int64_t lo = (int64_t)((unsigned long long)total * cta / (unsigned long long)ctas);
-    const int64_t hi = (int64_t)((unsigned long long)total * (cta + 1) / (unsigned long long)ctas);
-    if (f.b < 0 || lo >= hi) {
-        flags = __reduce_or_sync(0xffffffffu, flags);
-        if (flags && lane == 0 && p.error_flags)
-            atomicOr(p.error_flags, flags);
-        return;
-    }
-    const float ks = FP8 && p.k_scale ? __ldg(p.k_scale) : 1.0f;
-    const float base_scale = p.scale * kLog2e * ks;
-    struct Walk {
-        int64_t u;
-        int b, h, tile, tiles;
-        Request rq;
-    };
-    auto enter = [&](Walk &w) {
-        unsigned ignore = 0;
-        w.rq = checked(w.b, ignore);
-        w.tiles = (w.rq.ctx + kTile - 1) / kTile;
-    };
-    auto step = [&](Walk &w) {
-        w.u++;
-        if (++w.tile < w.tiles)
-            return;
-        w.tile = 0;
-        if (++w.h < p.num_kv_heads || w.u >= hi)
-            return;
-        w.h = 0;
-        do {
-            w.b++;
-            enter(w);
-        } while (w.tiles == 0);
-    };
-    Walk cp;
-    cp.u = lo;
-    cp.b = f.b;
-    enter(cp);
-    {
-        const int64_t in = lo - f.before;
-        cp.h = (int)(in / cp.tiles);
-        cp.tile = (int)(in - (int64_t)cp.h * cp.tiles);
-    }
-    Walk w = cp;
-    Loader<C::kRow, C::kCopy> ld;
-    ld.fetch(p, cp.b, cp.tile, cp.rq.ctx, flags);
-    auto issue = [&](int stage) {
-        if (cp.u < hi) {
-            ld.load(p, cp.h, stages + stage * C::kStage, live[stage], flags);
-            step(cp);
-            if (cp.u < hi)
-                ld.fetch(p, cp.b, cp.tile, cp.rq.ctx, flags);
-        }
-        cp_commit();
-    };
-#pragma unroll
-    for (int s = 0; s < C::kStages - 1; s++)
-        issue(s);
-    int stage = 0, buf = 0;
-    int have_b = -1, have_h = -1;
-    uint32_t qa[D / 16][4];
-    float c[2], z[2];  // scale and lse (base 2) of the lane's two rows
-    for (; w.u < hi; step(w)) {
-        cp_wait<C::kStages - 2>();
-        __syncthreads();
-        issue((stage + C::kStages - 1) % C::kStages);
-        const int rows = w.rq.nq * p.group;
-        const bool single = rows <= 16 * kWarps;
-        float total_w = 0.0f;  // thread < kTile: its key's sum
-        for (int row0 = 0; row0 < rows; row0 += 16 * kWarps) {
-            if (!single || w.b != have_b || w.h != have_h) {
-                float rs[2];
-                load_q<D, FP8>(p, w.rq, w.h, row0 + 16 * warp, qa, rs);
-#pragma unroll
-                for (int s = 0; s < 2; s++) {
-                    const int r = row0 + 16 * warp + g + 8 * s, i = r / p.group;
-                    c[s] = base_scale * rs[s];
-                    z[s] = INFINITY;
-                    if (r < rows) {
-                        const float l = __ldg(p.lse + (int64_t)(w.rq.q0 + i) * p.num_heads + w.h * p.group + (r - i * p.group));
-                        z[s] = l == -INFINITY ? INFINITY : l * kLog2e;  // a row that saw nothing adds nothing
-                    }
-                }
-                have_b = w.b, have_h = w.h;
-            }
-#pragma unroll
-            for (int half = 0; half < 2; half++) {
-                float s[kTile / 16][4];
-#pragma unroll
-                for (int n = 0; n < kTile / 16; n++)
-                    s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-                scores<D, FP8, kTile / 16, C::kCopy>(s, qa, stages + stage * C::kStage, half * (kTile / 2));
-#pragma unroll
-                for (int n = 0; n < kTile / 16; n++) {
-                    float x0 = ex2(fmaf(s[n][0], c[0], -z[0])) + ex2(fmaf(s[n][2], c[1], -z[1]));
-                    float x1 = ex2(fmaf(s[n][1], c[0], -z[0])) + ex2(fmaf(s[n][3], c[1], -z[1]));
-#pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        x0 += __shfl_xor_sync(0xffffffffu, x0, d);
-                        x1 += __shfl_xor_sync(0xffffffffu, x1, d);
-                    }
-                    if (g == 0)
-                        *reinterpret_cast<float2 *>(&sums[buf][warp][half * (kTile / 2) + 8 * n + 2 * lane]) = make_float2(x0, x1);
-                }
-            }
-            __syncthreads();
-            if (tid < kTile)
-                total_w += (sums[buf][0][tid] + sums[buf][1][tid]) + (sums[buf][2][tid] + sums[buf][3][tid]);
-            buf ^= 1;  // the next round's sums go to the other buffer: no second barrier
-        }
-        if (tid < kTile) {
-            const int j = w.tile * kTile + tid;
-            if (j < w.rq.ctx && ((live[stage][tid >> 4] >> (tid & 15)) & 1u)) {
-                float *at = p.weights + ((int64_t)w.b * p.num_kv_heads + w.h) * p.weight_stride + j;
-                *at = fmaf(p.decay, *at, total_w);
-            }
-        }
-        stage = stage + 1 == C::kStages ? 0 : stage + 1;
-    }
-    cp_wait<0>();
-    flags = __reduce_or_sync(0xffffffffu, flags);
-    if (flags && lane == 0 && p.error_flags)
-        atomicOr(p.error_flags, flags);
-}
-
 // ------------------------------------------------------------------ launches
 
 struct Plan {
@@ -1211,27 +1041,6 @@ cudaError_t attention(const AttnParams &p, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, join_kernel<D, FP8, WR>, p, ctas);
 }
 
-template <int D, bool FP8>
-cudaError_t weight(const AttnParams &p, cudaStream_t stream)
-{
-    using C = WeightCfg<D, FP8>;
-    static int cached[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
-        return e;
-    if (dev < 0 || dev >= 64)
-        return cudaErrorInvalidDevice;
-    int have = __atomic_load_n(&cached[dev], __ATOMIC_ACQUIRE);
-    if (have == 0) {
-        e = prepare(weight_kernel<D, FP8>, C::kSmem, 8, have);
-        if (e != cudaSuccess)
-            return e;
-        __atomic_store_n(&cached[dev], have, __ATOMIC_RELEASE);
-    }
-    return launch_pdl(weight_kernel<D, FP8>, have, kThreads, C::kSmem, stream, p);
-}
-
 // Rows of an item: the smallest of 16, 32 and 64 that holds the mean request's
 // rows, 64 beyond.  Lengths are on the device; rows / requests is what the
 // host knows of them.
@@ -1261,21 +1070,13 @@ cudaError_t attention_d(const AttnParams &p, int wr, bool fp8, cudaStream_t stre
     }
 }
 
-template <int D>
-cudaError_t weight_d(const AttnParams &p, bool fp8, cudaStream_t stream)
-{
-    return fp8 ? weight<D, true>(p, stream) : weight<D, false>(p, stream);
-}
-
 // one translation unit per head dim
 #define DSPARK_ATTN_DECLARE(D)                                                     \
     extern template int64_t workspace_d<D>(int, bool, cudaError_t &);              \
-    extern template cudaError_t attention_d<D>(const AttnParams &, int, bool, cudaStream_t); \
-    extern template cudaError_t weight_d<D>(const AttnParams &, bool, cudaStream_t);
+    extern template cudaError_t attention_d<D>(const AttnParams &, int, bool, cudaStream_t);
 #define DSPARK_ATTN_DEFINE(D)                                                      \
     template int64_t workspace_d<D>(int, bool, cudaError_t &);                     \
-    template cudaError_t attention_d<D>(const AttnParams &, int, bool, cudaStream_t); \
-    template cudaError_t weight_d<D>(const AttnParams &, bool, cudaStream_t);
+    template cudaError_t attention_d<D>(const AttnParams &, int, bool, cudaStream_t);
 
 }  // namespace attn
 }  // namespace dspark

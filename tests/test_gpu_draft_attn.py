@@ -419,6 +419,9 @@ WEIGHTS = [  # ctx, nq, Hq, Hkv, D, bs, fp8, decay
     ((64, 500), (40, 9), 8, 1, 64, 48, True, 1.0),
     ((300, 65), (66, 2), 2, 2, 256, 100, False, 0.5),
     ((300, 65), (3, 64), 12, 4, 256, 16, True, 1.0),
+    ((700, 300, 1), (40, 33, 34), 16, 2, 128, 16, False, 0.7),
+    ((300, 1500), (64, 33), 20, 2, 64, 32, True, 0.7),
+    (tuple(range(0, 300)), tuple(i % 3 for i in range(300)), 2, 2, 64, 16, False, 0.5),
 ]
 
 
