@@ -240,15 +240,15 @@ __global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_const
                 }
             }
         };
-        Cursor cp, lk;
-        cp.w = w;
-        cp.skip(p);
-        lk = cp;
-        int phys = 0, off = -1, look_h = 0;
+        Cursor lk;
+        lk.w = w;
+        lk.skip(p);
+        int phys = 0, off = -1, look_h = 0, looked = 0;  // looked: tiles looked up, two ahead while there are any
         auto look = [&]() {
             off = -1;
             if (!lk.w.more())
                 return;
+            looked++;
             look_h = lk.w.h;
             const int j = lk.tile * kWKeys + 32 * pw + lane, blk = block_of(p, j);
             phys = 0;
@@ -275,103 +275,63 @@ __global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_const
             __syncwarp();
         };
         constexpr int kW = D * (FP8 ? 1 : 2) / 16;  // 16-byte words of a row's K
-        constexpr int kIt = kW;                    // words per lane: 32 rows of them
-        constexpr int kB = kIt < 8 ? kIt : 8;
-        auto where = [&](int i, int &y, int &c) { y = (i * 32 + lane) / kW, c = (i * 32 + lane) % kW; };
-        uint4 v[FP8 ? kB : 1];
-        auto load = [&](const uint32_t *from, int i0) {
-            if constexpr (FP8) {
+        constexpr int kB = kW < 8 ? kW : 8;        // of the kW words per lane (32 rows of them) this many at a time
+        bool ok = true;
+        // issues the copies of tile x (its rows are resolved), and resolves the next one's
+        auto issue = [&](int x) {
+            const uint32_t dst0 = tc::saddr(sk) + (x % NS) * C::kTileBytes;
+            const uint32_t *from = rows[pw][x & 1];
+            resolve((x & 1) ^ 1);
+            look();
+#pragma unroll 1
+            for (int i0 = 0; i0 < kW; i0 += kB) {
+                uint32_t src[kB];
+#pragma unroll
+                for (int i = 0; i < kB; i++)
+                    src[i] = from[((i0 + i) * 32 + lane) / kW];
 #pragma unroll
                 for (int i = 0; i < kB; i++) {
-                    int y, c;
-                    where(i0 + i, y, c);
-                    const uint32_t src = from[y];
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (src != ~0u)
-                        v[i] = __ldg(reinterpret_cast<const uint4 *>(p.cache + (int64_t)src * C::kRow + 16 * c));
-                }
-            }
-        };
-        bool ok = true;
-        int x = 0;
-        look();
-        resolve(0);
-        if (FP8 && cp.w.more())
-            load(rows[pw][0], 0);
-        look();
-        while (cp.w.more() && ok) {
-            const int st = x % NS, slot = x & 1;
-            unsigned char *dst = sk + st * C::kTileBytes;
-            const uint32_t dst0 = tc::saddr(dst);
-            const uint32_t *from = rows[pw][slot];
-            resolve(slot ^ 1);
-            look();
-            ok = bar_wait(kempty + st, ((uint32_t)(x / NS) & 1u) ^ 1u, abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok)
-                break;
-            if constexpr (FP8) {
-#pragma unroll 1
-                for (int i0 = 0; i0 < kIt; i0 += kB) {
-#pragma unroll
-                    for (int i = 0; i < kB; i++) {
-                        int y, c;
-                        where(i0 + i, y, c);
-                        y += 32 * pw;
-                        const uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            o[2 * k] = e4m3_to_half2((uint16_t)q[k]), o[2 * k + 1] = e4m3_to_half2((uint16_t)(q[k] >> 16));
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            const int kk = k ^ (c & 1), cc = 2 * c + kk;
-                            const uint32_t at = dst0 + (cc >> 3) * 16384 + y * 128 + (((cc & 7) ^ (y & 7)) << 4);
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(kk ? o[4] : o[0]), "r"(kk ? o[5] : o[1]),
-                                         "r"(kk ? o[6] : o[2]), "r"(kk ? o[7] : o[3])
-                                         : "memory");
-                        }
-                    }
-                    // the rest of this tile, or the next one's first words
-                    if (i0 + kB < kIt)
-                        load(from, i0 + kB);
-                    else
-                        load(rows[pw][slot ^ 1], 0);
-                }
-            } else {
-#pragma unroll 1
-                for (int i0 = 0; i0 < kIt; i0 += kB) {
-                    uint32_t src[kB];
-#pragma unroll
-                    for (int i = 0; i < kB; i++) {
-                        int y, c;
-                        where(i0 + i, y, c);
-                        src[i] = from[y];
-                    }
-#pragma unroll
-                    for (int i = 0; i < kB; i++) {
-                        int y, c;
-                        where(i0 + i, y, c);
-                        y += 32 * pw;
-                        cp16(dst0 + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4),
-                             src[i] != ~0u ? p.cache + (int64_t)src[i] * C::kRow + 16 * c : p.cache, src[i] != ~0u);
-                    }
+                    const int y = 32 * pw + ((i0 + i) * 32 + lane) / kW, c = ((i0 + i) * 32 + lane) % kW;
+                    const uint32_t at = FP8 ? raw_at<D>(dst0, y, c) : dst0 + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4);
+                    cp16(at, src[i] != ~0u ? p.cache + (int64_t)src[i] * C::kRow + 16 * c : p.cache, src[i] != ~0u);
                 }
             }
             const unsigned bits = __ballot_sync(0xffffffffu, from[lane] != ~0u);
-            if (lane == 0) {
+            if (lane == 0)
                 live[x & 15][pw] = bits;
-                bar_arrive(kfull + st);
-            }
-            if (FP8) {
-                fence_async();
-                bar_arrive(kfull + st);
-            } else {
-                bar_arrive_copies(kfull + st);
-            }
+            if (FP8)
+                cp_commit();
             __syncwarp();  // every lane is done with this tile's row numbers
-            x++;
-            cp.step(p);
+        };
+        auto free_parity = [&](int x) { return ((uint32_t)(x / NS) & 1u) ^ 1u; };
+        int issued = 0;
+        look();
+        resolve(0);
+        look();
+        for (int x = 0; x < looked && ok; x++) {
+            const int st = x % NS;
+            if (issued == x) {
+                ok = bar_wait(kempty + st, free_parity(x), abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                issue(issued++);
+            }
+            if constexpr (FP8) {
+                // the codes of the next tiles, as far as their stages are free
+                while (issued < looked && issued < x + NS && __all_sync(0xffffffffu, bar_test(kempty + issued % NS, free_parity(issued))))
+                    issue(issued++);
+                cp_wait_most(issued - x - 1);
+                __syncwarp();
+                convert_rows<D, 32>(tc::saddr(sk) + st * C::kTileBytes, 32 * pw, kWKeys);
+                fence_async();
+            }
+            if (lane == 0)
+                bar_arrive(kfull + st);  // the live mask
+            if (FP8)
+                bar_arrive(kfull + st);
+            else
+                bar_arrive_copies(kfull + st);
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {

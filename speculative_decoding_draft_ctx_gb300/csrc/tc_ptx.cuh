@@ -52,6 +52,19 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
+// bar_try without a wait
+__device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(saddr(bar)), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+
 // Waits for the phase of `bar` with this parity; false after kTimeoutNs or
 // once another thread of the CTA has given up (which it then records).
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort)

@@ -371,6 +371,95 @@ struct Loader {
     }
 };
 
+// whether a 32-bit word of V holds an infinity or NaN
+__device__ __forceinline__ bool nonfinite_word(uint32_t w, bool fp8)
+{
+    if (fp8) {  // any byte 0x7f or 0xff
+        const uint32_t x = (w & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;
+        return ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
+    }
+    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+// ------------------------------------------------------------------ fp8 tiles of the tensor-core kernels
+
+// A tile's operand holds a row of D fp16 values as D / 64 pieces of 128 bytes,
+// 16384 bytes apart, 16-byte words of row y at word ^ (y & 7).  The row's D
+// codes are copied into the upper half of the row's own bytes (word c at
+// raw_at) and converted from there in place: no row touches another's bytes,
+// and a short rolled loop does it (from registers, unrolled, a 16-byte word
+// took 330 cycles of a warp, mostly instruction fetches).
+template <int D>
+__device__ __forceinline__ uint32_t raw_at(uint32_t tile, int y, int c)
+{
+    return tile + (D == 64 ? 0 : (D / 128 + (c >> 3)) * 16384) + y * 128 + ((c & 7) << 4);
+}
+
+// Rows [row0, row0 + ROWS) of a tile by one warp, after their codes have
+// landed.  Rows from `clean` on have NaN codes zeroed; true if there were any.
+template <int D, int ROWS>
+__device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean)
+{
+    constexpr int kW = D / 16, kR = 32 / kW, kU = 2;
+    const int lane = threadIdx.x & 31, c = lane % kW, r = lane / kW;
+    bool any = false;
+#pragma unroll 1
+    for (int y0 = row0; y0 < row0 + ROWS; y0 += kU * kR) {
+        uint32_t q[kU][4];
+#pragma unroll
+        for (int u = 0; u < kU; u++)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(q[u][0]), "=r"(q[u][1]), "=r"(q[u][2]), "=r"(q[u][3])
+                         : "r"(raw_at<D>(tile, y0 + u * kR + r, c))
+                         : "memory");
+        __syncwarp();  // the rows' codes are read before their bytes are written
+#pragma unroll
+        for (int u = 0; u < kU; u++) {
+            const int y = y0 + u * kR + r;
+            if (y >= clean) {
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    if (nonfinite_word(q[u][k], true)) {
+                        any = true;
+#pragma unroll 1
+                        for (int e = 0; e < 32; e += 8)
+                            if (((q[u][k] >> e) & 0x7fu) == 0x7fu)
+                                q[u][k] &= ~(0xffu << e);
+                    }
+            }
+            uint32_t o[8];
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                o[2 * k] = e4m3_to_half2((uint16_t)q[u][k]), o[2 * k + 1] = e4m3_to_half2((uint16_t)(q[u][k] >> 16));
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                // 16-byte words 2 c and 2 c + 1 of the fp16 row, odd lanes the other way round (bank conflicts)
+                const int kk = k ^ (c & 1), cc = 2 * c + kk;
+                const uint32_t at = tile + (cc >> 3) * 16384 + y * 128 + (((cc & 7) ^ (y & 7)) << 4);
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(kk ? o[4] : o[0]), "r"(kk ? o[5] : o[1]),
+                             "r"(kk ? o[6] : o[2]), "r"(kk ? o[7] : o[3])
+                             : "memory");
+            }
+        }
+    }
+    return any;
+}
+
+// Waits until at most `pending` (0 to 7) of this thread's newest copy groups are in flight.
+__device__ __forceinline__ void cp_wait_most(int pending)
+{
+    switch (pending) {
+    case 0: cp_wait<0>(); break;
+    case 1: cp_wait<1>(); break;
+    case 2: cp_wait<2>(); break;
+    case 3: cp_wait<3>(); break;
+    case 4: cp_wait<4>(); break;
+    case 5: cp_wait<5>(); break;
+    case 6: cp_wait<6>(); break;
+    default: cp_wait<7>(); break;
+    }
+}
+
 // ------------------------------------------------------------------ queries
 
 // The A operands of a warp's 16 rows: reg 0 / 1 row g / g + 8 of the lower 8
@@ -515,15 +604,6 @@ __device__ __forceinline__ bool sees(const AttnParams &p, const Request &rq, int
     if (p.mask_kind == 1)
         return a <= i;
     return (__ldg(p.tree_mask + (int64_t)(rq.q0 + i) * p.mask_words + (a >> 6)) >> (a & 63)) & 1ull;
-}
-
-__device__ __forceinline__ bool nonfinite_word(uint32_t w, bool fp8)
-{
-    if (fp8) {  // any byte 0x7f or 0xff
-        const uint32_t x = (w & 0x7f7f7f7fu) ^ 0x7f7f7f7fu;
-        return ((x - 0x01010101u) & ~x & 0x80808080u) != 0;
-    }
-    return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
 // V[a, d] of the request's drafted token a as a float (0 where its block is out of range)

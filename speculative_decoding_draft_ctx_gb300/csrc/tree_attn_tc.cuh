@@ -288,19 +288,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         // Two warps copy K, two V, each 64 rows of every tile.  While a warp
         // copies a tile it has the next one's rows fetched into L2, so that what
         // is in flight is not bounded by the rings, and looks up the blocks of
-        // the one after.
+        // the one after.  bf16 lands in place and the copies themselves arrive
+        // on the tile's barrier; fp8 lands as codes, is converted, and the next
+        // tile is issued before that where its stage is free already.
         const int pw = warp - 8, half = pw >> 1, sub = pw & 1;  // half 0: K, 1: V
         const bool is_v = half != 0;
         const unsigned char *cache = p.cache + half * (C::kRow / 2);
         unsigned char *ring = is_v ? sv : sk;
+        uint64_t *fulls = is_v ? vfull : kfull, *empties = is_v ? vempty : kempty;
         const int ns = is_v ? NV : NK;
         int phys[2], off[2];  // of the tile looked up last: rows lane and lane + 32 of the warp's; off < 0: past the end
-        int look_tile = w.t0, look_head = w.more() ? w.head() : 0;
-        W lw = w;  // the walk of the look-ups; w is the walk of the copies
+        int look_tile = w.t0, look_head = 0, looked = 0;  // looked: tiles looked up, two ahead while there are any
+        W lw = w;  // the walk of the look-ups; w is the walk of the tiles that are finished
         auto look = [&]() {
             off[0] = off[1] = -1;
             if (!lw.more())
                 return;
+            looked++;
             const int len = lw.rq.ctx + lw.rq.nq;
             look_head = lw.head();
 #pragma unroll
@@ -338,124 +342,27 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             __syncwarp();
         };
         constexpr int kW = D * (FP8 ? 1 : 2) / 16, kR = 32 / kW;  // 16-byte words of a row's half; rows a warp takes at once
+        constexpr int kB = 64 / kR < 8 ? 64 / kR : 8;
         const int c = lane % kW, r = lane / kW;
-        // fp8: half of the warp's rows at a time in registers, loaded a tile ahead
-        constexpr int kB = FP8 ? 32 / kR : 8;
-        uint4 va[FP8 ? kB : 1], vb[FP8 ? kB : 1];
-        auto load = [&](const uint32_t *from, uint4 *to) {
-            if constexpr (FP8) {
+        bool ok = true;
+        // issues the copies of tile number x of the share (its rows are resolved),
+        // and resolves the next one's
+        auto issue = [&](int x) {
+            const uint32_t dst0 = tc::saddr(ring) + (x % ns) * C::kTileBytes;
+            const uint32_t *from = rows[pw][x & 1];
+            resolve((x & 1) ^ 1);
+            look();
+#pragma unroll 1
+            for (int y0 = 0; y0 < 64; y0 += kR * kB) {
                 uint32_t src[kB];
 #pragma unroll
                 for (int i = 0; i < kB; i++)
-                    src[i] = from[i * kR + r];
+                    src[i] = from[y0 + i * kR + r];
 #pragma unroll
                 for (int i = 0; i < kB; i++) {
-                    to[i] = make_uint4(0, 0, 0, 0);
-                    if (src[i] != ~0u)
-                        to[i] = __ldg(reinterpret_cast<const uint4 *>(cache + (int64_t)src[i] * C::kRow + 16 * c));
-                }
-            }
-        };
-        bool ok = true;
-        int x = 0, item = 0, tile = w.t0;  // tile and item number of the share; the request's tile
-        look();
-        resolve(0);
-        if (FP8 && w.more()) {
-            load(rows[pw][0], va);
-            load(rows[pw][0] + 32, vb);
-        }
-        look();
-        while (w.more() && ok) {
-            const int st = x % ns, key0 = tile * kKeysTc + 64 * sub, slot = x & 1;
-            const uint32_t parity = ((uint32_t)(x / ns) & 1u) ^ 1u;
-            const bool drafted = is_v && key0 + 64 > w.rq.ctx;
-            uint64_t *full = (is_v ? vfull : kfull) + st, *empty = (is_v ? vempty : kempty) + st;
-            unsigned char *dst = ring + st * C::kTileBytes;
-            const uint32_t dst0 = tc::saddr(dst);
-            const uint32_t *from = rows[pw][slot];
-            resolve(slot ^ 1);  // the next tile
-            look();
-            ok = bar_wait(empty, parity, abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok)
-                break;
-            if constexpr (FP8) {
-                auto store = [&](const uint4 *v, int row0) {
-#pragma unroll
-                    for (int i = 0; i < kB; i++) {
-                        const int y = 64 * sub + row0 + i * kR + r;
-                        uint32_t q[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                        if (drafted && tile * kKeysTc + y >= w.rq.ctx) {
-                            // NaN among the drafted V: zeroed here, accounted for at the end
-                            if (nonfinite_word(q[0], true) || nonfinite_word(q[1], true) || nonfinite_word(q[2], true) || nonfinite_word(q[3], true)) {
-                                bad[item & 15] = item + 1;
-#pragma unroll
-                                for (int k = 0; k < 4; k++)
-#pragma unroll 1
-                                    for (int e = 0; e < 32; e += 8)
-                                        if (((q[k] >> e) & 0x7fu) == 0x7fu)
-                                            q[k] &= ~(0xffu << e);
-                            }
-                        }
-                        uint32_t o[8];
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            o[2 * k] = e4m3_to_half2((uint16_t)q[k]), o[2 * k + 1] = e4m3_to_half2((uint16_t)(q[k] >> 16));
-#pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            // 16-byte words 2 c and 2 c + 1 of the fp16 row, odd lanes the other way round (bank conflicts)
-                            const int kk = k ^ (c & 1), cc = 2 * c + kk;
-                            const uint32_t at = dst0 + (cc >> 3) * 16384 + y * 128 + (((cc & 7) ^ (y & 7)) << 4);
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(kk ? o[4] : o[0]), "r"(kk ? o[5] : o[1]),
-                                         "r"(kk ? o[6] : o[2]), "r"(kk ? o[7] : o[3])
-                                         : "memory");
-                        }
-                    }
-                };
-                store(va, 0);
-                load(rows[pw][slot ^ 1], va);
-                store(vb, 32);
-                load(rows[pw][slot ^ 1] + 32, vb);
-            } else {
-                const uint32_t dc = dst0 + (c >> 3) * 16384;
-#pragma unroll 1
-                for (int y0 = 0; y0 < 64; y0 += kR * kB) {
-                    uint32_t src[kB];
-#pragma unroll
-                    for (int i = 0; i < kB; i++)
-                        src[i] = from[y0 + i * kR + r];
-#pragma unroll
-                    for (int i = 0; i < kB; i++) {
-                        const int y = 64 * sub + y0 + i * kR + r;
-                        cp16(dc + y * 128 + (((c & 7) ^ (y & 7)) << 4), src[i] != ~0u ? cache + (int64_t)src[i] * C::kRow + 16 * c : p.cache,
-                             src[i] != ~0u);
-                    }
-                }
-                if (drafted) {
-                    // infinities and NaN among the drafted V: zeroed here, accounted for at the end
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
-                    for (int y = 64 * sub + r; y < 64 * sub + 64; y += kR) {
-                        if (tile * kKeysTc + y < w.rq.ctx)
-                            continue;
-                        uint4 *at = reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4));
-                        const uint4 v = *at;
-                        uint32_t q[4] = {v.x, v.y, v.z, v.w};
-                        bool hit = false;
-#pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            if (nonfinite_word(q[k], false)) {
-                                hit = true;
-                                if ((q[k] & 0x7f80u) == 0x7f80u)
-                                    q[k] &= 0xffff0000u;
-                                if ((q[k] & 0x7f800000u) == 0x7f800000u)
-                                    q[k] &= 0xffffu;
-                            }
-                        if (hit) {
-                            *at = make_uint4(q[0], q[1], q[2], q[3]);
-                            bad[item & 15] = item + 1;
-                        }
-                    }
+                    const int y = 64 * sub + y0 + i * kR + r;
+                    const uint32_t at = FP8 ? raw_at<D>(dst0, y, c) : dst0 + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4);
+                    cp16(at, src[i] != ~0u ? cache + (int64_t)src[i] * C::kRow + 16 * c : p.cache, src[i] != ~0u);
                 }
             }
             if (!is_v) {
@@ -465,17 +372,71 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     if (lane == 0)
                         live[x & 7][2 * sub + g] = bits;
                 }
-                if (lane == 0)
-                    bar_arrive(full);
             }
-            if (FP8 || drafted) {
-                fence_async();
-                bar_arrive(full);
-            } else {
-                bar_arrive_copies(full);
-            }
+            if (FP8)
+                cp_commit();
             __syncwarp();  // every lane is done with this tile's row numbers
-            x++;
+        };
+        auto free_parity = [&](int x) { return ((uint32_t)(x / ns) & 1u) ^ 1u; };
+        int x = 0, item = 0, tile = w.t0, issued = 0;  // tile and item number of the share; the request's tile
+        look();
+        resolve(0);
+        look();
+        for (; x < looked && ok; x++) {
+            const int st = x % ns, key0 = tile * kKeysTc + 64 * sub;
+            const bool drafted = is_v && key0 + 64 > w.rq.ctx;
+            if (issued == x) {
+                ok = bar_wait(empties + st, free_parity(x), abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                issue(x);
+                issued++;
+            }
+            if (FP8 && x + 1 < looked && __all_sync(0xffffffffu, bar_test(empties + (x + 1) % ns, free_parity(x + 1)))) {
+                issue(x + 1);
+                issued++;
+            }
+            if constexpr (FP8) {
+                cp_wait_most(issued - x - 1);
+                __syncwarp();
+                if (convert_rows<D, 64>(tc::saddr(ring) + st * C::kTileBytes, 64 * sub, drafted ? w.rq.ctx - tile * kKeysTc : kKeysTc))
+                    bad[item & 15] = item + 1;
+                fence_async();
+            } else if (drafted) {
+                // infinities and NaN among the drafted V: zeroed here, accounted for at the end
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                unsigned char *dst = ring + st * C::kTileBytes;
+#pragma unroll 1
+                for (int y = 64 * sub + r; y < 64 * sub + 64; y += kR) {
+                    if (tile * kKeysTc + y < w.rq.ctx)
+                        continue;
+                    uint4 *at = reinterpret_cast<uint4 *>(dst + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4));
+                    const uint4 v = *at;
+                    uint32_t q[4] = {v.x, v.y, v.z, v.w};
+                    bool hit = false;
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        if (nonfinite_word(q[k], false)) {
+                            hit = true;
+                            if ((q[k] & 0x7f80u) == 0x7f80u)
+                                q[k] &= 0xffff0000u;
+                            if ((q[k] & 0x7f800000u) == 0x7f800000u)
+                                q[k] &= 0xffffu;
+                        }
+                    if (hit) {
+                        *at = make_uint4(q[0], q[1], q[2], q[3]);
+                        bad[item & 15] = item + 1;
+                    }
+                }
+                fence_async();
+            }
+            if (!is_v && lane == 0)
+                bar_arrive(fulls + st);  // the live masks
+            if (FP8 || drafted)
+                bar_arrive(fulls + st);
+            else
+                bar_arrive_copies(fulls + st);
             if (++tile >= w.t1) {
                 w.next(p);
                 tile = w.t0;
