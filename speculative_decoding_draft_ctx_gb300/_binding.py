@@ -140,7 +140,7 @@ def lib() -> ctypes.CDLL:
         L.dspark_ctx_kv_validate_layers_general.restype = I
         # include/dspark_draft_attn.h
         F, D = ctypes.c_float, ctypes.c_double
-        L.dspark_rope_table.argtypes = [P, I64, I64, I, ctypes.POINTER(D), D, I, P]
+        L.dspark_rope_table.argtypes = [P, I64, I64, I, P, D, I, P]
         L.dspark_rope_kv_insert.argtypes = [P, I64, I64] * 5 + [P, I, I64, P, I64, I, I, I, I, I, I, P, P, I64, I, I,
                                                                 P, P, P, P]
         queries = [P, I64, I64, I64, I, I, I, P, I64, I, I]

@@ -14,8 +14,8 @@
 // 64 requests x 7 tokens x 8 heads took 165 us, two long fp8 contexts 184 us.
 //
 // One CTA per SM takes an equal share of the tiles of all (request, KV head)
-// pairs.  Four producer warps gather K through the block table into a ring
-// (as in tree_attn_tc.cuh), one warp issues the products, two warpgroups of
+// pairs.  Producer warps gather K through the block table into a ring (as in
+// tree_attn_tc.cuh), one warp issues the products, two warpgroups of
 // 128 threads (one key each) take every other tile from their own buffer of
 // scores.  The rows' lse (negated, base 2) and scale sit in shared memory and
 // are read as broadcasts.  Heads of more than kRows query rows take them in
@@ -29,17 +29,23 @@
 namespace dspark {
 namespace attn {
 
-constexpr int kWThreads = 416, kWKeys = 128, kWItemCost = 3;  // warps 0-7 sum, 8-11 gather, 12 issues
+constexpr int kWKeys = 128, kWItemCost = 3;
 
 template <int D, bool FP8>
 struct WeightTc {
     static constexpr int kRows = D == 256 ? 128 : 256;     // query rows of a group
     static constexpr int kTileBytes = kWKeys * D * 2;
     static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 2;
+    // Warps 0-7 sum, four gather, the last issues.  A bf16 tile is gathered by
+    // all four, 32 rows each; fp8 tiles, which wait for their codes and are
+    // converted, go in turn to kGroups groups of them.
+    static constexpr int kProducers = 4, kGroups = !FP8 ? 1 : kStages < 4 ? kStages : 4;
+    static constexpr int kWarpRows = 128 * kGroups / kProducers;  // rows of a tile per producer warp
+    static constexpr int kIssuer = 8 + kProducers, kThreads = 32 * (kIssuer + 1);
     static constexpr int kQBytes = kRows * D * 2;
     static constexpr int kRow = 2 * D * (FP8 ? 1 : 2);     // bytes of a cached token
     static constexpr int kSmem = 1024 + kQBytes + kStages * kTileBytes;
-    static_assert(kSmem + 8 * 1024 <= 227 * 1024, "shared memory");
+    static_assert(kSmem + 8 * 1024 <= 227 * 1024 && kStages % kGroups == 0, "shared memory");
 };
 
 // This CTA's share: per pair kWItemCost units and a unit per (tile, row group).
@@ -108,7 +114,7 @@ struct WeightWalk {
         if (lo >= hi)
             return;
         enter(p);
-        h = (int)((lo - before) / span());
+        h = (int)Shares::div(lo - before, span());
         at = before + (int64_t)h * span();
         clip();
         if (t0 >= t1)
@@ -117,7 +123,7 @@ struct WeightWalk {
 };
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel(const __grid_constant__ AttnParams p)
 {
     using C = WeightTc<D, FP8>;
     using namespace tc;
@@ -126,16 +132,17 @@ __global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_const
     unsigned char *smem = smem_raw + ((1024u - (tc::saddr(smem_raw) & 1023u)) & 1023u);
     unsigned char *sq = smem, *sk = smem + C::kQBytes;
     __shared__ uint64_t kfull[NS], kempty[NS], sfull[2], sempty[2], qfull, qempty, done;
-    __shared__ uint32_t tmem_slot, live[16][4], rows[4][2][32];
+    constexpr int PG = C::kGroups, WR = C::kWarpRows, RG = WR / 32;
+    __shared__ uint32_t tmem_slot, live[16][4], rows[C::kProducers][2][WR];
     __shared__ int abort_flag;
     __shared__ __align__(16) float zneg[2][kRows], cscale[2][FP8 ? kRows : 4];  // of a group's rows: -lse, scale (base 2)
-    __shared__ int64_t scratch[kWThreads / 32 + 4];
+    __shared__ int64_t scratch[C::kThreads / 32 + 4];
     volatile int *abort = &abort_flag;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int s = 0; s < NS; s++) {
-            bar_init(kfull + s, 128 + 4);  // the producers' copies, and their live masks
+            bar_init(kfull + s, C::kProducers / PG * 33);  // a group's copies, and its live masks
             bar_init(kempty + s, 1);
         }
         for (int s = 0; s < 2; s++) {
@@ -148,7 +155,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_const
         abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 12) {
+    if (warp == C::kIssuer) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::saddr(&tmem_slot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -156,17 +163,16 @@ __global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_const
     unsigned flags = 0;
     using W = WeightWalk<kRows>;
     const int ctas = gridDim.x, cta = blockIdx.x;
-    const Find f = find_request<kWThreads>(
-        p.num_requests, scratch, [&](int b) { return W::units(p, W::checked(p, b, flags)); },
-        [&](int64_t total) { return share_start(total, cta, ctas); });
+    const Find f = find_request<C::kThreads>(p.num_requests, scratch, [&](int b) { return W::units(p, W::checked(p, b, flags)); });
+    const Shares shares(f.total, ctas);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = tmem_slot;
     W w;
-    w.start(p, f.b >= 0 ? share_start(f.total, cta, ctas) : 0, f.b >= 0 ? share_start(f.total, cta + 1, ctas) : 0, f.b, f.before);
+    w.start(p, f.b >= 0 ? shares.start(cta) : 0, f.b >= 0 ? shares.start(cta + 1) : 0, f.b, f.before);
 
-    if (warp == 12) {
+    if (warp == C::kIssuer) {
         // ------------------------------------------------------------ the issuing warp
         const bool leader = elect();
         int x = 0, ng = 0;  // tiles, groups so far
@@ -217,9 +223,8 @@ __global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_const
             mma_commit(&done);
         __syncwarp();
     } else if (warp >= 8) {
-        // ------------------------------------------------------------ producers: 32 rows of every tile each
-        // (see tree_attn_tc.cuh; a tile is gathered once per row group)
-        const int pw = warp - 8;
+        // ------------------------------------------------------------ producers (a tile is gathered once per row group)
+        const int pw = warp - 8, mine = pw % PG, row0 = pw / PG * WR;  // tiles number mine, mine + PG, ...; rows row0 ...
         struct Cursor {
             W w;
             int tile, group;
@@ -243,87 +248,87 @@ __global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_const
         Cursor lk;
         lk.w = w;
         lk.skip(p);
-        int phys = 0, off = -1, look_h = 0, looked = 0;  // looked: tiles looked up, two ahead while there are any
+        for (int i = 0; i < mine && lk.w.more(); i++)
+            lk.step(p);
+        int phys[RG], off[RG], look_h = 0, looked = 0;  // looked: tiles looked up, two ahead while there are any
         auto look = [&]() {
-            off = -1;
+#pragma unroll
+            for (int g = 0; g < RG; g++)
+                off[g] = -1;
             if (!lk.w.more())
                 return;
             looked++;
             look_h = lk.w.h;
-            const int j = lk.tile * kWKeys + 32 * pw + lane, blk = block_of(p, j);
-            phys = 0;
-            if (j < lk.w.rq.ctx) {
-                off = j - blk * p.block_size;
-                phys = __ldg(p.table + lk.w.b * p.table_stride + blk);
-            }
-            lk.step(p);
-        };
-        auto resolve = [&](int slot) {
-            uint32_t at = ~0u;
-            if (off >= 0) {
-                if (phys < 0 || phys >= p.num_blocks) {
-                    flags |= kFlagBlockRange;
-                } else {
-                    at = (uint32_t)(((int64_t)phys * p.num_kv_heads + look_h) * p.block_size + off);
-                    const unsigned char *row = p.cache + (int64_t)at * C::kRow;
 #pragma unroll
-                    for (int y = 0; y < C::kRow / 2; y += 128)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(row + y));
+            for (int g = 0; g < RG; g++) {
+                const int j = lk.tile * kWKeys + row0 + 32 * g + lane, blk = block_of(p, j);
+                phys[g] = 0;
+                if (j < lk.w.rq.ctx) {
+                    off[g] = j - blk * p.block_size;
+                    phys[g] = __ldg(p.table + lk.w.b * p.table_stride + blk);
                 }
             }
-            rows[pw][slot][lane] = at;
+            for (int i = 0; i < PG && lk.w.more(); i++)
+                lk.step(p);
+        };
+        auto resolve = [&](int slot) {
+#pragma unroll
+            for (int g = 0; g < RG; g++) {
+                uint32_t at = ~0u;
+                if (off[g] >= 0) {
+                    if (phys[g] < 0 || phys[g] >= p.num_blocks) {
+                        flags |= kFlagBlockRange;
+                    } else {
+                        at = (uint32_t)(((int64_t)phys[g] * p.num_kv_heads + look_h) * p.block_size + off[g]);
+                        const unsigned char *row = p.cache + (int64_t)at * C::kRow;
+#pragma unroll
+                        for (int y = 0; y < C::kRow / 2; y += 128)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(row + y));
+                    }
+                }
+                rows[pw][slot][32 * g + lane] = at;
+            }
             __syncwarp();
         };
         constexpr int kW = D * (FP8 ? 1 : 2) / 16;  // 16-byte words of a row's K
-        constexpr int kB = kW < 8 ? kW : 8;        // of the kW words per lane (32 rows of them) this many at a time
+        constexpr int kIt = WR * kW / 32, kB = kIt < 8 ? kIt : 8;  // words per lane, so many at a time
         bool ok = true;
-        // issues the copies of tile x (its rows are resolved), and resolves the next one's
-        auto issue = [&](int x) {
-            const uint32_t dst0 = tc::saddr(sk) + (x % NS) * C::kTileBytes;
-            const uint32_t *from = rows[pw][x & 1];
-            resolve((x & 1) ^ 1);
-            look();
-#pragma unroll 1
-            for (int i0 = 0; i0 < kW; i0 += kB) {
-                uint32_t src[kB];
-#pragma unroll
-                for (int i = 0; i < kB; i++)
-                    src[i] = from[((i0 + i) * 32 + lane) / kW];
-#pragma unroll
-                for (int i = 0; i < kB; i++) {
-                    const int y = 32 * pw + ((i0 + i) * 32 + lane) / kW, c = ((i0 + i) * 32 + lane) % kW;
-                    const uint32_t at = FP8 ? raw_at<D>(dst0, y, c) : dst0 + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4);
-                    cp16(at, src[i] != ~0u ? p.cache + (int64_t)src[i] * C::kRow + 16 * c : p.cache, src[i] != ~0u);
-                }
-            }
-            const unsigned bits = __ballot_sync(0xffffffffu, from[lane] != ~0u);
-            if (lane == 0)
-                live[x & 15][pw] = bits;
-            if (FP8)
-                cp_commit();
-            __syncwarp();  // every lane is done with this tile's row numbers
-        };
-        auto free_parity = [&](int x) { return ((uint32_t)(x / NS) & 1u) ^ 1u; };
-        int issued = 0;
         look();
         resolve(0);
         look();
-        for (int x = 0; x < looked && ok; x++) {
-            const int st = x % NS;
-            if (issued == x) {
-                ok = bar_wait(kempty + st, free_parity(x), abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
-                issue(issued++);
+        for (int i = 0; i < looked && ok; i++) {
+            const int x = mine + PG * i, st = x % NS;
+            const uint32_t dst0 = tc::saddr(sk) + st * C::kTileBytes;
+            const uint32_t *from = rows[pw][i & 1];
+            resolve((i & 1) ^ 1);
+            look();
+            ok = bar_wait(kempty + st, ((uint32_t)(x / NS) & 1u) ^ 1u, abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok)
+                break;
+#pragma unroll 1
+            for (int i0 = 0; i0 < kIt; i0 += kB) {
+                uint32_t src[kB];
+#pragma unroll
+                for (int k = 0; k < kB; k++)
+                    src[k] = from[((i0 + k) * 32 + lane) / kW];
+#pragma unroll
+                for (int k = 0; k < kB; k++) {
+                    const int y = row0 + ((i0 + k) * 32 + lane) / kW, c = ((i0 + k) * 32 + lane) % kW;
+                    const uint32_t at = FP8 ? raw_at<D>(dst0, y, c) : dst0 + (c >> 3) * 16384 + y * 128 + (((c & 7) ^ (y & 7)) << 4);
+                    cp16(at, src[k] != ~0u ? p.cache + (int64_t)src[k] * C::kRow + 16 * c : p.cache, src[k] != ~0u);
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < RG; g++) {
+                const unsigned bits = __ballot_sync(0xffffffffu, from[32 * g + lane] != ~0u);
+                if (lane == 0)
+                    live[x & 15][row0 / 32 + g] = bits;
             }
             if constexpr (FP8) {
-                // the codes of the next tiles, as far as their stages are free
-                while (issued < looked && issued < x + NS && __all_sync(0xffffffffu, bar_test(kempty + issued % NS, free_parity(issued))))
-                    issue(issued++);
-                cp_wait_most(issued - x - 1);
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 __syncwarp();
-                convert_rows<D, 32>(tc::saddr(sk) + st * C::kTileBytes, 32 * pw, kWKeys);
+                convert_rows<D, WR>(dst0, row0, kWKeys);
                 fence_async();
             }
             if (lane == 0)
@@ -332,6 +337,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_const
                 bar_arrive(kfull + st);
             else
                 bar_arrive_copies(kfull + st);
+            __syncwarp();  // every lane is done with this tile's row numbers
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
     } else {
@@ -472,7 +478,7 @@ __global__ void __launch_bounds__(kWThreads, 1) weight_kernel(const __grid_const
         }
     }
     __syncthreads();
-    if (warp == 12) {
+    if (warp == C::kIssuer) {
         if (lane == 0) {
             const unsigned long long t0 = gtimer();
             while (!bar_try(&done, 0) && gtimer() - t0 < kTimeoutNs) {
@@ -508,7 +514,7 @@ cudaError_t weight(const AttnParams &p, cudaStream_t stream)
             return e;
         __atomic_store_n(&cached[dev], have, __ATOMIC_RELEASE);
     }
-    return launch_pdl(weight_kernel<D, FP8>, have, kWThreads, C::kSmem, stream, p);
+    return launch_pdl(weight_kernel<D, FP8>, have, C::kThreads, C::kSmem, stream, p);
 }
 
 }  // namespace attn

@@ -172,58 +172,91 @@ __device__ __forceinline__ Request request(const AttnParams &p, int b, int mask_
     return r;
 }
 
-// Block-wide search of the request that holds unit `target`, and the sum of
-// all units (THREADS threads, scratch of THREADS / 32 + 4 words): `units(b)`
-// is evaluated once per request and pass by one thread.
-struct Find {
-    int64_t total, before;  // all units; those of the requests before `b`
-    int b;
+// n CTAs share `total` units: CTA c gets [start(c), start(c + 1)), the first
+// `more` of them one unit more.
+struct Shares {
+    int64_t each;
+    int more, n;
+
+    __device__ __forceinline__ static int64_t div(int64_t a, int64_t b)  // of nonnegative numbers; most fit 32 bits
+    {
+        return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+    }
+    __device__ __forceinline__ Shares(int64_t total, int ctas)
+    {
+        n = total < ctas ? (int)total : ctas;
+        each = n ? div(total, n) : 0;
+        more = (int)(total - each * n);
+    }
+    __device__ __forceinline__ int64_t start(int c) const { return c < n ? each * c + min(c, more) : each * n + more; }
+    __device__ __forceinline__ int owner(int64_t unit) const  // the CTA whose share holds it
+    {
+        const int64_t edge = (each + 1) * more;
+        return (int)(unit < edge ? div(unit, each + 1) : more + div(unit - edge, each));
+    }
 };
 
-template <int THREADS, typename F, typename S>
-__device__ Find find_request(int requests, int64_t *scratch, F units, S share)
+// Block-wide search (THREADS threads, scratch of THREADS / 32 + 4 words) of the
+// request that holds this CTA's first unit: `units(b)` is evaluated by one thread.
+struct Find {
+    int64_t total, before;  // all units; those of the requests before `b`
+    int b;                  // < 0: the CTA has no share
+};
+
+template <int THREADS, typename F>
+__device__ __forceinline__ Find find_request(int requests, int64_t *scratch, F units)
 {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Find f{0, 0, -1};
-    int64_t mine = 0;
-    for (int pass = 0; pass < 2; pass++) {
-        int64_t base = 0, target = 0;
-        if (pass == 1) {
-            target = share(f.total);
-            if (target < 0 || target >= f.total)
-                return f;
+    int64_t base = 0, mine = 0, end = 0;  // before this chunk of THREADS requests; of this thread's; up to and with it
+    auto scan = [&](int b0) {
+        const int b = b0 + tid;
+        mine = b < requests ? units(b) : 0;
+        int64_t x = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d)
+                x += y;
         }
+        if (b0)
+            __syncthreads();
+        if (lane == 31)
+            scratch[warp] = x;
+        __syncthreads();
+        // each warp sums the warps' totals with its own lanes
+        int64_t t = lane < W ? scratch[lane] : 0, all = t;
+        t = lane < warp ? t : 0;
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) {
+            t += __shfl_xor_sync(0xffffffffu, t, d);
+            all += __shfl_xor_sync(0xffffffffu, all, d);
+        }
+        end = base + t + x;
+        base += all;
+    };
+    for (int b0 = 0; b0 < requests; b0 += THREADS)
+        scan(b0);
+    f.total = base;
+    const int64_t target = Shares(base, gridDim.x).start(blockIdx.x);
+    if ((int64_t)blockIdx.x >= base)  // fewer units than CTAs
+        return f;
+    auto hit = [&](int b0) {
+        if (target >= end - mine && target < end) {
+            scratch[W] = b0 + tid;
+            scratch[W + 1] = end - mine;
+        }
+    };
+    if (requests <= THREADS) {
+        hit(0);
+    } else {
+        base = 0;
+        __syncthreads();
         for (int b0 = 0; b0 < requests; b0 += THREADS) {
-            const int b = b0 + tid;
-            if (pass == 0 || requests > THREADS)
-                mine = b < requests ? units(b) : 0;
-            int64_t x = mine;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-                if (lane >= d)
-                    x += y;
-            }
-            __syncthreads();
-            if (lane == 31)
-                scratch[warp] = x;
-            __syncthreads();
-            int64_t below = 0, all = 0;
-#pragma unroll
-            for (int w = 0; w < W; w++) {
-                below += w < warp ? scratch[w] : 0;
-                all += scratch[w];
-            }
-            const int64_t end = base + below + x;
-            if (pass == 1 && target >= end - mine && target < end) {
-                scratch[W] = b;
-                scratch[W + 1] = end - mine;
-            }
-            base += all;
+            scan(b0);
+            hit(b0);
         }
-        if (pass == 0)
-            f.total = base;
     }
     __syncthreads();
     f.b = (int)scratch[W];
@@ -291,7 +324,7 @@ struct Walk {
         if (lo >= hi)
             return;
         enter(p);
-        item = (int)((lo - before) / (tiles + EXTRA));
+        item = (int)Shares::div(lo - before, tiles + EXTRA);
         at = before + (int64_t)item * (tiles + EXTRA);
         clip();
         if (t0 >= t1)
@@ -301,18 +334,9 @@ struct Walk {
     __device__ __forceinline__ int row0() const { return (item % groups) * ROWS; }
     __device__ __forceinline__ bool begun() const { return t0 == 0; }
     __device__ __forceinline__ bool finished() const { return t1 == tiles; }
-    // the CTA that has the item's last tile, of n that share `total` units: the largest c with floor(total c / n) <= its unit
-    __device__ __forceinline__ int last_cta(int64_t total, int64_t n) const
-    {
-        return (int)(((unsigned long long)(at + EXTRA + tiles) * n - 1) / (unsigned long long)total);
-    }
+    // the CTA that has the item's last tile
+    __device__ __forceinline__ int last_cta(const Shares &shares) const { return shares.owner(at + EXTRA + tiles - 1); }
 };
-
-// Share c of n of `total` units.
-__device__ __forceinline__ int64_t share_start(int64_t total, int64_t c, int64_t n)
-{
-    return (int64_t)((unsigned long long)total * (unsigned long long)c / (unsigned long long)n);
-}
 
 // ------------------------------------------------------------------ the cached tiles
 
@@ -662,14 +686,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
     // ---- this CTA's share of the units
     const int ctas = gridDim.x, cta = blockIdx.x;
     using W = Walk<C::kRows, kTile, kItemCost>;
-    const Find f = find_request<kThreads>(
-        p.num_requests, scratch, [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); },
-        [&](int64_t total) {
-            const int64_t n = min(total, (int64_t)ctas);
-            return cta < n ? share_start(total, cta, n) : (int64_t)-1;
-        });
-    const int64_t total = f.total;
-    const int64_t n_cta = total < ctas ? total : ctas;
+    const Find f = find_request<kThreads>(p.num_requests, scratch,
+                                          [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); });
+    const Shares shares(f.total, ctas);
     PartDesc *descs = reinterpret_cast<PartDesc *>(p.parts);
     float *parts = p.parts + (int64_t)ctas * (sizeof(PartDesc) / 4);
     if (tid == 0)
@@ -685,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
 
     // ---- two walks over the share: one for the copies, one for the products
     W w;
-    w.start(p, share_start(total, cta, n_cta), share_start(total, cta + 1, n_cta), f.b, f.before, mask_limit);
+    w.start(p, shares.start(cta), shares.start(cta + 1), f.b, f.before, mask_limit);
     W cp = w;
     int cp_tile = cp.t0;
 
@@ -949,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
         if (begun && !done && tid == 0) {
             PartDesc &d = descs[cta];
             d.q0 = rq.q0, d.rows = rows, d.row0 = row0, d.h = h, d.nq = rq.nq, d.ctx = rq.ctx, d.b = b;
-            d.last = w.last_cta(total, n_cta);
+            d.last = w.last_cta(shares);
         }
         if (bad && !(begun && done) && tid == 0)
             descs[cta].bad[begun ? 1 : 0] = 1;

@@ -137,13 +137,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     // ---- this CTA's share of the units
     const int ctas = gridDim.x, cta = blockIdx.x;
     using W = Walk<256, kKeysTc, kItemCostTc>;
-    const Find f = find_request<kTcThreads>(
-        p.num_requests, scratch, [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); },
-        [&](int64_t total) {
-            const int64_t n = min(total, (int64_t)ctas);
-            return cta < n ? share_start(total, cta, n) : (int64_t)-1;
-        });
-    const int64_t total = f.total, n_cta = total < ctas ? total : ctas;
+    const Find f = find_request<kTcThreads>(p.num_requests, scratch,
+                                            [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); });
+    const Shares shares(f.total, ctas);
     PartDesc *descs = reinterpret_cast<PartDesc *>(p.parts);
     float *parts = p.parts + (int64_t)ctas * (sizeof(PartDesc) / 4);
     if (tid == 0)
@@ -154,8 +150,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     const uint32_t tmem = tmem_slot;
     // every role walks the CTA's share on its own, item by item
     W w;
-    w.start(p, f.b >= 0 ? share_start(total, cta, n_cta) : 0, f.b >= 0 ? share_start(total, cta + 1, n_cta) : 0, f.b, f.before,
-            mask_limit);
+    w.start(p, f.b >= 0 ? shares.start(cta) : 0, f.b >= 0 ? shares.start(cta + 1) : 0, f.b, f.before, mask_limit);
 
     if (warp >= 12) {
         // ------------------------------------------------------------ the issuing warps, one per stream
@@ -746,7 +741,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 if (begun && !finished) {
                     PartDesc &d = descs[cta];
                     d.q0 = w.rq.q0, d.rows = rows, d.row0 = row0, d.h = h, d.nq = w.rq.nq, d.ctx = w.rq.ctx, d.b = w.b;
-                    d.last = w.last_cta(total, n_cta);
+                    d.last = w.last_cta(shares);
                 }
                 if (is_bad && !(begun && finished))
                     descs[cta].bad[begun ? 1 : 0] = 1;

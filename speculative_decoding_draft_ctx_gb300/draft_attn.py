@@ -149,6 +149,52 @@ def _table(block_table, context_lens, device):
 # ------------------------------------------------------------------ rotary positions
 
 
+def _frequencies(rotary_dim, theta, scaling):
+    """``rope_frequencies`` with the frequencies as an fp64 array."""
+    import numpy as np
+
+    r, theta = int(rotary_dim), float(theta)
+    if r < 2 or r % 2 or r > 512:
+        raise DSparkError(2, f"rotary_dim {rotary_dim} must be even and in [2, 512]")
+    if not (theta > 1.0 and math.isfinite(theta)):
+        _fail(f"theta {theta} must be finite and above 1")
+    i = np.arange(r // 2)
+    f = theta ** (i * (-2.0 / r))
+    if scaling is None:
+        return f, 1.0
+    s = dict(scaling)
+    kind = s.pop("kind", None)
+    factor = float(s.pop("factor", 0.0))
+    if not (factor >= 1.0 and math.isfinite(factor)):
+        _fail(f"scaling factor {factor} must be finite and at least 1")
+    amplitude = 1.0
+    if kind == "linear":
+        f = f / factor
+    elif kind in ("by_parts", "bands"):
+        L = float(s.pop("original_positions", 0.0))
+        if not (L >= 1.0 and math.isfinite(L)):
+            _fail("scaling needs original_positions >= 1")
+        if kind == "by_parts":
+            fast, slow = float(s.pop("beta_fast", 32.0)), float(s.pop("beta_slow", 1.0))
+            if not fast > slow > 0.0:
+                _fail("by_parts scaling needs beta_fast > beta_slow > 0")
+            amplitude = float(s.pop("amplitude", 0.1 * math.log(factor) + 1.0))
+            lo, hi = (r * math.log(L / (t * 2.0 * math.pi)) / (2.0 * math.log(theta)) for t in (fast, slow))
+            lo, hi = max(0, math.floor(lo)), min(r - 1, math.ceil(hi))
+            share = 1.0 - np.clip((i - lo) / max(hi - lo, 0.001), 0.0, 1.0)
+        else:
+            low, high = float(s.pop("low_freq_factor", 1.0)), float(s.pop("high_freq_factor", 4.0))
+            if not high > low:
+                _fail("bands scaling needs high_freq_factor > low_freq_factor")
+            share = np.clip((f * (L / (2.0 * math.pi)) - low) / (high - low), 0.0, 1.0)
+        f = f * (share + (1.0 - share) / factor)
+    else:
+        _fail(f"scaling kind {kind!r} unknown: linear, by_parts or bands")
+    if s:
+        _fail(f"scaling entries unknown to {kind}: {sorted(s)}")
+    return f, amplitude
+
+
 def rope_frequencies(rotary_dim, theta=10000.0, scaling=None):
     """(``rotary_dim / 2`` frequencies in radians per position, amplitude) of a
     cos|sin table.
@@ -167,45 +213,8 @@ def rope_frequencies(rotary_dim, theta=10000.0, scaling=None):
       of itself and has the rest divided by the factor
       (``low_freq_factor`` 1, ``high_freq_factor`` 4).
     """
-    r, theta = int(rotary_dim), float(theta)
-    if r < 2 or r % 2 or r > 512:
-        raise DSparkError(2, f"rotary_dim {rotary_dim} must be even and in [2, 512]")
-    if not (theta > 1.0 and math.isfinite(theta)):
-        _fail(f"theta {theta} must be finite and above 1")
-    f = [theta ** (-2.0 * i / r) for i in range(r // 2)]
-    if scaling is None:
-        return f, 1.0
-    s = dict(scaling)
-    kind = s.pop("kind", None)
-    factor = float(s.pop("factor", 0.0))
-    if not (factor >= 1.0 and math.isfinite(factor)):
-        _fail(f"scaling factor {factor} must be finite and at least 1")
-    amplitude = 1.0
-    if kind == "linear":
-        f = [x / factor for x in f]
-    elif kind in ("by_parts", "bands"):
-        L = float(s.pop("original_positions", 0.0))
-        if not (L >= 1.0 and math.isfinite(L)):
-            _fail("scaling needs original_positions >= 1")
-        if kind == "by_parts":
-            fast, slow = float(s.pop("beta_fast", 32.0)), float(s.pop("beta_slow", 1.0))
-            if not fast > slow > 0.0:
-                _fail("by_parts scaling needs beta_fast > beta_slow > 0")
-            amplitude = float(s.pop("amplitude", 0.1 * math.log(factor) + 1.0))
-            lo, hi = (r * math.log(L / (t * 2.0 * math.pi)) / (2.0 * math.log(theta)) for t in (fast, slow))
-            lo, hi = max(0, math.floor(lo)), min(r - 1, math.ceil(hi))
-            share = [1.0 - min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(r // 2)]
-        else:
-            low, high = float(s.pop("low_freq_factor", 1.0)), float(s.pop("high_freq_factor", 4.0))
-            if not high > low:
-                _fail("bands scaling needs high_freq_factor > low_freq_factor")
-            share = [min(1.0, max(0.0, (L * x / (2.0 * math.pi) - low) / (high - low))) for x in f]
-        f = [x * k + x / factor * (1.0 - k) for x, k in zip(f, share)]
-    else:
-        _fail(f"scaling kind {kind!r} unknown: linear, by_parts or bands")
-    if s:
-        _fail(f"scaling entries unknown to {kind}: {sorted(s)}")
-    return f, amplitude
+    f, amplitude = _frequencies(rotary_dim, theta, scaling)
+    return f.tolist(), amplitude
 
 
 def rope_table(num_positions, rotary_dim, theta=10000.0, scaling=None, first_position=0, dtype=None, device=None,
@@ -217,11 +226,9 @@ def rope_table(num_positions, rotary_dim, theta=10000.0, scaling=None, first_pos
     take) or fp32 (``rope_kv_insert`` takes both).  ``scaling``: see
     ``rope_frequencies``.  Angles are reduced exactly: far positions are as
     precise as near ones."""
-    import ctypes
-
     import torch
 
-    freqs, amplitude = rope_frequencies(rotary_dim, theta, scaling)
+    freqs, amplitude = _frequencies(rotary_dim, theta, scaling)
     n, r = int(num_positions), int(rotary_dim)
     if out is not None:
         if not isinstance(out, torch.Tensor) or out.dtype not in (torch.bfloat16, torch.float32):
@@ -245,8 +252,8 @@ def rope_table(num_positions, rotary_dim, theta=10000.0, scaling=None, first_pos
             return rope_table(n, r, theta, scaling, first_position, dtype, device, out)
     if out is None:
         out = torch.empty((n, r), dtype=dtype, device=device)
-    check(lib().dspark_rope_table(out.data_ptr(), int(first_position), n, r, (ctypes.c_double * len(freqs))(*freqs),
-                                  amplitude, int(dtype is torch.float32), _current(device)))
+    check(lib().dspark_rope_table(out.data_ptr(), int(first_position), n, r, freqs.ctypes.data, amplitude,
+                                  int(dtype is torch.float32), _current(device)))
     return out
 
 
