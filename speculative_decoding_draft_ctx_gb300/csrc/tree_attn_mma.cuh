@@ -424,47 +424,62 @@ __device__ __forceinline__ uint32_t raw_at(uint32_t tile, int y, int c)
 template <int D, int ROWS>
 __device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean)
 {
-    constexpr int kW = D / 16, kR = 32 / kW, kU = 2;
+    constexpr int kW = D / 16, kR = 32 / kW, kU = kR < 8 ? 8 / kR : 1, kStep = kU * kR;  // whole groups of 8 rows a step
     const int lane = threadIdx.x & 31, c = lane % kW, r = lane / kW;
     bool any = false;
+    if (clean < row0 + ROWS) {
 #pragma unroll 1
-    for (int y0 = row0; y0 < row0 + ROWS; y0 += kU * kR) {
+        for (int y = row0 + r; y < row0 + ROWS; y += kR)
+#pragma unroll 1
+            for (int k = 0; k < 4 && y >= clean; k++) {
+                const uint32_t at = raw_at<D>(tile, y, c) + 4 * k;
+                uint32_t q;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q) : "r"(at) : "memory");
+                if (nonfinite_word(q, true)) {
+                    any = true;
+#pragma unroll 1
+                    for (int e = 0; e < 32; e += 8)
+                        if (((q >> e) & 0x7fu) == 0x7fu)
+                            q &= ~(0xffu << e);
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(q) : "memory");
+                }
+            }
+        __syncwarp();
+    }
+    // 16-byte words 2 c and 2 c + 1 of the fp16 row, odd lanes the other way
+    // round (bank conflicts)
+    uint32_t from[kU], to[kU][2];
+#pragma unroll
+    for (int u = 0; u < kU; u++) {
+        const int y = row0 + u * kR + r;
+        from[u] = raw_at<D>(tile, y, c);
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            const int cc = 2 * c + (k ^ (c & 1));
+            to[u][k] = tile + (cc >> 3) * 16384 + y * 128 + (((cc & 7) ^ (y & 7)) << 4);
+        }
+    }
+#pragma unroll 1
+    for (int d = 0; d < ROWS * 128; d += kStep * 128) {
         uint32_t q[kU][4];
 #pragma unroll
         for (int u = 0; u < kU; u++)
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(q[u][0]), "=r"(q[u][1]), "=r"(q[u][2]), "=r"(q[u][3])
-                         : "r"(raw_at<D>(tile, y0 + u * kR + r, c))
+                         : "r"(from[u] + d)
                          : "memory");
         __syncwarp();  // the rows' codes are read before their bytes are written
 #pragma unroll
-        for (int u = 0; u < kU; u++) {
-            const int y = y0 + u * kR + r;
-            if (y >= clean) {
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    if (nonfinite_word(q[u][k], true)) {
-                        any = true;
-#pragma unroll 1
-                        for (int e = 0; e < 32; e += 8)
-                            if (((q[u][k] >> e) & 0x7fu) == 0x7fu)
-                                q[u][k] &= ~(0xffu << e);
-                    }
-            }
-            uint32_t o[8];
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                o[2 * k] = e4m3_to_half2((uint16_t)q[u][k]), o[2 * k + 1] = e4m3_to_half2((uint16_t)(q[u][k] >> 16));
+        for (int u = 0; u < kU; u++)
 #pragma unroll
             for (int k = 0; k < 2; k++) {
-                // 16-byte words 2 c and 2 c + 1 of the fp16 row, odd lanes the other way round (bank conflicts)
-                const int kk = k ^ (c & 1), cc = 2 * c + kk;
-                const uint32_t at = tile + (cc >> 3) * 16384 + y * 128 + (((cc & 7) ^ (y & 7)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(kk ? o[4] : o[0]), "r"(kk ? o[5] : o[1]),
-                             "r"(kk ? o[6] : o[2]), "r"(kk ? o[7] : o[3])
+                const bool upper = (k != 0) != ((c & 1) != 0);
+                const uint32_t a = upper ? q[u][2] : q[u][0], b = upper ? q[u][3] : q[u][1];
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to[u][k] + d), "r"(e4m3_to_half2((uint16_t)a)),
+                             "r"(e4m3_to_half2((uint16_t)(a >> 16))), "r"(e4m3_to_half2((uint16_t)b)),
+                             "r"(e4m3_to_half2((uint16_t)(b >> 16)))
                              : "memory");
             }
-        }
     }
     return any;
 }
