@@ -548,10 +548,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                         return vis;
                     };
                     // 32 scores, -inf where not seen
-                    auto load32 = [&](int g, uint32_t (&x)[32]) {
+                    auto load32 = [&](auto gc, int g, uint32_t (&x)[32]) {
                         tmem_ld32(ts + 32 * g, x);
-                        if (masked) {
-                            const uint32_t vis = visible(g);
+                        if constexpr (decltype(gc)::value) {
+                            const uint32_t vis = masked ? visible(g) : 0xffffffffu;
 #pragma unroll
                             for (int e = 0; e < 32; e++)
                                 if (!((vis >> e) & 1u))
@@ -560,19 +560,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     };
                     // ---- maximum (the scores are read again below)
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto maxima = [&](auto gc) {
 #pragma unroll 1
-                    for (int g = 0; g < 2 * nh; g++) {
-                        uint32_t x[32];
-                        load32(g, x);
+                        for (int g = 0; g < 2 * nh; g++) {
+                            uint32_t x[32];
+                            load32(gc, g, x);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
+                            for (int e = 0; e < 32; e += 8)
 #pragma unroll
-                            for (int k2 = 0; k2 < 4; k2++)
-                                top[k2] = max3(top[k2], __uint_as_float(x[e + 2 * k2]), __uint_as_float(x[e + 2 * k2 + 1]));
-                    }
+                                for (int k2 = 0; k2 < 4; k2++)
+                                    top[k2] = max3(top[k2], __uint_as_float(x[e + 2 * k2]), __uint_as_float(x[e + 2 * k2 + 1]));
+                        }
+                    };
+                    if (__builtin_expect(masked, 0))
+                        maxima(std::true_type{});
+                    else
+                        maxima(std::false_type{});
                     const float t = max3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
                     const bool grow = t > m + kLazy || (m == -INFINITY && t > m);
-                    if (__any_sync(0xffffffffu, grow)) {
+                    if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
                         const float old = m;
                         m = fmaxf(m, t);
                         const float fr = old == m ? 1.0f : ex2(old - m);  // 0 from -inf
@@ -596,41 +602,49 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     // (scores beyond 2^24): the product is rounded first there
                     const bool apart = __any_sync(0xffffffffu, fabsf(mu) > 16777216.0f);
                     uint64_t sum0 = 0, sum1 = 0;
+                    auto raise = [&](auto gc) {
 #pragma unroll 1
-                    for (int g = 0; g < 2 * nh; g++) {
-                        uint32_t x[32], pk[16];
-                        load32(g, x);
-                        if (apart) {
+                        for (int g = 0; g < 2 * nh; g++) {
+                            uint32_t x[32], pk[16];
+                            load32(gc, g, x);
+                            if (decltype(gc)::value && apart) {
 #pragma unroll
-                            for (int e = 0; e < 32; e++)
-                                x[e] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x[e]), c), mu));
-                        } else {
+                                for (int e = 0; e < 32; e++)
+                                    x[e] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x[e]), c), mu));
+                            } else {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                float a0, a1;
-                                unpr(fma2(pr(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, m2), a0, a1);
-                                x[e] = __float_as_uint(a0), x[e + 1] = __float_as_uint(a1);
+                                for (int e = 0; e < 32; e += 2) {
+                                    float a0, a1;
+                                    unpr(fma2(pr(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, m2), a0, a1);
+                                    x[e] = __float_as_uint(a0), x[e + 1] = __float_as_uint(a1);
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4) {
+                                const float a0 = ex2(__uint_as_float(x[e])), a1 = ex2(__uint_as_float(x[e + 1]));
+                                const float a2 = ex2(__uint_as_float(x[e + 2])), a3 = ex2(__uint_as_float(x[e + 3]));
+                                sum0 = add2(sum0, pr(a0, a1));
+                                sum1 = add2(sum1, pr(a2, a3));
+                                pk[e / 2] = pack2<FP8>(a0, a1);
+                                pk[e / 2 + 1] = pack2<FP8>(a2, a3);
+                            }
+                            // columns 16 g .. of P lie over scores that are used up
+                            tmem_st16(ts + 16 * g, pk);
+                            if (g & 1) {  // a half's weights are out: its product may begin
+                                tmem_wait_st();
+                                fence_before();
+                                __syncwarp();
+                                if (lane == 0)
+                                    bar_arrive(pfull + 2 * s + (g >> 1));
                             }
                         }
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float a0 = ex2(__uint_as_float(x[e])), a1 = ex2(__uint_as_float(x[e + 1]));
-                            const float a2 = ex2(__uint_as_float(x[e + 2])), a3 = ex2(__uint_as_float(x[e + 3]));
-                            sum0 = add2(sum0, pr(a0, a1));
-                            sum1 = add2(sum1, pr(a2, a3));
-                            pk[e / 2] = pack2<FP8>(a0, a1);
-                            pk[e / 2 + 1] = pack2<FP8>(a2, a3);
-                        }
-                        // columns 16 g .. of P lie over scores that are used up
-                        tmem_st16(ts + 16 * g, pk);
-                        if (g & 1) {  // a half's weights are out: its product may begin
-                            tmem_wait_st();
-                            fence_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                bar_arrive(pfull + 2 * s + (g >> 1));
-                        }
-                    }
+                    };
+                    // Tiles without a mask run a short loop of their own: the
+                    // instructions a warp has to fetch per tile are what bounds it.
+                    if (__builtin_expect(masked || apart, 0))
+                        raise(std::true_type{});
+                    else
+                        raise(std::false_type{});
                     float a0, a1;
                     unpr(add2(sum0, sum1), a0, a1);
                     l += a0 + a1;
