@@ -397,7 +397,7 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
                         fix = ex > 126 ? 0.5f : 1.0f;
                     }
                     const uint32_t dst0 = tc::saddr(sq);
-#pragma unroll 4
+#pragma unroll (FP8 ? 4 : 8)
                     for (int k = 0; k < D / 8; k++) {
                         uint4 q = make_uint4(0, 0, 0, 0);
                         if (mine)

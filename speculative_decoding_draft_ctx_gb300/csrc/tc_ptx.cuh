@@ -65,8 +65,12 @@ __device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-static __device__ __noinline__ bool bar_wait_long(uint64_t *bar, uint32_t parity, volatile int *abort)
+// Waits for the phase of `bar` with this parity; false after kTimeoutNs or
+// once another thread of the CTA has given up (which it then records).
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
+    if (bar_try(bar, parity))
+        return true;
     const unsigned long long t0 = gtimer();
     while (true) {
         if (bar_try(bar, parity))
@@ -78,13 +82,6 @@ static __device__ __noinline__ bool bar_wait_long(uint64_t *bar, uint32_t parity
             return false;
         }
     }
-}
-
-// Waits for the phase of `bar` with this parity; false after kTimeoutNs or
-// once another thread of the CTA has given up (which it then records).
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
-{
-    return bar_try(bar, parity) || bar_wait_long(bar, parity, abort);
 }
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }

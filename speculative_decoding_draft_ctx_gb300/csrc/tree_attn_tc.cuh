@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     __shared__ uint64_t kfull[NK], kempty[NK], vfull[NV], vempty[NV], qfull[2], sfull[2], pfull[4], ofull[2], jfull, jempty, go1, done[2];
     __shared__ uint32_t tmem_slot, live[8][4];
     __shared__ uint32_t rows[kProducers][2][64];  // cache rows of each producer's tile and its next; ~0: not there
-    __shared__ int abort_flag;
+    __shared__ int abort_flag, lock;
     __shared__ int bad[16];  // item number + 1 where infinities or NaN came up among an item's drafted V
     __shared__ float join_ml[256];
     __shared__ int64_t scratch[kTcThreads / 32 + 4];
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         bar_init(&jfull, 128);
         bar_init(&jempty, 128);
         bar_init(&go1, 4);
-        abort_flag = 0;
+        abort_flag = 0, lock = 0;
         for (int i = 0; i < 16; i++)
             bad[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -225,6 +225,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     }
                     __syncwarp();
                 };
+                // One stream's products at a time: interleaved, both streams' scores
+                // came late and their softmax ran at the same time.
+                auto take = [&]() {
+                    if (leader && two) {
+                        const unsigned long long t0 = gtimer();
+                        while (atomicExch(&lock, 1) != 0 && gtimer() - t0 < kTimeoutNs) {
+                        }
+                    }
+                    __syncwarp();
+                };
+                auto give = [&]() {
+                    if (leader && two)
+                        atomicExch(&lock, 0);
+                    __syncwarp();
+                };
                 auto kwait = [&](int k) {
                     const int x = base + tile_of(k);
                     wait(kfull + x % NK, (uint32_t)(x / NK) & 1u);
@@ -258,11 +273,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     if (both && ok) {
                         wait(pfull + 2 * s + 1, (par >> 1) & 1u);
                         par ^= 2u;
-                        if (ok)
-                            pv(k, 1, true);
                     }
+                    if (both && ok)
+                        pv(k, 1, true);
+                    take();
                     if (k + 1 < steps && ok)
                         qk(k + 1);
+                    give();
                 }
                 if (steps > 0 && leader)
                     mma_commit(ofull + s);
@@ -489,7 +506,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     fix = e > 126 ? 0.5f : 1.0f;
                 }
                 if (two || s == 0) {
-#pragma unroll 4
+#pragma unroll (FP8 ? 4 : 8)
                     for (int k = 0; k < D / 8; k++) {
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (!zero)
