@@ -14,8 +14,10 @@
 // reduction.  The top bits give the nearest quarter turn, the signed rest
 // x (|x| <= pi/4) goes to fp32 with a relative rounding and into the Taylor
 // series of sine (to x^9: the next term is below 2^-29 x) and cosine (to x^8:
-// below 2^-25).  Bound: the store of 2 or 4 bytes per entry; a thread makes 4
-// neighbouring angles, so it stores 8 or 16 bytes of cos and of sin.
+// below 2^-25).  A thread makes 4 neighbouring angles, so it stores 8 or 16
+// bytes of cos and of sin, and stays with them from row to row: the next
+// angle is a 64-bit sum.  Bound: the store of 2 or 4 bytes per entry and some
+// 40 instructions per angle.
 //
 // Rotation.  A head row of D dims is held by D / 8 lanes, 8 dims (16 bytes)
 // each, so a warp takes 256 / D rows at once.  Half layout: the partner of
@@ -66,16 +68,23 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
 {
     pdl_enter();
     const int half = p.rotary_dim >> 1, per_row = half / V;
-    const int64_t units = p.count * per_row;
-    for (int64_t u = (int64_t)blockIdx.x * kTableThreads + threadIdx.x; u < units;
-         u += (int64_t)gridDim.x * kTableThreads) {
-        const int64_t row = u / per_row;
-        const int i0 = (int)(u - row * per_row) * V;
-        const uint64_t pos = (uint64_t)(p.first + row);
+    const unsigned t = blockIdx.x * kTableThreads + threadIdx.x;
+    const int step = (int)(gridDim.x * kTableThreads / (unsigned)per_row);  // rows all threads make at once
+    const int row0 = (int)(t / (unsigned)per_row), i0 = (int)(t - (unsigned)row0 * per_row) * V;
+    if (row0 >= step)
+        return;
+    uint64_t turn[V], more[V];  // the angles of a row, and from one row to the next
+#pragma unroll
+    for (int j = 0; j < V; j++) {
+        turn[j] = (uint64_t)(p.first + row0) * p.turns[i0 + j];
+        more[j] = (uint64_t)step * p.turns[i0 + j];
+    }
+    for (int64_t row = row0; row < p.count; row += step) {
         float c[V], s[V];
 #pragma unroll
         for (int j = 0; j < V; j++) {
-            turn_cos_sin(pos * p.turns[i0 + j], c[j], s[j]);
+            turn_cos_sin(turn[j], c[j], s[j]);
+            turn[j] += more[j];
             c[j] *= p.amplitude;
             s[j] *= p.amplitude;
         }
