@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const EvictPar
     __syncthreads();
     // ---- the keys, the first digit's histogram, and (not in place) the places
     // that no move will write: a hole is written again by its mover below
-#pragma unroll 4
+#pragma unroll 8
     for (int j = s0 + lane; j < s1; j += 32) {
         const float wv = w[j];
         const int32_t pv = pos[j];
