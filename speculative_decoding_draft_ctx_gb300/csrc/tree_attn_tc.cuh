@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         }
         bar_init(&jfull, 128);
         bar_init(&jempty, 128);
-        bar_init(&go1, 4);
+        bar_init(&go1, 8);
         abort_flag = 0, lock = 0;
         for (int i = 0; i < 16; i++)
             bad[i] = 0;
@@ -244,9 +244,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     const int x = base + tile_of(k);
                     wait(kfull + x % NK, (uint32_t)(x / NK) & 1u);
                 };
-                // Where the streams share the rows, stream 1 waits for its own
-                // softmax to be here first: then everything before this item is
-                // done, and the phases below are the next ones of their barriers.
+                // Where the streams share the rows, stream 1 waits for both
+                // streams' softmax to be here first.  Over items of two row tiles
+                // the streams drift apart by as many items as tiles fit the ring;
+                // with both here everything before this item is done, and the
+                // phases below are the next ones of their barriers.
                 if (steps > 0) {
                     if (s == 1 && !two)
                         wait(&go1, (uint32_t)(ngo++) & 1u);
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             const int i = mine ? my / p.group : 0, hq = h * p.group + (mine ? my - i * p.group : 0);
             const int halves = tile_halves(w, n);
             const int steps = two ? n : s == 0 ? (n + 1) / 2 : n / 2;  // tiles of the stream
-            if (!two && s == 1 && steps > 0 && lane == 0)
+            if (!two && n > 1 && lane == 0)
                 bar_arrive(&go1);
             // ---- the query row.  A negative scale turns its sign, a zero one
             // zeroes it, so that the factor c of the scores is positive.

@@ -222,6 +222,21 @@ def test_attention(ctx, nq, Hq, Hkv, D, bs, fp8, kind, kernel):
     assert int(p.d_flags) == 0
 
 
+@pytest.mark.parametrize("D,fp8", [(64, False), (128, False), (128, True), (64, True), (256, True)])
+def test_attention_many_small_items(D, fp8, kernel):
+    """More (request, KV head) pairs than CTAs, of one and of two row tiles in turn: a CTA's state from item to item."""
+    g = gen(D + fp8)
+    nq = tuple(int(x) for x in torch.tensor([3, 6, 27, 30, 1, 40, 25, 26])[torch.randint(0, 8, (48,), generator=g)])
+    ctx = tuple(int(x) for x in torch.tensor([0, 3, 40, 100, 120, 167, 200, 300])[torch.randint(0, 8, (48,), generator=g)])
+    p = Problem(D, ctx, nq, 40, 8, D, 16, fp8).cuda()
+    mask = tree_mask(nq, 1, D)
+    out, lse = run_attention(p, "tree", mask)
+    want, z, to, tl = attention(p, "tree", mask)
+    close(lse, z, tl)
+    close(out, want, to)
+    assert int(p.d_flags) == 0
+
+
 def test_attention_rows_without_anything_and_rows_behind(kernel):
     """A row that sees nothing: zeros and -inf.  Rows of no request and outputs behind them stay."""
     p = Problem(3, (0, 4), (3, 2), 4, 2, 128, 16, False, pad_rows=3).cuda()
@@ -441,6 +456,20 @@ def test_weight(ctx, nq, Hq, Hkv, D, bs, fp8, decay):
     dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, e, decay=decay, k_scale=p.d_ks)
     assert torch.equal(d, e)
 
+
+@pytest.mark.parametrize("D,fp8", [(64, True), (128, False), (128, True), (256, False)])
+def test_weight_many_small_items(D, fp8):
+    """More (request, KV head) pairs than CTAs, of no, one and two row groups in turn."""
+    g = gen(D + fp8)
+    nq = tuple(int(x) for x in torch.tensor([3, 6, 27, 60, 0, 40, 1, 26])[torch.randint(0, 8, (48,), generator=g)])
+    ctx = tuple(int(x) for x in torch.tensor([0, 3, 40, 100, 128, 167, 200, 300])[torch.randint(0, 8, (48,), generator=g)])
+    p = Problem(D, ctx, nq, 40, 8, D, 16, fp8).cuda()
+    _, lse = run_attention(p, "tree", tree_mask(nq, 1, 3))
+    w = torch.rand((48, 8, 305), generator=gen(1))
+    d = w.cuda()
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, d, decay=0.75, k_scale=p.d_ks, error_flags=p.d_flags)
+    close(d, *weight(p, lse, w, 0.75))
+    assert int(p.d_flags) == 0
 
 def test_weight_sums_to_the_rows_and_rows_without_anything():
     """Without drafted tokens seen, a head's weights sum to its rows; a row of lse -inf adds nothing."""
