@@ -29,6 +29,14 @@ from ._binding import KV_BF16, KV_FP8_E4M3, DSparkError, check, lib
 
 MASK_DENSE, MASK_CAUSAL, MASK_TREE = 0, 1, 2
 
+torch = None  # loaded by the first call: an import statement per helper cost a call of a few tokens 4 us
+
+
+def _load():
+    global torch
+    if torch is None:
+        import torch
+
 
 def _fail(message: str):
     raise DSparkError(1, message)
@@ -36,8 +44,6 @@ def _fail(message: str):
 
 def _on(device, stream):
     """A context in which ``device`` and ``stream`` are current."""
-    import torch
-
     stack = contextlib.ExitStack()
     stack.enter_context(torch.cuda.device(device))
     if stream is not None:
@@ -49,23 +55,17 @@ def _on(device, stream):
 
 def _elsewhere(device, stream) -> bool:
     """Whether a call has to change the current device or stream first."""
-    import torch
-
     if device.type != "cuda":
         _fail(f"tensors are on {device}, expected a CUDA device")
     return stream is not None or device.index != torch.cuda.current_device()
 
 
 def _current(device) -> int:
-    import torch
-
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _tensor(name, x, dtype, device, ndim):
     """A contiguous tensor of this type, device and number of dims; its shape."""
-    import torch
-
     if not isinstance(x, torch.Tensor):
         _fail(f"{name} must be a tensor, got {type(x).__name__}")
     if x.dtype is not dtype:
@@ -81,8 +81,6 @@ def _tensor(name, x, dtype, device, ndim):
 
 def _heads(name, x, device=None):
     """A bf16 [tokens, heads, head_dim] view with contiguous head rows; its shape."""
-    import torch
-
     if not isinstance(x, torch.Tensor):
         _fail(f"{name} must be a tensor, got {type(x).__name__}")
     if x.dtype is not torch.bfloat16:
@@ -97,8 +95,6 @@ def _heads(name, x, device=None):
 
 
 def _scalar(name, x, device):
-    import torch
-
     if x is None:
         return 0
     if not isinstance(x, torch.Tensor) or x.dtype is not torch.float32 or x.device != device or x.numel() < 1:
@@ -107,8 +103,6 @@ def _scalar(name, x, device):
 
 
 def _flags(error_flags, device):
-    import torch
-
     if error_flags is None:
         return 0
     if (not isinstance(error_flags, torch.Tensor) or error_flags.dtype is not torch.int32 or error_flags.device != device
@@ -119,8 +113,6 @@ def _flags(error_flags, device):
 
 def _cache(kv_cache, device):
     """(num_blocks, num_kv_heads, block_size, head_dim, kv dtype) of a layer's cache."""
-    import torch
-
     if not isinstance(kv_cache, torch.Tensor) or kv_cache.dtype not in (torch.bfloat16, torch.uint8):
         _fail("kv_cache must be a bf16 or uint8 (fp8 e4m3) tensor")
     n, h, bs, row = _tensor("kv_cache", kv_cache, kv_cache.dtype, device, 4)
@@ -131,8 +123,6 @@ def _cache(kv_cache, device):
 
 def _table(block_table, context_lens, device):
     """(requests, table row stride, entries a row); the rows may be a column slice of a wider table."""
-    import torch
-
     if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32 or block_table.dim() != 2:
         _fail("block_table must be an int32 tensor [requests, blocks]")
     if block_table.device != device:
@@ -181,12 +171,12 @@ def _frequencies(rotary_dim, theta, scaling):
             amplitude = float(s.pop("amplitude", 0.1 * math.log(factor) + 1.0))
             lo, hi = (r * math.log(L / (t * 2.0 * math.pi)) / (2.0 * math.log(theta)) for t in (fast, slow))
             lo, hi = max(0, math.floor(lo)), min(r - 1, math.ceil(hi))
-            share = 1.0 - np.clip((i - lo) / max(hi - lo, 0.001), 0.0, 1.0)
+            share = 1.0 - np.minimum(np.maximum((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)
         else:
             low, high = float(s.pop("low_freq_factor", 1.0)), float(s.pop("high_freq_factor", 4.0))
             if not high > low:
                 _fail("bands scaling needs high_freq_factor > low_freq_factor")
-            share = np.clip((f * (L / (2.0 * math.pi)) - low) / (high - low), 0.0, 1.0)
+            share = np.minimum(np.maximum((f * (L / (2.0 * math.pi)) - low) / (high - low), 0.0), 1.0)
         f = f * (share + (1.0 - share) / factor)
     else:
         _fail(f"scaling kind {kind!r} unknown: linear, by_parts or bands")
@@ -226,8 +216,7 @@ def rope_table(num_positions, rotary_dim, theta=10000.0, scaling=None, first_pos
     take) or fp32 (``rope_kv_insert`` takes both).  ``scaling``: see
     ``rope_frequencies``.  Angles are reduced exactly: far positions are as
     precise as near ones."""
-    import torch
-
+    _load()
     freqs, amplitude = _frequencies(rotary_dim, theta, scaling)
     n, r = int(num_positions), int(rotary_dim)
     if out is not None:
@@ -252,7 +241,7 @@ def rope_table(num_positions, rotary_dim, theta=10000.0, scaling=None, first_pos
             return rope_table(n, r, theta, scaling, first_position, dtype, device, out)
     if out is None:
         out = torch.empty((n, r), dtype=dtype, device=device)
-    check(lib().dspark_rope_table(out.data_ptr(), int(first_position), n, r, freqs.ctypes.data, amplitude,
+    check(lib().dspark_rope_table(out.data_ptr(), int(first_position), n, r, freqs.__array_interface__["data"][0], amplitude,
                                   int(dtype is torch.float32), _current(device)))
     return out
 
@@ -276,8 +265,7 @@ def rope_kv_insert(q, k, cos_sin_cache, positions, rotary_dim, v=None, layout="h
     whose position is outside the table comes out unrotated, is not inserted
     and raises FLAG_POS_RANGE.
     """
-    import torch
-
+    _load()
     T, Hq, D = _heads("q", q)
     dev = q.device
     Tk, Hkv, Dk = _heads("k", k, dev)
@@ -334,8 +322,6 @@ def rope_kv_insert(q, k, cos_sin_cache, positions, rotary_dim, v=None, layout="h
 
 def _queries(q, kv_cache, block_table, query_start, context_lens, scale):
     """What the attention and the weight accumulation check alike."""
-    import torch
-
     T, Hq, D = _heads("q", q)
     dev = q.device
     num_blocks, Hkv, block_size, hd, kv_dtype = _cache(kv_cache, dev)
@@ -375,8 +361,7 @@ def tree_attention(q, kv_cache, block_table, query_start, context_lens, tree_mas
     left as they were (uninitialised where this call makes the outputs).
     ``scale``: 1 / sqrt(D) if not given.
     """
-    import torch
-
+    _load()
     T, Hq, Hkv, D, B, dev, kv_dtype, scale, head, table = _queries(q, kv_cache, block_table, query_start, context_lens,
                                                                   scale)
     kind, words = (MASK_CAUSAL, 0) if causal else (MASK_DENSE, 0)
@@ -421,8 +406,7 @@ def accumulate_attention_weight(q, kv_cache, block_table, query_start, context_l
     multiplying the old value by ``decay``; places behind a request's context
     stay.  ``lse`` is what ``tree_attention`` returned for the same arguments
     (the other arguments are as there)."""
-    import torch
-
+    _load()
     T, Hq, Hkv, D, B, dev, kv_dtype, scale, head, table = _queries(q, kv_cache, block_table, query_start, context_lens,
                                                                   scale)
     if tuple(_tensor("lse", lse, torch.float32, dev, 2)) != (T, Hq):
@@ -463,8 +447,7 @@ def evict_kv(kv_cache, block_table, context_lens, weights, token_positions, seq_
     blocks.  Layers keep different tokens: call it once per layer, with that
     layer's weights and positions.
     """
-    import torch
-
+    _load()
     if not isinstance(kv_cache, torch.Tensor):
         _fail("kv_cache must be a bf16 or uint8 (fp8 e4m3) tensor")
     dev = kv_cache.device
