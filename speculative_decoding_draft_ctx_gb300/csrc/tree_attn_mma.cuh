@@ -1016,29 +1016,53 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     auto part = [&](int c) {
         return parts + ((int64_t)c * 2 + (c == (int)blockIdx.x ? 1 : 0)) * C::kPart + wr * kWarpPart;
     };
+    // loads of several parts at a time: one after the other, an item over 19
+    // CTAs took 30 us to join
+    const int first = blockIdx.x;
     float t0 = -INFINITY, t1 = -INFINITY;
-    bool bad = d.bad[1] != 0;
-    for (int c = blockIdx.x; c <= d.last; c++) {
-        if (c != (int)blockIdx.x)
-            bad |= descs[c].bad[0] != 0;
-        t0 = fmaxf(t0, part(c)[C::kNT * 128 + g]);
-        t1 = fmaxf(t1, part(c)[C::kNT * 128 + 8 + g]);
+    bool bad = false;
+    for (int c0 = first; c0 <= d.last; c0 += 8) {
+        float v0[8], v1[8];
+        int any[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int c = min(c0 + k, d.last);
+            v0[k] = part(c)[C::kNT * 128 + g], v1[k] = part(c)[C::kNT * 128 + 8 + g];
+            any[k] = descs[c].bad[c == first ? 1 : 0];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            t0 = fmaxf(t0, v0[k]), t1 = fmaxf(t1, v1[k]), bad |= any[k] != 0;
     }
     const float u0 = t0 == -INFINITY ? 0.0f : t0, u1 = t1 == -INFINITY ? 0.0f : t1;
     float l0 = 0.0f, l1 = 0.0f, o[NW][4];
 #pragma unroll
     for (int n = 0; n < NW; n++)
         o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.0f;
-#pragma unroll 2
-    for (int c = blockIdx.x; c <= d.last; c++) {
-        const float *at = part(c);
-        const float x0 = ex2(at[C::kNT * 128 + g] - u0), x1 = ex2(at[C::kNT * 128 + 8 + g] - u1);
-        l0 = fmaf(at[C::kNT * 128 + 16 + g], x0, l0), l1 = fmaf(at[C::kNT * 128 + 24 + g], x1, l1);
+    for (int c0 = first; c0 <= d.last; c0 += 4) {
+        float v[4][NW][4], ml[4][4];
 #pragma unroll
-        for (int n = 0; n < NW; n++) {
-            const float *q = at + (warp * NW + n) * 128 + lane;
-            o[n][0] = fmaf(q[0], x0, o[n][0]), o[n][1] = fmaf(q[32], x0, o[n][1]);
-            o[n][2] = fmaf(q[64], x1, o[n][2]), o[n][3] = fmaf(q[96], x1, o[n][3]);
+        for (int k = 0; k < 4; k++) {
+            const bool there = c0 + k <= d.last;
+            const float *at = part(there ? c0 + k : d.last);
+#pragma unroll
+            for (int x = 0; x < 4; x++)
+                ml[k][x] = there ? at[C::kNT * 128 + 8 * x + g] : x < 2 ? -INFINITY : 0.0f;
+#pragma unroll
+            for (int n = 0; n < NW; n++)
+#pragma unroll
+                for (int x = 0; x < 4; x++)
+                    v[k][n][x] = there ? at[(warp * NW + n) * 128 + 32 * x + lane] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float x0 = ex2(ml[k][0] - u0), x1 = ex2(ml[k][1] - u1);
+            l0 = fmaf(ml[k][2], x0, l0), l1 = fmaf(ml[k][3], x1, l1);
+#pragma unroll
+            for (int n = 0; n < NW; n++) {
+                o[n][0] = fmaf(v[k][n][0], x0, o[n][0]), o[n][1] = fmaf(v[k][n][1], x0, o[n][1]);
+                o[n][2] = fmaf(v[k][n][2], x1, o[n][2]), o[n][3] = fmaf(v[k][n][3], x1, o[n][3]);
+            }
         }
     }
     const float vs = FP8 && p.v_scale ? __ldg(p.v_scale) : 1.0f;

@@ -803,14 +803,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         atomicOr(p.error_flags, flags);
 }
 
+constexpr int kJoinDims = 16;
+
 // Joins the parts of the item that CTA blockIdx.x began and did not finish:
-// block y takes 32 dims (y % (D / 32)) of row tile y / (D / 32), a thread per row.
+// block y takes kJoinDims dims of row tile y / (D / kJoinDims), a thread per
+// row.  Loads of several parts go out at a time: one after the other, an item
+// over 19 CTAs took 30 us to join.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(128) join_tc_kernel(const __grid_constant__ AttnParams p, int ctas)
 {
     using C = TcCfg<D, FP8>;
     pdl_enter();
-    const int r = threadIdx.x, rt = blockIdx.y / (D / 32), d0 = (blockIdx.y % (D / 32)) * 32;
+    const int r = threadIdx.x, rt = blockIdx.y / (D / kJoinDims), d0 = (blockIdx.y % (D / kJoinDims)) * kJoinDims;
     const PartDesc *descs = reinterpret_cast<const PartDesc *>(p.parts);
     const PartDesc d = descs[blockIdx.x];
     const int my = d.row0 + rt * 128 + r;
@@ -820,25 +824,45 @@ __global__ void __launch_bounds__(128) join_tc_kernel(const __grid_constant__ At
     auto part = [&](int c) {
         return parts + ((int64_t)c * 2 + (c == (int)blockIdx.x ? 1 : 0)) * C::kPart + rt * C::kRowPart + r;
     };
+    const int first = blockIdx.x;
     float m = -INFINITY;
-    bool bad = d.bad[1] != 0;
-    for (int c = blockIdx.x; c <= d.last; c++) {
-        m = fmaxf(m, part(c)[D * 128]);
-        if (c != (int)blockIdx.x)
-            bad |= descs[c].bad[0] != 0;
+    bool bad = false;
+    for (int c0 = first; c0 <= d.last; c0 += 8) {  // the loads of eight parts at a time
+        float v[8];
+        int any[8];
+#pragma unroll
+        for (int k = 0; k < 8; k++) {
+            const int c = min(c0 + k, d.last);
+            v[k] = part(c)[D * 128], any[k] = descs[c].bad[c == first ? 1 : 0];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            m = fmaxf(m, v[k]), bad |= any[k] != 0;
     }
     const float u = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o[32];
+    float l = 0.0f, o[kJoinDims];
 #pragma unroll
-    for (int e = 0; e < 32; e++)
+    for (int e = 0; e < kJoinDims; e++)
         o[e] = 0.0f;
-    for (int c = blockIdx.x; c <= d.last; c++) {
-        const float *at = part(c);
-        const float x = ex2(at[D * 128] - u);
-        l = fmaf(at[(D + 1) * 128], x, l);
+    for (int c0 = first; c0 <= d.last; c0 += 4) {
+        float v[4][kJoinDims], pm[4], pl[4];
 #pragma unroll
-        for (int e = 0; e < 32; e++)
-            o[e] = fmaf(at[(d0 + e) * 128], x, o[e]);
+        for (int k = 0; k < 4; k++) {
+            const bool there = c0 + k <= d.last;
+            const float *at = part(there ? c0 + k : d.last);
+            pm[k] = there ? at[D * 128] : -INFINITY, pl[k] = there ? at[(D + 1) * 128] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < kJoinDims; e++)
+                v[k][e] = there ? at[(d0 + e) * 128] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float x = ex2(pm[k] - u);
+            l = fmaf(pl[k], x, l);
+#pragma unroll
+            for (int e = 0; e < kJoinDims; e++)
+                o[e] = fmaf(v[k][e], x, o[e]);
+        }
     }
     const float vs = FP8 && p.v_scale ? __ldg(p.v_scale) : 1.0f;
     const float inv = l > 0.0f ? vs / l : l == 0.0f ? 0.0f : l;
@@ -847,15 +871,15 @@ __global__ void __launch_bounds__(128) join_tc_kernel(const __grid_constant__ At
     if (d0 == 0)
         p.lse[at] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 #pragma unroll
-    for (int e = 0; e < 32; e++)
+    for (int e = 0; e < kJoinDims; e++)
         o[e] *= inv;
 #pragma unroll
-    for (int e = 0; e < 32; e += 8)
+    for (int e = 0; e < kJoinDims; e += 8)
         *reinterpret_cast<uint4 *>(p.out + at * D + d0 + e) =
             make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]), pack_bf16x2(o[e + 4], o[e + 5]),
                        pack_bf16x2(o[e + 6], o[e + 7]));
     if (bad)
-        add_nonfinite<D, FP8>(p, d.b, Request{d.q0, d.nq, d.ctx}, d.h, i, p.out + at * D, d0, d0 + 32);
+        add_nonfinite<D, FP8>(p, d.b, Request{d.q0, d.nq, d.ctx}, d.h, i, p.out + at * D, d0, d0 + kJoinDims);
 }
 
 // ------------------------------------------------------------------ launches
@@ -903,7 +927,7 @@ cudaError_t attention_tc(const AttnParams &p, cudaStream_t stream)
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(2 * (D / 32)));
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(2 * (D / kJoinDims)));
     cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
