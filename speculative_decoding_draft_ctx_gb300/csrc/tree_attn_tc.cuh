@@ -47,7 +47,7 @@ namespace dspark {
 namespace attn {
 
 constexpr int kTcThreads = 448, kKeysTc = 128;  // 8 softmax warps, 4 producers, 2 that issue the products
-constexpr int kProducers = 4, kItemCostTc = 3;   // EXTRA of Walk, in tiles of kKeysTc keys
+constexpr int kProducers = 4, kItemCostTc = 6;   // EXTRA of Walk, in tiles of kKeysTc keys
 constexpr float kLazy = 8.0f;  // growth of a maximum (log2) that waits for a rescale
 
 __device__ __forceinline__ float max3(float a, float b, float c)
