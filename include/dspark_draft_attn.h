@@ -15,6 +15,9 @@
  * a CUDA graph), return a dspark_status and never throw.  Lengths, offsets
  * and block numbers live in device memory, so the kernels check them: what
  * is out of range is never dereferenced and raises a bit in *error_flags.
+ * Every wait inside the attention and the weight accumulation is bounded; one
+ * that ran out raises DSPARK_FLAG_TIMEOUT, and that call's outputs hold nothing
+ * of use.
  */
 #ifndef DSPARK_DRAFT_ATTN_H
 #define DSPARK_DRAFT_ATTN_H

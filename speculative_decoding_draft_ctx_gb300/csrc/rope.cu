@@ -16,8 +16,8 @@
 // series of sine (to x^9: the next term is below 2^-29 x) and cosine (to x^8:
 // below 2^-25).  A thread makes 4 neighbouring angles, so it stores 8 or 16
 // bytes of cos and of sin, and stays with them from row to row: the next
-// angle is a 64-bit sum.  Bound: the store of 2 or 4 bytes per entry and some
-// 40 instructions per angle.
+// angle is a 64-bit sum.  Bound: some 40 instructions per angle (131,072
+// positions of 64 entries: 8.9 us, the bytes' time 2.5).
 //
 // Rotation.  A head row of D dims is held by D / 8 lanes, 8 dims (16 bytes)
 // each, so a warp takes 256 / D rows at once.  Half layout: the partner of
@@ -31,7 +31,8 @@
 // token: their loads go out before the position is waited for and the cos|sin
 // words (whole 8- or 16-byte loads) after it, so a unit waits twice; four
 // CTAs per SM keep 32 warps' units in flight (with a CTA per token, 104
-// registers and a scalar load per cos and sin, a prefill batch took 97 us).
+// registers and a scalar load per cos and sin, a prefill batch of 8,192 tokens into an fp8
+// cache took 97 us; it takes 50, the bytes' time 30).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -16,31 +16,32 @@ DSPARK_ATTN_TC_DECLARE(128)
 namespace {
 
 // The tensor-core kernel takes head dims 64 and 128 where the mean request
-// has more than kTcRows query rows per KV head.  DSPARK_TREE_ATTN_KERNEL=mma
-// or =tc pins one (tc: for the head dims it has) for the calls made while it
-// is set; the tests run both.
+// has more than kTcRows query rows per KV head and the block table has room
+// for more than one tile of 128 keys per two SMs (lengths are on the device:
+// the room is what the host knows).  Measured, D 128, mma.sync against it, us:
+//   rows 32, 8 requests x 8 heads over 4,000 tokens   36 / 40, fp8 31 / 46
+//   rows 56, 16 x 8 over 8,000                        135 / 103, fp8 141 / 132
+//   rows 504, 1 x 4 over 16,000                       71 / 39, fp8 74 / 43
+//   rows 56, 1 x 8 over 500 (32 tiles)                11.7 / 12.9
+//   rows 56, 1 x 8 over 2,000 (128 tiles)             18.2 / 17.6
+//   rows 504, 1 x 4 over 2,000 (68 tiles)             23.6 / 25.3
+// DSPARK_TREE_ATTN_KERNEL=mma or =tc pins one (tc: for the head dims it has)
+// for the calls made while it is set; the tests run both.
 constexpr int64_t kTcRows = 32;
 
-bool use_tc(int64_t rows, int group, int requests, int head_dim)
+enum Pin { kNone, kMma, kTc };
+
+Pin pinned(int head_dim)
 {
     if (head_dim > 128)
-        return false;
+        return kMma;
     const char *e = std::getenv("DSPARK_TREE_ATTN_KERNEL");
-    if (e && std::strcmp(e, "mma") == 0)
-        return false;
-    if (e && std::strcmp(e, "tc") == 0)
-        return true;
-    return rows * group > kTcRows * requests;
+    return !e ? kNone : std::strcmp(e, "mma") == 0 ? kMma : std::strcmp(e, "tc") == 0 ? kTc : kNone;
 }
 
-}  // namespace
-
-int64_t tree_attention_workspace(int64_t rows, int num_heads, int num_kv_heads, int head_dim, int requests, bool fp8,
-                                 cudaError_t &e)
+int64_t workspace_mma(int64_t rows, int group, int head_dim, int requests, bool fp8, cudaError_t &e)
 {
-    if (use_tc(rows, num_heads / num_kv_heads, requests, head_dim))
-        return head_dim == 64 ? attn::workspace_tc<64>(fp8, e) : attn::workspace_tc<128>(fp8, e);
-    const int wr = attn::row_warps(rows, num_heads / num_kv_heads, requests);
+    const int wr = attn::row_warps(rows, group, requests);
     switch (head_dim) {
     case 64: return attn::workspace_d<64>(wr, fp8, e);
     case 128: return attn::workspace_d<128>(wr, fp8, e);
@@ -48,9 +49,39 @@ int64_t tree_attention_workspace(int64_t rows, int num_heads, int num_kv_heads, 
     }
 }
 
+}  // namespace
+
+// enough for every kernel that the launch may choose
+int64_t tree_attention_workspace(int64_t rows, int num_heads, int num_kv_heads, int head_dim, int requests, bool fp8,
+                                 cudaError_t &e)
+{
+    const int group = num_heads / num_kv_heads;
+    const Pin pin = pinned(head_dim);
+    int64_t n = 0;
+    if (pin != kTc)
+        n = workspace_mma(rows, group, head_dim, requests, fp8, e);
+    if (pin == kTc || (pin == kNone && e == cudaSuccess && rows * group > kTcRows * requests)) {
+        const int64_t m = head_dim == 64 ? attn::workspace_tc<64>(fp8, e) : attn::workspace_tc<128>(fp8, e);
+        n = n > m ? n : m;
+    }
+    return n;
+}
+
 cudaError_t launch_tree_attention(const AttnParams &p, int head_dim, bool fp8, cudaStream_t stream)
 {
-    if (use_tc(p.num_rows, p.group, p.num_requests, head_dim))
+    const Pin pin = pinned(head_dim);
+    bool tc = pin == kTc;
+    if (pin == kNone && p.num_rows * p.group > kTcRows * p.num_requests) {
+        int dev = 0, sms = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess)
+            e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess)
+            return e;
+        const int64_t tiles = (p.table_blocks * p.block_size + 127) / 128;
+        tc = tiles * p.num_requests * p.num_kv_heads > sms / 2;
+    }
+    if (tc)
         return head_dim == 64 ? attn::attention_tc_d<64>(p, fp8, stream) : attn::attention_tc_d<128>(p, fp8, stream);
     const int wr = attn::row_warps(p.num_rows, p.group, p.num_requests);
     switch (head_dim) {

@@ -4,8 +4,9 @@
 //
 // Why.  With r rows of queries a cached token of D 128 brings 512 bytes and
 // 512 r flops: the card's rates balance at r = 283, but mma.sync, whose
-// operands pass through registers, was bound by issue from r = 56 on (64
-// requests x 7 tokens x 8 heads: 234 us against 136 us of memory time).
+// operands pass through registers, is bound by issue from r = 56 on (64
+// requests x 7 tokens x 8 heads: 234 us, this kernel 193, memory time 136; two
+// trees of 64 over 131k tokens: 848 us, this kernel 255, its products' time 132).
 //
 // One CTA per SM, an item is up to 256 rows of a (request, KV head), a tile
 // 128 keys.  Two streams of softmax (a warpgroup each, a thread per query
@@ -17,15 +18,19 @@
 // the second product from there) and both outputs (D columns each).
 //
 //  - producer warps (2 for K, 2 for V): gather the tiles through the block
-//    table into separate rings, bf16 with 16-byte asynchronous copies straight
-//    into the operands' 128-byte swizzle, fp8 through registers, converted to
-//    fp16 once per tile instead of once per row tile;
+//    table into separate rings with 16-byte asynchronous copies, bf16 straight
+//    into the operands' 128-byte swizzle, fp8 as codes that the warp turns into
+//    fp16 in place, once per tile instead of once per row tile (a bulk copy per
+//    row, 64 to 128 bytes, took 131 against 108 us on ragged fp8 trees);
 //  - a warp per stream issues S = Q K^T (depth D) and O += P V (V as the cache
 //    holds it: its N direction contiguous).  An MMA of 128 rows takes 64 cycles
 //    for any width up to 128, so scores come 128 keys at a time (half tiles
 //    with two buffers took the wait out of the softmax but doubled the first
 //    product: 395 against 293 us on two 131k contexts), while the weights of
-//    the first 64 keys go into the second product as soon as they are there;
+//    the first 64 keys go into the second product as soon as they are there.
+//    With two row tiles the streams take turns with the scores' products:
+//    interleaved, both streams' scores came late and both softmaxes ran at the
+//    same time (298 against 271 us on two 131k contexts);
 //  - softmax warps (8): 32 scores of a row at a time in registers, maximum,
 //    base-2 exponentials with paired fp32 instructions, P back to tensor
 //    memory.  The output is rescaled only when a row's maximum has grown by
@@ -34,7 +39,11 @@
 //
 // Loops are rolled where a role's straight-line code would not stay in the
 // instruction caches beside the others' (unrolled, a warp's instruction took
-// about ten cycles).  14 warps leave 128 registers a thread.
+// about ten cycles), and tiles without a mask have loops of their own.  14
+// warps leave 128 registers a thread.  What bounds it now: with two row tiles
+// the softmax (about 2,500 of 4,300 cycles a tile, where the same loops alone
+// on an SM take 1,800), with one the tiles' arrival (a stage is held from its
+// copy until its stream's softmax is done with the tile before).
 // Every wait is bounded; on expiry the CTA raises DSPARK_FLAG_TIMEOUT, stops
 // issuing, waits for its copies and products in flight, frees its tensor
 // memory and returns.

@@ -542,6 +542,23 @@ def test_evict(ctx, Hkv, D, bs, fp8, budget, sinks, recent, values, in_place):
         assert torch.equal(dw.cpu().view(torch.int32), w.view(torch.int32)) and torch.equal(dp.cpu(), pos)
 
 
+@pytest.mark.parametrize("what", ["weights_out", "positions_out"])
+def test_evict_one_of_two_in_place(what):
+    p = Problem(9, (600, 40, 700), (0, 0, 0), 2, 2, 64, 16, False).cuda()
+    w, pos = torch.rand((3, 2, 705), generator=gen(2)), torch.arange(705, dtype=torch.int32).repeat(3, 2, 1)
+    want = evict(p.cache, p.table, 16, (600, 40, 700), w, pos, [600, 40, 700], 300, 4, 8)
+    dw, dp = w.cuda(), pos.cuda()
+    out = torch.full_like(dw if what == "weights_out" else dp, 9)
+    lens = dk.evict_kv(p.d_cache, p.d_table, p.d_ctx, dw, dp, torch.tensor([600, 40, 700], dtype=torch.int32, device="cuda"), 300, 4, 8,
+                       error_flags=p.d_flags, **{what: out})
+    assert lens.tolist() == want[3] and int(p.d_flags) == 0
+    ow, op = (out, dp) if what == "weights_out" else (dw, out)
+    assert torch.equal(ow.cpu(), want[1]) and torch.equal(op.cpu(), want[2])
+    assert torch.equal(p.d_cache.cpu().view(torch.uint8), want[0].view(torch.uint8))
+    kept = dw.cpu() if what == "weights_out" else dp.cpu()
+    assert torch.equal(kept, w if what == "weights_out" else pos)
+
+
 def test_evict_many_places_and_a_long_slice():
     """More places than the keys a CTA holds: one pair per cluster and many pairs."""
     for B, H, n, budget in ((1, 1, 300001, 100000), (160, 2, 17000, 16999)):
