@@ -32,7 +32,7 @@
 // words (whole 8- or 16-byte loads) after it, so a unit waits twice; four
 // CTAs per SM keep 32 warps' units in flight (with a CTA per token, 104
 // registers and a scalar load per cos and sin, a prefill batch of 8,192 tokens into an fp8
-// cache took 97 us; it takes 50, the bytes' time 30).
+// cache took 97 us; it takes 46, the bytes' time 30).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -171,6 +171,11 @@ __global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) rope_insert_kernel(cons
     const int lanes_half = r >> 4;                   // VEC, half layout: lanes of one half
     const int partner_lane = q < lanes_half ? lane + lanes_half : q < 2 * lanes_half ? lane - lanes_half : lane;
     const float sign = p.inverse ? -1.0f : 1.0f;
+    Fp8Scale ks{}, vs{};
+    if (insert && p.fp8) {
+        ks = fp8_scale(p.k_scale ? __ldg(p.k_scale) : 1.0f);
+        vs = fp8_scale(p.v_scale ? __ldg(p.v_scale) : 1.0f);
+    }
     unsigned flags = 0;
 
     const int64_t units = p.num_tokens * groups, stride = (int64_t)gridDim.x * kWarps;
@@ -179,10 +184,19 @@ __global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) rope_insert_kernel(cons
         const int g = (int)(u - t * groups) * RPW * kBatch + sub;  // the lane's first row
         int64_t pos = __ldg(p.positions + t);
         int64_t slot = insert ? __ldg(p.slot_mapping + t) : -1;
+        // units of query rows alone, most of them, take one address and a step
+        // (a third of the instructions, which bound a prefill batch, were addresses)
+        const bool only_q = VEC && g - sub + RPW * kBatch <= Hq;  // uniform over the warp
         uint4 x[kBatch];
         uint32_t partner[VEC ? 1 : kBatch][4];
+        if (only_q) {
+            const uint16_t *src = p.q + t * p.q_ts + g * p.q_hs + d0;
 #pragma unroll
-        for (int b = 0; b < kBatch; b++) {
+            for (int b = 0; b < kBatch; b++)
+                x[b] = *reinterpret_cast<const uint4 *>(src + b * (RPW * p.q_hs));
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch && !only_q; b++) {
             const int hh = g + b * RPW;
             x[b] = make_uint4(0, 0, 0, 0);
             if (hh < rows) {
@@ -258,9 +272,13 @@ __global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) rope_insert_kernel(cons
             }
             __syncwarp();  // in place: every partner is read before any row of the unit is written
         }
-        const int64_t blk = slot >= 0 ? slot / p.block_size : 0;
-        const int64_t row0 = slot >= 0 ? (blk * Hkv * p.block_size + (slot - blk * p.block_size)) * (2 * D) : 0;
         const int64_t hstride = (int64_t)p.block_size * (2 * D);
+        int64_t row0 = 0;
+        if (!only_q && slot >= 0) {
+            const int64_t blk = slot <= 0x7fffffff ? (int64_t)((uint32_t)slot / (uint32_t)p.block_size) : slot / p.block_size;
+            row0 = (blk * Hkv * p.block_size + (slot - blk * p.block_size)) * (2 * D);
+        }
+        uint16_t *qdst = p.q_out + t * p.qo_ts + g * p.qo_hs + d0;
 #pragma unroll
         for (int b = 0; b < kBatch; b++) {
             const int hh = g + b * RPW;
@@ -282,6 +300,10 @@ __global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) rope_insert_kernel(cons
                     y[j] = pack_bf16x2(fmaf(bfl(w[j]), c[2 * j], bfl(pw[j]) * s[2 * j]),
                                        fmaf(bfh(w[j]), c[2 * j + 1], bfh(pw[j]) * s[2 * j + 1]));
             }
+            if (only_q) {
+                *reinterpret_cast<uint4 *>(qdst + b * (RPW * p.qo_hs)) = make_uint4(y[0], y[1], y[2], y[3]);
+                continue;
+            }
             if (hh >= rows)
                 continue;
             if (hh < Hq + Hkv) {
@@ -301,8 +323,7 @@ __global__ void __launch_bounds__(kThreads, VEC ? 4 : 2) rope_insert_kernel(cons
                 const uint4 o = is_k ? make_uint4(y[0], y[1], y[2], y[3]) : x[b];
                 const int64_t at = row0 + (is_k ? hh - Hq : hh - Hq - Hkv) * hstride + (is_k ? 0 : D) + d0;
                 if (p.fp8) {
-                    const float *sc = is_k ? p.k_scale : p.v_scale;
-                    *reinterpret_cast<uint2 *>(p.cache + at) = quantise8(o, fp8_scale(sc ? __ldg(sc) : 1.0f));
+                    *reinterpret_cast<uint2 *>(p.cache + at) = quantise8(o, is_k ? ks : vs);
                 } else {
                     *reinterpret_cast<uint4 *>(p.cache + 2 * at) = o;
                 }
