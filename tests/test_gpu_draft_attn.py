@@ -237,6 +237,23 @@ def test_attention_many_small_items(D, fp8, kernel):
     assert int(p.d_flags) == 0
 
 
+def test_attention_and_weight_more_requests_than_threads(kernel):
+    """The search for a CTA's first request takes them in chunks of a CTA's threads."""
+    n = 1500
+    ctx, nq = [0 if i % 97 else i // 97 for i in range(n)], [(i % 11 == 0) * (1 + i % 3) for i in range(n)]
+    ctx[-1], nq[-1] = 700, 20
+    p = Problem(11, ctx, nq, 4, 2, 64, 16, False).cuda()
+    out, lse = run_attention(p, "dense", None)
+    want, z, to, tl = attention(p, "dense", None)
+    close(lse, z, tl)
+    close(out, want, to)
+    w = torch.rand((n, 2, 701), generator=gen(1))
+    d = w.cuda()
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, d, decay=0.5, error_flags=p.d_flags)
+    close(d, *weight(p, lse, w, 0.5))
+    assert int(p.d_flags) == 0
+
+
 def test_attention_rows_without_anything_and_rows_behind(kernel):
     """A row that sees nothing: zeros and -inf.  Rows of no request and outputs behind them stay."""
     p = Problem(3, (0, 4), (3, 2), 4, 2, 128, 16, False, pad_rows=3).cuda()
