@@ -38,11 +38,13 @@ template <int D, bool FP8>
 struct WeightTc {
     static constexpr int kRows = D == 256 ? 128 : 256;     // query rows of a group
     static constexpr int kTileBytes = kWKeys * D * 2;
-    static constexpr int kStages = D == 64 ? 8 : D == 128 ? 4 : 2;
-    // Warps 0-7 sum, four gather, the last issues.  A bf16 tile is gathered by
-    // all four, 32 rows each; fp8 tiles, which wait for their codes and are
-    // converted, go in turn to kGroups groups of them.
-    static constexpr int kProducers = 4, kGroups = !FP8 ? 1 : kStages < 4 ? kStages : 4;
+    static constexpr int kStages = D == 256 ? 2 : FP8 ? 384 / D : 512 / D;
+    // Warps 0-7 sum, kProducers gather, the last issues.  A bf16 tile is
+    // gathered by four, 32 rows each.  An fp8 tile, which waits for its codes
+    // and is converted, by two of six that take turns in pairs (four, a tile
+    // each, were busy 8,100 cycles with one: 55 us on two long contexts); more
+    // than 16 warps would leave the sums 96 registers.
+    static constexpr int kProducers = FP8 && D < 256 ? 6 : 4, kGroups = !FP8 ? 1 : D < 256 ? 3 : 2;
     static constexpr int kWarpRows = 128 * kGroups / kProducers;  // rows of a tile per producer warp
     static constexpr int kIssuer = 8 + kProducers, kThreads = 32 * (kIssuer + 1);
     static constexpr int kQBytes = kRows * D * 2;

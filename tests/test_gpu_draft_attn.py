@@ -488,6 +488,23 @@ def test_weight_many_small_items(D, fp8):
     close(d, *weight(p, lse, w, 0.75))
     assert int(p.d_flags) == 0
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_weight_ragged_rows_over_fp8(D):
+    """Heads of no, few and more rows than a group, several tiles and pairs per CTA, the same bits again."""
+    nq = tuple((3, 6, 27, 60, 0, 1, 2, 19)[i % 8] for i in range(40))
+    ctx = tuple((700, 3, 40, 1000, 128, 0, 2000, 300)[i * 5 % 8] for i in range(40))
+    p = Problem(D + 1, ctx, nq, 20, 4, D, 16, True).cuda()
+    _, lse = run_attention(p, "tree", tree_mask(nq, 1, 3))
+    w = torch.rand((40, 4, 2003), generator=gen(1))
+    d = w.cuda()
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, d, decay=0.75, k_scale=p.d_ks, error_flags=p.d_flags)
+    close(d, *weight(p, lse, w, 0.75))
+    assert int(p.d_flags) == 0
+    e = w.cuda()
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, e, decay=0.75, k_scale=p.d_ks)
+    assert torch.equal(d, e)
+
+
 def test_weight_sums_to_the_rows_and_rows_without_anything():
     """Without drafted tokens seen, a head's weights sum to its rows; a row of lse -inf adds nothing."""
     p = Problem(2, (200,), (4,), 8, 2, 128, 16, False).cuda()
