@@ -5,13 +5,22 @@
 // Mathematics.  For a query row q and the keys j it sees, with s_j = scale
 // q.k_j:  out = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m),  lse = m +
 // log sum_j e^(s_j - m), for any m.  Keys are taken tile by tile with m the
-// maximum so far; when it grows, the sums are multiplied by e^(m_old - m).
-// Two results over disjoint keys join the same way, so the keys of one query
-// row can be split over warps and CTAs.  Exponentials are base 2 with log2(e)
-// folded into the scale.  Scores, statistics and sums are fp32; the weights
-// e^(s - m) are rounded to bf16 (fp16 with an fp8 cache) for the second
-// product, an error of at most half a step of 2^-8 (2^-11) each against
-// weights summed unrounded.
+// maximum so far (less a constant, next paragraph); when it grows, the sums
+// are multiplied by e^(m_old - m).  Two results over disjoint keys join the
+// same way, so the keys of one query row can be split over warps and CTAs.
+// Exponentials are base 2 with log2(e) folded into the scale.  Scores,
+// statistics and sums are fp32.
+//
+// Rounding of the weights.  For the second product the weights 2^(s - m) are
+// rounded to the type of the tile: bf16 over a bf16 cache, each by at most
+// 2^-8 of itself against weights summed unrounded; fp16 over an fp8 cache,
+// whose codes are exact in fp16, by at most 2^-11 of itself while it is a
+// normal number.  fp16 has normal numbers from 2^-14 on and 15 octaves above
+// 1, so m is the maximum less kLift = 14 there: the largest weight is 2^14, a
+// weight keeps its 2^-11 down to 2^-28 of the largest (below, it is off by at
+// most 2^-39 of the largest).  With the largest at 1 a thin tail behind one
+// heavy token lost its bits below 2^-14 and vanished below 2^-25, while the
+// sum still counted it (32,768 tokens with 0.03% of the weight: all of it).
 //
 // Rows and items.  The G query heads of a KV head and the drafted tokens of a
 // request are the rows of one matrix: row r is token r / G, head r % G, so K|V
@@ -65,6 +74,17 @@ namespace attn {
 constexpr int kThreads = 128, kWarps = 4, kTile = 64;
 constexpr int kItemCost = 4;  // of an item besides its tiles, in tiles of kTile keys (see Walk)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLift = 14.0f;             // of the weights over an fp8 cache, in octaves
+constexpr float kLiftBelow = 1048576.0f;   // scores from here on are too coarse to take kLift off
+
+// The m that a row with this maximum (base 2) subtracts.  From 2^20 on steps
+// of fp32 are an eighth and more: m - kLift could round to beyond fp16's
+// range, so such a maximum is taken as it is.
+template <bool FP8>
+__device__ __forceinline__ float reference_of(float top)
+{
+    return FP8 && fabsf(top) < kLiftBelow ? top - kLift : top;
+}
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -827,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
                 }
             }
             // ---- softmax statistics
-            float t0 = m0, t1 = m1;
+            float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
             for (int n = 0; n < NS; n++) {
                 t0 = fmaxf(t0, fmaxf(s[n][0], s[n][1]));
@@ -837,6 +857,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
             t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 1));
             t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, 2));
             t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, 2));
+            t0 = fmaxf(m0, reference_of<FP8>(t0)), t1 = fmaxf(m1, reference_of<FP8>(t1));
             const float u0 = t0 == -INFINITY ? 0.0f : t0, u1 = t1 == -INFINITY ? 0.0f : t1;  // nothing seen yet
             const float f0 = ex2(m0 - u0), f1 = ex2(m1 - u1);
             m0 = t0, m1 = t1;

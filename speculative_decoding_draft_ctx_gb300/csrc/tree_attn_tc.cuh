@@ -33,9 +33,10 @@
 //    same time (298 against 271 us on two 131k contexts);
 //  - softmax warps (8): 32 scores of a row at a time in registers, maximum,
 //    base-2 exponentials with paired fp32 instructions, P back to tensor
-//    memory.  The output is rescaled only when a row's maximum has grown by
-//    more than 2^8 since the value in use: until then the weights exceed 1,
-//    which costs neither range nor precision.
+//    memory.  The output is rescaled only when a row's weights would exceed
+//    2^kMost otherwise: until then they exceed 1, which costs neither range nor
+//    precision.  Over an fp8 cache fp16's range is used up by kLift but for one
+//    octave.
 //
 // Loops are rolled where a role's straight-line code would not stay in the
 // instruction caches beside the others' (unrolled, a warp's instruction took
@@ -57,7 +58,10 @@ namespace attn {
 
 constexpr int kTcThreads = 448, kKeysTc = 128;  // 8 softmax warps, 4 producers, 2 that issue the products
 constexpr int kProducers = 4, kItemCostTc = 6;   // EXTRA of Walk, in tiles of kKeysTc keys
-constexpr float kLazy = 8.0f;  // growth of a maximum (log2) that waits for a rescale
+// The largest weight 2^(s - m) that waits for a rescale, as an exponent: fp32
+// sums and bf16 weights have room for any; fp16 weights begin at 2^kLift and
+// end below 2^16 (a score is off by 2^-4 at most where kLift is taken off).
+constexpr float kMost = 8.0f, kMostFp8 = kLift + 1.0f;
 
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             }
             c = c == 0.0f ? 1.0f : fabsf(c);
             const uint64_t c2 = pr(c, c);
-            float m = -INFINITY, l = 0.0f;  // the maximum in use (scaled, base 2), the sum of weights
+            float m = -INFINITY, l = 0.0f;  // what the row subtracts (scaled, base 2), the sum of weights
 
             for (int k = 0; k < steps; k++) {
                 const int j = two ? k : 2 * k + s;
@@ -605,10 +609,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     else
                         maxima(std::false_type{});
                     const float t = max3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
-                    const bool grow = t > m + kLazy || (m == -INFINITY && t > m);
+                    const float most = !FP8 ? kMost : fabsf(t) < kLiftBelow ? kMostFp8 : 1.0f;
+                    const bool grow = t > m + most || (m == -INFINITY && t > m);
                     if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
                         const float old = m;
-                        m = fmaxf(m, t);
+                        m = fmaxf(m, reference_of<FP8>(t));
                         const float fr = old == m ? 1.0f : ex2(old - m);  // 0 from -inf
                         l *= fr;
                         if (k > 0) {
