@@ -191,7 +191,8 @@ int dspark_attention_weight_accumulate(const void *q, int64_t q_token_stride, in
  *                place), must not overlap them otherwise.
  *  seq_lens      device, int32 [num_requests]: positions seen so far.
  *  new_lens      device, int32 [num_requests]: receives min(n, budget) (a
- *                request left out for a bad length: its n).
+ *                request left out for a bad length: its n); may be context_lens
+ *                or seq_lens itself (in place), must not overlap them otherwise.
  *  budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget.
  *  workspace     device, 16-byte aligned, dspark_kv_evict_workspace bytes.
  * A request whose length exceeds stride or its table row is left out

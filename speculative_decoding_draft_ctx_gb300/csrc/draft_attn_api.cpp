@@ -76,6 +76,13 @@ int check_table(const int32_t *table, int64_t stride, int64_t blocks, int reques
     return DSPARK_OK;
 }
 
+// Two arrays of n 4-byte entries that share some memory without being the same.
+bool overlap_partly(const void *a, const void *b, int64_t n)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x != y && (x < y ? y - x : x - y) < (uint64_t)n * 4;
+}
+
 bool stride_ok(int64_t s) { return s >= -((int64_t)1 << 40) && s <= (int64_t)1 << 40; }
 
 // What the attention and the weight accumulation check alike.
@@ -384,6 +391,8 @@ int dspark_kv_evict(void *kv_cache, int64_t num_blocks, int num_kv_heads, int bl
     if (!aligned(weights, 4) || !aligned(positions, 4) || !aligned(weights_out, 4) || !aligned(positions_out, 4) ||
         !aligned(new_lens, 4) || !aligned(seq_lens, 4) || !aligned(workspace, 16) || !aligned(error_flags, 4))
         return fail(DSPARK_ERR_ALIGNMENT, "workspace must be 16-byte, the other buffers 4-byte aligned");
+    if (overlap_partly(new_lens, context_lens, num_requests) || overlap_partly(new_lens, seq_lens, num_requests))
+        return fail(DSPARK_ERR_INVALID_ARG, "new_lens overlaps context_lens or seq_lens without being one of them");
     const int64_t need = dspark_kv_evict_workspace(num_requests, num_kv_heads, stride, budget);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return fail(DSPARK_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,

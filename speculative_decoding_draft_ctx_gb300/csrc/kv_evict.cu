@@ -81,6 +81,16 @@ __device__ __forceinline__ unsigned warps_before(unsigned v, Shared &sh, unsigne
     return before;
 }
 
+// Whether a length lies outside its bounds, and what the request keeps.
+__device__ __forceinline__ bool bad_length(const EvictParams &p, int n)
+{
+    return n < 0 || n > p.stride || n > p.table_blocks * p.block_size;
+}
+__device__ __forceinline__ int32_t new_length(const EvictParams &p, int n)
+{
+    return !bad_length(p, n) && n > p.budget ? (int32_t)p.budget : n;
+}
+
 template <int kThreads, int kBlocks>
 __global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const EvictParams p, int NC)
 {
@@ -102,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const EvictPar
     };
 
     const int n = __ldg(p.context_lens + b);
-    const bool bad = n < 0 || n > p.stride || n > p.table_blocks * p.block_size;
+    const bool bad = bad_length(p, n);
     const float *w = p.weights + bh * p.stride;
     const int32_t *pos = p.positions + bh * p.stride;
     float *wo = p.weights_out + bh * p.stride;
@@ -110,7 +120,12 @@ __global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const EvictPar
     const bool copies = wo != w, copies_pos = po != pos;
     const bool cut = !bad && n > p.budget;
     if (h == 0 && rank == 0 && tid == 0) {
-        p.new_lens[b] = cut ? (int32_t)p.budget : n;
+        // The new lengths may take the place of the old ones (or of seq_lens),
+        // which other CTAs of this grid still read: the second kernel writes
+        // them, or, where there is none (no list can be too long), this one the
+        // same numbers.
+        if (p.list_len == 0)
+            p.new_lens[b] = new_length(p, n);
         if (bad && p.error_flags)
             atomicOr(p.error_flags, kFlagLength);
     }
@@ -320,12 +335,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) evict_kernel(const EvictPar
         atomicOr(p.error_flags, kFlagBlockRange);
 }
 
-// Copies the rows of the lists: blockIdx.x is the (request, KV head) pair,
-// blockIdx.y its share of the moves.
+// Copies the rows of the lists (blockIdx.x is the (request, KV head) pair,
+// blockIdx.y its share of the moves) and writes the new lengths.
 __global__ void __launch_bounds__(256, 3) move_kernel(const EvictParams p)
 {
     pdl_enter();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.y == 0 && threadIdx.x == 0 && blockIdx.x % p.num_kv_heads == 0) {
+        const int b = blockIdx.x / p.num_kv_heads;  // nobody else reads or writes its lengths any more
+        p.new_lens[b] = new_length(p, __ldg(p.context_lens + b));
+    }
     const unsigned moves = (unsigned)p.counts[blockIdx.x];
     const int32_t *holes = p.lists + (int64_t)blockIdx.x * 2 * p.list_len, *movers = holes + p.list_len;
     const int clog = __ffs(p.row_bytes >> 4) - 1, chunks = 1 << clog;  // 16-byte words of a row: 8, 16, 32 or 64

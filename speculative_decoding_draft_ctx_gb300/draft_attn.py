@@ -445,7 +445,8 @@ def evict_kv(kv_cache, block_table, context_lens, weights, token_positions, seq_
     if not given; places behind the new length hold 0 and -1 up to the old
     one).  Each KV head keeps its own tokens, so requests must not share
     blocks.  Layers keep different tokens: call it once per layer, with that
-    layer's weights and positions.
+    layer's weights and positions.  ``new_lens=context_lens`` updates the
+    lengths in place (in the last layer's call: the others need the old ones).
     """
     _load()
     if not isinstance(kv_cache, torch.Tensor):

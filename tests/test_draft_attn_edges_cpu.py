@@ -1,0 +1,17 @@
+"""Refusals and host arithmetic of the draft-attention operators at the edges
+of what their documentation allows.  No test here launches a kernel."""
+
+import pytest
+
+import speculative_decoding_draft_ctx_gb300 as dk
+from test_draft_attn_cpu import EVICT, EVICT_BASE, FAKE, L, status  # noqa: F401
+
+# arrays of their own, 64 KB apart: every call below is refused before any CUDA call
+APART = {**EVICT_BASE, **{k: FAKE * (2 + i) for i, k in enumerate("ctx w pos wo po seen lens".split())}}
+
+
+@pytest.mark.parametrize("over", [
+    dict(lens=APART["ctx"] + 4), dict(lens=APART["ctx"] - 4), dict(lens=APART["seen"] + 4), dict(ctx=APART["lens"] + 4)])
+def test_evict_refuses_lengths_that_overlap_partly(L, over):  # noqa: F811
+    assert status(L, "dspark_kv_evict", EVICT, APART, over) == "DSPARK_ERR_INVALID_ARG"
+    assert "new_lens" in dk.dspark_ctx_kv_last_error()

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import speculative_decoding_draft_ctx_gb300 as dk
-from draft_attn_ref import Problem, attention, close, gen, tree_mask
+from draft_attn_ref import Problem, attention, close, evict, gen
 from test_gpu_draft_attn import kernel, run_attention  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -60,3 +60,35 @@ def test_attention_tail_behind_a_heavy_token_over_fp8(n, B, nq, G, Hkv, D, at, g
     close(lse, z, tl)
     close(out, want, to)
     assert int(p.d_flags) == 0
+
+
+# ------------------------------------------------------------------ eviction: lengths in place
+
+
+EVICT_LENS = [  # ctx, Hkv, budget, bad lengths in between
+    (tuple(300 + i % 40 for i in range(64)), 8, 300, False),  # more (request, head) pairs than CTAs run at once
+    ((9000, 30, 8000), 2, 4000, True),  # clusters of several CTAs
+    ((50, 60), 3, 80, False),  # nothing to evict: one kernel
+]
+
+
+@pytest.mark.parametrize("ctx,Hkv,budget,bad", EVICT_LENS)
+@pytest.mark.parametrize("where", ["context_lens", "seq_lens"])
+def test_evict_new_lengths_in_the_place_of_the_old(ctx, Hkv, budget, bad, where):
+    """Every head sees the old lengths, and the results are those of a call with lengths of its own."""
+    B, S = len(ctx), max(ctx) + 2
+    p = Problem(B + Hkv, ctx, (0,) * B, Hkv, Hkv, 64, 16, True).cuda()
+    w = torch.rand((B, Hkv, S), generator=gen(3))
+    pos = torch.arange(S, dtype=torch.int32).repeat(B, Hkv, 1)
+    if bad:
+        p.ctx[1] = S + 1
+        p.d_ctx[1] = S + 1
+    want = evict(p.cache, p.table, 16, [0 if bad and b == 1 else c for b, c in enumerate(p.ctx)], w, pos, ctx, budget, 2, 8)
+    want[3][1] = S + 1 if bad else want[3][1]
+    for _ in range(3):
+        cache, dw, dp = p.d_cache.clone(), w.cuda(), pos.cuda()
+        lens, seen = p.d_ctx.clone(), torch.tensor(ctx, dtype=torch.int32, device="cuda")
+        new = lens if where == "context_lens" else seen
+        assert dk.evict_kv(cache, p.d_table, lens, dw, dp, seen, budget, 2, 8, new_lens=new, error_flags=p.d_flags) is new
+        assert new.tolist() == want[3] and int(p.d_flags) == (dk.FLAG_LENGTH if bad else 0)
+        assert torch.equal(dw.cpu(), want[1]) and torch.equal(dp.cpu(), want[2]) and torch.equal(cache.cpu(), want[0])
