@@ -393,6 +393,14 @@ int dspark_kv_evict(void *kv_cache, int64_t num_blocks, int num_kv_heads, int bl
         return fail(DSPARK_ERR_ALIGNMENT, "workspace must be 16-byte, the other buffers 4-byte aligned");
     if (overlap_partly(new_lens, context_lens, num_requests) || overlap_partly(new_lens, seq_lens, num_requests))
         return fail(DSPARK_ERR_INVALID_ARG, "new_lens overlaps context_lens or seq_lens without being one of them");
+    // weights that change while they are ranked would give lists longer than the workspace's
+    const int64_t entries = (int64_t)num_requests * num_kv_heads * stride;
+    if (overlap_partly(weights_out, weights, entries) || overlap_partly(positions_out, positions, entries))
+        return fail(DSPARK_ERR_INVALID_ARG, "weights_out or positions_out overlaps its input without being it");
+    if (entries > 0 && (weights_out == (const void *)positions || overlap_partly(weights_out, positions, entries) ||
+                        positions_out == (const void *)weights || overlap_partly(positions_out, weights, entries) ||
+                        weights_out == (void *)positions_out || overlap_partly(weights_out, positions_out, entries)))
+        return fail(DSPARK_ERR_INVALID_ARG, "weights and positions overlap");
     const int64_t need = dspark_kv_evict_workspace(num_requests, num_kv_heads, stride, budget);
     if (workspace_bytes < need || (need > 0 && !workspace))
         return fail(DSPARK_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,

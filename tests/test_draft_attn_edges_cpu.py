@@ -15,3 +15,12 @@ APART = {**EVICT_BASE, **{k: FAKE * (2 + i) for i, k in enumerate("ctx w pos wo 
 def test_evict_refuses_lengths_that_overlap_partly(L, over):  # noqa: F811
     assert status(L, "dspark_kv_evict", EVICT, APART, over) == "DSPARK_ERR_INVALID_ARG"
     assert "new_lens" in dk.dspark_ctx_kv_last_error()
+
+
+@pytest.mark.parametrize("over", [
+    dict(wo=APART["w"] + 4), dict(wo=APART["w"] - 1020), dict(po=APART["pos"] + 1020), dict(w=APART["wo"] + 4), dict(wo=APART["pos"]),
+    dict(po=APART["w"]), dict(wo=APART["po"]), dict(wo=APART["po"] + 4), dict(po=APART["w"] + 8)])
+def test_evict_refuses_outputs_that_overlap_partly(L, over):  # noqa: F811
+    """2 requests x 2 heads x 64 places of 4 bytes: 1,024 bytes each."""
+    assert status(L, "dspark_kv_evict", EVICT, APART, over) == "DSPARK_ERR_INVALID_ARG"
+    assert "overlap" in dk.dspark_ctx_kv_last_error()
