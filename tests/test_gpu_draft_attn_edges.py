@@ -92,3 +92,19 @@ def test_evict_new_lengths_in_the_place_of_the_old(ctx, Hkv, budget, bad, where)
         assert dk.evict_kv(cache, p.d_table, lens, dw, dp, seen, budget, 2, 8, new_lens=new, error_flags=p.d_flags) is new
         assert new.tolist() == want[3] and int(p.d_flags) == (dk.FLAG_LENGTH if bad else 0)
         assert torch.equal(dw.cpu(), want[1]) and torch.equal(dp.cpu(), want[2]) and torch.equal(cache.cpu(), want[0])
+
+
+# ------------------------------------------------------------------ scales
+
+
+@pytest.mark.parametrize("scale,q", [(1e-38, 1e-12), (-1e-38, 1e-12), (1e-30, 2.0 ** -120), (3e-39, 1.0)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_attention_scores_that_underflow(scale, q, fp8, kernel):  # noqa: F811
+    """Scores below fp32's range are zero: every row is the mean of what it sees."""
+    p = Problem(13, (70, 300), (3, 40), 8, 2, 128, 16, fp8)
+    p.qkv = (p.qkv.double() * q).to(torch.bfloat16)
+    p.cuda()
+    out, lse = run_attention(p, "causal", None, scale=scale)
+    want, z, to, tl = attention(p, "causal", None, scale=scale)
+    close(lse, z, tl)
+    close(out, want, to)
