@@ -15,9 +15,12 @@ request b sits in block ``block_table[b, j // block_size]`` at offset
 what is out of range there is left out and raises a bit in ``error_flags``
 (an int32 CUDA tensor of one element, if given).
 
-``stream`` (a stream or its handle) runs the call there; outputs that the
-call makes then belong to that stream.  Without it the current stream of the
-tensors' device is used.
+``stream`` (a stream of the tensors' device, or its handle) runs the call
+there; outputs that the call makes then belong to that stream.  The inputs are
+used there without a record of it in PyTorch's allocator: the caller orders
+that stream behind their producers and keeps them until the call has run (or
+calls ``record_stream``).  Without it the current stream of the tensors'
+device is used.
 """
 
 from __future__ import annotations
@@ -57,6 +60,8 @@ def _elsewhere(device, stream) -> bool:
     """Whether a call has to change the current device or stream first."""
     if device.type != "cuda":
         _fail(f"tensors are on {device}, expected a CUDA device")
+    if stream is not None and not isinstance(stream, int) and stream.device != device:
+        _fail(f"stream is on {stream.device}, the tensors are on {device}")
     return stream is not None or device.index != torch.cuda.current_device()
 
 

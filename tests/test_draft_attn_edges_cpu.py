@@ -1,9 +1,13 @@
 """Refusals and host arithmetic of the draft-attention operators at the edges
 of what their documentation allows.  No test here launches a kernel."""
 
+import types
+
 import pytest
+import torch
 
 import speculative_decoding_draft_ctx_gb300 as dk
+from speculative_decoding_draft_ctx_gb300 import draft_attn
 from test_draft_attn_cpu import EVICT, EVICT_BASE, FAKE, L, status  # noqa: F401
 
 # arrays of their own, 64 KB apart: every call below is refused before any CUDA call
@@ -24,3 +28,12 @@ def test_evict_refuses_outputs_that_overlap_partly(L, over):  # noqa: F811
     """2 requests x 2 heads x 64 places of 4 bytes: 1,024 bytes each."""
     assert status(L, "dspark_kv_evict", EVICT, APART, over) == "DSPARK_ERR_INVALID_ARG"
     assert "overlap" in dk.dspark_ctx_kv_last_error()
+
+
+def test_a_stream_of_another_device_is_refused():
+    draft_attn._load()
+    here, there = torch.device("cuda", 0), torch.device("cuda", 1)
+    with pytest.raises(dk.DSparkError, match="stream is on cuda:1"):
+        draft_attn._elsewhere(here, types.SimpleNamespace(device=there, cuda_stream=FAKE))
+    assert draft_attn._elsewhere(there, types.SimpleNamespace(device=there, cuda_stream=FAKE))
+    assert draft_attn._elsewhere(here, FAKE)  # a handle says nothing about its device

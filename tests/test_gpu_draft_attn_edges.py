@@ -108,3 +108,35 @@ def test_attention_scores_that_underflow(scale, q, fp8, kernel):  # noqa: F811
     want, z, to, tl = attention(p, "causal", None, scale=scale)
     close(lse, z, tl)
     close(out, want, to)
+
+
+# ------------------------------------------------------------------ streams
+
+
+def test_every_operator_on_a_stream_that_is_given():
+    """By stream and by handle, with the outputs made by the call: the bits of a call on the current stream."""
+    p = Problem(17, (400, 90), (5, 30), 8, 2, 128, 16, True).cuda()
+    pos, S = torch.arange(35, device="cuda"), 400
+    k = torch.randn((35, 2, 128), device="cuda").to(torch.bfloat16)
+    seen = torch.tensor([400, 90], dtype=torch.int32, device="cuda")
+
+    def chain(**kw):
+        cache = p.d_cache.clone()
+        w, at = torch.zeros((2, 2, S), device="cuda"), torch.arange(S, dtype=torch.int32, device="cuda").repeat(2, 2, 1)
+        if kw:
+            torch.cuda.synchronize()
+        table = dk.rope_table(64, 128, **kw)
+        q, k2 = dk.rope_kv_insert(p.d_q, k, table, pos, 128, **kw)
+        out, lse = dk.tree_attention(q, cache, p.d_table, p.d_start, p.d_ctx, causal=True, **p.scale_kw(), **kw)
+        dk.accumulate_attention_weight(q, cache, p.d_table, p.d_start, p.d_ctx, lse, w, k_scale=p.d_ks, **kw)
+        lens = dk.evict_kv(cache, p.d_table, p.d_ctx, w, at, seen, 100, 2, 4, **kw)
+        torch.cuda.synchronize()
+        return table, q, k2, out, lse, w, at, lens, cache
+
+    want = chain()
+    s = torch.cuda.Stream()
+    for kw in (dict(stream=s), dict(stream=s.cuda_stream), dict(stream=0)):
+        before = torch.cuda.current_stream()
+        for a, b in zip(want, chain(**kw)):
+            assert torch.equal(a, b)
+        assert torch.cuda.current_stream() == before
