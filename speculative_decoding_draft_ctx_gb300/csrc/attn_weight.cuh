@@ -472,10 +472,11 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
                     __syncwarp();
                     if (lane == 0)
                         bar_arrive(sempty + e);  // the scores (and the tile's live bits) are read
-                    if (key < w.rq.ctx && here) {
+                    if (key < w.rq.ctx) {
                         float a, b2;
                         unpr(add2(s0, s1), a, b2);
-                        weights[key] = first ? fmaf(p.decay, old, a + b2) : old + (a + b2);
+                        const float sum = here ? a + b2 : 0.0f;  // nothing for a token in a block out of range
+                        weights[key] = first ? fmaf(p.decay, old, sum) : old + sum;
                     }
                 }
             }

@@ -140,3 +140,26 @@ def test_every_operator_on_a_stream_that_is_given():
         for a, b in zip(want, chain(**kw)):
             assert torch.equal(a, b)
         assert torch.cuda.current_stream() == before
+
+
+# ------------------------------------------------------------------ the accumulated weight
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_weight_of_tokens_in_blocks_out_of_range_decays(fp8):
+    """With drafted tokens (one group of rows and two) and without."""
+    ctx, nq = (100, 100, 300, 40), (3, 0, 40, 2)
+    p = Problem(19, ctx, nq, 16, 2, 128, 16, fp8).cuda()
+    _, lse = run_attention(p, "dense", None)
+    before = torch.rand((4, 2, 305), generator=gen(4))
+    good = before.cuda()
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, good, decay=0.5, k_scale=p.d_ks, error_flags=p.d_flags)
+    assert int(p.d_flags) == 0
+    for b, entry in ((0, -1), (1, 10 ** 6), (2, p.blocks)):
+        p.d_table[b, 2] = entry  # tokens 32..47
+    got = before.cuda()
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, got, decay=0.5, k_scale=p.d_ks, error_flags=p.d_flags)
+    assert int(p.d_flags) == dk.FLAG_BLOCK_RANGE
+    want = good.clone()
+    want[:3, :, 32:48] = before[:3, :, 32:48].cuda() * 0.5
+    assert torch.equal(got, want)
