@@ -153,7 +153,8 @@ int64_t dspark_tree_attention_workspace(int64_t num_rows, int num_heads, int num
  *   weights[b, h, j] = decay * weights[b, h, j]
  *                    + sum_{i, g} exp(scale * q[t_i, h G + g] . k_j - lse[t_i, h G + g])
  * for j < context_lens[b], with lse as dspark_tree_attention wrote it (a row
- * whose lse is -inf saw nothing and adds nothing); other entries stay.  A token
+ * whose lse is -inf saw nothing and adds nothing, whatever its query holds);
+ * other entries stay.  A token
  * in a block out of range receives nothing: its weight only decays
  * (DSPARK_FLAG_BLOCK_RANGE where the request has drafted tokens).  The sums run
  * in a fixed order.

@@ -140,6 +140,7 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
     constexpr int PG = C::kGroups, WR = C::kWarpRows, RG = WR / 32;
     __shared__ uint32_t tmem_slot, live[16][4], rows[C::kProducers][2][WR];
     __shared__ int abort_flag;
+    __shared__ int silent[2];  // group number + 1 where a group has rows that saw nothing
     __shared__ __align__(16) float zneg[2][kRows], cscale[2][FP8 ? kRows : 4];  // of a group's rows: -lse, scale (base 2)
     __shared__ int64_t scratch[C::kThreads / 32 + 4];
     volatile int *abort = &abort_flag;
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
         bar_init(&qfull, 256);
         bar_init(&qempty, 1);
         bar_init(&done, 1);
-        abort_flag = 0;
+        abort_flag = silent[0] = silent[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == C::kIssuer) {
@@ -379,10 +380,11 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
                     const int i = mine ? row / p.group : 0, hq = w.h * p.group + (mine ? row - i * p.group : 0);
                     const uint16_t *src = p.q + (int64_t)(w.rq.q0 + i) * p.q_ts + (int64_t)hq * p.q_hs;
                     float inv = 1.0f, fix = 1.0f;
-                    if (mine) {
-                        const float l = __ldg(p.lse + (int64_t)(w.rq.q0 + i) * p.num_heads + hq);
-                        zneg[zb][tid] = l == -INFINITY ? -INFINITY : -l * kLog2e;  // a row that saw nothing adds nothing
-                    }
+                    // a row that saw nothing, or none at all, adds nothing whatever its scores hold
+                    const float lse = mine ? __ldg(p.lse + (int64_t)(w.rq.q0 + i) * p.num_heads + hq) : -INFINITY;
+                    zneg[zb][tid] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+                    if (mine && lse == -INFINITY)
+                        silent[zb] = ng + 1;
                     if constexpr (FP8) {
                         float top = 0.0f;
                         if (mine)
@@ -440,13 +442,14 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
                     if (!first && key < w.rq.ctx)
                         old = weights[key];
                     uint64_t s0 = 0, s1 = 0;
+                    const bool mute = silent[zb] == ng + 1;
 #pragma unroll 1
                     for (int c0 = 0; c0 < cols; c0 += 32) {
                         uint32_t y[32];
                         tmem_ld32(tmem + lanes + 256 * e + c0, y);
                         const float4 *z = reinterpret_cast<const float4 *>(zneg[zb] + c0);
                         const float4 *cs = reinterpret_cast<const float4 *>(cscale[zb] + (FP8 ? c0 : 0));
-                        const int left = cols - c0;
+                        const bool some = cols - c0 < 32 || mute;  // some of the columns count for nothing
 #pragma unroll
                         for (int k = 0; k < 8; k++) {
                             const float4 zv = z[k];
@@ -459,9 +462,9 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
                             unpr(fma2(pr(__uint_as_float(y[4 * k]), __uint_as_float(y[4 * k + 1])), f0, pr(zv.x, zv.y)), a0, a1);
                             unpr(fma2(pr(__uint_as_float(y[4 * k + 2]), __uint_as_float(y[4 * k + 3])), f1, pr(zv.z, zv.w)), a2, a3);
                             a0 = ex2(a0), a1 = ex2(a1), a2 = ex2(a2), a3 = ex2(a3);
-                            if (left < 32) {  // columns behind the last row hold nothing
-                                a0 = 4 * k < left ? a0 : 0.0f, a1 = 4 * k + 1 < left ? a1 : 0.0f;
-                                a2 = 4 * k + 2 < left ? a2 : 0.0f, a3 = 4 * k + 3 < left ? a3 : 0.0f;
+                            if (some) {
+                                a0 = zv.x != -INFINITY ? a0 : 0.0f, a1 = zv.y != -INFINITY ? a1 : 0.0f;
+                                a2 = zv.z != -INFINITY ? a2 : 0.0f, a3 = zv.w != -INFINITY ? a3 : 0.0f;
                             }
                             s0 = add2(s0, pr(a0, a1));
                             s1 = add2(s1, pr(a2, a3));

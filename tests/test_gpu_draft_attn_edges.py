@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import speculative_decoding_draft_ctx_gb300 as dk
-from draft_attn_ref import Problem, attention, close, evict, gen
+from draft_attn_ref import Problem, attention, close, evict, gen, weight
 from test_gpu_draft_attn import kernel, run_attention  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +163,22 @@ def test_weight_of_tokens_in_blocks_out_of_range_decays(fp8):
     want = good.clone()
     want[:3, :, 32:48] = before[:3, :, 32:48].cuda() * 0.5
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("D,fp8", [(64, False), (128, True), (128, False), (256, True)])
+def test_weight_ignores_rows_without_lse_whatever_they_hold(D, fp8):
+    """Rows marked as having seen nothing (lse -inf) may hold NaN and infinities; one request has no other rows."""
+    ctx, nq = (300, 70, 40), (7, 3, 20)
+    p = Problem(23, ctx, nq, 16, 1, D, 16, fp8).cuda()
+    _, lse = run_attention(p, "dense", None)
+    gone = [2, 5, 7, 8, 9, 29]
+    lse[gone] = -math.inf
+    w = torch.rand((3, 1, 305), generator=gen(5))
+    want = weight(p, lse, w, 0.5)
+    blk, off = int(p.table[1, 1]), 3  # token 19 of the request without other rows
+    p.d_cache[blk, 0, off, :D] = 0x7F if fp8 else math.nan
+    p.d_q[gone] = torch.tensor([math.nan, math.inf, -math.inf, 3e38], dtype=torch.bfloat16, device="cuda").repeat(D // 4)
+    got = w.cuda()
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, got, decay=0.5, k_scale=p.d_ks, error_flags=p.d_flags)
+    close(got, *want)
+    assert int(p.d_flags) == 0
