@@ -15,9 +15,11 @@
  * a CUDA graph), return a dspark_status and never throw.  Lengths, offsets
  * and block numbers live in device memory, so the kernels check them: what
  * is out of range is never dereferenced and raises a bit in *error_flags.
- * Every wait inside the attention and the weight accumulation is bounded; one
- * that ran out raises DSPARK_FLAG_TIMEOUT, and that call's outputs hold nothing
- * of use.
+ * The waits inside the attention and the weight accumulation for their own
+ * copies and products are bounded (4 s); one that ran out raises
+ * DSPARK_FLAG_TIMEOUT, and that call's outputs hold nothing of use.  Their
+ * allocation of tensor memory has no limit of its own: it waits for another
+ * kernel's CTA on the same SM to free what it holds.
  */
 #ifndef DSPARK_DRAFT_ATTN_H
 #define DSPARK_DRAFT_ATTN_H

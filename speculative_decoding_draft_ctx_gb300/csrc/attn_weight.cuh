@@ -143,7 +143,7 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
     __shared__ int silent[2];  // group number + 1 where a group has rows that saw nothing
     __shared__ __align__(16) float zneg[2][kRows], cscale[2][FP8 ? kRows : 4];  // of a group's rows: -lse, scale (base 2)
     __shared__ int64_t scratch[C::kThreads / 32 + 4];
-    volatile int *abort = &abort_flag;
+    const Patience limit{&abort_flag, p.wait_ns};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
         int x = 0, ng = 0;  // tiles, groups so far
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
-            ok = ok && bar_wait(bar, parity, abort);
+            ok = ok && bar_wait(bar, parity, limit);
             ok = __all_sync(0xffffffffu, ok);
         };
         while (w.more() && ok) {
@@ -302,13 +302,15 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
         look();
         resolve(0);
         look();
+        if (p.test_hold)
+            looked = 0;  // test hook: nothing is copied, the other roles' waits run out
         for (int i = 0; i < looked && ok; i++) {
             const int x = mine + PG * i, st = x % NS;
             const uint32_t dst0 = tc::saddr(sk) + st * C::kTileBytes;
             const uint32_t *from = rows[pw][i & 1];
             resolve((i & 1) ^ 1);
             look();
-            ok = bar_wait(kempty + st, ((uint32_t)(x / NS) & 1u) ^ 1u, abort);
+            ok = bar_wait(kempty + st, ((uint32_t)(x / NS) & 1u) ^ 1u, limit);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok)
                 break;
@@ -369,7 +371,7 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
                 const int cols = min(kRows, all - row0), zb = ng & 1;
                 // ---- the group's rows: thread tid takes row row0 + tid, once no product reads the last ones
                 if (ng > 0) {
-                    ok = bar_wait(&qempty, (uint32_t)(ng - 1) & 1u, abort);
+                    ok = bar_wait(&qempty, (uint32_t)(ng - 1) & 1u, limit);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok)
                         break;
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
                     float old = 0.0f;
                     if (first && key < w.rq.ctx)
                         old = weights[key];
-                    ok = bar_wait(sfull + e, (uint32_t)(x >> 1) & 1u, abort);
+                    ok = bar_wait(sfull + e, (uint32_t)(x >> 1) & 1u, limit);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok)
                         break;
@@ -490,13 +492,14 @@ __global__ void __launch_bounds__((WeightTc<D, FP8>::kThreads), 1) weight_kernel
     if (warp == C::kIssuer) {
         if (lane == 0) {
             const unsigned long long t0 = gtimer();
-            while (!bar_try(&done, 0) && gtimer() - t0 < kTimeoutNs) {
-            }
+            while (!bar_try(&done, 0) && !(flags & kFlagTimeout))
+                if (gtimer() - t0 > limit.ns)
+                    flags |= kFlagTimeout;
         }
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
-    if (tid == 0 && *abort)
+    if (tid == 0 && *limit.abort)
         flags |= kFlagTimeout;
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (lane == 0 && flags && p.error_flags)

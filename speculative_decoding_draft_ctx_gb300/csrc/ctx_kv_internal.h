@@ -59,6 +59,13 @@ __device__ __forceinline__ void pdl_enter()
 // defined outside the host layer.
 int api_fail(int status, const char *message);
 
+// DSPARK_TEST_HOLD_NS=<ns> (tests of the timeout paths only), at most 1 s; 0
+// without it.  The writes' kernels first wait that long on a device word that
+// nothing sets, then stop as on any expired wait; the tensor-core kernels of
+// the draft-attention operators copy no tile, so that their own waits run out,
+// after that long.  Either reports DSPARK_FLAG_TIMEOUT.
+uint64_t test_hold_ns();
+
 constexpr int kHeadDim = 128;
 constexpr int kRowElems = 256;
 

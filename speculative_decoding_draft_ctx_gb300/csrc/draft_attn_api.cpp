@@ -14,6 +14,8 @@ namespace {
 
 using namespace dspark;
 
+constexpr uint64_t kWaitNs = 4000000000;  // of a wait inside a kernel, which takes microseconds
+
 int fail(int status, const char *fmt, ...)
 {
     char text[384];
@@ -132,6 +134,9 @@ int check_attention(AttnParams &p, const void *q, int64_t q_ts, int64_t q_hs, in
     p.block_magic = block_size > 1 ? UINT64_MAX / (uint64_t)block_size + 1 : 0;
     p.num_requests = requests;
     p.scale = scale;
+    const uint64_t hold = test_hold_ns();
+    p.test_hold = hold != 0;
+    p.wait_ns = hold ? hold : kWaitNs;
     return DSPARK_OK;
 }
 

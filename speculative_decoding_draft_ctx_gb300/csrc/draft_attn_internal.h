@@ -64,6 +64,8 @@ struct AttnParams {
     uint64_t block_magic;  // floor(2^64 / block_size) + 1; 0 for size 1
     int32_t mask_kind, mask_words;
     float scale;        // softmax scale
+    uint64_t wait_ns;   // limit of every wait of the tensor-core kernels
+    bool test_hold;     // test hook (see dspark::test_hold_ns): their producers copy nothing
     // attention
     uint16_t *out;
     float *parts;       // workspace: partial results, see tree_attn_mma.cuh

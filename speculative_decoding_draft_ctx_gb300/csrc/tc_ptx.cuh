@@ -12,7 +12,6 @@ namespace dspark {
 namespace tc {
 
 constexpr unsigned kFlagTimeout = 0x4u;
-constexpr unsigned long long kTimeoutNs = 4000000000ull;
 constexpr uint32_t kSuspendNs = 200000;
 
 __device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -65,9 +64,15 @@ __device__ __forceinline__ bool bar_test(uint64_t *bar, uint32_t parity)
     return ok != 0;
 }
 
-// Waits for the phase of `bar` with this parity; false after kTimeoutNs or
-// once another thread of the CTA has given up (which it then records).
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+// How long a CTA's waits may take, and its word that says one has run out.
+struct Patience {
+    volatile int *abort;
+    unsigned long long ns;
+};
+
+// Waits for the phase of `bar` with this parity; false once the wait has run
+// out (which it records) or another thread of the CTA has given up.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, const Patience &limit)
 {
     if (bar_try(bar, parity))
         return true;
@@ -75,10 +80,10 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
     while (true) {
         if (bar_try(bar, parity))
             return true;
-        if (*abort)
+        if (*limit.abort)
             return false;
-        if (gtimer() - t0 > kTimeoutNs) {
-            *abort = 1;
+        if (gtimer() - t0 > limit.ns) {
+            *limit.abort = 1;
             return false;
         }
     }

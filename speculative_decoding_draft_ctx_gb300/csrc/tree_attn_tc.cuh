@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     __shared__ int bad[16];  // item number + 1 where infinities or NaN came up among an item's drafted V
     __shared__ float join_ml[256];
     __shared__ int64_t scratch[kTcThreads / 32 + 4];
-    volatile int *abort = &abort_flag;
+    const Patience limit{&abort_flag, p.wait_ns};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 const int steps = two ? n : s == 0 ? (n + 1) >> 1 : n >> 1;
                 auto tile_of = [&](int k) { return two ? k : 2 * k + s; };
                 auto wait = [&](uint64_t *bar, uint32_t parity) {
-                    ok = ok && bar_wait(bar, parity, abort);
+                    ok = ok && bar_wait(bar, parity, limit);
                     ok = __all_sync(0xffffffffu, ok);
                 };
                 // a stage is free when both streams are done with it; where the
@@ -243,8 +243,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 auto take = [&]() {
                     if (leader && two) {
                         const unsigned long long t0 = gtimer();
-                        while (atomicExch(&lock, 1) != 0 && gtimer() - t0 < kTimeoutNs) {
-                        }
+                        while (atomicExch(&lock, 1) != 0 && !*limit.abort)
+                            if (gtimer() - t0 > limit.ns)
+                                *limit.abort = 1;
                     }
                     __syncwarp();
                 };
@@ -409,11 +410,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         look();
         resolve(0);
         look();
+        if (p.test_hold)
+            looked = 0;  // test hook: nothing is copied, the other roles' waits run out
         for (; x < looked && ok; x++) {
             const int st = x % ns, key0 = tile * kKeysTc + 64 * sub;
             const bool drafted = is_v && key0 + 64 > w.rq.ctx;
             if (issued == x) {
-                ok = bar_wait(empties + st, free_parity(x), abort);
+                ok = bar_wait(empties + st, free_parity(x), limit);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
                     break;
@@ -552,7 +555,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 const int key0 = (w.t0 + j) * kKeysTc;
                 const int nh = 2 * j + 1 == halves ? 1 : 2;  // 64-key halves that hold tokens
                 const uint32_t ts = tmem + lanes + 128 * s;
-                ok = ok && bar_wait(sfull + s, (uint32_t)nS & 1u, abort);
+                ok = ok && bar_wait(sfull + s, (uint32_t)nS & 1u, limit);
                 nS++;
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok)
@@ -695,7 +698,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 break;
             // ---- the item ends here, or the CTA's share of it does
             if (steps > 0) {
-                ok = bar_wait(ofull + s, (uint32_t)nO & 1u, abort);
+                ok = bar_wait(ofull + s, (uint32_t)nO & 1u, limit);
                 ok = __all_sync(0xffffffffu, ok);
                 nO++;
             }
@@ -707,9 +710,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     fence_before();
                     bar_arrive(&jfull);
                     // its output and statistics stay until stream 0 has read them
-                    ok = ok && bar_wait(&jempty, (uint32_t)nJ & 1u, abort);
+                    ok = ok && bar_wait(&jempty, (uint32_t)nJ & 1u, limit);
                 } else {
-                    ok = ok && bar_wait(&jfull, (uint32_t)nJ & 1u, abort);
+                    ok = ok && bar_wait(&jfull, (uint32_t)nJ & 1u, limit);
                     fence_after();
                     const float om = join_ml[r], ol = join_ml[128 + r], t = fmaxf(m, om), u = t == -INFINITY ? 0.0f : t;
                     y0 = ex2(m - u), y1 = ex2(om - u);
@@ -807,13 +810,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         if (lane == 0) {
             const unsigned long long t0 = gtimer();
             for (int s = 0; s < 2; s++)
-                while (!bar_try(done + s, 0) && gtimer() - t0 < kTimeoutNs) {
-                }
+                while (!bar_try(done + s, 0) && !(flags & kFlagTimeout))
+                    if (gtimer() - t0 > limit.ns)
+                        flags |= kFlagTimeout;
         }
         __syncwarp();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
-    if (tid == 0 && *abort)
+    if (tid == 0 && *limit.abort)
         flags |= kFlagTimeout;
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (lane == 0 && flags && p.error_flags)

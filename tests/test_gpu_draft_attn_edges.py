@@ -182,3 +182,50 @@ def test_weight_ignores_rows_without_lse_whatever_they_hold(D, fp8):
     dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, got, decay=0.5, k_scale=p.d_ks, error_flags=p.d_flags)
     close(got, *want)
     assert int(p.d_flags) == 0
+
+
+# ------------------------------------------------------------------ waits that run out
+
+
+@pytest.mark.parametrize("D,fp8", [(64, False), (64, True), (128, False), (128, True)])
+def test_expired_waits_report_timeout_and_leave_the_context_usable(D, fp8, monkeypatch):
+    """With the test hook the tensor-core kernels' producers copy nothing, so that every role's wait runs out after
+    2 ms: the call ends, says so, and the next one is right.  Items of one and of two row tiles, whole and split."""
+    p = Problem(29, (900, 3, 400, 3000), (7, 5, 30, 40), 16, 2, D, 16, fp8).cuda()
+    monkeypatch.setenv("DSPARK_TREE_ATTN_KERNEL", "tc")
+    monkeypatch.setenv("DSPARK_TEST_HOLD_NS", "2000000")
+    run_attention(p, "causal", None)
+    assert int(p.d_flags) == dk.FLAG_TIMEOUT
+    monkeypatch.delenv("DSPARK_TEST_HOLD_NS")
+    p.d_flags.zero_()
+    out, lse = run_attention(p, "causal", None)
+    want, z, to, tl = attention(p, "causal", None)
+    close(lse, z, tl)
+    close(out, want, to)
+    assert int(p.d_flags) == 0
+    before = torch.rand((4, 2, 3000), generator=gen(6))
+    w = before.cuda()
+    kw = dict(decay=0.5, k_scale=p.d_ks, error_flags=p.d_flags)
+    monkeypatch.setenv("DSPARK_TEST_HOLD_NS", "2000000")
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, w, **kw)
+    assert int(p.d_flags) == dk.FLAG_TIMEOUT
+    monkeypatch.delenv("DSPARK_TEST_HOLD_NS")
+    p.d_flags.zero_()
+    w = before.cuda()
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, w, **kw)
+    close(w, *weight(p, lse, before, 0.5))
+    assert int(p.d_flags) == 0
+
+
+def test_expired_waits_of_the_weight_kernel_at_head_dim_256(monkeypatch):
+    p = Problem(31, (300, 70), (7, 20), 16, 2, 256, 16, True).cuda()
+    _, lse = run_attention(p, "causal", None)
+    w = torch.zeros((2, 2, 300), device="cuda")
+    monkeypatch.setenv("DSPARK_TEST_HOLD_NS", "2000000")
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, w, k_scale=p.d_ks, error_flags=p.d_flags)
+    assert int(p.d_flags) == dk.FLAG_TIMEOUT
+    monkeypatch.delenv("DSPARK_TEST_HOLD_NS")
+    p.d_flags.zero_(), w.zero_()
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, w, k_scale=p.d_ks, error_flags=p.d_flags)
+    close(w, *weight(p, lse, torch.zeros((2, 2, 300)), 1.0))
+    assert int(p.d_flags) == 0
