@@ -21,24 +21,38 @@ namespace dspark {
 // Launches `kernel` with programmatic stream serialization allowed, so that
 // it may start while the previous kernel of the stream drains (the kernel
 // itself executes griddepcontrol.wait before touching global memory).
-// DSPARK_PDL=0 launches it the plain way.
+// DSPARK_PDL=0 launches it the plain way.  cluster > 0: clusters of so many
+// CTAs along x.
+template <typename... Params, typename... Args>
+cudaError_t launch_pdl_grid(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, int cluster,
+                            cudaStream_t stream, Args &&...args)
+{
+    const char *env = std::getenv("DSPARK_PDL");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    if (!(env && std::strcmp(env, "0") == 0)) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (cluster > 0) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = (unsigned)cluster;
+        attr[cfg.numAttrs].val.clusterDim.y = 1;
+        attr[cfg.numAttrs++].val.clusterDim.z = 1;
+    }
+    cfg.attrs = attr;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 template <typename... Params, typename... Args>
 cudaError_t launch_pdl(void (*kernel)(Params...), int blocks, int threads, size_t smem, cudaStream_t stream,
                        Args &&...args)
 {
-    const char *env = std::getenv("DSPARK_PDL");
-    const bool pdl = !(env && std::strcmp(env, "0") == 0);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)blocks);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = pdl ? attr : nullptr;
-    cfg.numAttrs = pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+    return launch_pdl_grid(kernel, dim3((unsigned)blocks), threads, smem, 0, stream, std::forward<Args>(args)...);
 }
 
 // The kernel side of launch_pdl, before any global load or store (L2

@@ -402,21 +402,8 @@ cudaError_t launch(const EvictParams &p, int64_t pairs, int nc, int dev, cudaStr
         }
     }
     const int64_t per = (p.stride + nc - 1) / nc;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pairs * nc));
-    cfg.blockDim = dim3((unsigned)kThreads);
-    cfg.dynamicSmemBytes = (size_t)(per < kKeysMax ? per : kKeysMax) * 4;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)nc;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, evict_kernel<kThreads, kBlocks>, p, nc);
+    const size_t smem = (size_t)(per < kKeysMax ? per : kKeysMax) * 4;
+    return launch_pdl_grid(evict_kernel<kThreads, kBlocks>, dim3((unsigned)(pairs * nc)), kThreads, smem, nc, stream, p, nc);
 }
 
 }  // namespace
@@ -444,16 +431,7 @@ cudaError_t launch_kv_evict(const EvictParams &p, cudaStream_t stream)
     const int64_t most = (p.list_len + 63) / 64;
     int64_t shares = (3 * (int64_t)sms + pairs - 1) / pairs;
     shares = shares < most ? shares : most;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)pairs, (unsigned)shares);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, move_kernel, p);
+    return launch_pdl_grid(move_kernel, dim3((unsigned)pairs, (unsigned)shares), 256, 0, 0, stream, p);
 }
 
 }  // namespace dspark

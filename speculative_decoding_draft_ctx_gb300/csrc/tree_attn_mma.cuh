@@ -1188,16 +1188,7 @@ cudaError_t attention(const AttnParams &p, cudaStream_t stream)
     e = launch_pdl(attention_kernel<D, FP8, WR>, ctas, kThreads, C::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)WR);
-    cfg.blockDim = dim3((unsigned)kThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D, FP8, WR>, p, ctas);
+    return launch_pdl_grid(join_kernel<D, FP8, WR>, dim3((unsigned)ctas, (unsigned)WR), kThreads, 0, 0, stream, p, ctas);
 }
 
 // Rows of an item: the smallest of 16, 32 and 64 that holds the mean request's

@@ -947,16 +947,7 @@ cudaError_t attention_tc(const AttnParams &p, cudaStream_t stream)
         e = launch_pdl(attention_tc_kernel<D, FP8>, ctas, kTcThreads, C::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(2 * (D / kJoinDims)));
-    cfg.blockDim = dim3(128);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_tc_kernel<D, FP8>, p, ctas);
+    return launch_pdl_grid(join_tc_kernel<D, FP8>, dim3((unsigned)ctas, (unsigned)(2 * (D / kJoinDims))), 128, 0, 0, stream, p, ctas);
 }
 
 template <int D>

@@ -1,6 +1,7 @@
 """Calls of the draft-attention operators at the edges of what their
 documentation allows, against the definitions in 64 bits (draft_attn_ref.py)."""
 
+import ctypes
 import math
 
 import pytest
@@ -229,3 +230,42 @@ def test_expired_waits_of_the_weight_kernel_at_head_dim_256(monkeypatch):
     dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, w, k_scale=p.d_ks, error_flags=p.d_flags)
     close(w, *weight(p, lse, torch.zeros((2, 2, 300)), 1.0))
     assert int(p.d_flags) == 0
+
+
+# ------------------------------------------------------------------ how kernels follow one another
+
+
+def programmatic_edges(f):
+    """(all edges, those that let a kernel start while the one before drains) of the graph captured from f."""
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        f()
+    get = ctypes.CDLL("libcudart.so.13").cudaGraphGetEdges
+    get.argtypes, get.restype = [ctypes.c_void_p] * 5, ctypes.c_int
+    n = ctypes.c_size_t(0)
+    assert get(g.raw_cuda_graph(), None, None, None, ctypes.addressof(n)) == 0
+    a, b, data = (ctypes.c_void_p * n.value)(), (ctypes.c_void_p * n.value)(), (ctypes.c_ubyte * (8 * n.value))()
+    assert get(g.raw_cuda_graph(), a, b, data, ctypes.addressof(n)) == 0
+    return n.value, sum(data[8 * i + 2] == 1 for i in range(n.value))  # from port, to port, type (1: programmatic), reserved
+
+
+def test_every_launch_follows_the_switch_for_programmatic_overlap(kernel, monkeypatch):  # noqa: F811
+    p = Problem(37, (600, 40), (7, 5), 16, 2, 128, 16, False).cuda()
+    out, lse = run_attention(p, "dense", None)
+    w, at = torch.rand((2, 2, 600), device="cuda"), torch.arange(600, dtype=torch.int32, device="cuda").repeat(2, 2, 1)
+    cos_sin, pos = dk.rope_table(16, 64), torch.arange(12, device="cuda")
+    wo, po, lens = torch.empty_like(w), torch.empty_like(at), torch.empty_like(p.d_ctx)
+
+    def chain():
+        dk.rope_table(16, 64, out=cos_sin)
+        dk.rope_kv_insert(p.d_q, p.d_q[:, :2], cos_sin, pos, 64)
+        run_attention(p, "dense", None, out=out, lse=lse)
+        dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, w)
+        dk.evict_kv(p.d_cache, p.d_table, p.d_ctx, w, at, p.d_ctx, 64, weights_out=wo, positions_out=po, new_lens=lens)
+
+    chain()
+    torch.cuda.synchronize()
+    edges, overlapped = programmatic_edges(chain)  # table, rotation, attention, join, weight, ranking, moves
+    assert edges == 6 and overlapped == 6
+    monkeypatch.setenv("DSPARK_PDL", "0")
+    assert programmatic_edges(chain) == (6, 0)
