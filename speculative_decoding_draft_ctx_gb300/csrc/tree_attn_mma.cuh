@@ -90,12 +90,10 @@ __device__ __forceinline__ uint32_t saddr(const void *p) { return (uint32_t)__cv
 
 // 16-byte words of row x are stored at word ^ swz(x): eight consecutive rows
 // use eight different words (ldmatrix), rows 2i and 2i + 1 differ in bit 2
-// (four neighbouring words of both rows at once: the fp8 key reads).  Rows of
-// only four words (PITCH 64) need none: two of them fill the eight.
-template <int PITCH>
+// (four neighbouring words of both rows at once: the fp8 key reads).
 __device__ __forceinline__ int swz(int x)
 {
-    return PITCH == 64 ? 0 : ((x & 1) << 2) | ((x >> 1) & 3);
+    return ((x & 1) << 2) | ((x >> 1) & 3);
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool live)
@@ -360,18 +358,18 @@ struct Walk {
 
 // ------------------------------------------------------------------ the cached tiles
 
-// Copies kTile rows of `ROW` bytes (the first COPY of them wanted) of one
-// (request, KV head) into a stage, through the block table.  A warp takes 16
+// Copies kTile rows of `ROW` bytes of one (request, KV head) into a stage,
+// through the block table.  A warp takes 16
 // rows; its lanes 0..15 (and 16..31 alike) hold the block of their row, which
 // `fetch` has read for the tile that `load` will copy next.
-template <int ROW, int COPY>
+template <int ROW>
 struct Loader {
-    static constexpr int kWords = COPY / 16;
+    static constexpr int kWords = ROW / 16;
     int64_t phys;
     int off;
     bool live;
 
-    __device__ __forceinline__ void fetch(const AttnParams &p, int b, int tile, int len, unsigned &flags)
+    __device__ __forceinline__ void fetch(const AttnParams &p, int b, int tile, int len)
     {
         const int j = tile * kTile + (threadIdx.x >> 5) * 16 + (threadIdx.x & 15);
         live = j < len;
@@ -408,7 +406,7 @@ struct Loader {
             for (int i = 0; i < kBatch; i++) {
                 const int idx = (i0 + i) * 32 + lane;
                 const int x = idx / kWords, c = idx % kWords, y = warp * 16 + x;
-                cp16(stage + y * COPY + ((c ^ swz<COPY>(y)) << 4), reinterpret_cast<const unsigned char *>(src[i]) + 16 * c,
+                cp16(stage + y * ROW + ((c ^ swz(y)) << 4), reinterpret_cast<const unsigned char *>(src[i]) + 16 * c,
                      (bits >> x) & 1u);
             }
         }
@@ -504,21 +502,6 @@ __device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean)
     return any;
 }
 
-// Waits until at most `pending` (0 to 7) of this thread's newest copy groups are in flight.
-__device__ __forceinline__ void cp_wait_most(int pending)
-{
-    switch (pending) {
-    case 0: cp_wait<0>(); break;
-    case 1: cp_wait<1>(); break;
-    case 2: cp_wait<2>(); break;
-    case 3: cp_wait<3>(); break;
-    case 4: cp_wait<4>(); break;
-    case 5: cp_wait<5>(); break;
-    case 6: cp_wait<6>(); break;
-    default: cp_wait<7>(); break;
-    }
-}
-
 // ------------------------------------------------------------------ queries
 
 // The A operands of a warp's 16 rows: reg 0 / 1 row g / g + 8 of the lower 8
@@ -590,7 +573,7 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&a)[D 
         for (int i = 0; i < NT; i += 2) {
             const int x = key + 8 * i;
             const uint32_t row = stage + x * PITCH;
-            const int z = swz<PITCH>(x);
+            const int z = swz(x);
 #pragma unroll
             for (int k = 0; k < D / 16; k++) {
                 uint32_t b[4];
@@ -604,7 +587,7 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&a)[D 
         for (int i = 0; i < NT; i++) {
             const int x = key0 + 8 * i + (lane >> 2);
             const uint32_t row = stage + x * PITCH;
-            const int z = swz<PITCH>(x);
+            const int z = swz(x);
 #pragma unroll
             for (int u = 0; u < D / 64; u++) {
                 uint32_t w[4];
@@ -743,9 +726,9 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
     W cp = w;
     int cp_tile = cp.t0;
 
-    Loader<C::kRow, C::kRow> ld;
+    Loader<C::kRow> ld;
     if (cp.more())
-        ld.fetch(p, cp.b, cp_tile, cp.rq.ctx + cp.rq.nq, flags);
+        ld.fetch(p, cp.b, cp_tile, cp.rq.ctx + cp.rq.nq);
     auto issue = [&](int stage) {
         if (cp.more()) {
             ld.load(p, cp.head(), stages + stage * C::kStage, live[stage], flags);
@@ -754,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
                 cp_tile = cp.t0;
             }
             if (cp.more())
-                ld.fetch(p, cp.b, cp_tile, cp.rq.ctx + cp.rq.nq, flags);
+                ld.fetch(p, cp.b, cp_tile, cp.rq.ctx + cp.rq.nq);
         }
         cp_commit();
     };
@@ -795,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
                     const int y = x / (C::kRow / 32), c = C::kRow / 32 + x % (C::kRow / 32);
                     if (key0 + y < rq.ctx || key0 + y >= len)
                         continue;
-                    uint4 *at = reinterpret_cast<uint4 *>(smem + stage * C::kStage + y * C::kRow + ((c ^ swz<C::kRow>(y)) << 4));
+                    uint4 *at = reinterpret_cast<uint4 *>(smem + stage * C::kStage + y * C::kRow + ((c ^ swz(y)) << 4));
                     uint4 v = *at;
                     uint32_t vw[4] = {v.x, v.y, v.z, v.w};
                     bool hit = false;
@@ -883,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
                                         pack2<FP8>(s[2 * j + 1][2], s[2 * j + 1][3])};
                 const int x = wk * C::kKeys + 16 * j + (lane & 15);
                 const uint32_t row = st + x * C::kRow;
-                const int z = swz<C::kRow>(x);
+                const int z = swz(x);
                 if constexpr (!FP8) {
 #pragma unroll
                     for (int n = 0; n < D / 16; n++) {  // 16 dims: words 2 n and 2 n + 1 of V
@@ -1125,11 +1108,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ launches
-
-struct Plan {
-    int wr, ctas;
-    int64_t bytes;
-};
 
 template <typename K>
 cudaError_t prepare(K kernel, int smem, int per_sm_most, int &ctas)

@@ -428,7 +428,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 issued++;
             }
             if constexpr (FP8) {
-                cp_wait_most(issued - x - 1);
+                if (issued > x + 1)  // the next tile's copies are in flight as well
+                    cp_wait<1>();
+                else
+                    cp_wait<0>();
                 __syncwarp();
                 if (convert_rows<D, 64>(tc::saddr(ring) + st * C::kTileBytes, 64 * sub, drafted ? w.rq.ctx - tile * kKeysTc : kKeysTc))
                     bad[item & 15] = item + 1;
