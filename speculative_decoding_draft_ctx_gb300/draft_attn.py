@@ -171,12 +171,13 @@ def _frequencies(rotary_dim, theta, scaling):
             _fail("scaling needs original_positions >= 1")
         if kind == "by_parts":
             fast, slow = float(s.pop("beta_fast", 32.0)), float(s.pop("beta_slow", 1.0))
-            if not fast > slow > 0.0:
-                _fail("by_parts scaling needs beta_fast > beta_slow > 0")
+            if not (fast > slow > 0.0 and math.isfinite(fast)):
+                _fail("by_parts scaling needs beta_fast > beta_slow > 0, both finite")
             amplitude = float(s.pop("amplitude", 0.1 * math.log(factor) + 1.0))
             lo, hi = (r * math.log(L / (t * 2.0 * math.pi)) / (2.0 * math.log(theta)) for t in (fast, slow))
             lo, hi = max(0, math.floor(lo)), min(r - 1, math.ceil(hi))
             share = 1.0 - np.minimum(np.maximum((i - lo) / max(hi - lo, 0.001), 0.0), 1.0)
+            share[i >= hi] = 0.0  # hi <= 0: no dim turns more than beta_slow times
         else:
             low, high = float(s.pop("low_freq_factor", 1.0)), float(s.pop("high_freq_factor", 4.0))
             if not high > low:

@@ -1,6 +1,7 @@
 """Refusals and host arithmetic of the draft-attention operators at the edges
 of what their documentation allows.  No test here launches a kernel."""
 
+import math
 import types
 
 import pytest
@@ -37,3 +38,27 @@ def test_a_stream_of_another_device_is_refused():
         draft_attn._elsewhere(here, types.SimpleNamespace(device=there, cuda_stream=FAKE))
     assert draft_attn._elsewhere(there, types.SimpleNamespace(device=there, cuda_stream=FAKE))
     assert draft_attn._elsewhere(here, FAKE)  # a handle says nothing about its device
+
+
+@pytest.mark.parametrize("r", [2, 6, 64, 128])
+@pytest.mark.parametrize("theta", [1.5, 1e4, 1e6])
+@pytest.mark.parametrize("L,fast,slow", [(4096, 32, 1), (64, 32, 16), (64, 32, 11), (6, 32, 1), (1, 32, 1), (1, 0.5, 0.1), (2 ** 20, 32, 1), (100, 8, 7.9)])
+def test_by_parts_keeps_and_divides_what_it_says(r, theta, L, fast, slow):
+    """Dims that turn at least beta_fast times in L keep their frequency, those that turn at most beta_slow times are
+    divided, the others lie between, falling."""
+    base, _ = dk.rope_frequencies(r, theta)
+    got, _ = dk.rope_frequencies(r, theta, dict(kind="by_parts", factor=8, original_positions=L, beta_fast=fast, beta_slow=slow))
+    shares = [(y / x - 1 / 8) / (1 - 1 / 8) for x, y in zip(base, got)]
+    for f, share in zip(base, shares):
+        turns = f * L / (2 * math.pi)
+        assert -1e-12 <= share <= 1 + 1e-12
+        if turns >= fast * (1 + 1e-9):
+            assert abs(share - 1) < 1e-12
+        if turns <= slow * (1 - 1e-9):
+            assert abs(share) < 1e-12
+    assert all(a >= b - 1e-12 for a, b in zip(shares, shares[1:]))
+
+
+def test_by_parts_refuses_betas_without_end():
+    with pytest.raises(dk.DSparkError, match="beta_fast"):
+        dk.rope_frequencies(64, 1e4, dict(kind="by_parts", factor=8, original_positions=64, beta_fast=math.inf))
