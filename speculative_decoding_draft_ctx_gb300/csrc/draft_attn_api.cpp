@@ -153,8 +153,8 @@ int dspark_rope_table(void *out, int64_t first_position, int64_t num_positions, 
     if (first_position < 0 || num_positions < 0 || first_position > most || num_positions > most - first_position)
         return fail(DSPARK_ERR_INVALID_ARG, "positions [%lld, +%lld) not in [0, 2^31)", (long long)first_position,
                     (long long)num_positions);
-    if (!std::isfinite(amplitude))
-        return fail(DSPARK_ERR_INVALID_ARG, "amplitude must be finite");
+    if (!std::isfinite((float)amplitude))
+        return fail(DSPARK_ERR_INVALID_ARG, "amplitude must be finite in fp32");
     if (!freqs)
         return fail(DSPARK_ERR_INVALID_ARG, "null freqs");
     RopeTableParams p;

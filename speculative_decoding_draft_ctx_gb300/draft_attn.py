@@ -224,7 +224,9 @@ def rope_table(num_positions, rotary_dim, theta=10000.0, scaling=None, first_pos
     precise as near ones."""
     _load()
     freqs, amplitude = _frequencies(rotary_dim, theta, scaling)
-    n, r = int(num_positions), int(rotary_dim)
+    n, r, first = int(num_positions), int(rotary_dim), int(first_position)
+    if not (0 <= first <= 1 << 31 and 0 <= n <= (1 << 31) - first):  # ctypes cuts longer numbers off without a word
+        _fail(f"num_positions {n} from {first}: positions in [0, 2^31) expected")
     if out is not None:
         if not isinstance(out, torch.Tensor) or out.dtype not in (torch.bfloat16, torch.float32):
             _fail("out must be a bf16 or fp32 tensor")
@@ -237,17 +239,15 @@ def rope_table(num_positions, rotary_dim, theta=10000.0, scaling=None, first_pos
         dtype = torch.bfloat16 if dtype is None else dtype
         if dtype not in (torch.bfloat16, torch.float32):
             _fail(f"dtype must be bf16 or fp32, got {dtype}")
-        if n < 0:
-            _fail(f"num_positions {n} < 0")
         device = torch.device("cuda" if device is None else device)
         if device.type == "cuda" and device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
     if _elsewhere(device, stream):
         with _on(device, stream):
-            return rope_table(n, r, theta, scaling, first_position, dtype, device, out)
+            return rope_table(n, r, theta, scaling, first, dtype, device, out)
     if out is None:
         out = torch.empty((n, r), dtype=dtype, device=device)
-    check(lib().dspark_rope_table(out.data_ptr(), int(first_position), n, r, freqs.__array_interface__["data"][0], amplitude,
+    check(lib().dspark_rope_table(out.data_ptr(), first, n, r, freqs.__array_interface__["data"][0], amplitude,
                                   int(dtype is torch.float32), _current(device)))
     return out
 
@@ -481,6 +481,8 @@ def evict_kv(kv_cache, block_table, context_lens, weights, token_positions, seq_
     budget, sinks, recent = int(budget), int(sinks), int(recent)
     if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
         _fail(f"budget {budget}, sinks {sinks}, recent {recent}: 0 <= sinks + recent <= budget, budget >= 1 expected")
+    # beyond any length and position; ctypes cuts numbers of more than 64 bits off without a word
+    budget, sinks, recent = min(budget, 1 << 62), min(sinks, 1 << 60), min(recent, 1 << 60)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return evict_kv(kv_cache, block_table, context_lens, weights, token_positions, seq_lens, budget, sinks, recent,

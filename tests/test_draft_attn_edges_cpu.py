@@ -9,7 +9,7 @@ import torch
 
 import speculative_decoding_draft_ctx_gb300 as dk
 from speculative_decoding_draft_ctx_gb300 import draft_attn
-from test_draft_attn_cpu import EVICT, EVICT_BASE, FAKE, L, status  # noqa: F401
+from test_draft_attn_cpu import EVICT, EVICT_BASE, FAKE, L, args, refuses, status, table_call  # noqa: F401
 
 # arrays of their own, 64 KB apart: every call below is refused before any CUDA call
 APART = {**EVICT_BASE, **{k: FAKE * (2 + i) for i, k in enumerate("ctx w pos wo po seen lens".split())}}
@@ -62,3 +62,28 @@ def test_by_parts_keeps_and_divides_what_it_says(r, theta, L, fast, slow):
 def test_by_parts_refuses_betas_without_end():
     with pytest.raises(dk.DSparkError, match="beta_fast"):
         dk.rope_frequencies(64, 1e4, dict(kind="by_parts", factor=8, original_positions=64, beta_fast=math.inf))
+
+
+# ------------------------------------------------------------------ numbers that the C types do not hold
+
+
+@pytest.mark.parametrize("kw", [dict(first_position=1 << 64), dict(first_position=(1 << 31) + 1), dict(first_position=-1), dict(num_positions=1 << 64),
+                                dict(num_positions=(1 << 31) - 9, first_position=10)])
+def test_table_refuses_positions_beyond_its_range(kw):
+    with pytest.raises(dk.DSparkError, match="2.31"):
+        dk.rope_table(**{**dict(num_positions=4, rotary_dim=16, device="cpu"), **kw})
+
+
+@pytest.mark.parametrize("amp", [1e39, -1e300])
+def test_table_refuses_an_amplitude_beyond_fp32(L, amp):  # noqa: F811
+    assert table_call(L, amp=amp) == "DSPARK_ERR_INVALID_ARG"
+
+
+@pytest.mark.parametrize("kw,match", [(dict(budget=1 << 64), "expected a CUDA device"), (dict(budget=(1 << 64) + 5, sinks=9), "expected a CUDA device"),
+                                      (dict(budget=5, sinks=1 << 64), "budget"), (dict(budget=1 << 64, recent=1 << 64), "expected a CUDA device"), (dict(budget=-1 << 64), "budget")])
+def test_evict_takes_budgets_beyond_64_bits_for_what_they_are(kw, match):
+    """A budget above every length: the call is refused for its CPU tensors alone; counts above the budget are not."""
+    a = args()
+    base = dict(kv_cache=a["kv_cache"], block_table=a["block_table"], context_lens=a["context_lens"], weights=torch.zeros((2, 2, 9)),
+                token_positions=torch.zeros((2, 2, 9), dtype=torch.int32), seq_lens=torch.zeros(2, dtype=torch.int32))
+    refuses(dk.evict_kv, **{**base, **kw}, match=match)
