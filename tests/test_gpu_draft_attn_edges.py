@@ -3,6 +3,7 @@ documentation allows, against the definitions in 64 bits (draft_attn_ref.py)."""
 
 import ctypes
 import math
+import os
 
 import pytest
 import torch
@@ -269,3 +270,29 @@ def test_every_launch_follows_the_switch_for_programmatic_overlap(kernel, monkey
     assert edges == 6 and overlapped == 6
     monkeypatch.setenv("DSPARK_PDL", "0")
     assert programmatic_edges(chain) == (6, 0)
+
+
+# ------------------------------------------------------------------ the kernel that the sizes choose
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_a_batch_of_requests_runs_on_the_tensor_core_kernel(fp8):
+    """56 query rows a KV head: without a pin the call has the bits of the tcgen05 kernel, and they are right; so are
+    the weights over them."""
+    p = Problem(41, (1500, 900, 200, 1300), (7, 7, 7, 7), 16, 2, 128, 16, fp8).cuda()
+    out, lse = run_attention(p, "causal", None)
+    want, z, to, tl = attention(p, "causal", None)
+    close(lse, z, tl)
+    close(out, want, to)
+    w = torch.zeros((4, 2, 1500), device="cuda")
+    dk.accumulate_attention_weight(p.d_q, p.d_cache, p.d_table, p.d_start, p.d_ctx, lse, w, k_scale=p.d_ks, error_flags=p.d_flags)
+    close(w, *weight(p, lse, torch.zeros((4, 2, 1500)), 1.0))
+    before = os.environ.get("DSPARK_TREE_ATTN_KERNEL")
+    os.environ["DSPARK_TREE_ATTN_KERNEL"] = "tc"
+    try:
+        again = run_attention(p, "causal", None)
+    finally:
+        os.environ.pop("DSPARK_TREE_ATTN_KERNEL")
+        if before is not None:
+            os.environ["DSPARK_TREE_ATTN_KERNEL"] = before
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and int(p.d_flags) == 0
