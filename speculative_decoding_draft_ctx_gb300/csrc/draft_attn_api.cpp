@@ -85,6 +85,21 @@ bool overlap_partly(const void *a, const void *b, int64_t n)
     return x != y && (x < y ? y - x : x - y) < (uint64_t)n * 4;
 }
 
+// f radians as a fraction of a turn in units of 2^-64, off by one at most:
+// whole turns do not matter (positions are whole).  The quotient by 2 pi (its
+// first 107 bits) is taken as a double and what that leaves over; a double
+// alone is off by 2^-56 of a turn for f near 1, 2^-22 radians at position 2^31.
+uint64_t fraction_of_a_turn(double f)
+{
+    constexpr double kTwoPi = 6.283185307179586232, kTwoPiRest = 2.4492935982947064e-16;
+    const double q = f / kTwoPi;
+    const double rest = (std::fma(-q, kTwoPi, f) - q * kTwoPiRest) / kTwoPi;
+    const double a = std::nearbyint(std::ldexp(q - std::floor(q), 64));       // in [0, 2^64]
+    const double b = std::nearbyint(std::ldexp(rest - std::nearbyint(rest), 64));  // in [-2^63, 2^63]
+    const uint64_t whole = a >= 18446744073709551616.0 ? 0u : (uint64_t)a;
+    return b >= 0.0 ? whole + (uint64_t)b : whole - (uint64_t)-b;
+}
+
 bool stride_ok(int64_t s) { return s >= -((int64_t)1 << 40) && s <= (int64_t)1 << 40; }
 
 // What the attention and the weight accumulation check alike.
@@ -161,12 +176,7 @@ int dspark_rope_table(void *out, int64_t first_position, int64_t num_positions, 
     for (int i = 0; i < rotary_dim / 2; i++) {
         if (!std::isfinite(freqs[i]))
             return fail(DSPARK_ERR_INVALID_ARG, "freqs[%d] is not finite", i);
-        // turns per position: whole turns do not matter (p is whole), the
-        // fraction in units of 2^-64
-        double turn = freqs[i] / 6.283185307179586476925;
-        turn -= std::floor(turn);
-        const double scaled = std::ldexp(turn, 64);
-        p.turns[i] = scaled >= 18446744073709551616.0 ? 0u : (uint64_t)scaled;
+        p.turns[i] = fraction_of_a_turn(freqs[i]);
     }
     if (num_positions == 0)
         return ok();

@@ -10,11 +10,12 @@
 // Table.  The angle p f of a far position in fp32 loses the turn it is in.
 // Here the frequency is a 64-bit fixed-point fraction F = f / 2 pi * 2^64 of a
 // turn, so p F mod 2^64 is the angle's fraction of a turn, exact but for F's
-// own rounding (p 2^-65 turns): the wrap of the integer product is the range
-// reduction.  The top bits give the nearest quarter turn, the signed rest
+// own rounding (p 2^-64 turns, 2^-30 radians at position 2^31): the wrap of
+// the integer product is the range reduction.  The top bits give the nearest quarter turn, the signed rest
 // x (|x| <= pi/4) goes to fp32 with a relative rounding and into the Taylor
-// series of sine (to x^9: the next term is below 2^-29 x) and cosine (to x^8:
-// below 2^-25).  A thread makes 4 neighbouring angles, so it stores 8 or 16
+// series of sine (to x^9: the next term is below 2^-28.7 x) and cosine (to
+// x^8: below 2^-25); with the roundings of fp32 an entry is off by 2^-22 at
+// most.  A thread makes 4 neighbouring angles, so it stores 8 or 16
 // bytes of cos and of sin, and stays with them from row to row: the next
 // angle is a 64-bit sum.  Bound: some 40 instructions per angle (131,072
 // positions of 64 entries: 8.9 us, the bytes' time 2.5).

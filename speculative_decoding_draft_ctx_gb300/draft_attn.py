@@ -220,8 +220,8 @@ def rope_table(num_positions, rotary_dim, theta=10000.0, scaling=None, first_pos
     ``rope_kv_insert`` read, for positions ``first_position`` onwards, made on
     the device: bf16 (the default; what the write and ``qknorm_rope_kv_insert``
     take) or fp32 (``rope_kv_insert`` takes both).  ``scaling``: see
-    ``rope_frequencies``.  Angles are reduced exactly: far positions are as
-    precise as near ones."""
+    ``rope_frequencies``.  Angles are reduced exactly, so a far position loses
+    only the frequency's own rounding (fp64) times the position."""
     _load()
     freqs, amplitude = _frequencies(rotary_dim, theta, scaling)
     n, r, first = int(num_positions), int(rotary_dim), int(first_position)

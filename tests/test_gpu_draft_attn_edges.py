@@ -10,7 +10,7 @@ import torch
 
 import speculative_decoding_draft_ctx_gb300 as dk
 from draft_attn_ref import Problem, attention, close, evict, gen, weight
-from test_gpu_draft_attn import kernel, run_attention  # noqa: F401
+from test_gpu_draft_attn import cos_sin, kernel, run_attention  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -296,3 +296,20 @@ def test_a_batch_of_requests_runs_on_the_tensor_core_kernel(fp8):
         if before is not None:
             os.environ["DSPARK_TREE_ATTN_KERNEL"] = before
     assert torch.equal(out, again[0]) and torch.equal(lse, again[1]) and int(p.d_flags) == 0
+
+
+# ------------------------------------------------------------------ the table
+
+
+@pytest.mark.parametrize("theta", [1.5, 1e4])
+def test_table_at_the_farthest_positions(theta):
+    """The fixed-point turns are off by 2^-64 of a turn (2^-63 with the last one's rounding), 2^-29 radians at 2^31.
+    In units of 2^-24: the reduced angle x by 2.47 x (two roundings, and 0.47 of the constant's), which moves an entry
+    by x sin x or x cos x of that, 1.37 at pi/4; the last rounding 0.5; of a cosine x^2's 0.25, the series' 0.2 and
+    the terms left out 0.42, of a sine 0.2 in all: 2.8."""
+    first, r = (1 << 31) - 24, 512
+    got = dk.rope_table(24, r, theta=theta, first_position=first, dtype=torch.float32).double().cpu()
+    f, _ = dk.rope_frequencies(r, theta)
+    want = torch.tensor([[cos_sin(first + p, x) for x in f] for p in range(24)], dtype=torch.float64)
+    off = (got.view(24, 2, r // 2) - want.transpose(1, 2)).abs()
+    assert off.max() <= 2.8 * 2.0 ** -24 + 2.0 ** -29, float(off.max()) * 2 ** 24
