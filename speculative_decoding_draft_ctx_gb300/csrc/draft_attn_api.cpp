@@ -102,6 +102,18 @@ uint64_t fraction_of_a_turn(double f)
 
 bool stride_ok(int64_t s) { return s >= -((int64_t)1 << 40) && s <= (int64_t)1 << 40; }
 
+// The sizes that the calls and their workspace queries refuse alike.
+bool attention_sizes_ok(int64_t rows, int heads, int nkv, int requests)
+{
+    return nkv >= 1 && nkv <= 65535 && heads >= 1 && heads % nkv == 0 && heads <= (1 << 20) && rows >= 0 &&
+           rows <= ((int64_t)INT32_MAX - 1024) / (heads / nkv) && requests >= 0 && requests <= (1 << 24);
+}
+bool evict_sizes_ok(int requests, int nkv, int64_t stride)
+{
+    return requests >= 0 && nkv >= 1 && (int64_t)requests * nkv <= ((int64_t)1 << 31) / 16 - 1 && stride >= 0 &&
+           stride <= (int64_t)INT32_MAX - 1024;
+}
+
 // What the attention and the weight accumulation check alike.
 int check_attention(AttnParams &p, const void *q, int64_t q_ts, int64_t q_hs, int64_t rows, int heads, int nkv,
                     int head_dim, const void *cache, int64_t num_blocks, int block_size, int kv_dtype,
@@ -276,8 +288,8 @@ int dspark_rope_kv_insert(const void *q, int64_t q_token_stride, int64_t q_head_
 int64_t dspark_tree_attention_workspace(int64_t num_rows, int num_heads, int num_kv_heads, int head_dim,
                                         int num_requests, int kv_dtype)
 {
-    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || num_kv_heads < 1 || num_heads < 1 ||
-        num_heads % num_kv_heads != 0 || num_rows < 0 || num_requests < 0 ||
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        !attention_sizes_ok(num_rows, num_heads, num_kv_heads, num_requests) ||
         (kv_dtype != DSPARK_KV_BF16 && kv_dtype != DSPARK_KV_FP8_E4M3)) {
         fail(DSPARK_ERR_INVALID_ARG, "tree attention workspace: invalid sizes");
         return -1;
@@ -370,7 +382,7 @@ int dspark_attention_weight_accumulate(const void *q, int64_t q_token_stride, in
 
 int64_t dspark_kv_evict_workspace(int num_requests, int num_kv_heads, int64_t stride, int64_t budget)
 {
-    if (num_requests < 0 || num_kv_heads < 1 || stride < 0 || budget < 1) {
+    if (!evict_sizes_ok(num_requests, num_kv_heads, stride) || budget < 1) {
         fail(DSPARK_ERR_INVALID_ARG, "evict workspace: invalid sizes");
         return -1;
     }
@@ -397,7 +409,7 @@ int dspark_kv_evict(void *kv_cache, int64_t num_blocks, int num_kv_heads, int bl
     if (budget < 1 || sinks < 0 || recent < 0 || sinks > budget || recent > budget - sinks)
         return fail(DSPARK_ERR_INVALID_ARG, "budget %lld, sinks %lld, recent %lld: 1 <= sinks + recent <= budget wanted",
                     (long long)budget, (long long)sinks, (long long)recent);
-    if ((int64_t)num_requests * num_kv_heads > ((int64_t)1 << 31) / 16 - 1)
+    if (!evict_sizes_ok(num_requests, num_kv_heads, stride))
         return fail(DSPARK_ERR_INVALID_ARG, "%d requests of %d heads: too many", num_requests, num_kv_heads);
     if (num_requests == 0)
         return ok();

@@ -394,9 +394,8 @@ def tree_attention(q, kv_cache, block_table, query_start, context_lens, tree_mas
     L = lib()
     # the partial results of requests that are split over CTAs: made anew by
     # each call, on its stream (or in the graph's own pool), so calls never share it
-    size = L.dspark_tree_attention_workspace(T, Hq, Hkv, D, B, kv_dtype)
-    if size < 0:
-        check(7)
+    # (a size below 0: the call refuses the same sizes, with its status)
+    size = max(0, L.dspark_tree_attention_workspace(T, Hq, Hkv, D, B, kv_dtype))
     work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     check(L.dspark_tree_attention(*head, ks, vs, *table, kind, tree_mask.data_ptr() if words else 0, words, scale,
                                   out.data_ptr(), lse.data_ptr(), work.data_ptr() if size else 0, size, flags,
@@ -490,9 +489,7 @@ def evict_kv(kv_cache, block_table, context_lens, weights, token_positions, seq_
     if new_lens is None:
         new_lens = torch.empty(B, dtype=torch.int32, device=dev)
     L = lib()
-    size = L.dspark_kv_evict_workspace(B, Hkv, shape[2], budget)
-    if size < 0:
-        check(1)
+    size = max(0, L.dspark_kv_evict_workspace(B, Hkv, shape[2], budget))
     work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     check(L.dspark_kv_evict(kv_cache.data_ptr(), num_blocks, Hkv, block_size, D, kv_dtype, block_table.data_ptr(), stride,
                             entries, context_lens.data_ptr(), B, weights.data_ptr(), token_positions.data_ptr(),

@@ -87,3 +87,14 @@ def test_evict_takes_budgets_beyond_64_bits_for_what_they_are(kw, match):
     base = dict(kv_cache=a["kv_cache"], block_table=a["block_table"], context_lens=a["context_lens"], weights=torch.zeros((2, 2, 9)),
                 token_positions=torch.zeros((2, 2, 9), dtype=torch.int32), seq_lens=torch.zeros(2, dtype=torch.int32))
     refuses(dk.evict_kv, **{**base, **kw}, match=match)
+
+
+def test_workspace_queries_refuse_the_sizes_that_the_calls_refuse(L):  # noqa: F811
+    big = 2 ** 31 - 1
+    for a in ((big, big, 100, 60), (1 << 27, 1, 100, 60), (1, 1, big, 60), (1, 1, 1 << 62, 1 << 61), (-1, 1, 9, 9), (1, 0, 9, 9), (1, 1, -1, 9)):
+        assert L.dspark_kv_evict_workspace(*a) == -1, a
+    assert L.dspark_kv_evict_workspace((1 << 27) - 1, 1, 1 << 30, 1 << 29) == ((1 << 27) - 1) * (1 + (1 << 30)) * 4
+    assert L.dspark_kv_evict_workspace(2, 3, 9, 1 << 62) == 24
+    for a in ((1 << 62, 8, 1, 128, 4, 0), (1 << 29, 8, 1, 128, 4, 0), (5, 1 << 21, 1, 128, 4, 0), (5, 1 << 17, 1 << 17, 128, 4, 0), (5, 8, 2, 128, 1 << 25, 0),
+              (-1, 8, 2, 128, 4, 0), (5, 8, 2, 128, -1, 0)):
+        assert L.dspark_tree_attention_workspace(*a) == -1, a
