@@ -21,7 +21,7 @@
 // are read as broadcasts.  Heads of more than kRows query rows take them in
 // groups, each a pass over the CTA's tiles that adds to what the one before
 // wrote (in order: a group's products wait for all sums of the one before).
-// Bound: the read of K (64 requests x 7 tokens x 8 heads: 94.6 us, 70 of it the
+// Bound: the read of K (64 requests x 7 tokens x 8 heads: 96 us, 70 of it the
 // bytes' time); over fp8 the conversion of the tiles (two contexts of 65k to
 // 131k tokens: 51 us against 17).
 #pragma once

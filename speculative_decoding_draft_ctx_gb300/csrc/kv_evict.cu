@@ -31,7 +31,7 @@
 // all SMs, nor do their registers allow 4 KB in flight per warp), and a warp
 // needs nothing but the two lists.  Bound: the weights' and positions' read
 // and write, and the rows that move (64 x 8 lists of 4,100 to 4,352 places cut to
-// 4,096: 40 us, the bytes' time 15; two 131k contexts halved: 84 against 42); on
+// 4,096: 45 us, the bytes' time 15; two 131k contexts halved: 85 against 42); on
 // small n the latency of the passes, some 3,500 cycles each.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>

@@ -18,7 +18,8 @@
 // most.  A thread makes 4 neighbouring angles, so it stores 8 or 16
 // bytes of cos and of sin, and stays with them from row to row: the next
 // angle is a 64-bit sum.  Bound: some 40 instructions per angle (131,072
-// positions of 64 entries: 8.9 us, the bytes' time 2.5).
+// positions of 64 entries: 9.1 us, the bytes' time 2.5; the instructions alone
+// would take half of that).
 //
 // Rotation.  A head row of D dims is held by D / 8 lanes, 8 dims (16 bytes)
 // each, so a warp takes 256 / D rows at once.  Half layout: the partner of

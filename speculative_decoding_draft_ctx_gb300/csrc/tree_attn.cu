@@ -19,12 +19,15 @@ namespace {
 // has more than kTcRows query rows per KV head and the block table has room
 // for more than one tile of 128 keys per two SMs (lengths are on the device:
 // the room is what the host knows).  Measured, D 128, mma.sync against it, us:
-//   rows 32, 8 requests x 8 heads over 4,000 tokens   36 / 40, fp8 31 / 46
-//   rows 56, 16 x 8 over 8,000                        135 / 103, fp8 141 / 132
-//   rows 504, 1 x 4 over 16,000                       71 / 39, fp8 74 / 43
-//   rows 56, 1 x 8 over 500 (32 tiles)                11.7 / 12.9
-//   rows 56, 1 x 8 over 2,000 (128 tiles)             18.2 / 17.6
-//   rows 504, 1 x 4 over 2,000 (68 tiles)             23.6 / 25.3
+//   rows 32, 8 requests x 8 heads over 4,000 tokens   37 / 39, fp8 32 / 45
+//   rows 56, 16 x 8 over 8,000                        135 / 102, fp8 142 / 129
+//   rows 504, 1 x 4 over 16,000                       70 / 39, fp8 74 / 44
+//   rows 56, 1 x 8 over 500 (32 tiles)                11.9 / 12.6, fp8 13.0 / 14.5
+//   rows 56, 1 x 8 over 2,000 (128 tiles)             18.2 / 18.3, fp8 18.7 / 19.5
+//   rows 504, 1 x 4 over 2,000 (68 tiles)             23.7 / 29.6, fp8 24.6 / 28.9
+//   rows 56, 64 x 8 over 1,024 to 8,192               233 / 194, fp8 246 / 246
+//   the same at D 64                                  166 / 160, fp8 155 / 233
+// The last figure is the rule's one loss among these: head dim 64 over fp8.
 // DSPARK_TREE_ATTN_KERNEL=mma or =tc pins one (tc: for the head dims it has)
 // for the calls made while it is set; the tests run both.
 constexpr int64_t kTcRows = 32;

@@ -6,7 +6,7 @@
 // 512 r flops: the card's rates balance at r = 283, but mma.sync, whose
 // operands pass through registers, is bound by issue from r = 56 on (64
 // requests x 7 tokens x 8 heads: 234 us, this kernel 193, memory time 136; two
-// trees of 64 over 131k tokens: 848 us, this kernel 255, its products' time 132).
+// trees of 64 over 131k tokens: 848 us, this kernel 248, its products' time 132).
 //
 // One CTA per SM, an item is up to 256 rows of a (request, KV head), a tile
 // 128 keys.  Two streams of softmax (a warpgroup each, a thread per query

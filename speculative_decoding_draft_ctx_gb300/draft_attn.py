@@ -348,7 +348,9 @@ def tree_attention(q, kv_cache, block_table, query_start, context_lens, tree_mas
                    k_scale=None, v_scale=None, out=None, lse=None, error_flags=None, stream=None):
     """The drafted tokens' attention over the paged cache; returns ``(out,
     lse)``: bf16 ``[T, num_heads, D]`` and fp32 ``[T, num_heads]`` (natural
-    log; -inf, and zeros in ``out``, where a row sees nothing).
+    log; -inf, and zeros in ``out``, where a row sees nothing).  Scores and sums
+    are fp32; the softmax weights enter the product with V as bf16 (as fp16 over
+    an fp8 cache), so ``out`` is off by two bf16 roundings rather than one.
 
     ``q``: bf16 ``[T, num_heads, D]``, any token and head strides that are
     multiples of 8 elements; rows ``[query_start[b], query_start[b + 1])``
