@@ -112,8 +112,10 @@ int dspark_rope_kv_insert(const void *q, int64_t q_token_stride, int64_t q_head_
  * with KV head h / (num_heads / num_kv_heads).  Scores, statistics and sums are
  * fp32.  For the product with V the weights are rounded to 16 bits: to bf16
  * over a bf16 cache (each by at most 2^-8 of itself), to fp16 over an fp8 cache
- * (2^-11 down to 2^-28 of the row's largest weight, 2^-39 of the largest below;
- * the queries to fp16 too, by at most 2^-24 of their row's largest element).
+ * (2^-11 down to 2^-28 of the row's largest weight, 2^-39 of the largest below,
+ * where scores stay below 2^19, beyond which fp32 tells them apart by 1/16 at
+ * best; the queries to fp16 too, by at most 2^-24 of their row's largest
+ * element).
  * out is rounded to bf16 once.  A row that sees nothing gives zeros and -inf.  Tokens that a row does not see do not reach its result,
  * whatever their K and V hold (NaN and infinities included).
  *

@@ -112,6 +112,33 @@ def test_attention_scores_that_underflow(scale, q, fp8, kernel):  # noqa: F811
     close(out, want, to)
 
 
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_scores_of_any_size_over_fp8(sign, kernel):  # noqa: F811
+    """Scores from 2^9 to 2^33 that grow by 0 to 15 from token to token, around the size from which the weights are
+    not lifted: fp32 scores that large decide little, but every result stays among the values it is a mean of."""
+    n, nq, G, Hkv, D = 3000, 7, 8, 4, 128
+    p = Problem(43, (n,), (nq,), G * Hkv, Hkv, D, 16, True)
+    p.k_scale, p.v_scale = torch.ones(1), torch.ones(1)
+    g = gen(43)
+    k, v = torch.zeros((n + nq, Hkv, D)), torch.randint(8, 17, (n + nq, Hkv, D), generator=g) / 8.0
+    k[..., 0], k[..., 1] = 8.0, torch.randint(0, 16, (n + nq, Hkv), generator=g).float()
+    p.write(0, torch.arange(n + nq), k, v)
+    q = torch.zeros((nq, G * Hkv, D))
+    q[..., 1] = 1.0
+    size = 2.0 ** (6 + torch.arange(nq * G * Hkv).view(nq, -1) % 24)
+    q[..., 0] = sign * size
+    p.qkv = q.to(torch.bfloat16)
+    p.cuda()
+    out, lse = run_attention(p, "dense", None, scale=1.0)
+    assert ((out >= 1) & (out <= 2)).all()
+    # the largest score, at least, and all tokens at it, at most; a score's own roundings: 3 of 2^-24, 3 more of lse
+    top = sign * 8.0 * size.double()
+    slack = 6 * 2.0 ** -24 * (top.abs() + 16) + 1e-4
+    z = lse.double().cpu()
+    assert (z >= top - slack).all() and (z <= top + 15 + math.log(n + nq) + slack).all()
+    assert int(p.d_flags) == 0
+
+
 # ------------------------------------------------------------------ streams
 
 
