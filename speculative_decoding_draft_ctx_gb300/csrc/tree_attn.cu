@@ -27,7 +27,10 @@ namespace {
 //   rows 504, 1 x 4 over 2,000 (68 tiles)             23.7 / 29.6, fp8 24.6 / 28.9
 //   rows 56, 64 x 8 over 1,024 to 8,192               233 / 194, fp8 246 / 246
 //   the same at D 64                                  166 / 160, fp8 155 / 233
-// The last figure is the rule's one loss among these: head dim 64 over fp8.
+// The last figure is the rule's one loss among these: head dim 64 over fp8.  It
+// also loses where the mean says little: 63 single tokens over 2,000 and a tree
+// of 64 over 131,072 (group 8) run in items of 16 rows, 2,485 / 438, fp8 2,123
+// / 473; rows of the largest request would have to come from the caller.
 // DSPARK_TREE_ATTN_KERNEL=mma or =tc pins one (tc: for the head dims it has)
 // for the calls made while it is set; the tests run both.
 constexpr int64_t kTcRows = 32;
