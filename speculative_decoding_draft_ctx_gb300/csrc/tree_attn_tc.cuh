@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
             // Not 0, or a masked score's -inf would become NaN: 1 where the queries
             // are zeroed, else the least number where the product underflows (a
             // tiny scale times the power of two of a tiny query over fp8).
-            c = base_scale == 0.0f ? 1.0f : fmaxf(fabsf(c), 1.4e-45f);
+            c = c == 0.0f ? (base_scale == 0.0f ? 1.0f : 1.4e-45f) : fabsf(c);
             const uint64_t c2 = pr(c, c);
             float m = -INFINITY, l = 0.0f;  // what the row subtracts (scaled, base 2), the sum of weights
 

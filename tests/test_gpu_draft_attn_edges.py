@@ -139,6 +139,14 @@ def test_attention_scores_of_any_size_over_fp8(sign, kernel):  # noqa: F811
     assert int(p.d_flags) == 0
 
 
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+def test_attention_a_scale_that_is_not_a_number_shows(which, kernel):  # noqa: F811
+    p = Problem(47, (70, 300), (3, 40), 8, 2, 128, 16, True).cuda()
+    (p.d_ks if which == "k_scale" else p.d_vs).fill_(math.nan)
+    out, lse = run_attention(p, "causal", None)
+    assert out.isnan().all() and (which == "v_scale" or lse.isnan().all())
+
+
 # ------------------------------------------------------------------ streams
 
 
