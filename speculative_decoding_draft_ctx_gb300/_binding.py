@@ -32,6 +32,9 @@ FLAG_TIMEOUT = 0x4
 FLAG_COUNTER = 0x8
 FLAG_BLOCK_RANGE = 0x10
 FLAG_LENGTH = 0x20
+FLAG_PAGES = 0x40
+FLAG_ROW = 0x80
+FLAG_REFS = 0x100
 
 # every function the header declares
 EXPORTS = (
@@ -45,7 +48,9 @@ EXPORTS = (
     "dspark_ctx_kv_write_general", "dspark_ctx_kv_general_supported", "dspark_ctx_kv_validate_layers_general",
     "dspark_ctx_kv_write_sched", "dspark_ctx_kv_write_noalloc", "dspark_rope_table", "dspark_rope_kv_insert",
     "dspark_tree_attention", "dspark_tree_attention_workspace", "dspark_attention_weight_accumulate",
-    "dspark_kv_evict", "dspark_kv_evict_workspace",
+    "dspark_kv_evict", "dspark_kv_evict_workspace", "dspark_verify_drafts", "dspark_kv_compact", "dspark_kv_fork",
+    "dspark_kv_fork_workspace", "dspark_kv_resize", "dspark_kv_resize_workspace", "dspark_kv_insert_scaled",
+    "dspark_tree_attention_scaled", "dspark_tree_attention_scaled_workspace",
 )
 
 
@@ -155,6 +160,23 @@ def lib() -> ctypes.CDLL:
                   "dspark_attention_weight_accumulate", "dspark_kv_evict"):
             getattr(L, n).restype = I
         for n in ("dspark_tree_attention_workspace", "dspark_kv_evict_workspace"):
+            getattr(L, n).restype = I64
+        # include/dspark_draft_step.h
+        layers = [P, P, I, I64, I, I, I, I]
+        L.dspark_verify_drafts.argtypes = [P, I, I64, P, I, I64, I64, I64, P, P, P, P, I, I, I, P, P, P, P, P]
+        L.dspark_kv_compact.argtypes = layers + [P, I64, I64, P, I, P, I64, I, P, I, P, P, P]
+        L.dspark_kv_fork.argtypes = layers + [P, I64, I64, P, P, I, P, P, I, P, P, I64, P, P]
+        L.dspark_kv_fork_workspace.argtypes = [I]
+        L.dspark_kv_resize.argtypes = [P, I64, I64, P, P, I, P, I64, I, P, I64, P, P]
+        L.dspark_kv_resize_workspace.argtypes = [I]
+        L.dspark_kv_insert_scaled.argtypes = [P, I64, I64, P, I64, I64, I64, P, P, I64, I, I, I] + table + [P, P]
+        L.dspark_tree_attention_scaled.argtypes = [P, I64, I64, I64, I, I, I, P, P, I64, I] + table + [I, P, I, F, P, P, P,
+                                                                                                    I64, P, P]
+        L.dspark_tree_attention_scaled_workspace.argtypes = [I64, I, I, I, I]
+        for n in ("dspark_verify_drafts", "dspark_kv_compact", "dspark_kv_fork", "dspark_kv_resize",
+                  "dspark_kv_insert_scaled", "dspark_tree_attention_scaled"):
+            getattr(L, n).restype = I
+        for n in ("dspark_kv_fork_workspace", "dspark_kv_resize_workspace", "dspark_tree_attention_scaled_workspace"):
             getattr(L, n).restype = I64
         _lib = L
         return L

@@ -31,17 +31,22 @@ NOALLOC_SRC = os.path.join(CSRC, "ctx_kv_noalloc.cu")
 ROPE_SRC = os.path.join(CSRC, "rope.cu")
 EVICT_SRC = os.path.join(CSRC, "kv_evict.cu")
 ATTN_SRCS = tuple(os.path.join(CSRC, f) for f in ("tree_attn.cu", "attn_weight.cu", "tree_attn_d64.cu", "tree_attn_d128.cu", "tree_attn_d256.cu",
-                                                     "tree_attn_tc_d64.cu", "tree_attn_tc_d128.cu"))
+                                                     "tree_attn_tc_d64.cu", "tree_attn_tc_d128.cu", "tree_attn_scaled_d64.cu",
+                                                     "tree_attn_scaled_d128.cu", "tree_attn_scaled_d256.cu"))
+STEP_SRCS = tuple(os.path.join(CSRC, f) for f in ("verify.cu", "kv_pages.cu", "kv_insert_scaled.cu"))
 CU_SRCS = (KERNEL_SRC, TMA_SRC, QK_SRC, PROJ_SRC, NORM_SRC, GENERAL_SRC, WARP_SRC, NOALLOC_SRC, ROPE_SRC, EVICT_SRC,
-           *ATTN_SRCS)
+           *ATTN_SRCS, *STEP_SRCS)
 API_SRC = os.path.join(CSRC, "ctx_kv_api.cpp")
 DRAFT_API_SRC = os.path.join(CSRC, "draft_attn_api.cpp")
-API_SRCS = (API_SRC, DRAFT_API_SRC)
+STEP_API_SRC = os.path.join(CSRC, "draft_step_api.cpp")
+API_SRCS = (API_SRC, DRAFT_API_SRC, STEP_API_SRC)
 HEADERS = [os.path.join(CSRC, "ctx_kv_internal.h"), os.path.join(CSRC, "ctx_kv_device.cuh"),
            os.path.join(CSRC, "ctx_kv_pipe.cuh"), os.path.join(CSRC, "draft_attn_internal.h"),
            os.path.join(CSRC, "tree_attn_mma.cuh"), os.path.join(CSRC, "tree_attn_tc.cuh"),
            os.path.join(CSRC, "tc_ptx.cuh"), os.path.join(CSRC, "attn_weight.cuh"),
-           os.path.join(INCLUDE, "dspark_ctx_kv.h"), os.path.join(INCLUDE, "dspark_draft_attn.h")]
+           os.path.join(CSRC, "draft_api_checks.h"), os.path.join(CSRC, "draft_step_internal.h"),
+           os.path.join(CSRC, "page_scale.cuh"), os.path.join(INCLUDE, "dspark_ctx_kv.h"),
+           os.path.join(INCLUDE, "dspark_draft_attn.h"), os.path.join(INCLUDE, "dspark_draft_step.h")]
 
 _lock = threading.Lock()
 

@@ -2,12 +2,13 @@
 // argument checks and launches.
 #include "../../include/dspark_draft_attn.h"
 
+#include "../../include/dspark_draft_step.h"
+
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 
 #include "ctx_kv_internal.h"
+#include "draft_api_checks.h"
 #include "draft_attn_internal.h"
 
 namespace {
@@ -15,75 +16,6 @@ namespace {
 using namespace dspark;
 
 constexpr uint64_t kWaitNs = 4000000000;  // of a wait inside a kernel, which takes microseconds
-
-int fail(int status, const char *fmt, ...)
-{
-    char text[384];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(text, sizeof text, fmt, ap);
-    va_end(ap);
-    return api_fail(status, text);
-}
-
-int ok() { return api_fail(DSPARK_OK, ""); }
-
-int launched(cudaError_t e, const char *what)
-{
-    return e == cudaSuccess ? ok() : fail(DSPARK_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-}
-
-bool aligned(const void *p, uintptr_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
-
-// The cache of every operator here; `rows` receives num_blocks * nkv * block_size.
-int check_cache(const void *cache, int64_t num_blocks, int nkv, int block_size, int head_dim, int kv_dtype)
-{
-    if (head_dim != 64 && head_dim != 128 && head_dim != 256)
-        return fail(DSPARK_ERR_INVALID_ARG, "head_dim %d not in {64, 128, 256}", head_dim);
-    if (nkv < 1 || nkv > 65535)
-        return fail(DSPARK_ERR_INVALID_ARG, "num_kv_heads %d not in [1, 65535]", nkv);
-    if (block_size < 1)
-        return fail(DSPARK_ERR_BLOCK_SIZE, "block size %d must be >= 1", block_size);
-    if (kv_dtype != DSPARK_KV_BF16 && kv_dtype != DSPARK_KV_FP8_E4M3)
-        return fail(DSPARK_ERR_DTYPE, "kv dtype %d unknown", kv_dtype);
-    if (num_blocks < 1 || num_blocks > ((INT64_MAX / nkv) / block_size) / (4 * head_dim))
-        return fail(DSPARK_ERR_INVALID_ARG, "cache of %lld blocks invalid", (long long)num_blocks);
-    if (num_blocks * nkv * block_size >= (int64_t)UINT32_MAX)  // more rows than 32 bits number: beyond any device's memory
-        return fail(DSPARK_ERR_INVALID_ARG, "cache of %lld blocks invalid", (long long)num_blocks);
-    if (!cache)
-        return fail(DSPARK_ERR_INVALID_ARG, "null kv_cache");
-    if (!aligned(cache, 16))
-        return fail(DSPARK_ERR_ALIGNMENT, "kv_cache must be 16-byte aligned");
-    return DSPARK_OK;
-}
-
-// Places of a request: block table columns that lengths may reach (lengths
-// are 32 bits; a tile past the last one must not overflow them).
-int64_t usable_blocks(int64_t table_blocks, int block_size)
-{
-    return std::min<int64_t>(table_blocks, ((int64_t)INT32_MAX - 1024) / block_size);
-}
-
-int check_table(const int32_t *table, int64_t stride, int64_t blocks, int requests, const int32_t *lens)
-{
-    if (requests < 0 || requests > (1 << 24))
-        return fail(DSPARK_ERR_INVALID_ARG, "num_requests %d not in [0, 2^24]", requests);
-    if (blocks < 1 || stride < blocks || stride > (int64_t)1 << 40)
-        return fail(DSPARK_ERR_INVALID_ARG, "block table of %lld entries a row, stride %lld", (long long)blocks,
-                    (long long)stride);
-    if (requests > 0 && (!table || !lens))
-        return fail(DSPARK_ERR_INVALID_ARG, "null block_table or context_lens");
-    if (!aligned(table, 4) || !aligned(lens, 4))
-        return fail(DSPARK_ERR_ALIGNMENT, "block_table and context_lens must be 4-byte aligned");
-    return DSPARK_OK;
-}
-
-// Two arrays of n 4-byte entries that share some memory without being the same.
-bool overlap_partly(const void *a, const void *b, int64_t n)
-{
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x != y && (x < y ? y - x : x - y) < (uint64_t)n * 4;
-}
 
 // f radians as a fraction of a turn in units of 2^-64, off by one at most:
 // whole turns do not matter (positions are whole).  The quotient by 2 pi (its
@@ -99,8 +31,6 @@ uint64_t fraction_of_a_turn(double f)
     const uint64_t whole = a >= 18446744073709551616.0 ? 0u : (uint64_t)a;
     return b >= 0.0 ? whole + (uint64_t)b : whole - (uint64_t)-b;
 }
-
-bool stride_ok(int64_t s) { return s >= -((int64_t)1 << 40) && s <= (int64_t)1 << 40; }
 
 // The sizes that the calls and their workspace queries refuse alike.
 bool attention_sizes_ok(int64_t rows, int heads, int nkv, int requests)
@@ -164,6 +94,29 @@ int check_attention(AttnParams &p, const void *q, int64_t q_ts, int64_t q_hs, in
     const uint64_t hold = test_hold_ns();
     p.test_hold = hold != 0;
     p.wait_ns = hold ? hold : kWaitNs;
+    return DSPARK_OK;
+}
+
+// The mask, outputs and workspace of an attention call go into p.
+int check_mask_and_outputs(AttnParams &p, int mask_kind, const uint64_t *tree_mask, int mask_words, void *out, float *lse,
+                           void *workspace)
+{
+    if (mask_kind != DSPARK_MASK_DENSE && mask_kind != DSPARK_MASK_CAUSAL && mask_kind != DSPARK_MASK_TREE)
+        return fail(DSPARK_ERR_INVALID_ARG, "mask kind %d unknown", mask_kind);
+    if (mask_kind == DSPARK_MASK_TREE && (mask_words < 1 || mask_words > (1 << 16)))
+        return fail(DSPARK_ERR_INVALID_ARG, "mask_words %d not in [1, 65536]", mask_words);
+    if (p.num_rows == 0 || p.num_requests == 0)
+        return DSPARK_OK;
+    if (!out || !lse || (mask_kind == DSPARK_MASK_TREE && !tree_mask))
+        return fail(DSPARK_ERR_INVALID_ARG, "null out, lse or tree_mask");
+    if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(tree_mask, 8) || !aligned(workspace, 16))
+        return fail(DSPARK_ERR_ALIGNMENT, "out and workspace must be 16-byte, tree_mask 8-byte, lse 4-byte aligned");
+    p.mask_kind = mask_kind;
+    p.tree_mask = tree_mask;
+    p.mask_words = mask_words;
+    p.out = static_cast<uint16_t *>(out);
+    p.lse = lse;
+    p.parts = static_cast<float *>(workspace);
     return DSPARK_OK;
 }
 
@@ -321,16 +274,11 @@ int dspark_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
                                    error_flags);
     if (st != DSPARK_OK)
         return st;
-    if (mask_kind != DSPARK_MASK_DENSE && mask_kind != DSPARK_MASK_CAUSAL && mask_kind != DSPARK_MASK_TREE)
-        return fail(DSPARK_ERR_INVALID_ARG, "mask kind %d unknown", mask_kind);
-    if (mask_kind == DSPARK_MASK_TREE && (mask_words < 1 || mask_words > (1 << 16)))
-        return fail(DSPARK_ERR_INVALID_ARG, "mask_words %d not in [1, 65536]", mask_words);
+    const int bad = check_mask_and_outputs(p, mask_kind, tree_mask, mask_words, out, lse, workspace);
+    if (bad != DSPARK_OK)
+        return bad;
     if (num_rows == 0 || num_requests == 0)
         return ok();
-    if (!out || !lse || (mask_kind == DSPARK_MASK_TREE && !tree_mask))
-        return fail(DSPARK_ERR_INVALID_ARG, "null out, lse or tree_mask");
-    if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(tree_mask, 8) || !aligned(workspace, 16))
-        return fail(DSPARK_ERR_ALIGNMENT, "out and workspace must be 16-byte, tree_mask 8-byte, lse 4-byte aligned");
     const bool fp8 = kv_dtype == DSPARK_KV_FP8_E4M3;
     cudaError_t e = cudaSuccess;
     const int64_t need = tree_attention_workspace(num_rows, num_heads, num_kv_heads, head_dim, num_requests, fp8, e);
@@ -339,13 +287,58 @@ int dspark_tree_attention(const void *q, int64_t q_token_stride, int64_t q_head_
     if (workspace_bytes < need || (need > 0 && !workspace))
         return fail(DSPARK_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,
                     (long long)need);
-    p.mask_kind = mask_kind;
-    p.tree_mask = tree_mask;
-    p.mask_words = mask_words;
-    p.out = static_cast<uint16_t *>(out);
-    p.lse = lse;
-    p.parts = static_cast<float *>(workspace);
     return launched(launch_tree_attention(p, head_dim, fp8, stream), "tree attention");
+}
+
+int64_t dspark_tree_attention_scaled_workspace(int64_t num_rows, int num_heads, int num_kv_heads, int head_dim,
+                                               int num_requests)
+{
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        !attention_sizes_ok(num_rows, num_heads, num_kv_heads, num_requests)) {
+        fail(DSPARK_ERR_INVALID_ARG, "scaled tree attention workspace: invalid sizes");
+        return -1;
+    }
+    if (num_rows == 0 || num_requests == 0)
+        return 0;
+    cudaError_t e = cudaSuccess;
+    const int64_t n = tree_attention_scaled_workspace(num_rows, num_heads, num_kv_heads, head_dim, num_requests, e);
+    if (e != cudaSuccess) {
+        launched(e, "scaled tree attention workspace");
+        return -1;
+    }
+    return n;
+}
+
+int dspark_tree_attention_scaled(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t num_rows,
+                                 int num_heads, int num_kv_heads, int head_dim, const void *kv_cache,
+                                 const int8_t *block_scales, int64_t num_blocks, int block_size,
+                                 const int32_t *block_table, int64_t table_stride, int64_t table_blocks,
+                                 const int32_t *query_start, const int32_t *context_lens, int num_requests,
+                                 int mask_kind, const uint64_t *tree_mask, int mask_words, float scale, void *out,
+                                 float *lse, void *workspace, int64_t workspace_bytes, unsigned int *error_flags,
+                                 cudaStream_t stream)
+{
+    AttnParams p;
+    int st = check_attention(p, q, q_token_stride, q_head_stride, num_rows, num_heads, num_kv_heads, head_dim, kv_cache,
+                             num_blocks, block_size, DSPARK_KV_FP8_E4M3, nullptr, nullptr, block_table, table_stride,
+                             table_blocks, query_start, context_lens, num_requests, scale, error_flags);
+    if (st != DSPARK_OK || (st = check_mask_and_outputs(p, mask_kind, tree_mask, mask_words, out, lse, workspace)) != DSPARK_OK)
+        return st;
+    if (num_rows == 0 || num_requests == 0)
+        return ok();
+    if (!block_scales)
+        return fail(DSPARK_ERR_INVALID_ARG, "null block_scales");
+    if (!aligned(block_scales, 2))
+        return fail(DSPARK_ERR_ALIGNMENT, "block_scales must be 2-byte aligned");
+    cudaError_t e = cudaSuccess;
+    const int64_t need = tree_attention_scaled_workspace(num_rows, num_heads, num_kv_heads, head_dim, num_requests, e);
+    if (e != cudaSuccess)
+        return launched(e, "scaled tree attention");
+    if (workspace_bytes < need || (need > 0 && !workspace))
+        return fail(DSPARK_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes,
+                    (long long)need);
+    p.block_scales = block_scales;
+    return launched(launch_tree_attention_scaled(p, head_dim, stream), "scaled tree attention");
 }
 
 int dspark_attention_weight_accumulate(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t num_rows,

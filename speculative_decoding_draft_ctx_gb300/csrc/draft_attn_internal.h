@@ -11,6 +11,8 @@ namespace dspark {
 constexpr unsigned kFlagBlockRange = 0x10u;
 constexpr unsigned kFlagLength = 0x20u;
 
+constexpr int kScaleMin = -32, kScaleMax = 31;  // exponents of page-scaled caches
+
 // ---------------------------------------------------------------- rope.cu
 
 constexpr int kMaxRotary = 512;
@@ -52,6 +54,7 @@ struct AttnParams {
     int64_t num_rows;
     const unsigned char *cache;
     const float *k_scale, *v_scale;
+    const int8_t *block_scales;  // page-scaled caches: exponents [num_blocks, nkv, 2]; null otherwise
     const int32_t *table;
     int64_t table_stride, table_blocks;
     const int32_t *query_start, *context_lens;
@@ -78,6 +81,9 @@ struct AttnParams {
 int64_t tree_attention_workspace(int64_t rows, int num_heads, int num_kv_heads, int head_dim, int requests, bool fp8,
                                  cudaError_t &e);
 cudaError_t launch_tree_attention(const AttnParams &p, int head_dim, bool fp8, cudaStream_t stream);
+// the same over a page-scaled cache (p.block_scales); the workspace covers both
+int64_t tree_attention_scaled_workspace(int64_t rows, int num_heads, int num_kv_heads, int head_dim, int requests, cudaError_t &e);
+cudaError_t launch_tree_attention_scaled(const AttnParams &p, int head_dim, cudaStream_t stream);
 cudaError_t launch_attention_weight(const AttnParams &p, int head_dim, bool fp8, cudaStream_t stream);
 
 // ---------------------------------------------------------------- kv_evict.cu

@@ -9,6 +9,9 @@ namespace attn {
 DSPARK_ATTN_DECLARE(64)
 DSPARK_ATTN_DECLARE(128)
 DSPARK_ATTN_DECLARE(256)
+DSPARK_ATTN_SCALED_DECLARE(64)
+DSPARK_ATTN_SCALED_DECLARE(128)
+DSPARK_ATTN_SCALED_DECLARE(256)
 DSPARK_ATTN_TC_DECLARE(64)
 DSPARK_ATTN_TC_DECLARE(128)
 }  // namespace attn
@@ -94,6 +97,26 @@ cudaError_t launch_tree_attention(const AttnParams &p, int head_dim, bool fp8, c
     case 64: return attn::attention_d<64>(p, wr, fp8, stream);
     case 128: return attn::attention_d<128>(p, wr, fp8, stream);
     default: return attn::attention_d<256>(p, wr, fp8, stream);
+    }
+}
+
+int64_t tree_attention_scaled_workspace(int64_t rows, int num_heads, int num_kv_heads, int head_dim, int requests, cudaError_t &e)
+{
+    const int wr = attn::row_warps(rows, num_heads / num_kv_heads, requests);
+    switch (head_dim) {
+    case 64: return attn::workspace_scaled_d<64>(wr, e);
+    case 128: return attn::workspace_scaled_d<128>(wr, e);
+    default: return attn::workspace_scaled_d<256>(wr, e);
+    }
+}
+
+cudaError_t launch_tree_attention_scaled(const AttnParams &p, int head_dim, cudaStream_t stream)
+{
+    const int wr = attn::row_warps(p.num_rows, p.group, p.num_requests);
+    switch (head_dim) {
+    case 64: return attn::attention_scaled_d<64>(p, wr, stream);
+    case 128: return attn::attention_scaled_d<128>(p, wr, stream);
+    default: return attn::attention_scaled_d<256>(p, wr, stream);
     }
 }
 

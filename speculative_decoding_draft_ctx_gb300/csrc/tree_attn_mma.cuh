@@ -53,6 +53,15 @@
 // 2 before its (then exact, but for what lies 2^-24 below the row's largest)
 // conversion to fp16, and the scores by its inverse.
 //
+// Page-scaled fp8 (SCALED).  A page and head has one power of two for K and one
+// for V, 2^ek and 2^ev.  The products take the codes as above; a score is
+// multiplied by its key's 2^ek, and the weight that the second product takes is
+// 2^(s + ev - m), with m of the running maximum of s + ev: the same rounding as
+// above, relative to the largest contribution.  The sum of weights takes 2^-ev of
+// it back, exactly but for fp32's own rounding (|ev| <= 32).  A key's three numbers
+// (2^ek, ev, 2^-ev) are read beside its page's number one tile before they are
+// stored, so that no load is waited for.
+//
 // What a row does not see.  Scores of masked keys are replaced by -inf
 // whatever they are; V rows of drafted tokens that hold infinities or NaN are
 // zeroed in the tile, and the results of the rows that do see them are set
@@ -368,6 +377,8 @@ struct Loader {
     int64_t phys;
     int off;
     bool live;
+    uint32_t exponents;  // page-scaled: of the row that was loaded last, not stored yet, and where they belong
+    float4 *scales_at = nullptr;
 
     __device__ __forceinline__ void fetch(const AttnParams &p, int b, int tile, int len)
     {
@@ -379,6 +390,25 @@ struct Loader {
             const int blk = block_of(p, j);
             off = j - blk * p.block_size;
             phys = __ldg(p.table + b * p.table_stride + blk);
+        }
+    }
+
+    // page-scaled: the numbers of the rows loaded last go to their stage, those of
+    // the rows that `load` has just copied are fetched for the next call
+    __device__ __forceinline__ void store_scales()
+    {
+        if (scales_at) {
+            const int ek = min(max((int)(int8_t)(exponents & 0xffu), kScaleMin), kScaleMax);
+            const int ev = min(max((int)(int8_t)(exponents >> 8), kScaleMin), kScaleMax);
+            *scales_at = make_float4(__int_as_float((127 + ek) << 23), (float)ev, __int_as_float((127 - ev) << 23), 0.0f);
+            scales_at = nullptr;
+        }
+    }
+    __device__ __forceinline__ void fetch_scales(const AttnParams &p, int h, float4 *stage)
+    {
+        if ((threadIdx.x & 31) < 16) {
+            scales_at = stage + (threadIdx.x >> 5) * 16 + (threadIdx.x & 15);
+            exponents = live ? __ldg(reinterpret_cast<const uint16_t *>(p.block_scales) + phys * p.num_kv_heads + h) : 0;
         }
     }
 
@@ -683,10 +713,12 @@ __device__ __noinline__ void add_nonfinite(const AttnParams &p, int b, Request r
     }
 }
 
-template <int D, bool FP8, int WR>
+template <int D, bool FP8, int WR, bool SCALED>
 __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_kernel(const __grid_constant__ AttnParams p)
 {
     using C = Cfg<D, FP8, WR>;
+    static_assert(FP8 || !SCALED, "page scales are of codes");
+    __shared__ float4 page_scales[SCALED ? C::kStages : 1][SCALED ? kTile : 1];
     constexpr int NS = C::kKeys / 8;  // n-tiles of a warp's scores
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t scratch[kWarps + 4];
@@ -730,8 +762,12 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
     if (cp.more())
         ld.fetch(p, cp.b, cp_tile, cp.rq.ctx + cp.rq.nq);
     auto issue = [&](int stage) {
+        if constexpr (SCALED)
+            ld.store_scales();
         if (cp.more()) {
             ld.load(p, cp.head(), stages + stage * C::kStage, live[stage], flags);
+            if constexpr (SCALED)
+                ld.fetch_scales(p, cp.head(), page_scales[stage]);
             if (++cp_tile >= cp.t1) {
                 cp.next(p);
                 cp_tile = cp.t0;
@@ -811,11 +847,21 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
                 s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
             scores<D, FP8, NS, C::kRow>(s, qa, st, wk * C::kKeys);
             const uint32_t lv[4] = {live[stage][0], live[stage][1], live[stage][2], live[stage][3]};
+            [[maybe_unused]] float back[SCALED ? NS : 1][2];  // 2^-ev of this lane's keys
             const bool masked = drafted || (lv[0] & lv[1] & lv[2] & lv[3]) != 0xffffu;
 #pragma unroll
             for (int n = 0; n < NS; n++) {
-                s[n][0] = __fmul_rn(s[n][0], c0), s[n][1] = __fmul_rn(s[n][1], c0);  // rounded apart from the
-                s[n][2] = __fmul_rn(s[n][2], c1), s[n][3] = __fmul_rn(s[n][3], c1);  // subtraction of m: exactly 0 at the maximum
+                float4 x0 = make_float4(1.0f, 0.0f, 1.0f, 0.0f), x1 = x0;
+                if constexpr (SCALED) {
+                    x0 = page_scales[stage][wk * C::kKeys + 8 * n + 2 * (lane & 3)];
+                    x1 = page_scales[stage][wk * C::kKeys + 8 * n + 2 * (lane & 3) + 1];
+                }
+                s[n][0] = __fmul_rn(s[n][0], c0 * x0.x), s[n][1] = __fmul_rn(s[n][1], c0 * x1.x);  // rounded apart from the
+                s[n][2] = __fmul_rn(s[n][2], c1 * x0.x), s[n][3] = __fmul_rn(s[n][3], c1 * x1.x);  // subtraction of m: exactly 0 at the maximum
+                if constexpr (SCALED) {
+                    s[n][0] += x0.y, s[n][1] += x1.y, s[n][2] += x0.y, s[n][3] += x1.y;
+                    back[n][0] = x0.z, back[n][1] = x1.z;
+                }
                 if (masked) {
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
@@ -849,8 +895,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
             for (int n = 0; n < NS; n++) {
                 s[n][0] = ex2(s[n][0] - u0), s[n][1] = ex2(s[n][1] - u0);
                 s[n][2] = ex2(s[n][2] - u1), s[n][3] = ex2(s[n][3] - u1);
-                a0 += s[n][0] + s[n][1];
-                a1 += s[n][2] + s[n][3];
+                if constexpr (SCALED) {
+                    a0 = fmaf(s[n][1], back[n][1], fmaf(s[n][0], back[n][0], a0));
+                    a1 = fmaf(s[n][3], back[n][1], fmaf(s[n][2], back[n][0], a1));
+                } else {
+                    a0 += s[n][0] + s[n][1];
+                    a1 += s[n][2] + s[n][3];
+                }
             }
             l0 = fmaf(l0, f0, a0), l1 = fmaf(l1, f1, a1);  // this lane's columns; joined over the quad at the end
             if (__any_sync(0xffffffffu, f0 != 1.0f || f1 != 1.0f)) {
@@ -1125,7 +1176,7 @@ cudaError_t prepare(K kernel, int smem, int per_sm_most, int &ctas)
 }
 
 // The attention's CTAs for this variant on the current device (cached).
-template <int D, bool FP8, int WR>
+template <int D, bool FP8, int WR, bool SCALED = false>
 cudaError_t attention_ctas(int &ctas)
 {
     static int cached[64];  // written with the same value by whoever comes first
@@ -1138,7 +1189,7 @@ cudaError_t attention_ctas(int &ctas)
     int have = __atomic_load_n(&cached[dev], __ATOMIC_ACQUIRE);
     if (have == 0) {
         using C = Cfg<D, FP8, WR>;
-        e = prepare(attention_kernel<D, FP8, WR>, C::kSmem, C::kCtas, have);
+        e = prepare(attention_kernel<D, FP8, WR, SCALED>, C::kSmem, C::kCtas, have);
         if (e != cudaSuccess)
             return e;
         __atomic_store_n(&cached[dev], have, __ATOMIC_RELEASE);
@@ -1155,15 +1206,15 @@ int64_t attention_bytes(cudaError_t &e)
     return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * (int64_t)Cfg<D, FP8, WR>::kPart * 4) : 0;
 }
 
-template <int D, bool FP8, int WR>
+template <int D, bool FP8, int WR, bool SCALED = false>
 cudaError_t attention(const AttnParams &p, cudaStream_t stream)
 {
     using C = Cfg<D, FP8, WR>;
     int ctas = 0;
-    cudaError_t e = attention_ctas<D, FP8, WR>(ctas);
+    cudaError_t e = attention_ctas<D, FP8, WR, SCALED>(ctas);
     if (e != cudaSuccess)
         return e;
-    e = launch_pdl(attention_kernel<D, FP8, WR>, ctas, kThreads, C::kSmem, stream, p);
+    e = launch_pdl(attention_kernel<D, FP8, WR, SCALED>, ctas, kThreads, C::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
     return launch_pdl_grid(join_kernel<D, FP8, WR>, dim3((unsigned)ctas, (unsigned)WR), kThreads, 0, 0, stream, p, ctas);
@@ -1198,7 +1249,32 @@ cudaError_t attention_d(const AttnParams &p, int wr, bool fp8, cudaStream_t stre
     }
 }
 
+template <int D>
+int64_t workspace_scaled_d(int wr, cudaError_t &e)
+{
+    int ctas = 0;
+    e = wr == 1 ? attention_ctas<D, true, 1, true>(ctas) : wr == 2 ? attention_ctas<D, true, 2, true>(ctas) : attention_ctas<D, true, 4, true>(ctas);
+    const int64_t part = wr == 1 ? Cfg<D, true, 1>::kPart : wr == 2 ? Cfg<D, true, 2>::kPart : Cfg<D, true, 4>::kPart;
+    return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * part * 4) : 0;
+}
+
+template <int D>
+cudaError_t attention_scaled_d(const AttnParams &p, int wr, cudaStream_t stream)
+{
+    switch (wr) {
+    case 1: return attention<D, true, 1, true>(p, stream);
+    case 2: return attention<D, true, 2, true>(p, stream);
+    default: return attention<D, true, 4, true>(p, stream);
+    }
+}
+
 // one translation unit per head dim
+#define DSPARK_ATTN_SCALED_DECLARE(D)                              \
+    extern template int64_t workspace_scaled_d<D>(int, cudaError_t &); \
+    extern template cudaError_t attention_scaled_d<D>(const AttnParams &, int, cudaStream_t);
+#define DSPARK_ATTN_SCALED_DEFINE(D)                               \
+    template int64_t workspace_scaled_d<D>(int, cudaError_t &);        \
+    template cudaError_t attention_scaled_d<D>(const AttnParams &, int, cudaStream_t);
 #define DSPARK_ATTN_DECLARE(D)                                                     \
     extern template int64_t workspace_d<D>(int, bool, cudaError_t &);              \
     extern template cudaError_t attention_d<D>(const AttnParams &, int, bool, cudaStream_t);

@@ -1,0 +1,494 @@
+// Verification of drafted tokens against the target's probabilities (sm_103a).
+//
+// Mathematics.  Rejections leave R_0 = p, R_{k+1} = max(R_k - Z_k q_k, 0) of the
+// target's distribution, Z_k = sum R_k.  q_k is q, or q without the rejected
+// children divided by what is left, 1 - Q_k.  Since max(max(a - b, 0) - c, 0) =
+// max(a - b - c, 0) for c >= 0, R_k = max(p - S_k q, 0) with one scalar, S_0 = 0,
+// S_{k+1} = S_k + Z_k / (1 - Q_k): nothing of a vocabulary's length is stored,
+// each round is a pass over one row of p and of q.  (A rejected child x has
+// R_k(x) <= u q_k(x) Z_k < q_k(x) Z_k, so it is 0 from then on by itself.)
+// The children's p and q are single entries, read all at once beforehand; a chain
+// needs no sums before its last row.
+//
+// Sums are integers in units of 2^-48: entries are rounded to them once (those
+// below 2^-25 lose bits), sums are exact and in any order the same.  The token
+// drawn is a whole number that a user compares with one drawn in 64-bit floating
+// point: with fp32 terms a rounding of 2^-26 in a heavy entry moves the border of
+// every one behind it, which changes one token in some hundreds over a vocabulary
+// of 2^17.
+//
+// Layout.  A cluster of 1 to 16 CTAs per request, each warp with a contiguous
+// piece of the vocabulary; all CTAs walk the tree alike (it is the same for
+// all), sums go over distributed shared memory, one cluster barrier each.  The
+// draw finds the warp's piece from the sums, its CTA splits that piece over its
+// warps again, and the one that holds the token goes through its share in order.
+#include <cooperative_groups.h>
+
+#include "ctx_kv_device.cuh"
+#include "ctx_kv_internal.h"
+#include "draft_step_internal.h"
+
+namespace dspark {
+
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32, kMost = 16;
+constexpr int kStep = 128;  // entries that a warp takes at once
+constexpr double kUnit = 281474976710656.0;  // 2^48
+
+typedef unsigned long long u64;
+
+__device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, 0.0f), 1.0f); }  // NaN: 0
+__device__ __forceinline__ u64 fixed(float x) { return __float2ull_rn(x * 281474976710656.0f); }
+
+template <bool BF16>
+__device__ __forceinline__ const unsigned char *row_of(const void *base, int64_t stride, int64_t row)
+{
+    return static_cast<const unsigned char *>(base) + row * stride * (BF16 ? 2 : 4);
+}
+
+template <bool BF16>
+__device__ __forceinline__ float entry(const unsigned char *row, int64_t i)
+{
+    if (BF16)
+        return clean(__uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row) + i) << 16));
+    return clean(__ldg(reinterpret_cast<const float *>(row) + i));
+}
+
+// Entries i .. i + 3 as they are; those from n on 0.  wide: the row takes loads of four.
+template <bool BF16>
+__device__ __forceinline__ void load4(const unsigned char *row, int64_t i, int64_t n, bool wide, float (&x)[4])
+{
+    if (wide && i + 4 <= n) {
+        if constexpr (BF16) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(row + i * 2));
+            x[0] = __uint_as_float(v.x << 16), x[1] = __uint_as_float(v.x & 0xffff0000u);
+            x[2] = __uint_as_float(v.y << 16), x[3] = __uint_as_float(v.y & 0xffff0000u);
+        } else {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(row + i * 4));
+            x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        x[k] = 0.0f;
+        if (i + k < n) {
+            if constexpr (BF16)
+                x[k] = __uint_as_float((uint32_t)__ldg(reinterpret_cast<const uint16_t *>(row) + i + k) << 16);
+            else
+                x[k] = __ldg(reinterpret_cast<const float *>(row) + i + k);
+        }
+    }
+}
+
+// S as mant * 2^-shift, mant in [2^52, 2^53); S >= 1 wherever it is not 0.
+struct Share {
+    double s;
+    u64 mant;
+    int shift;
+    __device__ __forceinline__ void set(double x)
+    {
+        s = x;
+        const long long b = __double_as_longlong(x);
+        mant = (u64)(b & 0xfffffffffffffll) | 0x10000000000000ull;
+        shift = 1075 - (int)((b >> 52) & 0x7ff);
+    }
+    // floor(S q), or the largest number where that takes more than 64 bits
+    __device__ __forceinline__ u64 times(u64 q) const
+    {
+        const u64 hi = __umul64hi(q, mant), lo = q * mant;
+        if (shift <= 0 || (hi >> shift) != 0)
+            return q ? ~0ull : 0ull;
+        return shift < 64 ? (lo >> shift) | (hi << (64 - shift)) : hi >> (shift - 64);
+    }
+};
+
+enum Left { kAll, kLessQ, kLessSQ };  // R = p; max(p - q, 0); max(p - S q, 0)
+
+template <int LEFT>
+__device__ __forceinline__ u64 left_of(float p, float q, const Share &s)
+{
+    const u64 a = fixed(clean(p));
+    if (LEFT == kAll)
+        return a;
+    const u64 b = LEFT == kLessQ ? fixed(clean(q)) : s.times(fixed(clean(q)));
+    return a > b ? a - b : 0;
+}
+
+__device__ __forceinline__ u64 warp_sum(u64 x)
+{
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1)
+        x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+
+template <bool TB, int DK>  // target bf16; draft: 0 none, 1 fp32, 2 bf16
+struct Rows {
+    const unsigned char *p, *q;
+    bool wide;
+    int64_t vocab;
+
+    __device__ __forceinline__ Rows(const VerifyParams &a, int64_t row)
+    {
+        p = row_of<TB>(a.target, a.target_stride, row);
+        q = DK ? row_of<DK == 2>(a.draft, a.draft_stride, row) : p;
+        wide = (((uintptr_t)p & (TB ? 7 : 15)) | ((uintptr_t)q & (DK == 0 ? (TB ? 7 : 15) : DK == 2 ? 7 : 15))) == 0;
+        vocab = a.vocab;
+    }
+    // this lane's entries of a warp's piece [from, to), multiples of kStep apart
+    template <int LEFT>
+    __device__ __forceinline__ u64 sum(int64_t from, int64_t to, const Share &s) const
+    {
+        const int lane = threadIdx.x & 31;
+        u64 t = 0;
+        to = min(to, vocab);
+        constexpr int kU = 4;
+        int64_t i = from + 4 * lane;
+        for (; i - 4 * lane + kU * kStep <= to; i += kU * kStep) {
+            float x[kU][4], y[kU][4];
+#pragma unroll
+            for (int u = 0; u < kU; u++) {
+                load4<TB>(p, i + u * kStep, vocab, wide, x[u]);
+                if (LEFT != kAll)
+                    load4<DK == 2>(q, i + u * kStep, vocab, wide, y[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < kU; u++)
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    t += left_of<LEFT>(x[u][k], LEFT != kAll ? y[u][k] : 0.0f, s);
+        }
+        for (; i < to; i += kStep) {
+            float x[4], y[4];
+            load4<TB>(p, i, to, wide, x);
+            if (LEFT != kAll)
+                load4<DK == 2>(q, i, to, wide, y);
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                t += left_of<LEFT>(x[k], LEFT != kAll ? y[k] : 0.0f, s);
+        }
+        return t;
+    }
+    __device__ __forceinline__ u64 sum_by(Left kind, int64_t from, int64_t to, const Share &s) const
+    {
+        if (DK == 0 || kind == kAll)
+            return sum<kAll>(from, to, s);
+        return kind == kLessQ ? sum<kLessQ>(from, to, s) : sum<kLessSQ>(from, to, s);
+    }
+};
+
+template <bool TB, int DK>
+__global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams a)
+{
+    __shared__ float tp[kVerifyRows], tq[kVerifyRows], tu[kVerifyRows];  // the rows' entries and random numbers
+    __shared__ int token[kVerifyRows];                                   // -1: out of range
+    __shared__ int16_t parent[kVerifyRows], path[kVerifyRows];
+    __shared__ int gone[kVerifyRows];                                    // rejected tokens of the last row (no draft)
+    __shared__ u64 sums[2][kMost], pieces[kWarps], parts[kWarps];
+    __shared__ int first_lost;
+    pdl_enter();
+    cg::cluster_group cluster = cg::this_cluster();
+    const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), b = blockIdx.x / nc;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned flags = 0;
+
+    const int r0 = __ldg(a.row_start + b), r1 = __ldg(a.row_start + b + 1);
+    int n = r1 - r0;
+    if (r0 < 0 || r1 < r0 || r1 > a.num_rows || n > kVerifyRows) {
+        flags |= kFlagLength;
+        n = 0;
+    }
+    int64_t *out_tokens = a.out_tokens + (int64_t)b * (a.max_accepted + 1);
+    int32_t *out_rows = a.out_rows + (int64_t)b * a.max_accepted;
+
+    // ---- the rows: all their loads at once
+    for (int i = tid; i < n; i += kThreads) {
+        int up = i - 1;
+        int64_t x = -1;
+        if (i > 0) {
+            x = __ldg(a.tokens + r0 + i);
+            if (a.parents)
+                up = __ldg(a.parents + r0 + i);
+            if (up < 0 || up >= i) {
+                up = -1;
+                flags |= kFlagRow;
+            }
+            if (x < 0 || x >= a.vocab) {
+                x = -1;
+                flags |= kFlagRow;
+            }
+        }
+        const bool there = up >= 0 && x >= 0;
+        parent[i] = (int16_t)up;
+        token[i] = (int)x;
+        tp[i] = there ? entry<TB>(row_of<TB>(a.target, a.target_stride, r0 + up), x) : 0.0f;
+        if (DK)
+            tq[i] = there ? entry<DK == 2>(row_of<DK == 2>(a.draft, a.draft_stride, r0 + up), x) : 0.0f;
+        tu[i] = clean(__ldg(a.uniforms + r0 + i));
+    }
+    if (tid == 0)
+        first_lost = kVerifyRows;
+    cluster.sync();  // every CTA of the cluster runs: its shared memory may be written
+
+    // pieces of the vocabulary: warp g of the cluster has [g * piece, (g + 1) * piece)
+    const int64_t all = (int64_t)nc * kWarps, piece = (a.vocab + all * kStep - 1) / (all * kStep) * kStep;
+    int round = 0, lost = 0;  // lost: entries of `gone`
+    Share share;
+    share.set(1.0);
+    share.s = 0.0;
+    // sum of what is left of row `cur`: pieces[] holds this CTA's warps', sums[] the CTAs'
+    auto total = [&](int cur, Left kind) -> u64 {
+        const Rows<TB, DK> rows(a, r0 + cur);
+        const int64_t g = (int64_t)rank * kWarps + warp;
+        u64 t = warp_sum(rows.sum_by(kind, g * piece, (g + 1) * piece, share));
+        if (DK == 0)
+            for (int k = 0; k < lost; k++)
+                if (gone[k] / piece == g)
+                    t -= fixed(entry<TB>(rows.p, gone[k]));
+        if (lane == 0)
+            pieces[warp] = t;
+        __syncthreads();
+        u64 c = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++)
+            c += pieces[w];
+        if (tid < nc)
+            cluster.map_shared_rank(&sums[round & 1][0], tid)[rank] = c;
+        cluster.sync();
+        c = 0;
+        for (int r = 0; r < nc; r++)
+            c += sums[round & 1][r];
+        round++;
+        return c;
+    };
+
+    // ---- the walk
+    int cur = 0, count = 0;
+    const int limit = min(n - 1, a.max_accepted);
+    if (!a.parents) {
+        for (int i = 1 + tid; i <= limit; i += kThreads) {
+            const bool take = DK ? (double)tu[i] * tq[i] < (double)tp[i] : tu[i] < tp[i];
+            if (!take)
+                atomicMin(&first_lost, i);
+        }
+        __syncthreads();
+        if (n > 0) {
+            count = min(first_lost - 1, limit);
+            cur = count;
+            if (count < limit) {
+                if (DK == 0) {
+                    if (token[cur + 1] >= 0) {
+                        if (tid == 0)
+                            gone[0] = token[cur + 1];
+                        lost = 1;
+                    }
+                } else {
+                    share.set(1.0);
+                }
+            }
+            for (int i = tid; i < count; i += kThreads)
+                path[i] = (int16_t)(i + 1);
+        }
+    } else {
+        while (n > 0 && count < a.max_accepted) {
+            double z = 1.0, q_gone = 0.0;
+            int taken = 0;
+            share.s = 0.0;
+            lost = 0;
+            bool stale = false;  // z is of the round before
+            for (int last = cur;;) {
+                // the next child in row order
+                int child = 0;
+                for (int i0 = last + 1; i0 < n && child == 0; i0 += 32) {
+                    const unsigned hit = __ballot_sync(0xffffffffu, i0 + lane < n && parent[i0 + lane] == cur);
+                    if (hit)
+                        child = i0 + __ffs(hit) - 1;
+                }
+                if (child == 0)
+                    break;
+                last = child;
+                const double p = tp[child], u = tu[child];
+                if (DK) {
+                    const double q = tq[child];
+                    if (stale)
+                        z = (double)total(cur, share.s == 1.0 ? kLessQ : kLessSQ) / kUnit;
+                    const double left = a.replacement ? 1.0 : 1.0 - q_gone;
+                    if (!(left > 0x1p-24) || !(z > 0.0))
+                        break;
+                    if (u * (q / left) * z < fmax(p - share.s * q, 0.0)) {
+                        taken = child;
+                        break;
+                    }
+                    share.set(share.s + z / left);
+                    q_gone += q;
+                    stale = true;
+                } else {
+                    bool before = token[child] < 0;
+                    for (int k = 0; k < lost; k++)
+                        before |= gone[k] == token[child];
+                    const double r = before ? 0.0 : p;
+                    if (!(z > 0.0))
+                        break;
+                    if (u * z < r) {
+                        taken = child;
+                        break;
+                    }
+                    z -= r;
+                    if (!before) {
+                        __syncthreads();  // nobody reads the entry any more
+                        if (tid == 0)
+                            gone[lost] = token[child];
+                        __syncthreads();
+                        lost++;
+                    }
+                }
+            }
+            if (!taken)
+                break;
+            if (tid == 0)
+                path[count] = (int16_t)taken;
+            count++;
+            cur = taken;
+            share.s = 0.0;
+            lost = 0;
+            __syncthreads();
+        }
+    }
+    __syncthreads();
+
+    // ---- what is known: written before the barrier that the draw waits at
+    if (rank == 0) {
+        for (int i = tid; i <= a.max_accepted; i += kThreads) {
+            out_tokens[i] = i < count ? (int64_t)token[path[i]] : -1;
+            if (i < a.max_accepted)
+                out_rows[i] = i < count ? path[i] : -1;
+        }
+        if (tid == 0)
+            a.counts[b] = count;
+    }
+    if (n > 0) {
+        // ---- the last token
+        Left kind = DK == 0 || share.s == 0.0 ? kAll : share.s == 1.0 ? kLessQ : kLessSQ;
+        u64 mass = total(cur, kind);
+        if (mass == 0 && (kind != kAll || lost)) {  // the rejections left nothing
+            kind = kAll;
+            lost = 0;
+            mass = total(cur, kind);
+        }
+        if (mass == 0)
+            flags |= kFlagRow;
+        // t = floor(u mass) < mass
+        const uint32_t bits = __float_as_uint(tu[0]), e = max(bits >> 23, 1u);
+        const u64 m = bits >> 23 ? (bits & 0x7fffffu) | 0x800000u : bits, hi = __umul64hi(m, mass), lo = m * mass;
+        const uint32_t sh = 150 - e;  // 23 .. 149
+        u64 t = sh < 64 ? (lo >> sh) | (hi << (64 - sh)) : sh < 128 ? hi >> (sh - 64) : 0;
+        t = min(t, mass - 1);  // u of 1
+        u64 before = 0, mine = sums[(round - 1) & 1][rank];
+        for (int r = 0; r < rank; r++)
+            before += sums[(round - 1) & 1][r];
+        if (mass != 0 && t >= before && t - before < mine) {
+            t -= before;
+            int w = 0;
+            while (w < kWarps - 1 && t >= pieces[w])
+                t -= pieces[w++];
+            // the piece, split over the warps again
+            const Rows<TB, DK> rows(a, r0 + cur);
+            const int64_t from = ((int64_t)rank * kWarps + w) * piece, to = min(from + piece, a.vocab);
+            const int64_t part = (piece + kWarps * kStep - 1) / (kWarps * kStep) * kStep;
+            const int64_t mine0 = from + warp * part, mine1 = min(mine0 + part, to);
+            u64 x = 0;
+            if (mine0 < mine1) {
+                x = warp_sum(rows.sum_by(kind, mine0, mine1, share));
+                if (DK == 0)
+                    for (int k = 0; k < lost; k++)
+                        if (gone[k] >= mine0 && gone[k] < mine1)
+                            x -= fixed(entry<TB>(rows.p, gone[k]));
+            }
+            if (lane == 0)
+                parts[warp] = x;
+            __syncthreads();
+            w = 0;
+            while (w < kWarps - 1 && t >= parts[w])
+                t -= parts[w++];
+            if (w == warp) {
+                for (int64_t i0 = mine0; i0 < mine1; i0 += kStep) {
+                    const int64_t i = i0 + 4 * lane;
+                    float p[4], q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    u64 v[4], s = 0;
+                    load4<TB>(rows.p, i, mine1, rows.wide, p);
+                    if (kind != kAll)
+                        load4<DK == 2>(rows.q, i, mine1, rows.wide, q);
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        v[k] = kind == kAll ? left_of<kAll>(p[k], q[k], share)
+                               : kind == kLessQ ? left_of<kLessQ>(p[k], q[k], share) : left_of<kLessSQ>(p[k], q[k], share);
+                        if (DK == 0)
+                            for (int g = 0; g < lost; g++)
+                                if (gone[g] == i + k)
+                                    v[k] = 0;
+                        s += v[k];
+                    }
+                    u64 up = s;  // with the lanes before
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const u64 y = __shfl_up_sync(0xffffffffu, up, d);
+                        if (lane >= d)
+                            up += y;
+                    }
+                    const unsigned hit = __ballot_sync(0xffffffffu, up > t);
+                    if (hit) {
+                        if (lane == __ffs(hit) - 1) {
+                            u64 c = up - s;
+                            int k = 0;
+                            while (k < 3 && c + v[k] <= t)
+                                c += v[k++];
+                            out_tokens[count] = i + k;
+                        }
+                        break;
+                    }
+                    t -= __shfl_sync(0xffffffffu, up, 31);
+                }
+            }
+        }
+    }
+    flags = __reduce_or_sync(0xffffffffu, flags);
+    if (flags && lane == 0 && a.error_flags)
+        atomicOr(a.error_flags, flags);
+}
+
+template <bool TB, int DK>
+cudaError_t launch(const VerifyParams &p, int nc, cudaStream_t stream)
+{
+    // (a driver call that costs nothing next to the launch; no state to keep per device)
+    cudaError_t e = nc > 8 ? cudaFuncSetAttribute(verify_kernel<TB, DK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl_grid(verify_kernel<TB, DK>, dim3((unsigned)p.num_requests * nc), kThreads, 0, nc, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream)
+{
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess)
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess)
+        return e;
+    // CTAs of a request: two per SM over all requests, each with some work
+    int nc = 1;
+    while (nc < kMost && (int64_t)p.num_requests * nc <= sms && p.vocab > (int64_t)2048 * nc)
+        nc *= 2;
+    if (!p.draft)
+        return p.target_bf16 ? launch<true, 0>(p, nc, stream) : launch<false, 0>(p, nc, stream);
+    if (p.draft_bf16)
+        return p.target_bf16 ? launch<true, 2>(p, nc, stream) : launch<false, 2>(p, nc, stream);
+    return p.target_bf16 ? launch<true, 1>(p, nc, stream) : launch<false, 1>(p, nc, stream);
+}
+
+}  // namespace dspark

@@ -126,6 +126,13 @@ def _cache(kv_cache, device):
     return n, h, bs, row // 2, KV_FP8_E4M3 if kv_cache.dtype is torch.uint8 else KV_BF16
 
 
+def _block_scales(name, x, kv_cache):
+    """The exponents of a page-scaled cache: int8, a pair per page and head."""
+    shape = (kv_cache.shape[0], kv_cache.shape[1], 2)
+    if tuple(_tensor(name, x, torch.int8, kv_cache.device, 3)) != shape:
+        _fail(f"{name} must have shape {shape}, got {tuple(x.shape)}")
+
+
 def _table(block_table, context_lens, device):
     """(requests, table row stride, entries a row); the rows may be a column slice of a wider table."""
     if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32 or block_table.dim() != 2:
@@ -345,7 +352,7 @@ def _queries(q, kv_cache, block_table, query_start, context_lens, scale):
 
 
 def tree_attention(q, kv_cache, block_table, query_start, context_lens, tree_mask=None, causal=False, scale=None,
-                   k_scale=None, v_scale=None, out=None, lse=None, error_flags=None, stream=None):
+                   k_scale=None, v_scale=None, out=None, lse=None, error_flags=None, stream=None, block_scales=None):
     """The drafted tokens' attention over the paged cache; returns ``(out,
     lse)``: bf16 ``[T, num_heads, D]`` and fp32 ``[T, num_heads]`` (natural
     log; -inf, and zeros in ``out``, where a row sees nothing).  Scores and sums
@@ -368,6 +375,11 @@ def tree_attention(q, kv_cache, block_table, query_start, context_lens, tree_mas
     reach its result, whatever they hold.  Rows that belong to no request are
     left as they were (uninitialised where this call makes the outputs).
     ``scale``: 1 / sqrt(D) if not given.
+
+    ``block_scales``: int8 ``[num_blocks, num_kv_heads, 2]``, in the place of
+    ``k_scale`` and ``v_scale``, for a page-scaled cache (uint8, as
+    ``insert_kv_scaled`` fills it): the K and V of a page and head are its codes
+    times 2 to these powers.
     """
     _load()
     T, Hq, Hkv, D, B, dev, kv_dtype, scale, head, table = _queries(q, kv_cache, block_table, query_start, context_lens,
@@ -385,10 +397,14 @@ def tree_attention(q, kv_cache, block_table, query_start, context_lens, tree_mas
     if lse is not None and tuple(_tensor("lse", lse, torch.float32, dev, 2)) != (T, Hq):
         _fail(f"lse must have shape {(T, Hq)}, got {tuple(lse.shape)}")
     ks, vs, flags = _scalar("k_scale", k_scale, dev), _scalar("v_scale", v_scale, dev), _flags(error_flags, dev)
+    if block_scales is not None:
+        if kv_dtype != KV_FP8_E4M3 or k_scale is not None or v_scale is not None:
+            _fail("block_scales go with a uint8 cache, without k_scale and v_scale")
+        _block_scales("block_scales", block_scales, kv_cache)
     if _elsewhere(dev, stream):
         with _on(dev, stream):
             return tree_attention(q, kv_cache, block_table, query_start, context_lens, tree_mask, causal, scale, k_scale,
-                                  v_scale, out, lse, error_flags)
+                                  v_scale, out, lse, error_flags, None, block_scales)
     if out is None:
         out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
     if lse is None:
@@ -397,11 +413,15 @@ def tree_attention(q, kv_cache, block_table, query_start, context_lens, tree_mas
     # the partial results of requests that are split over CTAs: made anew by
     # each call, on its stream (or in the graph's own pool), so calls never share it
     # (a size below 0: the call refuses the same sizes, with its status)
-    size = max(0, L.dspark_tree_attention_workspace(T, Hq, Hkv, D, B, kv_dtype))
+    size = max(0, L.dspark_tree_attention_workspace(T, Hq, Hkv, D, B, kv_dtype) if block_scales is None else
+               L.dspark_tree_attention_scaled_workspace(T, Hq, Hkv, D, B))
     work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    check(L.dspark_tree_attention(*head, ks, vs, *table, kind, tree_mask.data_ptr() if words else 0, words, scale,
-                                  out.data_ptr(), lse.data_ptr(), work.data_ptr() if size else 0, size, flags,
-                                  _current(dev)))
+    rest = (*table, kind, tree_mask.data_ptr() if words else 0, words, scale, out.data_ptr(), lse.data_ptr(),
+            work.data_ptr() if size else 0, size, flags, _current(dev))
+    if block_scales is None:
+        check(L.dspark_tree_attention(*head, ks, vs, *rest))
+    else:
+        check(L.dspark_tree_attention_scaled(*head[:8], block_scales.data_ptr(), *head[8:10], *rest))
     return out, lse
 
 
