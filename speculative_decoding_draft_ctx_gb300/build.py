@@ -32,7 +32,8 @@ ROPE_SRC = os.path.join(CSRC, "rope.cu")
 EVICT_SRC = os.path.join(CSRC, "kv_evict.cu")
 ATTN_SRCS = tuple(os.path.join(CSRC, f) for f in ("tree_attn.cu", "attn_weight.cu", "tree_attn_d64.cu", "tree_attn_d128.cu", "tree_attn_d256.cu",
                                                      "tree_attn_tc_d64.cu", "tree_attn_tc_d128.cu", "tree_attn_scaled_d64.cu",
-                                                     "tree_attn_scaled_d128.cu", "tree_attn_scaled_d256.cu"))
+                                                     "tree_attn_scaled_d128.cu", "tree_attn_scaled_d256.cu",
+                                                     "tree_attn_tc_scaled_d64.cu", "tree_attn_tc_scaled_d128.cu"))
 STEP_SRCS = tuple(os.path.join(CSRC, f) for f in ("verify.cu", "kv_pages.cu", "kv_insert_scaled.cu"))
 CU_SRCS = (KERNEL_SRC, TMA_SRC, QK_SRC, PROJ_SRC, NORM_SRC, GENERAL_SRC, WARP_SRC, NOALLOC_SRC, ROPE_SRC, EVICT_SRC,
            *ATTN_SRCS, *STEP_SRCS)

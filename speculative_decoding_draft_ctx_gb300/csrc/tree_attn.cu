@@ -12,6 +12,8 @@ DSPARK_ATTN_DECLARE(256)
 DSPARK_ATTN_SCALED_DECLARE(64)
 DSPARK_ATTN_SCALED_DECLARE(128)
 DSPARK_ATTN_SCALED_DECLARE(256)
+DSPARK_ATTN_TC_SCALED_DECLARE(64)
+DSPARK_ATTN_TC_SCALED_DECLARE(128)
 DSPARK_ATTN_TC_DECLARE(64)
 DSPARK_ATTN_TC_DECLARE(128)
 }  // namespace attn
@@ -58,6 +60,24 @@ int64_t workspace_mma(int64_t rows, int group, int head_dim, int requests, bool 
     }
 }
 
+// Which kernel a call takes.
+cudaError_t takes_tc(const AttnParams &p, int head_dim, bool &tc)
+{
+    const Pin pin = pinned(head_dim);
+    tc = pin == kTc;
+    if (pin == kNone && p.num_rows * p.group > kTcRows * p.num_requests) {
+        int dev = 0, sms = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess)
+            e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess)
+            return e;
+        const int64_t tiles = (p.table_blocks * p.block_size + 127) / 128;
+        tc = tiles * p.num_requests * p.num_kv_heads > sms / 2;
+    }
+    return cudaSuccess;
+}
+
 }  // namespace
 
 // enough for every kernel that the launch may choose
@@ -78,18 +98,10 @@ int64_t tree_attention_workspace(int64_t rows, int num_heads, int num_kv_heads, 
 
 cudaError_t launch_tree_attention(const AttnParams &p, int head_dim, bool fp8, cudaStream_t stream)
 {
-    const Pin pin = pinned(head_dim);
-    bool tc = pin == kTc;
-    if (pin == kNone && p.num_rows * p.group > kTcRows * p.num_requests) {
-        int dev = 0, sms = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess)
-            e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess)
-            return e;
-        const int64_t tiles = (p.table_blocks * p.block_size + 127) / 128;
-        tc = tiles * p.num_requests * p.num_kv_heads > sms / 2;
-    }
+    bool tc = false;
+    const cudaError_t e = takes_tc(p, head_dim, tc);
+    if (e != cudaSuccess)
+        return e;
     if (tc)
         return head_dim == 64 ? attn::attention_tc_d<64>(p, fp8, stream) : attn::attention_tc_d<128>(p, fp8, stream);
     const int wr = attn::row_warps(p.num_rows, p.group, p.num_requests);
@@ -102,16 +114,27 @@ cudaError_t launch_tree_attention(const AttnParams &p, int head_dim, bool fp8, c
 
 int64_t tree_attention_scaled_workspace(int64_t rows, int num_heads, int num_kv_heads, int head_dim, int requests, cudaError_t &e)
 {
-    const int wr = attn::row_warps(rows, num_heads / num_kv_heads, requests);
-    switch (head_dim) {
-    case 64: return attn::workspace_scaled_d<64>(wr, e);
-    case 128: return attn::workspace_scaled_d<128>(wr, e);
-    default: return attn::workspace_scaled_d<256>(wr, e);
+    const int group = num_heads / num_kv_heads, wr = attn::row_warps(rows, group, requests);
+    const Pin pin = pinned(head_dim);
+    int64_t n = 0;
+    if (pin != kTc)
+        n = head_dim == 64 ? attn::workspace_scaled_d<64>(wr, e) : head_dim == 128 ? attn::workspace_scaled_d<128>(wr, e)
+                                                                             : attn::workspace_scaled_d<256>(wr, e);
+    if (pin == kTc || (pin == kNone && e == cudaSuccess && rows * group > kTcRows * requests)) {
+        const int64_t m = head_dim == 64 ? attn::workspace_tc<64>(true, e) : attn::workspace_tc<128>(true, e);
+        n = n > m ? n : m;
     }
+    return n;
 }
 
 cudaError_t launch_tree_attention_scaled(const AttnParams &p, int head_dim, cudaStream_t stream)
 {
+    bool tc = false;
+    const cudaError_t e = takes_tc(p, head_dim, tc);
+    if (e != cudaSuccess)
+        return e;
+    if (tc)
+        return head_dim == 64 ? attn::attention_tc_scaled_d<64>(p, stream) : attn::attention_tc_scaled_d<128>(p, stream);
     const int wr = attn::row_warps(p.num_rows, p.group, p.num_requests);
     switch (head_dim) {
     case 64: return attn::attention_scaled_d<64>(p, wr, stream);

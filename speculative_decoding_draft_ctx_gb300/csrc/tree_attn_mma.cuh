@@ -469,8 +469,9 @@ __device__ __forceinline__ uint32_t raw_at(uint32_t tile, int y, int c)
 
 // Rows [row0, row0 + ROWS) of a tile by one warp, after their codes have
 // landed.  Rows from `clean` on have NaN codes zeroed; true if there were any.
-template <int D, int ROWS>
-__device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean)
+// SCALED: row row0 + i is multiplied by the fp16 pair factors[i], a power of two.
+template <int D, int ROWS, bool SCALED = false>
+__device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean, const uint32_t *factors = nullptr)
 {
     constexpr int kW = D / 16, kR = 32 / kW, kU = kR < 8 ? 8 / kR : 1, kStep = kU * kR;  // whole groups of 8 rows a step
     const int lane = threadIdx.x & 31, c = lane % kW, r = lane / kW;
@@ -510,6 +511,17 @@ __device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean)
 #pragma unroll 1
     for (int d = 0; d < ROWS * 128; d += kStep * 128) {
         uint32_t q[kU][4];
+        [[maybe_unused]] uint32_t f[kU];
+        if constexpr (SCALED)
+#pragma unroll
+            for (int u = 0; u < kU; u++)
+                f[u] = factors[d / 128 + u * kR + r];
+        auto half2_of = [&](uint32_t w, int u) {
+            uint32_t h = e4m3_to_half2((uint16_t)w);
+            if constexpr (SCALED)
+                asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(h) : "r"(f[u]));
+            return h;
+        };
 #pragma unroll
         for (int u = 0; u < kU; u++)
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
@@ -523,9 +535,8 @@ __device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean)
             for (int k = 0; k < 2; k++) {
                 const bool upper = (k != 0) != ((c & 1) != 0);
                 const uint32_t a = upper ? q[u][2] : q[u][0], b = upper ? q[u][3] : q[u][1];
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to[u][k] + d), "r"(e4m3_to_half2((uint16_t)a)),
-                             "r"(e4m3_to_half2((uint16_t)(a >> 16))), "r"(e4m3_to_half2((uint16_t)b)),
-                             "r"(e4m3_to_half2((uint16_t)(b >> 16)))
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to[u][k] + d), "r"(half2_of(a, u)),
+                             "r"(half2_of(a >> 16, u)), "r"(half2_of(b, u)), "r"(half2_of(b >> 16, u))
                              : "memory");
             }
     }

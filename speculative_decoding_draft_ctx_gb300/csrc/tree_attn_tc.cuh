@@ -38,6 +38,17 @@
 //    precision.  Over an fp8 cache fp16's range is used up by kLift but for one
 //    octave.
 //
+// Page-scaled fp8 (SCALED).  Every 64 keys that a producer warp brings have one
+// power of two for K and one for V, the largest of their pages': a row's codes
+// become fp16 divided by what its own page has less, exactly (a code has no bit
+// below 2^-9, fp16 none below 2^-24, and up to 2^kSpread are taken off).  So
+// the softmax knows two numbers per 64 keys: scores are multiplied by 2^ek, the
+// weights P are 2^(s + ev - m) with m of the maximum of s + ev, and the sum of
+// weights takes 2^-ev of it back.  Where the exponents of 64 keys are further
+// apart than kSpread, their codes are taken as they are and the softmax goes by
+// each key's exponents, in the loops that tiles with a mask have.  The V
+// warps come to the same numbers as the K warps, which hand them to the softmax.
+//
 // Loops are rolled where a role's straight-line code would not stay in the
 // instruction caches beside the others' (unrolled, a warp's instruction took
 // about ten cycles), and tiles without a mask have loops of their own.  14
@@ -62,6 +73,7 @@ constexpr int kProducers = 4, kItemCostTc = 6;   // EXTRA of Walk, in tiles of k
 // sums and bf16 weights have room for any; fp16 weights begin at 2^kLift and
 // end below 2^16 (a score is off by 2^-4 at most where kLift is taken off).
 constexpr float kMost = 8.0f, kMostFp8 = kLift + 1.0f;
+constexpr int kSpread = 15;  // of the exponents of 64 keys of a page-scaled cache
 
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -92,7 +104,7 @@ __device__ __forceinline__ int tile_halves(const W &w, int n)
     return 2 * n - (w.finished() && w.rq.ctx + w.rq.nq <= (w.t1 - 1) * kKeysTc + kKeysTc / 2 ? 1 : 0);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool SCALED = false>
 __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __grid_constant__ AttnParams p)
 {
     using C = TcCfg<D, FP8>;
@@ -110,6 +122,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
     __shared__ int abort_flag, lock;
     __shared__ int bad[16];  // item number + 1 where infinities or NaN came up among an item's drafted V
     __shared__ float join_ml[256];
+    // page-scaled: of each 64 keys 2^ek, ev and 2^-ev (x < 0: by key), the keys'
+    // exponents, and the producers' factors of their rows of two tiles
+    __shared__ float4 half_scale[SCALED ? 8 : 1][2];
+    __shared__ uint16_t key_exps[SCALED ? 8 : 1][SCALED ? kKeysTc : 1];
+    __shared__ uint32_t factors[SCALED ? kProducers : 1][2][SCALED ? 64 : 1];
     __shared__ int64_t scratch[kTcThreads / 32 + 4];
     const Patience limit{&abort_flag, p.wait_ns};
 
@@ -325,6 +342,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         unsigned char *ring = is_v ? sv : sk;
         uint64_t *fulls = is_v ? vfull : kfull, *empties = is_v ? vempty : kempty;
         const int ns = is_v ? NV : NK;
+        [[maybe_unused]] uint32_t exps[2] = {0x10000u, 0x10000u};  // page-scaled: of the rows resolved last; from 0x10000 on: none
         int phys[2], off[2];  // of the tile looked up last: rows lane and lane + 32 of the warp's; off < 0: past the end
         int look_tile = w.t0, look_head = 0, looked = 0;  // looked: tiles looked up, two ahead while there are any
         W lw = w;  // the walk of the look-ups; w is the walk of the tiles that are finished
@@ -354,11 +372,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
 #pragma unroll
             for (int g = 0; g < 2; g++) {
                 uint32_t at = ~0u;
+                if constexpr (SCALED)
+                    exps[g] = 0x10000u;
                 if (off[g] >= 0) {
                     if (phys[g] < 0 || phys[g] >= p.num_blocks) {
                         flags |= kFlagBlockRange;
                     } else {
                         at = (uint32_t)(((int64_t)phys[g] * p.num_kv_heads + look_head) * p.block_size + off[g]);
+                        if constexpr (SCALED)
+                            exps[g] = __ldg(reinterpret_cast<const uint16_t *>(p.block_scales) + (int64_t)phys[g] * p.num_kv_heads + look_head);
                         const unsigned char *row = cache + (int64_t)at * C::kRow;
 #pragma unroll
                         for (int y = 0; y < C::kRow / 2; y += 128)
@@ -378,6 +400,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
         auto issue = [&](int x) {
             const uint32_t dst0 = tc::saddr(ring) + (x % ns) * C::kTileBytes;
             const uint32_t *from = rows[pw][x & 1];
+            if constexpr (SCALED) {
+                // this tile's exponents have come: what its 64 keys have in common
+                int ek[2], ev[2], lo[2] = {kScaleMax, kScaleMax}, hi[2] = {kScaleMin, kScaleMin};
+#pragma unroll
+                for (int g = 0; g < 2; g++) {
+                    ek[g] = min(max((int)(int8_t)(exps[g] & 0xffu), kScaleMin), kScaleMax);
+                    ev[g] = min(max((int)(int8_t)((exps[g] >> 8) & 0xffu), kScaleMin), kScaleMax);
+                    if (exps[g] < 0x10000u) {
+                        lo[0] = min(lo[0], ek[g]), hi[0] = max(hi[0], ek[g]);
+                        lo[1] = min(lo[1], ev[g]), hi[1] = max(hi[1], ev[g]);
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < 2; v++)
+                    lo[v] = __reduce_min_sync(0xffffffffu, lo[v]), hi[v] = __reduce_max_sync(0xffffffffu, hi[v]);
+                const bool each = hi[0] - lo[0] > kSpread || hi[1] - lo[1] > kSpread;
+#pragma unroll
+                for (int g = 0; g < 2; g++) {
+                    const int d = each || exps[g] >= 0x10000u ? 0 : is_v ? hi[1] - ev[g] : hi[0] - ek[g];
+                    factors[pw][x & 1][32 * g + lane] = (uint32_t)(d < 15 ? (15 - d) << 10 : 1 << 9) * 0x10001u;  // 2^-d
+                    if (!is_v)
+                        key_exps[x & 7][64 * sub + 32 * g + lane] = (uint16_t)((ek[g] & 0xff) | (ev[g] & 0xff) << 8);
+                }
+                if (!is_v && lane == 0) {
+                    const int e = hi[1] < lo[1] ? 0 : hi[1];  // no key is there
+                    half_scale[x & 7][sub] = make_float4(each ? -1.0f : hi[0] < lo[0] ? 1.0f : __int_as_float((127 + hi[0]) << 23), (float)e,
+                                                         __int_as_float((127 - e) << 23), 0.0f);
+                }
+            }
             resolve((x & 1) ^ 1);
             look();
 #pragma unroll 1
@@ -433,7 +484,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                 else
                     cp_wait<0>();
                 __syncwarp();
-                if (convert_rows<D, 64>(tc::saddr(ring) + st * C::kTileBytes, 64 * sub, drafted ? w.rq.ctx - tile * kKeysTc : kKeysTc))
+                if (convert_rows<D, 64, SCALED>(tc::saddr(ring) + st * C::kTileBytes, 64 * sub, drafted ? w.rq.ctx - tile * kKeysTc : kKeysTc,
+                                                SCALED ? factors[pw][x & 1] : nullptr))
                     bad[item & 15] = item + 1;
                 fence_async();
             } else if (drafted) {
@@ -599,25 +651,55 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                                     x[e] = 0xff800000u;
                         }
                     };
+                    // page-scaled: the factor and exponent of 64 keys, or by key
+                    [[maybe_unused]] const bool by_key = SCALED && (half_scale[SCALED ? lx : 0][0].x < 0.0f || (nh > 1 && half_scale[SCALED ? lx : 0][1].x < 0.0f));
+                    [[maybe_unused]] auto half_of = [&](int hh) {
+                        float4 v = half_scale[SCALED ? lx : 0][hh];
+                        v.x = by_key && v.x < 0.0f ? c : fmaxf(c * v.x, 1.4e-45f);
+                        return v;
+                    };
+                    // by key: 32 scores times 2^ek c, plus ev (the half's own factor where it has one)
+                    [[maybe_unused]] auto scale32 = [&](int g, uint32_t (&x)[32]) {
+                        const float4 hs = half_scale[SCALED ? lx : 0][g >> 1];
+                        const float hc = fmaxf(c * hs.x, 1.4e-45f);
+#pragma unroll
+                        for (int e = 0; e < 32; e++) {
+                            const uint32_t ke = key_exps[SCALED ? lx : 0][SCALED ? 32 * g + e : 0];
+                            const float f = hs.x < 0.0f ? fmaxf(c * __int_as_float((127 + (int)(int8_t)(ke & 0xffu)) << 23), 1.4e-45f) : hc;
+                            const float a = hs.x < 0.0f ? (float)(int)(int8_t)(ke >> 8) : hs.y;
+                            x[e] = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(x[e]), f), a));
+                        }
+                    };
                     // ---- maximum (the scores are read again below)
+                    float t_scaled = -INFINITY;
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                     auto maxima = [&](auto gc) {
 #pragma unroll 1
                         for (int g = 0; g < 2 * nh; g++) {
                             uint32_t x[32];
                             load32(gc, g, x);
+                            if constexpr (SCALED && decltype(gc)::value)
+                                if (by_key)
+                                    scale32(g, x);
 #pragma unroll
                             for (int e = 0; e < 32; e += 8)
 #pragma unroll
                                 for (int k2 = 0; k2 < 4; k2++)
                                     top[k2] = max3(top[k2], __uint_as_float(x[e + 2 * k2]), __uint_as_float(x[e + 2 * k2 + 1]));
+                            if constexpr (SCALED)
+                                if (g & 1) {
+                                    const float u = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+                                    const float4 hs = half_of(g >> 1);
+                                    t_scaled = fmaxf(t_scaled, decltype(gc)::value && by_key ? u : __fadd_rn(__fmul_rn(u, hs.x), hs.y));
+                                    top[0] = top[1] = top[2] = top[3] = -INFINITY;
+                                }
                         }
                     };
-                    if (__builtin_expect(masked, 0))
+                    if (__builtin_expect(masked || by_key, 0))
                         maxima(std::true_type{});
                     else
                         maxima(std::false_type{});
-                    const float t = max3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
+                    const float t = SCALED ? t_scaled : max3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
                     const float most = !FP8 ? kMost : fabsf(t) < kLiftBelow ? kMostFp8 : 1.0f;
                     const bool grow = t > m + most || (m == -INFINITY && t > m);
                     if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
@@ -649,7 +731,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                         for (int g = 0; g < 2 * nh; g++) {
                             uint32_t x[32], pk[16];
                             load32(gc, g, x);
-                            if (decltype(gc)::value && apart) {
+                            uint64_t f2 = c2, a2s = m2;  // factor of the scores, what is added to them
+                            [[maybe_unused]] uint64_t back2 = 0;
+                            if constexpr (SCALED) {
+                                const float4 hs = half_of(g >> 1);
+                                f2 = pr(hs.x, hs.x), a2s = pr(hs.y - mu, hs.y - mu), back2 = pr(hs.z, hs.z);
+                            }
+                            if (SCALED && decltype(gc)::value && (by_key || apart)) {
+                                scale32(g, x);
+#pragma unroll
+                                for (int e = 0; e < 32; e++)
+                                    x[e] = __float_as_uint(__fsub_rn(__uint_as_float(x[e]), mu));
+                            } else if (!SCALED && decltype(gc)::value && apart) {
 #pragma unroll
                                 for (int e = 0; e < 32; e++)
                                     x[e] = __float_as_uint(__fsub_rn(__fmul_rn(__uint_as_float(x[e]), c), mu));
@@ -657,7 +750,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
                                     float a0, a1;
-                                    unpr(fma2(pr(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), c2, m2), a0, a1);
+                                    unpr(fma2(pr(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2, a2s), a0, a1);
                                     x[e] = __float_as_uint(a0), x[e + 1] = __float_as_uint(a1);
                                 }
                             }
@@ -665,8 +758,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                             for (int e = 0; e < 32; e += 4) {
                                 const float a0 = ex2(__uint_as_float(x[e])), a1 = ex2(__uint_as_float(x[e + 1]));
                                 const float a2 = ex2(__uint_as_float(x[e + 2])), a3 = ex2(__uint_as_float(x[e + 3]));
-                                sum0 = add2(sum0, pr(a0, a1));
-                                sum1 = add2(sum1, pr(a2, a3));
+                                if constexpr (SCALED) {
+                                    uint64_t b0 = back2, b1 = back2;
+                                    if (decltype(gc)::value && by_key && half_scale[lx][g >> 1].x < 0.0f) {
+                                        auto back = [&](int k) {
+                                            return __int_as_float((127 - (int)(int8_t)(key_exps[lx][32 * g + k] >> 8)) << 23);
+                                        };
+                                        b0 = pr(back(e), back(e + 1)), b1 = pr(back(e + 2), back(e + 3));
+                                    }
+                                    sum0 = fma2(pr(a0, a1), b0, sum0);
+                                    sum1 = fma2(pr(a2, a3), b1, sum1);
+                                } else {
+                                    sum0 = add2(sum0, pr(a0, a1));
+                                    sum1 = add2(sum1, pr(a2, a3));
+                                }
                                 pk[e / 2] = pack2<FP8>(a0, a1);
                                 pk[e / 2 + 1] = pack2<FP8>(a2, a3);
                             }
@@ -683,7 +788,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     };
                     // Tiles without a mask run a short loop of their own: the
                     // instructions a warp has to fetch per tile are what bounds it.
-                    if (__builtin_expect(masked || apart, 0))
+                    if (__builtin_expect(masked || apart || by_key, 0))
                         raise(std::true_type{});
                     else
                         raise(std::false_type{});
@@ -908,7 +1013,7 @@ __global__ void __launch_bounds__(128) join_tc_kernel(const __grid_constant__ At
 
 // ------------------------------------------------------------------ launches
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool SCALED = false>
 cudaError_t attention_tc_ctas(int &ctas)
 {
     static int cached[64];
@@ -922,7 +1027,7 @@ cudaError_t attention_tc_ctas(int &ctas)
     if (have == 0) {
         e = cudaDeviceGetAttribute(&have, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(attention_tc_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(attention_tc_kernel<D, FP8, SCALED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      TcCfg<D, FP8>::kSmem);
         if (e != cudaSuccess)
             return e;
@@ -940,14 +1045,14 @@ int64_t attention_tc_bytes(cudaError_t &e)
     return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * (int64_t)TcCfg<D, FP8>::kPart * 4) : 0;
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool SCALED = false>
 cudaError_t attention_tc(const AttnParams &p, cudaStream_t stream)
 {
     using C = TcCfg<D, FP8>;
     int ctas = 0;
-    cudaError_t e = attention_tc_ctas<D, FP8>(ctas);
+    cudaError_t e = attention_tc_ctas<D, FP8, SCALED>(ctas);
     if (e == cudaSuccess)
-        e = launch_pdl(attention_tc_kernel<D, FP8>, ctas, kTcThreads, C::kSmem, stream, p);
+        e = launch_pdl(attention_tc_kernel<D, FP8, SCALED>, ctas, kTcThreads, C::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
     return launch_pdl_grid(join_tc_kernel<D, FP8>, dim3((unsigned)ctas, (unsigned)(2 * (D / kJoinDims))), 128, 0, 0, stream, p, ctas);
@@ -965,6 +1070,15 @@ cudaError_t attention_tc_d(const AttnParams &p, bool fp8, cudaStream_t stream)
     return fp8 ? attention_tc<D, true>(p, stream) : attention_tc<D, false>(p, stream);
 }
 
+// (the workspace of an fp8 call: as many CTAs, the same parts)
+template <int D>
+cudaError_t attention_tc_scaled_d(const AttnParams &p, cudaStream_t stream)
+{
+    return attention_tc<D, true, true>(p, stream);
+}
+
+#define DSPARK_ATTN_TC_SCALED_DECLARE(D) extern template cudaError_t attention_tc_scaled_d<D>(const AttnParams &, cudaStream_t);
+#define DSPARK_ATTN_TC_SCALED_DEFINE(D) template cudaError_t attention_tc_scaled_d<D>(const AttnParams &, cudaStream_t);
 #define DSPARK_ATTN_TC_DECLARE(D)                                 \
     extern template int64_t workspace_tc<D>(bool, cudaError_t &); \
     extern template cudaError_t attention_tc_d<D>(const AttnParams &, bool, cudaStream_t);
