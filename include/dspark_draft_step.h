@@ -55,7 +55,7 @@ extern "C" {
  * Children that come up when no mass is left (Z_k = 0, or at most 2^-24 of q)
  * are rejected.
  *
- * Tests are done in 64-bit floating point, sums in integers of 2^-48, so the
+ * Tests are done in 64-bit floating point, sums in integers of 2^-46, so the
  * result does not depend on the order of the sums.
  *
  *  target, draft  device, [num_rows, vocab], DSPARK_PROB_FP32 or _BF16, row r at
@@ -154,7 +154,7 @@ int64_t dspark_kv_fork_workspace(int num_pairs);
 int dspark_kv_resize(int32_t *block_table, int64_t table_stride, int64_t table_blocks, int32_t *pages,
                      const int32_t *tokens, int num_rows, int32_t *refs, int64_t num_blocks, int block_size,
                      void *workspace, int64_t workspace_bytes, unsigned int *error_flags, cudaStream_t stream);
-int64_t dspark_kv_resize_workspace(int num_rows);
+int64_t dspark_kv_resize_workspace(int num_rows, int64_t num_blocks);
 
 /*
  * dspark_kv_insert_scaled -- stores new tokens' K and V in a page-scaled cache:

@@ -168,7 +168,7 @@ def lib() -> ctypes.CDLL:
         L.dspark_kv_fork.argtypes = layers + [P, I64, I64, P, P, I, P, P, I, P, P, I64, P, P]
         L.dspark_kv_fork_workspace.argtypes = [I]
         L.dspark_kv_resize.argtypes = [P, I64, I64, P, P, I, P, I64, I, P, I64, P, P]
-        L.dspark_kv_resize_workspace.argtypes = [I]
+        L.dspark_kv_resize_workspace.argtypes = [I, I64]
         L.dspark_kv_insert_scaled.argtypes = [P, I64, I64, P, I64, I64, I64, P, P, I64, I, I, I] + table + [P, P]
         L.dspark_tree_attention_scaled.argtypes = [P, I64, I64, I64, I, I, I, P, P, I64, I] + table + [I, P, I, F, P, P, P,
                                                                                                     I64, P, P]

@@ -177,7 +177,7 @@ int64_t dspark_kv_fork_workspace(int num_pairs)
         fail(DSPARK_ERR_INVALID_ARG, "%d pairs not in [0, %d]", num_pairs, kMaxPairs);
         return -1;
     }
-    return (int64_t)num_pairs * 2 * (int64_t)sizeof(int32_t) * 4;  // copies, and the pairs in need of a page
+    return (int64_t)num_pairs * 5 * 4;  // the copies and the free pages
 }
 
 int dspark_kv_fork(void *const *kv_caches, int8_t *const *block_scales, int num_layers, int64_t num_blocks,
@@ -222,6 +222,7 @@ int dspark_kv_fork(void *const *kv_caches, int8_t *const *block_scales, int num_
     p.src = src;
     p.dst = dst;
     p.copies = static_cast<int4 *>(workspace);
+    p.free_list = reinterpret_cast<int32_t *>(p.copies + num_pairs);
     p.error_flags = error_flags;
     p.num_rows = num_rows;
     p.num_pairs = num_pairs;
@@ -242,13 +243,13 @@ int dspark_kv_fork(void *const *kv_caches, int8_t *const *block_scales, int num_
     return launched(e, "fork");
 }
 
-int64_t dspark_kv_resize_workspace(int num_rows)
+int64_t dspark_kv_resize_workspace(int num_rows, int64_t num_blocks)
 {
-    if (num_rows < 0 || num_rows > (1 << 24)) {
-        fail(DSPARK_ERR_INVALID_ARG, "%d rows not in [0, 2^24]", num_rows);
+    if (num_rows < 0 || num_rows > (1 << 24) || num_blocks < 1 || num_blocks >= INT32_MAX) {
+        fail(DSPARK_ERR_INVALID_ARG, "%d rows not in [0, 2^24] or %lld pages not in [1, 2^31 - 1)", num_rows, (long long)num_blocks);
         return -1;
     }
-    return num_rows ? ((int64_t)num_rows + 1) * 4 : 0;
+    return num_rows ? ((int64_t)num_rows + 1 + num_blocks) * 4 : 0;  // what the rows ask for and the free pages
 }
 
 int dspark_kv_resize(int32_t *block_table, int64_t table_stride, int64_t table_blocks, int32_t *pages,
@@ -264,7 +265,7 @@ int dspark_kv_resize(int32_t *block_table, int64_t table_stride, int64_t table_b
         return fail(DSPARK_ERR_INVALID_ARG, "null tokens");
     if (!aligned(tokens, 4) || !aligned(error_flags, 4) || !aligned(workspace, 16))
         return fail(DSPARK_ERR_ALIGNMENT, "workspace must be 16-byte, the other buffers 4-byte aligned");
-    const int64_t need = dspark_kv_resize_workspace(num_rows), rows_bytes = (int64_t)num_rows * 4;
+    const int64_t need = dspark_kv_resize_workspace(num_rows, num_blocks), rows_bytes = (int64_t)num_rows * 4;
     if (workspace_bytes < need || !workspace)
         return fail(DSPARK_ERR_INVALID_ARG, "workspace of %lld bytes, %lld needed", (long long)workspace_bytes, (long long)need);
     const int64_t table_bytes = ((num_rows - 1) * table_stride + table_blocks) * 4;
@@ -281,6 +282,7 @@ int dspark_kv_resize(int32_t *block_table, int64_t table_stride, int64_t table_b
     p.refs = refs;
     p.tokens = tokens;
     p.before = static_cast<int32_t *>(workspace);
+    p.free_list = p.before + num_rows + 1;
     p.error_flags = error_flags;
     p.num_rows = num_rows;
     p.block_size = block_size;

@@ -61,7 +61,8 @@ struct ForkParams {
     int64_t table_stride, table_blocks, num_blocks;
     int32_t *pages, *lens, *refs;
     const int32_t *src, *dst;
-    int4 *copies;                // workspace: per pair old page, new page, tokens (0: none), -
+    int4 *copies;                // workspace: per pair old page, new page, tokens to copy (0: none), whether it is done
+    int32_t *free_list;          // workspace [num_pairs]
     unsigned int *error_flags;
     int32_t num_rows, num_pairs, block_size;
 };
@@ -83,6 +84,7 @@ struct ResizeParams {
     int32_t *pages, *refs;
     const int32_t *tokens;
     int32_t *before;             // workspace [num_rows + 1]: pages asked for by the rows before
+    int32_t *free_list;          // workspace [num_blocks]
     unsigned int *error_flags;
     int32_t num_rows, block_size;
 };

@@ -7,11 +7,12 @@
 // in fp32, the code's rounding the only one.  A page whose scale grows has its
 // codes divided by a power of two (page_scale.cuh).
 //
-// Work.  A unit is one (request, page, head); its tokens are read once: a
-// thread keeps up to kHold 16-byte words while the CTA finds the maximum.  Lengths
+// Work.  A unit is one (request, page, head, K or V); its tokens are read once: a
+// thread keeps up to kHold 16-byte words while the CTA finds the maximum (64
+// tokens of D 128; more are read again, from L1).  Lengths
 // are on the device, so each CTA sums the requests' units itself and takes an
 // equal share of them, as the attention does.  A CTA has 128 threads, so that
-// a draft step's units (7 tokens of 512 bytes) are there all at once.
+// a draft step's units (7 tokens of 256 bytes) are there all at once.
 #include "draft_step_internal.h"
 #include "page_scale.cuh"
 #include "tree_attn_mma.cuh"
@@ -67,15 +68,14 @@ __device__ __forceinline__ uint2 encode8(const uint4 &v, float s)
 template <int D>
 __global__ void __launch_bounds__(kThreads, 8) insert_scaled_kernel(const __grid_constant__ InsertScaledParams p)
 {
-    constexpr int kW = D / 4;  // 16-byte words of a token's K and V of a head: the same word for all of a thread's tokens
-    static_assert(kThreads % kW == 0, "a thread keeps to K or to V");
+    constexpr int kW = D / 8, kStep = kThreads / kW;  // 16-byte words of a token's K or V; tokens at once
     __shared__ int64_t scratch[kWarps + 4];
-    __shared__ uint32_t tops[2][kWarps][2];
+    __shared__ uint32_t tops[2][kWarps];
     pdl_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, H = p.num_kv_heads, bs = p.block_size;
     unsigned flags = 0;
     const attn::Find f = attn::find_request<kThreads>(
-        p.num_requests, scratch, [&](int b) { return (int64_t)pages_of(request_of(p, b, flags), bs) * H; });
+        p.num_requests, scratch, [&](int b) { return (int64_t)pages_of(request_of(p, b, flags), bs) * (2 * H); });
     const attn::Shares shares(f.total, gridDim.x);
     if (f.b >= 0) {
         int b = f.b;
@@ -84,72 +84,68 @@ __global__ void __launch_bounds__(kThreads, 8) insert_scaled_kernel(const __grid
         const int64_t u0 = shares.start(blockIdx.x), u1 = shares.start(blockIdx.x + 1);
         int64_t of = u0 - f.before;  // the unit's number in its request
         int turn = 0;
-        const int w = tid % kW, part = w >= kW / 2;
+        const int w = tid % kW;
         for (int64_t u = u0; u < u1; u++, of++) {
-            while (of >= (int64_t)pages_of(r, bs) * H) {
-                of -= (int64_t)pages_of(r, bs) * H;
+            while (of >= (int64_t)pages_of(r, bs) * (2 * H)) {
+                of -= (int64_t)pages_of(r, bs) * (2 * H);
                 r = request_of(p, ++b, ignore);
             }
-            const int pi = (int)(of / H), h = (int)(of - (int64_t)pi * H), blk = r.ctx / bs + pi;
+            // K and V of a head one after the other: their codes lie side by side
+            const int pi = (int)attn::Shares::div(of, 2 * H), hp = (int)(of - (int64_t)pi * (2 * H)), h = hp >> 1, part = hp & 1;
+            const int blk = r.ctx / bs + pi;
             const int64_t first = (int64_t)blk * bs;
             const int lo = pi ? (int)first : r.ctx, hi = (int)min((int64_t)r.ctx + r.n, first + bs);
             const int held = pi ? 0 : r.ctx - (int)first;  // the context's tokens in the page
             const int64_t page = __ldg(p.table + b * p.table_stride + blk);
-            if (page < 0 || page >= p.num_blocks) {
-                flags |= kFlagBlockRange;
-                continue;
-            }
-            int8_t *scale = p.scales + (page * H + h) * 2;
-            const int was0 = held ? page_exponent(p.scales, page, H, h, 0) : kScaleMin;
-            const int was1 = held ? page_exponent(p.scales, page, H, h, 1) : kScaleMin;
-            const uint16_t *src = (part ? p.v + h * p.v_hs : p.k + h * p.k_hs) + (w - part * (kW / 2)) * 8;
+            const uint16_t *src = (part ? p.v + h * p.v_hs : p.k + h * p.k_hs) + w * 8;
             const int64_t ts = part ? p.v_ts : p.k_ts;
-            const int row0 = r.q0 + lo - r.ctx, rows = hi - lo, step = kThreads / kW;
+            const int row0 = r.q0 + lo - r.ctx, rows = hi - lo;
             uint4 v[kHold];
             uint32_t top = 0;
 #pragma unroll
             for (int k = 0; k < kHold; k++) {
-                const int x = tid / kW + k * step;
+                const int x = tid / kW + k * kStep;
                 v[k] = x < rows ? __ldg(reinterpret_cast<const uint4 *>(src + (row0 + x) * ts)) : make_uint4(0, 0, 0, 0);
             }
+            if (page < 0 || page >= p.num_blocks) {
+                flags |= kFlagBlockRange;
+                continue;
+            }
+            const int was = held ? page_exponent(p.scales, page, H, h, part) : kScaleMin;
 #pragma unroll
             for (int k = 0; k < kHold; k++)
                 top = top2(top2(top2(top2(top, v[k].x), v[k].y), v[k].z), v[k].w);
-            for (int x = tid / kW + kHold * step; x < rows; x += step) {
+            for (int x = tid / kW + kHold * kStep; x < rows; x += kStep) {
                 const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src + (row0 + x) * ts));
                 top = top2(top2(top2(top2(top, y.x), y.y), y.z), y.w);
             }
-            top = max(top & 0xffffu, top >> 16);
-            const uint32_t tk = __reduce_max_sync(0xffffffffu, part ? 0u : top), tv = __reduce_max_sync(0xffffffffu, part ? top : 0u);
+            top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
             if (lane == 0)
-                tops[turn][warp][0] = tk, tops[turn][warp][1] = tv;
+                tops[turn][warp] = top;
             __syncthreads();  // everyone has read the old scale too
-            uint32_t most[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < kWarps; i++)
-                most[0] = max(most[0], tops[turn][i][0]), most[1] = max(most[1], tops[turn][i][1]);
+                top = max(top, tops[turn][i]);
             turn ^= 1;
-            const int e0 = max(exponent_of(most[0]), was0), e1 = max(exponent_of(most[1]), was1);
-            // the codes of the context's tokens in the page, where the scale grows: 16 bytes have one part
-            unsigned char *cache = p.cache + ((page * H + h) * bs) * (int64_t)(2 * D);
-            if (held && (e0 > was0 || e1 > was1))
-                for (int x = tid; x < held * (D / 8); x += kThreads) {
-                    const int d = x % (D / 8) >= D / 16 ? e1 - was1 : e0 - was0;
-                    uint4 *at = reinterpret_cast<uint4 *>(cache + (int64_t)x * 16);
-                    if (d)
-                        *at = scale_codes(*at, half2_power(d));
+            const int e = max(exponent_of(top), was);
+            unsigned char *codes = p.cache + ((page * H + h) * bs) * (int64_t)(2 * D) + part * D;
+            // the codes of the context's tokens in the page, where the scale grows
+            if (held && e > was)
+                for (int x = tid; x < held * (D / 16); x += kThreads) {
+                    uint4 *at = reinterpret_cast<uint4 *>(codes + (int64_t)(x / (D / 16)) * (2 * D) + x % (D / 16) * 16);
+                    *at = scale_codes(*at, half2_power(e - was));
                 }
             if (tid == 0)
-                scale[0] = (int8_t)e0, scale[1] = (int8_t)e1;
-            const float s = __int_as_float((127 - (part ? e1 : e0)) << 23);
-            unsigned char *dst = cache + (int64_t)(lo - first) * (2 * D) + w * 8;
+                p.scales[(page * H + h) * 2 + part] = (int8_t)e;
+            const float s = __int_as_float((127 - e) << 23);
+            unsigned char *dst = codes + (int64_t)(lo - first) * (2 * D) + w * 8;
 #pragma unroll
             for (int k = 0; k < kHold; k++) {
-                const int x = tid / kW + k * step;
+                const int x = tid / kW + k * kStep;
                 if (x < rows)
                     *reinterpret_cast<uint2 *>(dst + (int64_t)x * (2 * D)) = encode8(v[k], s);
             }
-            for (int x = tid / kW + kHold * step; x < rows; x += step)
+            for (int x = tid / kW + kHold * kStep; x < rows; x += kStep)
                 *reinterpret_cast<uint2 *>(dst + (int64_t)x * (2 * D)) =
                     encode8(__ldg(reinterpret_cast<const uint4 *>(src + (row0 + x) * ts)), s);
         }
@@ -169,7 +165,7 @@ cudaError_t launch_insert_scaled(const InsertScaledParams &p, cudaStream_t strea
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess)
         return e;
-    const int64_t units = p.num_rows * p.num_kv_heads;  // at most: a page each
+    const int64_t units = p.num_rows * p.num_kv_heads * 2;  // at most: a page each
     const int ctas = (int)(units < 8 * (int64_t)sms ? units : 8 * (int64_t)sms);
     switch (p.head_dim) {
     case 64: return launch_pdl(insert_scaled_kernel<64>, ctas, kThreads, 0, stream, p);

@@ -190,7 +190,13 @@ __global__ void __launch_bounds__(256) compact_kernel(const __grid_constant__ Co
 
 // ------------------------------------------------------------------ the pool
 
+// One cluster does a call's bookkeeping: the k-th free page is known only with all
+// pages before it counted.  A thread has a run of the pool to itself (4 to 16 pages
+// up to 131,072), loads it once, as 16-byte words, and keeps which are free; a
+// prefix over the CTA and one exchange over the cluster number them.  Small pools take
+// fewer CTAs, whose barriers cost less.
 constexpr int kPoolThreads = 1024, kPoolWarps = kPoolThreads / 32, kPoolCtas = 8;
+constexpr int kRun = 16;  // pages that a thread keeps in registers at once
 
 struct PoolShared {
     int sums[kPoolCtas], warps[kPoolWarps];
@@ -224,20 +230,70 @@ __device__ __forceinline__ T cta_prefix(T x, T &sum, T *warps)
     return t + up - x;
 }
 
-// Counts the free pages of this CTA's share [lo, hi) of the pool; returns how many
-// the CTAs before it have, `free` all of the cluster's.
-__device__ __forceinline__ int count_free(cg::cluster_group &cluster, const int32_t *refs, int64_t lo, int64_t hi, int &free, PoolShared &s)
+// This thread's run of the pool, and its free pages in it.
+struct Run {
+    int64_t lo, hi;
+    bool wide;  // 16-byte loads
+
+    __device__ __forceinline__ Run(cg::cluster_group &cluster, const int32_t *refs, int64_t pages)
+    {
+        const int64_t threads = (int64_t)cluster.num_blocks() * kPoolThreads, me = (int64_t)cluster.block_rank() * kPoolThreads + threadIdx.x;
+        const int64_t each = ((pages + threads - 1) / threads + 3) / 4 * 4;
+        lo = min(pages, each * me), hi = min(pages, lo + each);
+        wide = (reinterpret_cast<uintptr_t>(refs) & 15) == 0;
+    }
+    // calls f(i, whether pages i .. i + kRun are free, a bit each) for the run; REPAIR: numbers below 0 become 0 (true if there were any)
+    template <bool REPAIR, typename F>
+    __device__ __forceinline__ bool each(int32_t *refs, F f) const
+    {
+        bool below = false;
+        for (int64_t i = lo; i < hi; i += kRun) {
+            int v[kRun];
+            if (wide && i + kRun <= hi) {
+#pragma unroll
+                for (int k = 0; k < kRun; k += 4) {
+                    const int4 x = __ldcg(reinterpret_cast<const int4 *>(refs + i + k));
+                    v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
+                }
+            } else {
+#pragma unroll
+                for (int k = 0; k < kRun; k++)
+                    v[k] = i + k < hi ? __ldcg(refs + i + k) : 1;
+            }
+            unsigned bits = 0;
+#pragma unroll
+            for (int k = 0; k < kRun; k++) {
+                bits |= (v[k] == 0 || (REPAIR && v[k] < 0) ? 1u : 0u) << k;
+                if (REPAIR && v[k] < 0) {
+                    refs[i + k] = 0;
+                    below = true;
+                }
+            }
+            f(i, bits);
+        }
+        return below;
+    }
+};
+
+// Counts the free pages: this thread's rank of its first, `free` of them all.
+// `first` keeps the first kRun pages' bits.  A cluster barrier.
+template <bool REPAIR>
+__device__ __forceinline__ int rank_free(cg::cluster_group &cluster, const Run &run, int32_t *refs, unsigned &first, int &free, bool &below,
+                                         PoolShared &s)
 {
     int mine = 0;
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kPoolThreads)
-        mine += __ldcg(refs + i) == 0;
+    first = 0;
+    below = run.each<REPAIR>(refs, [&](int64_t i, unsigned bits) {
+        mine += __popc(bits);
+        if (i == run.lo)
+            first = bits;
+    });
     int sum;
-    cta_prefix(mine, sum, s.warps);
+    int before = cta_prefix(mine, sum, s.warps);
     const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     if ((int)threadIdx.x < nc)
         cluster.map_shared_rank(&s.sums[0], threadIdx.x)[rank] = sum;
     cluster.sync();
-    int before = 0;
     free = 0;
     for (int r = 0; r < nc; r++) {
         before += r < rank ? s.sums[r] : 0;
@@ -246,36 +302,44 @@ __device__ __forceinline__ int count_free(cg::cluster_group &cluster, const int3
     return before;
 }
 
-// give(k, page) for the free pages of [lo, hi) in rising order, k from `before` on, below `most`
-template <typename F>
-__device__ __forceinline__ void each_free(const int32_t *refs, int64_t lo, int64_t hi, int before, int most, PoolShared &s, F give)
+// list[k] = the k-th free page, for k < most
+__device__ __forceinline__ void list_free(const Run &run, int32_t *refs, unsigned first, int rank, int most, int32_t *list)
 {
-    for (int64_t i0 = lo; i0 < hi && before < most; i0 += kPoolThreads) {
-        const int64_t i = i0 + threadIdx.x;
-        const bool is = i < hi && __ldcg(refs + i) == 0;
-        int sum;
-        const int k = before + cta_prefix((int)is, sum, s.warps);
-        if (is && k < most)
-            give(k, (int)i);
-        before += sum;
-    }
+    if (run.hi <= run.lo || rank >= most)
+        return;
+    auto put = [&](int64_t i, unsigned bits) {
+        for (; bits && rank < most; bits &= bits - 1)
+            list[rank++] = (int32_t)(i + __ffs(bits) - 1);
+    };
+    if (run.hi - run.lo <= kRun)
+        put(run.lo, first);
+    else
+        run.each<false>(refs, put);
 }
 
-// Pairs, free pages and everything but the pages' contents, by one cluster (the
-// free pages' ranks need all of the pool; 65,536 pages are 32 KB per CTA).
+// Threads that share a row (or pair) where there are so many: whole warps.
+__device__ __forceinline__ int threads_per(int rows, int threads)
+{
+    int per = 32;
+    while (per * 2 * (int64_t)rows <= threads)
+        per *= 2;
+    return per;
+}
+
+// Pairs, free pages and everything but the pages' contents.
 __global__ void __launch_bounds__(kPoolThreads, 1) fork_kernel(const __grid_constant__ ForkParams p)
 {
     __shared__ PoolShared sh;
     pdl_enter();
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), nc = (int)cluster.num_blocks(), tid = threadIdx.x, bs = p.block_size;
+    const int threads = nc * kPoolThreads, me = rank * kPoolThreads + tid;
     unsigned flags = 0;
-    const int64_t share = (p.num_blocks + nc - 1) / nc, lo = min(p.num_blocks, share * rank), hi = min(p.num_blocks, lo + share);
 
-    // ---- the pairs: which are sound, what they copy (each CTA a part; z: the pair's state)
-    for (int i = rank * kPoolThreads + tid; i < p.num_pairs; i += nc * kPoolThreads) {
+    // ---- the pairs: which are sound (w), the page that they copy (x) and its tokens (z)
+    for (int i = me; i < p.num_pairs; i += threads) {
         const int s = __ldg(p.src + i), d = __ldg(p.dst + i);
-        bool ok = s >= 0 && s < p.num_rows && d >= 0 && d < p.num_rows;
+        bool ok = s >= 0 && s < p.num_rows && d >= 0 && d < p.num_rows, bad_page = false;
         int old = -1, tail = 0;
         if (ok) {
             const int64_t len = p.lens[s], held = p.pages[s];
@@ -286,65 +350,48 @@ __global__ void __launch_bounds__(kPoolThreads, 1) fork_kernel(const __grid_cons
                 tail = (int)(len % bs);
                 if (tail) {
                     old = p.table[s * p.table_stride + len / bs];
-                    if (ok && (old < 0 || old >= p.num_blocks)) {
-                        flags |= kFlagBlockRange;
-                        ok = false;
-                        tail = -1;
-                    }
+                    bad_page = ok && (old < 0 || old >= p.num_blocks);
                 }
             }
         }
-        if (!ok && tail >= 0)
-            flags |= kFlagLength;
+        if (!ok || bad_page)
+            flags |= bad_page ? kFlagBlockRange : kFlagLength;
+        ok = ok && !bad_page;
         p.copies[i] = make_int4(old, -1, ok ? tail : 0, ok);
     }
     cluster.sync();  // all of `copies` is there; every CTA of the cluster runs
 
-    // ---- the k-th free page goes to the k-th sound pair that needs one (found by every CTA for itself)
+    // ---- the k-th free page goes to the k-th sound pair in need
+    const Run run(cluster, p.refs, p.num_blocks);
+    unsigned first;
     int free;
-    const int before = count_free(cluster, p.refs, lo, hi, free, sh);
-    int need = 0;
-    for (int i0 = 0; i0 < p.num_pairs; i0 += kPoolThreads) {
-        const int i = i0 + tid;
-        const bool needs = i < p.num_pairs && __ldcg(&p.copies[i]).z > 0;
-        int sum;
-        cta_prefix((int)needs, sum, sh.warps);
-        need += sum;
-    }
-    cluster.sync();  // nobody reads `copies` as it was any more
-    // ranks of the pairs: as y = -2 - rank, by the first CTA; then the pages' owners look for them
+    bool below;
+    const int at = rank_free<false>(cluster, run, p.refs, first, free, below, sh);
+    list_free(run, p.refs, first, at, min(free, p.num_pairs), p.free_list);
+    cluster.sync();
     if (rank == 0) {
-        int at = 0;
+        int before = 0;
         for (int i0 = 0; i0 < p.num_pairs; i0 += kPoolThreads) {
             const int i = i0 + tid;
             const bool needs = i < p.num_pairs && __ldcg(&p.copies[i]).z > 0;
             int sum;
-            const int k = at + cta_prefix((int)needs, sum, sh.warps);
+            const int k = before + cta_prefix((int)needs, sum, sh.warps);
             if (needs) {
-                p.copies[i].y = -1;
-                p.copies[p.num_pairs + k].x = i;  // the k-th pair in need
-                if (k >= free) {                  // none left for it
+                if (k < free) {
+                    p.copies[i].y = __ldcg(p.free_list + k);
+                } else {
                     flags |= kFlagPages;
                     p.copies[i].z = 0;
                     p.copies[i].w = 0;
                 }
             }
-            at += sum;
+            before += sum;
         }
     }
     cluster.sync();
-    each_free(p.refs, lo, hi, before, min(need, free), sh, [&](int k, int page) {
-        const int i = __ldcg(&p.copies[p.num_pairs + k].x);
-        p.copies[i].y = page;
-    });
-    cluster.sync();
 
-    // ---- table rows, references, lengths: the pairs' entries over all threads
-    const int threads = nc * kPoolThreads, me = rank * kPoolThreads + tid;
-    // as many threads to a pair as there are for each, at least a warp
-    int per = 32;
-    while (per * 2 * p.num_pairs <= threads)
-        per *= 2;
+    // ---- table rows, references, lengths
+    const int per = threads_per(p.num_pairs, threads);
     for (int i = me / per; i < p.num_pairs; i += threads / per) {
         const int4 c = __ldcg(&p.copies[i]);
         if (!c.w)
@@ -353,6 +400,7 @@ __global__ void __launch_bounds__(kPoolThreads, 1) fork_kernel(const __grid_cons
         const int len = p.lens[s], full = len / bs;
         const int32_t *from = p.table + s * p.table_stride;
         int32_t *to = p.table + d * p.table_stride;
+#pragma unroll 4
         for (int k = me % per; k < full; k += per) {
             const int page = from[k];
             to[k] = page;
@@ -403,28 +451,26 @@ __global__ void __launch_bounds__(128) page_copy_kernel(const __grid_constant__ 
             p.layers.scales[layer][((int64_t)c.x * p.num_kv_heads + h) * 2 + tid];
 }
 
-// Entries given back, then pages taken, by one cluster.
+// Entries given back, then pages taken.
 __global__ void __launch_bounds__(kPoolThreads, 1) resize_kernel(const __grid_constant__ ResizeParams p)
 {
     __shared__ PoolShared sh;
     pdl_enter();
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), nc = (int)cluster.num_blocks(), tid = threadIdx.x, bs = p.block_size;
+    const int threads = nc * kPoolThreads, me = rank * kPoolThreads + tid;
     unsigned flags = 0;
-    const int64_t share = (p.num_blocks + nc - 1) / nc, lo = min(p.num_blocks, share * rank), hi = min(p.num_blocks, lo + share);
     // pages that row r holds and wants, whether both fit the table
     auto row = [&](int r, int &have, int &want) {
-        have = __ldcg(p.pages + r);
+        have = p.pages[r];
         const int tokens = __ldg(p.tokens + r);
         want = tokens / bs + (tokens % bs > 0);
         return have >= 0 && have <= p.table_blocks && tokens >= 0 && want <= p.table_blocks;
     };
 
-    // ---- back to the pool; p.before holds the rows' needs for now
-    const int threads = nc * kPoolThreads, me = rank * kPoolThreads + tid;
-    int per = 32;
-    while (per * 2 * (int64_t)p.num_rows <= threads)
-        per *= 2;
+    // ---- back to the pool (nothing waits for the counts: one that falls below 0
+    // is put right where the pool is read); what each row asks for
+    const int per = threads_per(p.num_rows, threads);
     for (int r = me / per; r < p.num_rows; r += threads / per) {
         int have, want;
         const bool ok = row(r, have, want);
@@ -432,26 +478,21 @@ __global__ void __launch_bounds__(kPoolThreads, 1) resize_kernel(const __grid_co
             flags |= kFlagLength;
         int32_t *entries = p.table + r * p.table_stride;
         if (ok)
+#pragma unroll 4
             for (int k = want + me % per; k < have; k += per) {
                 const int page = entries[k];
                 entries[k] = -1;
-                if (page < 0 || page >= p.num_blocks) {
+                if (page >= 0 && page < p.num_blocks)
+                    atomicSub(p.refs + page, 1);
+                else
                     flags |= kFlagBlockRange;
-                } else if (atomicSub(p.refs + page, 1) <= 0) {
-                    atomicAdd(p.refs + page, 1);  // nobody held it
-                    flags |= kFlagRefs;
-                }
             }
-        __syncwarp();  // (per >= 32: a row's threads are whole warps)
         if (me % per == 0)
             p.before[r] = ok && want > have ? want - have : 0;
     }
-    __threadfence();
     cluster.sync();
 
-    int free;
-    const int before = count_free(cluster, p.refs, lo, hi, free, sh);
-    // ---- the needs of the rows before each, by the first CTA
+    // ---- the first CTA sums the rows' needs while all count the pool
     if (rank == 0) {
         int64_t at = 0;
         for (int r0 = 0; r0 < p.num_rows; r0 += kPoolThreads) {
@@ -466,40 +507,52 @@ __global__ void __launch_bounds__(kPoolThreads, 1) resize_kernel(const __grid_co
         if (tid == 0)
             p.before[p.num_rows] = (int32_t)min(at, (int64_t)INT32_MAX);
     }
+    const Run run(cluster, p.refs, p.num_blocks);
+    unsigned first;
+    int free;
+    bool below;
+    const int at = rank_free<true>(cluster, run, p.refs, first, free, below, sh);
+    if (below)
+        flags |= kFlagRefs;
+    list_free(run, p.refs, first, at, min(free, __ldcg(p.before + p.num_rows)), p.free_list);
     cluster.sync();
-    const int need = __ldcg(p.before + p.num_rows);
-    each_free(p.refs, lo, hi, before, min(need, free), sh, [&](int k, int page) {
-        // the last row with before <= k: rows that need none share their `before` with the next
-        int a = 0, z = p.num_rows;
-        while (z - a > 1) {
-            const int m = (a + z) >> 1;
-            if (__ldcg(p.before + m) <= k)
-                a = m;
-            else
-                z = m;
-        }
-        const int first = __ldcg(p.before + a);
-        if (__ldcg(p.before + a + 1) > free)
-            return;  // not all of what the row asks for is there
+
+    // ---- rows served in their order, as far as the pages go
+    for (int r = me / per; r < p.num_rows; r += threads / per) {
         int have, want;
-        row(a, have, want);
-        p.table[a * p.table_stride + have + (k - first)] = page;
-        p.refs[page] = 1;
-    });
-    cluster.sync();  // everyone has read `pages`
+        const bool ok = row(r, have, want);
+        const int k0 = __ldcg(p.before + r), k1 = __ldcg(p.before + r + 1);
+        const bool served = ok && want > have && k1 <= free;
+        if (served) {
+            int32_t *entries = p.table + r * p.table_stride;
+#pragma unroll 4
+            for (int k = me % per; k < want - have; k += per) {
+                const int page = __ldcg(p.free_list + k0 + k);
+                entries[have + k] = page;
+                p.refs[page] = 1;
+            }
+        }
+        if (ok && want > have && !served)
+            flags |= kFlagPages;
+    }
+    cluster.sync();  // every warp has read `pages`
     for (int r = me; r < p.num_rows; r += threads) {
         int have, want;
-        if (!row(r, have, want) || have == want)
-            continue;
-        if (want > have && __ldcg(p.before + r + 1) > free) {
-            flags |= kFlagPages;
-            continue;
-        }
-        p.pages[r] = want;
+        if (row(r, have, want) && have != want && (want < have || __ldcg(p.before + r + 1) <= free))
+            p.pages[r] = want;
     }
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (flags && (tid & 31) == 0 && p.error_flags)
         atomicOr(p.error_flags, flags);
+}
+
+// CTAs of the cluster: 8 pages a thread, so that they are loaded at once.
+int pool_ctas(int64_t pages)
+{
+    int nc = 1;
+    while (nc < kPoolCtas && pages > (int64_t)nc * kPoolThreads * 8)
+        nc *= 2;
+    return nc;
 }
 
 }  // namespace
@@ -513,7 +566,8 @@ cudaError_t launch_compact(const CompactParams &p, bool scaled, cudaStream_t str
 
 cudaError_t launch_fork(const ForkParams &p, cudaStream_t stream)
 {
-    return launch_pdl_grid(fork_kernel, dim3(kPoolCtas), kPoolThreads, 0, kPoolCtas, stream, p);
+    const int nc = pool_ctas(p.num_blocks);
+    return launch_pdl_grid(fork_kernel, dim3((unsigned)nc), kPoolThreads, 0, nc, stream, p);
 }
 
 cudaError_t launch_page_copies(const PageCopyParams &p, cudaStream_t stream)
@@ -524,7 +578,8 @@ cudaError_t launch_page_copies(const PageCopyParams &p, cudaStream_t stream)
 
 cudaError_t launch_resize(const ResizeParams &p, cudaStream_t stream)
 {
-    return launch_pdl_grid(resize_kernel, dim3(kPoolCtas), kPoolThreads, 0, kPoolCtas, stream, p);
+    const int nc = pool_ctas(p.num_blocks);
+    return launch_pdl_grid(resize_kernel, dim3((unsigned)nc), kPoolThreads, 0, nc, stream, p);
 }
 
 }  // namespace dspark

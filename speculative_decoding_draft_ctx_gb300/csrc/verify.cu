@@ -10,8 +10,11 @@
 // The children's p and q are single entries, read all at once beforehand; a chain
 // needs no sums before its last row.
 //
-// Sums are integers in units of 2^-48: entries are rounded to them once (those
-// below 2^-25 lose bits), sums are exact and in any order the same.  The token
+// Sums are integers in units of 2^-46: entries are rounded to them once (those
+// below 2^-23 lose bits), sums are exact and in any order the same.  An entry
+// becomes two integers of 23 bits by additions of 2^23 in fp32 (four paired
+// operations at the full rate; a conversion to 64 bits runs at a small part of it:
+// 44 us against 21 for 64 draws from 131,072 tokens).  The token
 // drawn is a whole number that a user compares with one drawn in 64-bit floating
 // point: with fp32 terms a rounding of 2^-26 in a heavy entry moves the border of
 // every one behind it, which changes one token in some hundreds over a vocabulary
@@ -36,12 +39,22 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32, kMost = 16;
 constexpr int kStep = 128;  // entries that a warp takes at once
-constexpr double kUnit = 281474976710656.0;  // 2^48
+constexpr int kKept = 512;  // entries of p and q that a warp of a tree's CTA can keep in shared memory
+constexpr double kUnit = 70368744177664.0;  // 2^46
 
 typedef unsigned long long u64;
 
-__device__ __forceinline__ float clean(float x) { return fminf(fmaxf(x, 0.0f), 1.0f); }  // NaN: 0
-__device__ __forceinline__ u64 fixed(float x) { return __float2ull_rn(x * 281474976710656.0f); }
+__device__ __forceinline__ float clean(float x) { return __saturatef(x); }  // to [0, 1]; NaN: 0
+
+// x in [0, 1] in units of 2^-46: hi of 2^-23, what that leaves to nearest even
+__device__ __forceinline__ int64_t fixed(float x)
+{
+    constexpr float k = 8388608.0f;  // 2^23
+    const float t = fmaf(x, k, k);                    // bits: 0x4b000000 + the nearest integer to x 2^23
+    const float rest = fmaf(x, k, __fsub_rn(k, t));   // exact, at most 1/2
+    const float lo = fmaf(rest, k, 1.5f * k);         // bits: 0x4b400000 + the nearest integer to rest 2^23
+    return (int64_t)(__float_as_int(t) - 0x4b000000) * 8388608 + (__float_as_int(lo) - 0x4b400000);
+}
 
 template <bool BF16>
 __device__ __forceinline__ const unsigned char *row_of(const void *base, int64_t stride, int64_t row)
@@ -96,13 +109,13 @@ struct Share {
         mant = (u64)(b & 0xfffffffffffffll) | 0x10000000000000ull;
         shift = 1075 - (int)((b >> 52) & 0x7ff);
     }
-    // floor(S q), or the largest number where that takes more than 64 bits
-    __device__ __forceinline__ u64 times(u64 q) const
+    // floor(S q), or the largest number where that takes more than 63 bits (q at most 2^46, S at least 1)
+    __device__ __forceinline__ int64_t times(int64_t q) const
     {
-        const u64 hi = __umul64hi(q, mant), lo = q * mant;
-        if (shift <= 0 || (hi >> shift) != 0)
-            return q ? ~0ull : 0ull;
-        return shift < 64 ? (lo >> shift) | (hi << (64 - shift)) : hi >> (shift - 64);
+        const u64 hi = __umul64hi((u64)q, mant), lo = (u64)q * mant;
+        if (shift <= 0 || (hi >> (shift - 1)) != 0)
+            return q ? INT64_MAX : 0;
+        return (int64_t)((lo >> shift) | (hi << (64 - shift)));
     }
 };
 
@@ -111,11 +124,11 @@ enum Left { kAll, kLessQ, kLessSQ };  // R = p; max(p - q, 0); max(p - S q, 0)
 template <int LEFT>
 __device__ __forceinline__ u64 left_of(float p, float q, const Share &s)
 {
-    const u64 a = fixed(clean(p));
+    const int64_t a = fixed(clean(p));
     if (LEFT == kAll)
-        return a;
-    const u64 b = LEFT == kLessQ ? fixed(clean(q)) : s.times(fixed(clean(q)));
-    return a > b ? a - b : 0;
+        return (u64)a;
+    const int64_t b = fixed(clean(q));
+    return (u64)max((int64_t)0, a - (LEFT == kLessQ ? b : s.times(b)));
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 x)
@@ -173,6 +186,44 @@ struct Rows {
         }
         return t;
     }
+    // the same of a piece of up to kKept entries that is kept in shared memory:
+    // loaded where `fresh`, read from there in the next rounds of the same row
+    template <int LEFT>
+    __device__ __forceinline__ u64 sum_kept(int64_t from, int64_t to, const Share &s, float4 *kept, bool fresh) const
+    {
+        const int lane = threadIdx.x & 31;
+        to = min(to, vocab);
+        constexpr int kU = kKept / kStep;
+        float x[kU][4], y[kU][4];
+#pragma unroll
+        for (int u = 0; u < kU; u++) {
+            const int64_t i = from + u * kStep + 4 * lane;
+            if (fresh) {
+                load4<TB>(p, i, to, wide, x[u]);
+                load4<DK == 2>(q, i, to, wide, y[u]);
+            } else {
+                *reinterpret_cast<float4 *>(x[u]) = kept[(2 * u) * 32 + lane];
+                *reinterpret_cast<float4 *>(y[u]) = kept[(2 * u + 1) * 32 + lane];
+            }
+        }
+        u64 t = 0;
+#pragma unroll
+        for (int u = 0; u < kU; u++) {
+            if (fresh) {
+                kept[(2 * u) * 32 + lane] = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
+                kept[(2 * u + 1) * 32 + lane] = make_float4(y[u][0], y[u][1], y[u][2], y[u][3]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                t += left_of<LEFT>(x[u][k], y[u][k], s);
+        }
+        return t;
+    }
+    __device__ __forceinline__ u64 sum_kept_by(Left kind, int64_t from, int64_t to, const Share &s, float4 *kept, bool fresh) const
+    {
+        return kind == kAll ? sum_kept<kAll>(from, to, s, kept, fresh)
+               : kind == kLessQ ? sum_kept<kLessQ>(from, to, s, kept, fresh) : sum_kept<kLessSQ>(from, to, s, kept, fresh);
+    }
     __device__ __forceinline__ u64 sum_by(Left kind, int64_t from, int64_t to, const Share &s) const
     {
         if (DK == 0 || kind == kAll)
@@ -190,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     __shared__ int gone[kVerifyRows];                                    // rejected tokens of the last row (no draft)
     __shared__ u64 sums[2][kMost], pieces[kWarps], parts[kWarps];
     __shared__ int first_lost;
+    extern __shared__ float4 kept[];  // trees, pieces of up to kKept entries: [warps][kKept / kStep][p, q][32]
     pdl_enter();
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), b = blockIdx.x / nc;
@@ -236,7 +288,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 
     // pieces of the vocabulary: warp g of the cluster has [g * piece, (g + 1) * piece)
     const int64_t all = (int64_t)nc * kWarps, piece = (a.vocab + all * kStep - 1) / (all * kStep) * kStep;
-    int round = 0, lost = 0;  // lost: entries of `gone`
+    const bool keep = DK != 0 && a.parents && piece <= kKept;
+    int round = 0, lost = 0, kept_row = -1;  // lost: entries of `gone`; kept_row: the row in `kept`
     Share share;
     share.set(1.0);
     share.s = 0.0;
@@ -244,11 +297,18 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     auto total = [&](int cur, Left kind) -> u64 {
         const Rows<TB, DK> rows(a, r0 + cur);
         const int64_t g = (int64_t)rank * kWarps + warp;
-        u64 t = warp_sum(rows.sum_by(kind, g * piece, (g + 1) * piece, share));
+        u64 t;
+        if (keep) {
+            t = rows.sum_kept_by(kind, g * piece, (g + 1) * piece, share, kept + warp * (kKept / 2), cur != kept_row);
+            kept_row = cur;
+        } else {
+            t = rows.sum_by(kind, g * piece, (g + 1) * piece, share);
+        }
+        t = warp_sum(t);
         if (DK == 0)
             for (int k = 0; k < lost; k++)
                 if (gone[k] / piece == g)
-                    t -= fixed(entry<TB>(rows.p, gone[k]));
+                    t -= (u64)fixed(entry<TB>(rows.p, gone[k]));
         if (lane == 0)
             pieces[warp] = t;
         __syncthreads();
@@ -406,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                 if (DK == 0)
                     for (int k = 0; k < lost; k++)
                         if (gone[k] >= mine0 && gone[k] < mine1)
-                            x -= fixed(entry<TB>(rows.p, gone[k]));
+                            x -= (u64)fixed(entry<TB>(rows.p, gone[k]));
             }
             if (lane == 0)
                 parts[warp] = x;
@@ -463,11 +523,15 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 template <bool TB, int DK>
 cudaError_t launch(const VerifyParams &p, int nc, cudaStream_t stream)
 {
-    // (a driver call that costs nothing next to the launch; no state to keep per device)
+    // (driver calls that cost nothing next to the launch; no state to keep per device)
+    const int64_t all = (int64_t)nc * kWarps, piece = (p.vocab + all * kStep - 1) / (all * kStep) * kStep;
+    const int smem = DK != 0 && p.parents && piece <= kKept ? kWarps * kKept * 8 : 0;
     cudaError_t e = nc > 8 ? cudaFuncSetAttribute(verify_kernel<TB, DK>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) : cudaSuccess;
+    if (e == cudaSuccess && smem > 0)
+        e = cudaFuncSetAttribute(verify_kernel<TB, DK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl_grid(verify_kernel<TB, DK>, dim3((unsigned)p.num_requests * nc), kThreads, 0, nc, stream, p);
+    return launch_pdl_grid(verify_kernel<TB, DK>, dim3((unsigned)p.num_requests * nc), kThreads, smem, nc, stream, p);
 }
 
 }  // namespace

@@ -18,7 +18,7 @@ entries hold the page; 0 is free.  Pages are given out lowest number first.
 
 from __future__ import annotations
 
-import ctypes
+from array import array
 
 from . import draft_attn as _da
 from ._binding import KV_FP8_E4M3, check, lib
@@ -130,7 +130,7 @@ def verify_drafts(target_probs, draft_tokens, row_start, uniforms, max_accepted,
 
 
 def _layers(kv_caches, block_scales):
-    """(device, sizes of a layer's cache as the calls take them): layers alike, their addresses in host arrays."""
+    """(device, host arrays, the caches as the calls take them): layers alike."""
     caches = [kv_caches] if isinstance(kv_caches, torch.Tensor) else list(kv_caches)
     if not caches:
         _fail("kv_caches is empty")
@@ -138,7 +138,8 @@ def _layers(kv_caches, block_scales):
         _fail(f"kv_caches must be tensors, got {type(caches[0]).__name__}")
     dev, shape, dtype = caches[0].device, caches[0].shape, caches[0].dtype
     blocks, H, bs, D, kv_dtype = _cache(caches[0], dev)
-    for i, x in enumerate(caches[1:], 1):
+    for i in range(1, len(caches)):
+        x = caches[i]
         if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.device != dev or x.shape != shape or not x.is_contiguous():
             _fail(f"kv_caches[{i}] is not like kv_caches[0]: {dtype} of shape {tuple(shape)} on {dev}, contiguous")
     L = len(caches)
@@ -151,9 +152,13 @@ def _layers(kv_caches, block_scales):
             _fail(f"{len(scales)} block_scales, {L} caches")
         for i, x in enumerate(scales):
             _block_scales(f"block_scales[{i}]", x, caches[0])
-    at = (ctypes.c_void_p * L)(*[x.data_ptr() for x in caches])
-    scales_at = (ctypes.c_void_p * L)(*[x.data_ptr() for x in scales]) if scales is not None else None
-    return dev, bs, (at, scales_at, L, blocks, H, bs, D, kv_dtype)
+    # host arrays of addresses; the call keeps them (`hold`) until it has read them
+    hold = array("Q", [x.data_ptr() for x in caches])
+    at, scales_at = hold.buffer_info()[0], 0
+    if scales is not None:
+        hold = (hold, array("Q", [x.data_ptr() for x in scales]))
+        scales_at = hold[1].buffer_info()[0]
+    return dev, hold, (at, scales_at, L, blocks, H, bs, D, kv_dtype)
 
 
 def compact_kv(kv_caches, block_table, context_lens, rows, counts, first=1, block_scales=None, new_lens=None,
@@ -173,7 +178,7 @@ def compact_kv(kv_caches, block_table, context_lens, rows, counts, first=1, bloc
     largest that comes in, and what the page holds is encoded anew.
     """
     _load()
-    dev, _, layers = _layers(kv_caches, block_scales)
+    dev, hold, layers = _layers(kv_caches, block_scales)
     B, stride, entries = _table(block_table, context_lens, dev)
     R, width = _tensor("rows", rows, torch.int32, dev, 2)
     if R != B:
@@ -214,7 +219,7 @@ def fork_kv(kv_caches, block_table, pages, lens, src, dst, refs, block_scales=No
     free one (FLAG_PAGES; they are given out in the order of the pairs).
     """
     _load()
-    dev, bs, layers = _layers(kv_caches, block_scales)
+    dev, hold, layers = _layers(kv_caches, block_scales)
     R, stride, entries = _table(block_table, pages, dev)
     _ints("lens", lens, R, dev)
     n = _tensor("src", src, torch.int32, dev, 1)[0]
@@ -257,7 +262,7 @@ def resize_kv(block_table, pages, tokens, refs, block_size, error_flags=None, st
         with _on(dev, stream):
             return resize_kv(block_table, pages, tokens, refs, block_size, error_flags)
     L = lib()
-    size = max(0, L.dspark_kv_resize_workspace(R))
+    size = max(0, L.dspark_kv_resize_workspace(R, blocks))
     work = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
     check(L.dspark_kv_resize(block_table.data_ptr(), stride, entries, pages.data_ptr(), tokens.data_ptr(), R, refs.data_ptr(), blocks,
                              block_size, work.data_ptr() if size else 0, size, flags, _current(dev)))

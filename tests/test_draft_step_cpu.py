@@ -72,7 +72,7 @@ FORK_BASE = dict(caches=layers(FAKE), scales=None, L=1, blocks=4, nkv=2, bs=16, 
 
 @pytest.mark.parametrize("over,want", [
     (dict(L=-1), BAD), (dict(bs=0), BLOCK), (dict(blocks=0), BAD), (dict(cols=0), BAD), (dict(pages=0), BAD), (dict(lens=0), BAD), (dict(src=0), BAD),
-    (dict(dst=0), BAD), (dict(refs=0), BAD), (dict(refs=FAKE + 1282), ALIGN), (dict(n=4097), BAD), (dict(n=-1), BAD), (dict(bytes=63), BAD),
+    (dict(dst=0), BAD), (dict(refs=0), BAD), (dict(refs=FAKE + 1282), ALIGN), (dict(n=4097), BAD), (dict(n=-1), BAD), (dict(bytes=39), BAD),
     (dict(work=0), BAD), (dict(work=FAKE + 8), ALIGN), (dict(lens=FAKE + 256), BAD), (dict(dst=FAKE + 256), BAD), (dict(refs=FAKE + 16), BAD),
     (dict(n=0), OK), (dict(R=0), OK)])
 def test_fork_status(L, over, want):
@@ -86,7 +86,7 @@ RESIZE_BASE = dict(table=FAKE, stride=4, cols=4, pages=FAKE + 256, tokens=FAKE +
 
 @pytest.mark.parametrize("over,want", [
     (dict(bs=0), BLOCK), (dict(blocks=0), BAD), (dict(blocks=1 << 31), BAD), (dict(cols=0), BAD), (dict(stride=3), BAD), (dict(pages=0), BAD),
-    (dict(tokens=0), BAD), (dict(refs=0), BAD), (dict(R=-1), BAD), (dict(bytes=15), BAD), (dict(work=0), BAD), (dict(work=FAKE + 8), ALIGN),
+    (dict(tokens=0), BAD), (dict(refs=0), BAD), (dict(R=-1), BAD), (dict(bytes=51), BAD), (dict(work=0), BAD), (dict(work=FAKE + 8), ALIGN),
     (dict(tokens=FAKE + 256), BAD), (dict(refs=FAKE + 500), BAD), (dict(pages=FAKE + 32), BAD), (dict(R=0), OK)])
 def test_resize_status(L, over, want):
     assert status(L, "dspark_kv_resize", RESIZE, RESIZE_BASE, over) == want
@@ -120,7 +120,8 @@ def test_scaled_attention_status(L, over, want):
 
 def test_workspace_queries(L):
     assert L.dspark_kv_fork_workspace(0) == 0 and L.dspark_kv_fork_workspace(-1) == -1 and L.dspark_kv_fork_workspace(4097) == -1
-    assert L.dspark_kv_resize_workspace(0) == 0 and L.dspark_kv_resize_workspace(-1) == -1 and L.dspark_kv_resize_workspace(5) >= 24
+    assert L.dspark_kv_resize_workspace(0, 9) == 0 and L.dspark_kv_resize_workspace(5, 9) >= 60
+    assert L.dspark_kv_resize_workspace(-1, 9) == -1 and L.dspark_kv_resize_workspace(5, 0) == -1 and L.dspark_kv_resize_workspace(5, 1 << 31) == -1
     assert L.dspark_tree_attention_scaled_workspace(0, 4, 2, 128, 3) == 0
     for bad in ((-1, 4, 2, 128, 3), (5, 3, 2, 128, 3), (5, 4, 2, 96, 3), (5, 4, 0, 128, 3), (5, 4, 2, 128, -3)):
         assert L.dspark_tree_attention_scaled_workspace(*bad) == -1
