@@ -129,7 +129,7 @@ def _cache(kv_cache, device):
 def _block_scales(name, x, kv_cache):
     """The exponents of a page-scaled cache: int8, a pair per page and head."""
     shape = (kv_cache.shape[0], kv_cache.shape[1], 2)
-    if tuple(_tensor(name, x, torch.int8, kv_cache.device, 3)) != shape:
+    if _tensor(name, x, torch.int8, kv_cache.device, 3) != shape:
         _fail(f"{name} must have shape {shape}, got {tuple(x.shape)}")
 
 
