@@ -46,14 +46,28 @@ typedef unsigned long long u64;
 
 __device__ __forceinline__ float clean(float x) { return __saturatef(x); }  // to [0, 1]; NaN: 0
 
-// x in [0, 1] in units of 2^-46: hi of 2^-23, what that leaves to nearest even
-__device__ __forceinline__ int64_t fixed(float x)
+// x in [0, 1] as two integers, hi of 2^-23 and, of what that leaves, lo of 2^-46
+// to nearest even, offset by kHi and kLo: sums and differences are taken of the
+// offset ones.
+constexpr int kHi = 0x4b000000, kLo = 0x4b400000;
+
+__device__ __forceinline__ void split(float x, int &hi, int &lo)
 {
     constexpr float k = 8388608.0f;  // 2^23
-    const float t = fmaf(x, k, k);                    // bits: 0x4b000000 + the nearest integer to x 2^23
-    const float rest = fmaf(x, k, __fsub_rn(k, t));   // exact, at most 1/2
-    const float lo = fmaf(rest, k, 1.5f * k);         // bits: 0x4b400000 + the nearest integer to rest 2^23
-    return (int64_t)(__float_as_int(t) - 0x4b000000) * 8388608 + (__float_as_int(lo) - 0x4b400000);
+    const float t = fmaf(x, k, k);                   // bits: kHi + the nearest integer to x 2^23
+    const float rest = fmaf(x, k, __fsub_rn(k, t));  // exact, at most 1/2
+    hi = __float_as_int(t);
+    lo = __float_as_int(fmaf(rest, k, 1.5f * k));    // bits: kLo + the nearest integer to rest 2^23
+}
+
+__device__ __forceinline__ int64_t joined(int hi, int lo) { return (int64_t)hi * 8388608 + lo; }
+
+// x in [0, 1] in units of 2^-46
+__device__ __forceinline__ int64_t fixed(float x)
+{
+    int hi, lo;
+    split(x, hi, lo);
+    return joined(hi - kHi, lo - kLo);
 }
 
 template <bool BF16>
@@ -97,38 +111,42 @@ __device__ __forceinline__ void load4(const unsigned char *row, int64_t i, int64
     }
 }
 
-// S as mant * 2^-shift, mant in [2^52, 2^53); S >= 1 wherever it is not 0.
+// S, and as a sum of two fp32 numbers (48 bits).
 struct Share {
     double s;
-    u64 mant;
-    int shift;
+    float hi, lo;
     __device__ __forceinline__ void set(double x)
     {
         s = x;
-        const long long b = __double_as_longlong(x);
-        mant = (u64)(b & 0xfffffffffffffll) | 0x10000000000000ull;
-        shift = 1075 - (int)((b >> 52) & 0x7ff);
-    }
-    // floor(S q), or the largest number where that takes more than 63 bits (q at most 2^46, S at least 1)
-    __device__ __forceinline__ int64_t times(int64_t q) const
-    {
-        const u64 hi = __umul64hi((u64)q, mant), lo = (u64)q * mant;
-        if (shift <= 0 || (hi >> (shift - 1)) != 0)
-            return q ? INT64_MAX : 0;
-        return (int64_t)((lo >> shift) | (hi << (64 - shift)));
+        hi = (float)x;
+        lo = (float)(x - (double)hi);
     }
 };
 
 enum Left { kAll, kLessQ, kLessSQ };  // R = p; max(p - q, 0); max(p - S q, 0)
 
+// Adds one entry of what is left to (hi, lo), units of 2^-23 and 2^-46.
 template <int LEFT>
-__device__ __forceinline__ u64 left_of(float p, float q, const Share &s)
+__device__ __forceinline__ void add_left(float p, float q, const Share &s, int &hi, int &lo)
 {
-    const int64_t a = fixed(clean(p));
-    if (LEFT == kAll)
-        return (u64)a;
-    const int64_t b = fixed(clean(q));
-    return (u64)max((int64_t)0, a - (LEFT == kLessQ ? b : s.times(b)));
+    int xh, xl, yh = kHi, yl = kLo;
+    const float x = clean(p);
+    split(x, xh, xl);
+    if constexpr (LEFT == kAll) {
+        hi += xh - yh, lo += xl - yl;
+    } else if constexpr (LEFT == kLessQ) {
+        const float y = clean(q);
+        split(y, yh, yl);
+        if (x > y)
+            hi += xh - yh, lo += xl - yl;
+    } else {
+        // S q as y + rest, rest below half a unit of y; a y above 1 leaves nothing
+        const float z = clean(q), y = z * s.hi, rest = fmaf(z, s.lo, fmaf(z, s.hi, -y));
+        split(y, yh, yl);
+        const int r = __float_as_int(fmaf(rest, 70368744177664.0f, 12582912.0f)) - kLo;  // rest 2^46 to the nearest integer
+        if (y <= 1.0f && x - y > rest)
+            hi += xh - yh, lo += xl - yl - r;
+    }
 }
 
 __device__ __forceinline__ u64 warp_sum(u64 x)
@@ -139,98 +157,112 @@ __device__ __forceinline__ u64 warp_sum(u64 x)
     return x;
 }
 
+// N entries of what is left, in 32 bits until they are joined
+template <int LEFT, int N>
+__device__ __forceinline__ u64 left_of(const float (&p)[N], const float (&q)[N], const Share &s)
+{
+    static_assert(N <= 64, "32-bit sums");
+    int hi = 0, lo = 0;
+#pragma unroll
+    for (int k = 0; k < N; k++)
+        add_left<LEFT>(p[k], q[k], s, hi, lo);
+    return (u64)joined(hi, lo);
+}
+
+template <int LEFT>
+__device__ __forceinline__ u64 left_of_one(float p, float q, const Share &s)
+{
+    int hi = 0, lo = 0;
+    add_left<LEFT>(p, q, s, hi, lo);
+    return (u64)joined(hi, lo);
+}
+
 template <bool TB, int DK>  // target bf16; draft: 0 none, 1 fp32, 2 bf16
 struct Rows {
     const unsigned char *p, *q;
     bool wide;
-    int64_t vocab;
 
     __device__ __forceinline__ Rows(const VerifyParams &a, int64_t row)
     {
         p = row_of<TB>(a.target, a.target_stride, row);
         q = DK ? row_of<DK == 2>(a.draft, a.draft_stride, row) : p;
         wide = (((uintptr_t)p & (TB ? 7 : 15)) | ((uintptr_t)q & (DK == 0 ? (TB ? 7 : 15) : DK == 2 ? 7 : 15))) == 0;
-        vocab = a.vocab;
     }
-    // this lane's entries of a warp's piece [from, to), multiples of kStep apart
-    template <int LEFT>
-    __device__ __forceinline__ u64 sum(int64_t from, int64_t to, const Share &s) const
-    {
-        const int lane = threadIdx.x & 31;
-        u64 t = 0;
-        to = min(to, vocab);
-        constexpr int kU = 4;
-        int64_t i = from + 4 * lane;
-        for (; i - 4 * lane + kU * kStep <= to; i += kU * kStep) {
-            float x[kU][4], y[kU][4];
-#pragma unroll
-            for (int u = 0; u < kU; u++) {
-                load4<TB>(p, i + u * kStep, vocab, wide, x[u]);
-                if (LEFT != kAll)
-                    load4<DK == 2>(q, i + u * kStep, vocab, wide, y[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < kU; u++)
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    t += left_of<LEFT>(x[u][k], LEFT != kAll ? y[u][k] : 0.0f, s);
-        }
-        for (; i < to; i += kStep) {
-            float x[4], y[4];
-            load4<TB>(p, i, to, wide, x);
-            if (LEFT != kAll)
-                load4<DK == 2>(q, i, to, wide, y);
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                t += left_of<LEFT>(x[k], LEFT != kAll ? y[k] : 0.0f, s);
-        }
-        return t;
-    }
-    // the same of a piece of up to kKept entries that is kept in shared memory:
-    // loaded where `fresh`, read from there in the next rounds of the same row
-    template <int LEFT>
-    __device__ __forceinline__ u64 sum_kept(int64_t from, int64_t to, const Share &s, float4 *kept, bool fresh) const
-    {
-        const int lane = threadIdx.x & 31;
-        to = min(to, vocab);
-        constexpr int kU = kKept / kStep;
+};
+
+// This lane's entries of a warp's piece [from, to) of a row.  (Functions of their
+// own: inlined where they are used, the kernel was four times as long, and half of
+// a short launch went into fetching it.)
+template <bool TB, int DK, int LEFT>
+__device__ __noinline__ u64 sum_of(Rows<TB, DK> rows, int64_t from, int64_t to, Share s)
+{
+    const int lane = threadIdx.x & 31;
+    u64 t = 0;
+    constexpr int kU = 4;
+    int64_t i = from + 4 * lane;
+    for (; i - 4 * lane + kU * kStep <= to; i += kU * kStep) {
         float x[kU][4], y[kU][4];
 #pragma unroll
         for (int u = 0; u < kU; u++) {
-            const int64_t i = from + u * kStep + 4 * lane;
-            if (fresh) {
-                load4<TB>(p, i, to, wide, x[u]);
-                load4<DK == 2>(q, i, to, wide, y[u]);
-            } else {
-                *reinterpret_cast<float4 *>(x[u]) = kept[(2 * u) * 32 + lane];
-                *reinterpret_cast<float4 *>(y[u]) = kept[(2 * u + 1) * 32 + lane];
-            }
+            load4<TB>(rows.p, i + u * kStep, to, rows.wide, x[u]);
+            if (LEFT != kAll)
+                load4<DK == 2>(rows.q, i + u * kStep, to, rows.wide, y[u]);
         }
-        u64 t = 0;
+#pragma unroll
+        for (int u = 0; u < kU; u++)
+            t += left_of<LEFT>(x[u], LEFT != kAll ? y[u] : x[u], s);
+    }
+    for (; i < to; i += kStep) {
+        float x[4], y[4];
+        load4<TB>(rows.p, i, to, rows.wide, x);
+        if (LEFT != kAll)
+            load4<DK == 2>(rows.q, i, to, rows.wide, y);
+        t += left_of<LEFT>(x, LEFT != kAll ? y : x, s);
+    }
+    return t;
+}
+
+template <bool TB, int DK>
+__device__ __forceinline__ u64 sum_of(const Rows<TB, DK> &rows, Left kind, int64_t from, int64_t to, const Share &s)
+{
+    if (DK == 0 || kind == kAll)
+        return sum_of<TB, DK, kAll>(rows, from, to, s);
+    return kind == kLessQ ? sum_of<TB, DK, kLessQ>(rows, from, to, s) : sum_of<TB, DK, kLessSQ>(rows, from, to, s);
+}
+
+// The same of a piece of up to kKept entries that is kept in shared memory:
+// loaded where `fresh`, read from there in the next rounds of the same row.
+template <bool TB, int DK>
+__device__ __noinline__ u64 sum_of_kept(Rows<TB, DK> rows, Left kind, int64_t from, int64_t to, Share s, float4 *kept, bool fresh)
+{
+    const int lane = threadIdx.x & 31;
+    constexpr int kU = kKept / kStep;
+    float x[kU][4], y[kU][4];
+    if (fresh) {
 #pragma unroll
         for (int u = 0; u < kU; u++) {
-            if (fresh) {
-                kept[(2 * u) * 32 + lane] = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
-                kept[(2 * u + 1) * 32 + lane] = make_float4(y[u][0], y[u][1], y[u][2], y[u][3]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                t += left_of<LEFT>(x[u][k], y[u][k], s);
+            const int64_t i = from + u * kStep + 4 * lane;
+            load4<TB>(rows.p, i, to, rows.wide, x[u]);
+            load4<DK == 2>(rows.q, i, to, rows.wide, y[u]);
         }
-        return t;
+#pragma unroll
+        for (int u = 0; u < kU; u++) {
+            kept[(2 * u) * 32 + lane] = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
+            kept[(2 * u + 1) * 32 + lane] = make_float4(y[u][0], y[u][1], y[u][2], y[u][3]);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < kU; u++) {
+            *reinterpret_cast<float4 *>(x[u]) = kept[(2 * u) * 32 + lane];
+            *reinterpret_cast<float4 *>(y[u]) = kept[(2 * u + 1) * 32 + lane];
+        }
     }
-    __device__ __forceinline__ u64 sum_kept_by(Left kind, int64_t from, int64_t to, const Share &s, float4 *kept, bool fresh) const
-    {
-        return kind == kAll ? sum_kept<kAll>(from, to, s, kept, fresh)
-               : kind == kLessQ ? sum_kept<kLessQ>(from, to, s, kept, fresh) : sum_kept<kLessSQ>(from, to, s, kept, fresh);
-    }
-    __device__ __forceinline__ u64 sum_by(Left kind, int64_t from, int64_t to, const Share &s) const
-    {
-        if (DK == 0 || kind == kAll)
-            return sum<kAll>(from, to, s);
-        return kind == kLessQ ? sum<kLessQ>(from, to, s) : sum<kLessSQ>(from, to, s);
-    }
-};
+    u64 t = 0;
+#pragma unroll
+    for (int u = 0; u < kU; u++)
+        t += kind == kAll ? left_of<kAll>(x[u], x[u], s) : kind == kLessQ ? left_of<kLessQ>(x[u], y[u], s) : left_of<kLessSQ>(x[u], y[u], s);
+    return t;
+}
 
 template <bool TB, int DK>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams a)
@@ -242,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     __shared__ u64 sums[2][kMost], pieces[kWarps], parts[kWarps];
     __shared__ int first_lost;
     extern __shared__ float4 kept[];  // trees, pieces of up to kKept entries: [warps][kKept / kStep][p, q][32]
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for where the first sum is exchanged
     pdl_enter();
     cg::cluster_group cluster = cg::this_cluster();
     const int nc = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), b = blockIdx.x / nc;
@@ -284,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     }
     if (tid == 0)
         first_lost = kVerifyRows;
-    cluster.sync();  // every CTA of the cluster runs: its shared memory may be written
+    __syncthreads();
 
     // pieces of the vocabulary: warp g of the cluster has [g * piece, (g + 1) * piece)
     const int64_t all = (int64_t)nc * kWarps, piece = (a.vocab + all * kStep - 1) / (all * kStep) * kStep;
@@ -299,10 +332,10 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
         const int64_t g = (int64_t)rank * kWarps + warp;
         u64 t;
         if (keep) {
-            t = rows.sum_kept_by(kind, g * piece, (g + 1) * piece, share, kept + warp * (kKept / 2), cur != kept_row);
+            t = sum_of_kept(rows, kind, g * piece, min((g + 1) * piece, a.vocab), share, kept + warp * (kKept / 2), cur != kept_row);
             kept_row = cur;
         } else {
-            t = rows.sum_by(kind, g * piece, (g + 1) * piece, share);
+            t = sum_of(rows, kind, g * piece, min((g + 1) * piece, a.vocab), share);
         }
         t = warp_sum(t);
         if (DK == 0)
@@ -316,6 +349,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 #pragma unroll
         for (int w = 0; w < kWarps; w++)
             c += pieces[w];
+        if (round == 0)  // every CTA of the cluster runs: its shared memory may be written
+            asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
         if (tid < nc)
             cluster.map_shared_rank(&sums[round & 1][0], tid)[rank] = c;
         cluster.sync();
@@ -462,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
             const int64_t mine0 = from + warp * part, mine1 = min(mine0 + part, to);
             u64 x = 0;
             if (mine0 < mine1) {
-                x = warp_sum(rows.sum_by(kind, mine0, mine1, share));
+                x = warp_sum(sum_of(rows, kind, mine0, mine1, share));
                 if (DK == 0)
                     for (int k = 0; k < lost; k++)
                         if (gone[k] >= mine0 && gone[k] < mine1)
@@ -484,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                         load4<DK == 2>(rows.q, i, mine1, rows.wide, q);
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        v[k] = kind == kAll ? left_of<kAll>(p[k], q[k], share)
-                               : kind == kLessQ ? left_of<kLessQ>(p[k], q[k], share) : left_of<kLessSQ>(p[k], q[k], share);
+                        v[k] = kind == kAll ? left_of_one<kAll>(p[k], q[k], share)
+                               : kind == kLessQ ? left_of_one<kLessQ>(p[k], q[k], share) : left_of_one<kLessSQ>(p[k], q[k], share);
                         if (DK == 0)
                             for (int g = 0; g < lost; g++)
                                 if (gone[g] == i + k)
@@ -515,6 +550,8 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
             }
         }
     }
+    if (round == 0)  // (a request without rows)
+        asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (flags && lane == 0 && a.error_flags)
         atomicOr(a.error_flags, flags);
