@@ -264,6 +264,14 @@ __device__ __noinline__ u64 sum_of_kept(Rows<TB, DK> rows, Left kind, int64_t fr
     return t;
 }
 
+// What warp 0 of a tree's CTA tells the others.
+struct Step {
+    int cur, count, lost;  // row reached, tokens accepted, entries of `gone`
+    Left kind;
+    float hi, lo;          // S
+    bool done;
+};
+
 template <bool TB, int DK>
 __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_constant__ VerifyParams a)
 {
@@ -273,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     __shared__ int gone[kVerifyRows];                                    // rejected tokens of the last row (no draft)
     __shared__ u64 sums[2][kMost], pieces[kWarps], parts[kWarps];
     __shared__ int first_lost;
+    __shared__ Step walk;
     extern __shared__ float4 kept[];  // trees, pieces of up to kKept entries: [warps][kKept / kStep][p, q][32]
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");  // waited for where the first sum is exchanged
     pdl_enter();
@@ -363,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
 
     // ---- the walk
     int cur = 0, count = 0;
+    Left kind = kAll;  // what the rejections behind the last row leave
     const int limit = min(n - 1, a.max_accepted);
     if (!a.parents) {
         for (int i = 1 + tid; i <= limit; i += kThreads) {
@@ -382,75 +392,97 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
                         lost = 1;
                     }
                 } else {
-                    share.set(1.0);
+                    kind = kLessQ;
                 }
             }
             for (int i = tid; i < count; i += kThreads)
                 path[i] = (int16_t)(i + 1);
         }
-    } else {
-        while (n > 0 && count < a.max_accepted) {
-            double z = 1.0, q_gone = 0.0;
-            int taken = 0;
-            share.s = 0.0;
-            lost = 0;
-            bool stale = false;  // z is of the round before
-            for (int last = cur;;) {
-                // the next child in row order
-                int child = 0;
-                for (int i0 = last + 1; i0 < n && child == 0; i0 += 32) {
-                    const unsigned hit = __ballot_sync(0xffffffffu, i0 + lane < n && parent[i0 + lane] == cur);
-                    if (hit)
-                        child = i0 + __ffs(hit) - 1;
-                }
-                if (child == 0)
-                    break;
-                last = child;
-                const double p = tp[child], u = tu[child];
-                if (DK) {
-                    const double q = tq[child];
+    } else if (n > 0) {
+        // Warp 0 walks, and hands the row and S over where it needs the sum of what
+        // is left.  (64-bit floating point runs at a fraction of the rate: walked by
+        // all warps alike, a batch of trees took 61 us, not 31.)
+        int last = 0, lost_now = 0;  // the child tested last; entries of `gone`
+        double z = 1.0, q_gone = 0.0;
+        bool stale = false;          // z is of the round before
+        for (;;) {
+            if (warp == 0) {
+                bool done = false;
+                while (!done) {
+                    // the next child in row order
+                    int child = 0;
+                    if (count < a.max_accepted)
+                        for (int i0 = last + 1; i0 < n && child == 0; i0 += 32) {
+                            const unsigned hit = __ballot_sync(0xffffffffu, i0 + lane < n && parent[i0 + lane] == cur);
+                            if (hit)
+                                child = i0 + __ffs(hit) - 1;
+                        }
+                    if (child == 0) {
+                        done = true;
+                        break;
+                    }
                     if (stale)
-                        z = (double)total(cur, share.s == 1.0 ? kLessQ : kLessSQ) / kUnit;
-                    const double left = a.replacement ? 1.0 : 1.0 - q_gone;
-                    if (!(left > 0x1p-24) || !(z > 0.0))
-                        break;
-                    if (u * (q / left) * z < fmax(p - share.s * q, 0.0)) {
-                        taken = child;
-                        break;
+                        break;  // for its test the sum is needed
+                    const double p = tp[child], u = tu[child];
+                    bool take;
+                    if (DK) {
+                        const double q = tq[child], left = a.replacement ? 1.0 : 1.0 - q_gone;
+                        if (!(left > 0x1p-24) || !(z > 0.0)) {
+                            done = true;
+                            break;
+                        }
+                        take = u * (q / left) * z < fmax(p - share.s * q, 0.0);
+                        if (!take) {
+                            share.set(share.s + z / left);
+                            q_gone += q;
+                            stale = true;
+                        }
+                    } else {
+                        bool before = token[child] < 0;
+                        for (int k = 0; k < lost_now; k++)
+                            before |= gone[k] == token[child];
+                        const double r = before ? 0.0 : p;
+                        if (!(z > 0.0)) {
+                            done = true;
+                            break;
+                        }
+                        take = u * z < r;
+                        if (!take) {
+                            z -= r;
+                            if (!before) {
+                                __syncwarp();
+                                if (lane == 0)
+                                    gone[lost_now] = token[child];
+                                __syncwarp();
+                                lost_now++;
+                            }
+                        }
                     }
-                    share.set(share.s + z / left);
-                    q_gone += q;
-                    stale = true;
-                } else {
-                    bool before = token[child] < 0;
-                    for (int k = 0; k < lost; k++)
-                        before |= gone[k] == token[child];
-                    const double r = before ? 0.0 : p;
-                    if (!(z > 0.0))
-                        break;
-                    if (u * z < r) {
-                        taken = child;
-                        break;
-                    }
-                    z -= r;
-                    if (!before) {
-                        __syncthreads();  // nobody reads the entry any more
-                        if (tid == 0)
-                            gone[lost] = token[child];
-                        __syncthreads();
-                        lost++;
+                    last = child;
+                    if (take) {
+                        if (lane == 0)
+                            path[count] = (int16_t)child;
+                        count++;
+                        cur = child;
+                        share.s = 0.0, z = 1.0, q_gone = 0.0;
+                        stale = false;
+                        lost_now = 0;
                     }
                 }
+                if (lane == 0)
+                    walk = Step{cur, count, lost_now, share.s == 0.0 ? kAll : share.s == 1.0 ? kLessQ : kLessSQ, share.hi, share.lo, done};
             }
-            if (!taken)
-                break;
-            if (tid == 0)
-                path[count] = (int16_t)taken;
-            count++;
-            cur = taken;
-            share.s = 0.0;
-            lost = 0;
             __syncthreads();
+            const Step w = walk;
+            cur = w.cur, count = w.count, lost = w.lost, kind = w.kind;
+            share.hi = w.hi, share.lo = w.lo;
+            if (w.done)
+                break;
+            const u64 mass = total(cur, kind);
+            if (warp == 0) {
+                z = (double)mass / kUnit;
+                stale = false;
+            }
         }
     }
     __syncthreads();
@@ -467,7 +499,6 @@ __global__ void __launch_bounds__(kThreads, 2) verify_kernel(const __grid_consta
     }
     if (n > 0) {
         // ---- the last token
-        Left kind = DK == 0 || share.s == 0.0 ? kAll : share.s == 1.0 ? kLessQ : kLessSQ;
         u64 mass = total(cur, kind);
         if (mass == 0 && (kind != kAll || lost)) {  // the rejections left nothing
             kind = kAll;
