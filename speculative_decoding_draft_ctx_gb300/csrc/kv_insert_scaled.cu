@@ -9,7 +9,9 @@
 //
 // Work.  A unit is one (request, page, head, K or V); its tokens are read once: a
 // thread keeps up to kHold 16-byte words while the CTA finds the maximum (64
-// tokens of D 128; more are read again, from L1).  Lengths
+// tokens of D 128; more are read again, from L1).  Six CTAs per SM leave registers
+// for that (8,192 tokens of 8 heads 13.9 us; 15.4 with eight and spills, 14.3 with
+// twelve and the words in shared memory, which cost a draft step 2.5 us).  Lengths
 // are on the device, so each CTA sums the requests' units itself and takes an
 // equal share of them, as the attention does.  A CTA has 128 threads, so that
 // a draft step's units (7 tokens of 256 bytes) are there all at once.
@@ -21,7 +23,7 @@ namespace dspark {
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32, kHold = 8;
+constexpr int kThreads = 128, kWarps = kThreads / 32, kHold = 8, kCtas = 6;
 
 struct Fresh {
     int q0, n, ctx;
@@ -66,7 +68,7 @@ __device__ __forceinline__ uint2 encode8(const uint4 &v, float s)
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 8) insert_scaled_kernel(const __grid_constant__ InsertScaledParams p)
+__global__ void __launch_bounds__(kThreads, kCtas) insert_scaled_kernel(const __grid_constant__ InsertScaledParams p)
 {
     constexpr int kW = D / 8, kStep = kThreads / kW;  // 16-byte words of a token's K or V; tokens at once
     __shared__ int64_t scratch[kWarps + 4];
@@ -166,7 +168,7 @@ cudaError_t launch_insert_scaled(const InsertScaledParams &p, cudaStream_t strea
     if (e != cudaSuccess)
         return e;
     const int64_t units = p.num_rows * p.num_kv_heads * 2;  // at most: a page each
-    const int ctas = (int)(units < 8 * (int64_t)sms ? units : 8 * (int64_t)sms);
+    const int ctas = (int)(units < kCtas * (int64_t)sms ? units : kCtas * (int64_t)sms);
     switch (p.head_dim) {
     case 64: return launch_pdl(insert_scaled_kernel<64>, ctas, kThreads, 0, stream, p);
     case 128: return launch_pdl(insert_scaled_kernel<128>, ctas, kThreads, 0, stream, p);
