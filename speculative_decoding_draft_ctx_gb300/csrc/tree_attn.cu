@@ -40,6 +40,16 @@ namespace {
 // for the calls made while it is set; the tests run both.
 constexpr int64_t kTcRows = 32;
 
+// Page-scaled caches: an item of mma.sync has up to 64 rows, and beyond these reads
+// the cache again, while the tensor-core kernel is bound by its producers, whose
+// time does not depend on the rows.  Measured, mma.sync / tensor cores, us:
+//   rows 56, 64 requests x 8 heads over 4,000   D 128 305 / 337, D 64 214 / 303
+//   rows 72, the same                           D 128 582 / 335, D 64 410 / 303
+//   rows 56, 1 x 8 over 2,000                   D 128 19.2 / 21.3, D 64 19.6 / 19.7
+//   rows 72, the same                           D 128 20.4 / 21.6, D 64 21.6 / 19.8
+//   rows 504, 1 x 4 over 16,000                 D 128 82 / 46, D 64 59 / 38
+constexpr int64_t kTcRowsScaled = 64;
+
 enum Pin { kNone, kMma, kTc };
 
 Pin pinned(int head_dim)
@@ -60,12 +70,12 @@ int64_t workspace_mma(int64_t rows, int group, int head_dim, int requests, bool 
     }
 }
 
-// Which kernel a call takes.
-cudaError_t takes_tc(const AttnParams &p, int head_dim, bool &tc)
+// Whether a call of more than `rows` rows a KV head takes the tensor cores.
+cudaError_t takes_tc(const AttnParams &p, int head_dim, int64_t rows, bool &tc)
 {
     const Pin pin = pinned(head_dim);
     tc = pin == kTc;
-    if (pin == kNone && p.num_rows * p.group > kTcRows * p.num_requests) {
+    if (pin == kNone && p.num_rows * p.group > rows * p.num_requests) {
         int dev = 0, sms = 0;
         cudaError_t e = cudaGetDevice(&dev);
         if (e == cudaSuccess)
@@ -99,7 +109,7 @@ int64_t tree_attention_workspace(int64_t rows, int num_heads, int num_kv_heads, 
 cudaError_t launch_tree_attention(const AttnParams &p, int head_dim, bool fp8, cudaStream_t stream)
 {
     bool tc = false;
-    const cudaError_t e = takes_tc(p, head_dim, tc);
+    const cudaError_t e = takes_tc(p, head_dim, kTcRows, tc);
     if (e != cudaSuccess)
         return e;
     if (tc)
@@ -120,7 +130,7 @@ int64_t tree_attention_scaled_workspace(int64_t rows, int num_heads, int num_kv_
     if (pin != kTc)
         n = head_dim == 64 ? attn::workspace_scaled_d<64>(wr, e) : head_dim == 128 ? attn::workspace_scaled_d<128>(wr, e)
                                                                              : attn::workspace_scaled_d<256>(wr, e);
-    if (pin == kTc || (pin == kNone && e == cudaSuccess && rows * group > kTcRows * requests)) {
+    if (pin == kTc || (pin == kNone && e == cudaSuccess && rows * group > kTcRowsScaled * requests)) {
         const int64_t m = head_dim == 64 ? attn::workspace_tc<64>(true, e) : attn::workspace_tc<128>(true, e);
         n = n > m ? n : m;
     }
@@ -130,7 +140,7 @@ int64_t tree_attention_scaled_workspace(int64_t rows, int num_heads, int num_kv_
 cudaError_t launch_tree_attention_scaled(const AttnParams &p, int head_dim, cudaStream_t stream)
 {
     bool tc = false;
-    const cudaError_t e = takes_tc(p, head_dim, tc);
+    const cudaError_t e = takes_tc(p, head_dim, kTcRowsScaled, tc);
     if (e != cudaSuccess)
         return e;
     if (tc)
