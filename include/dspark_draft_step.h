@@ -75,7 +75,8 @@ extern "C" {
  * A request without rows gets -1 and 0; one of more than 1024 rows too
  * (DSPARK_FLAG_LENGTH).  A drafted token outside [0, vocab) is rejected, one
  * whose parent is not a row before it is not tested (DSPARK_FLAG_ROW); a last row
- * without any probability gives token -1 (DSPARK_FLAG_ROW).
+ * without any probability gives token -1 (DSPARK_FLAG_ROW).  The outputs must not overlap the
+ * inputs.  A row's entries sum to less than 65,536 (they are probabilities).
  */
 typedef enum { DSPARK_PROB_FP32 = 0, DSPARK_PROB_BF16 = 1 } dspark_prob_dtype;
 
@@ -91,9 +92,9 @@ int dspark_verify_drafts(const void *target, int target_dtype, int64_t target_st
  * layer: of request b, the token at place context_lens[b] + rows[b][j] moves to
  * place context_lens[b] + first + j, for j < counts[b].
  *
- *  kv_caches      HOST, num_layers device pointers; block_scales: HOST,
- *                 num_layers device pointers or NULL (page-scaled caches).  Read
- *                 before the call returns.
+ *  kv_caches      HOST, num_layers (1 to 1024) device pointers, no two alike;
+ *                 block_scales: HOST, num_layers device pointers or NULL
+ *                 (page-scaled caches).  Read before the call returns.
  *  rows           device, int32, row b at b * rows_stride, `width` entries:
  *                 ascending, rows[b][j] >= first + j.
  *  first          >= 0: 1 where row 0 is a token that stays.
@@ -182,9 +183,11 @@ int dspark_kv_insert_scaled(const void *k, int64_t k_token_stride, int64_t k_hea
  * dspark_tree_attention_scaled -- dspark_tree_attention over a page-scaled cache
  * (kv_cache: e4m3 codes; block_scales in the place of k_scale and v_scale).  The
  * products take codes, exact in fp16; the scale of K multiplies the scores, that
- * of V the weights before they are rounded to fp16: with 2^(s + e) the weight of
- * a token of V scale e, relative to the row's largest of these, to 2^-11 of
- * itself down to 2^-28 of the largest, 2^-39 of it below.
+ * of V the weights before they are rounded to fp16: 2^(s + e) for a token of V
+ * scale e is off by at most 2^-11 of itself down to 2^-22 of the row's largest of
+ * these, by 2^-33 of that below.  The other operators that read a cache
+ * (dspark_attention_weight_accumulate, dspark_kv_evict, the writes) take its
+ * per-tensor form only.
  */
 int dspark_tree_attention_scaled(const void *q, int64_t q_token_stride, int64_t q_head_stride, int64_t num_rows,
                                  int num_heads, int num_kv_heads, int head_dim, const void *kv_cache,

@@ -14,8 +14,8 @@ using namespace dspark;
 int check_layers(void *const *caches, int8_t *const *scales, int num_layers, int64_t num_blocks, int nkv, int block_size,
                  int head_dim, int kv_dtype)
 {
-    if (num_layers < 1 || num_layers > 65536)
-        return fail(DSPARK_ERR_INVALID_ARG, "num_layers %d not in [1, 65536]", num_layers);
+    if (num_layers < 1 || num_layers > 1024)
+        return fail(DSPARK_ERR_INVALID_ARG, "num_layers %d not in [1, 1024]", num_layers);
     if (!caches)
         return fail(DSPARK_ERR_INVALID_ARG, "null kv_caches");
     const int st = check_cache(caches[0], num_blocks, nkv, block_size, head_dim, kv_dtype);
@@ -28,6 +28,9 @@ int check_layers(void *const *caches, int8_t *const *scales, int num_layers, int
             return fail(DSPARK_ERR_INVALID_ARG, "null cache or block_scales of layer %d", l);
         if (!aligned(caches[l], 16))
             return fail(DSPARK_ERR_ALIGNMENT, "cache of layer %d must be 16-byte aligned", l);
+        for (int k = 0; k < l; k++)
+            if (caches[k] == caches[l] || (scales && scales[k] == scales[l]))
+                return fail(DSPARK_ERR_INVALID_ARG, "layers %d and %d have the same cache or block_scales", k, l);
     }
     return DSPARK_OK;
 }

@@ -73,6 +73,12 @@ constexpr int kProducers = 4, kItemCostTc = 6;   // EXTRA of Walk, in tiles of k
 // sums and bf16 weights have room for any; fp16 weights begin at 2^kLift and
 // end below 2^16 (a score is off by 2^-4 at most where kLift is taken off).
 constexpr float kMost = 8.0f, kMostFp8 = kLift + 1.0f;
+// Page-scaled: weights begin at 2^kLiftScaled, so that the maximum of s + ev, which
+// the pages' exponents move too, may grow by seven octaves before a rescale of the
+// output (with kLift, by one: 35 of 50 tiles rescaled in a draft step of 64
+// requests, 1,500 cycles each).  A weight keeps its 2^-11 down to 2^-22 of the
+// largest; below it is off by at most 2^-33 of that.
+constexpr float kLiftScaled = 8.0f, kMostScaled = 15.0f;
 constexpr int kSpread = 15;  // of the exponents of 64 keys of a page-scaled cache
 
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -297,7 +303,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     const int x = base + tile_of(k);
                     const bool both = 2 * tile_of(k) + 1 != halves;
                     wait(vfull + x % NV, (uint32_t)(x / NV) & 1u);
-                    if (k + 1 < steps)
+                    if (!SCALED && k + 1 < steps)
                         kwait(k + 1);
                     wait(pfull + 2 * s, par & 1u);
                     par ^= 1u;
@@ -309,6 +315,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     }
                     if (both && ok)
                         pv(k, 1, true);
+                    if (SCALED && k + 1 < steps)  // after the product that frees V's stage
+                        kwait(k + 1);
                     take();
                     if (k + 1 < steps && ok)
                         qk(k + 1);
@@ -700,11 +708,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __gri
                     else
                         maxima(std::false_type{});
                     const float t = SCALED ? t_scaled : max3(fmaxf(top[0], top[1]), top[2], top[3]) * c;
-                    const float most = !FP8 ? kMost : fabsf(t) < kLiftBelow ? kMostFp8 : 1.0f;
+                    const float most = !FP8 ? kMost : fabsf(t) < kLiftBelow ? (SCALED ? kMostScaled : kMostFp8) : 1.0f;
                     const bool grow = t > m + most || (m == -INFINITY && t > m);
                     if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
                         const float old = m;
-                        m = fmaxf(m, reference_of<FP8>(t));
+                        m = fmaxf(m, SCALED && fabsf(t) < kLiftBelow ? t - kLiftScaled : reference_of<FP8>(t));
                         const float fr = old == m ? 1.0f : ex2(old - m);  // 0 from -inf
                         l *= fr;
                         if (k > 0) {

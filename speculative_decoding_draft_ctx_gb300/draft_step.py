@@ -4,7 +4,8 @@ accepted path's K/V behind the context, ``resize_kv`` gives pages back to the
 pool and takes the next step's, ``fork_kv`` lets one request's cache continue
 as several, and ``insert_kv_scaled`` fills a page-scaled cache (8-bit codes
 with one power-of-two scale per page and head), which ``tree_attention`` reads
-with ``block_scales``.
+with ``block_scales``.  (``accumulate_attention_weight``, ``evict_kv`` and the
+context-KV writes take caches with per-tensor scales only.)
 
 No call needs a length on the host, so a whole step can be captured into a
 CUDA graph.  Caches, block tables, ``error_flags`` and ``stream`` are as in
@@ -101,7 +102,7 @@ def verify_drafts(target_probs, draft_tokens, row_start, uniforms, max_accepted,
     ``tokens``: int64 ``[B, max_accepted + 1]``, the accepted tokens, the last
     one, then -1; ``rows``: int32 ``[B, max_accepted]``, the accepted tokens' rows
     (what ``compact_kv`` takes), then -1; ``counts``: int32 ``[B]``, how many
-    stand.  Made by the call if not given.  A request has up to 1024 rows; one
+    stand.  Made by the call if not given; they must not overlap the inputs.  A request has up to 1024 rows; one
     without rows gets -1 and 0.  FLAG_ROW: a token outside the vocabulary
     (rejected), a parent that is not a row before it (never tested), or a last row
     without any probability (token -1).

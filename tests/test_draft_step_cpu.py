@@ -50,13 +50,14 @@ def test_verify_status(L, over, want):
 
 
 COMPACT = "caches scales L blocks nkv bs D dt table stride cols ctx B rows rstride width counts first lens flags stream"
-COMPACT_BASE = dict(caches=layers(FAKE, FAKE), scales=None, L=2, blocks=4, nkv=2, bs=16, D=128, dt=0, table=FAKE, stride=4, cols=4, ctx=FAKE, B=3,
+COMPACT_BASE = dict(caches=layers(FAKE, FAKE + 4096), scales=None, L=2, blocks=4, nkv=2, bs=16, D=128, dt=0, table=FAKE, stride=4, cols=4, ctx=FAKE, B=3,
                     rows=FAKE + 256, rstride=4, width=4, counts=FAKE + 512, first=1, lens=FAKE + 1024, flags=0, stream=0)
 
 
 @pytest.mark.parametrize("over,want", [
     (dict(L=0), BAD), (dict(caches=None), BAD), (dict(caches=layers(FAKE, 0)), BAD), (dict(caches=layers(FAKE, FAKE + 8)), ALIGN),
-    (dict(scales=layers(FAKE, FAKE)), DTYPE), (dict(scales=layers(FAKE, 0), dt=1), BAD), (dict(D=96), BAD), (dict(bs=0), BLOCK), (dict(dt=7), DTYPE),
+    (dict(scales=layers(FAKE, FAKE + 64)), DTYPE), (dict(caches=layers(FAKE, FAKE)), BAD), (dict(scales=layers(FAKE, FAKE), dt=1), BAD),
+    (dict(L=1025), BAD), (dict(scales=layers(FAKE, 0), dt=1), BAD), (dict(D=96), BAD), (dict(bs=0), BLOCK), (dict(dt=7), DTYPE),
     (dict(blocks=0), BAD), (dict(blocks=1 << 40), BAD), (dict(nkv=0), BAD), (dict(cols=0), BAD), (dict(stride=3), BAD), (dict(B=-1), BAD),
     (dict(table=0), BAD), (dict(ctx=0), BAD), (dict(width=-1), BAD), (dict(rstride=3), BAD), (dict(first=-1), BAD), (dict(rows=0), BAD),
     (dict(counts=0), BAD), (dict(counts=FAKE + 2), ALIGN), (dict(lens=FAKE + 8), BAD), (dict(lens=FAKE + 256 + 40), BAD), (dict(lens=FAKE + 512), BAD),

@@ -497,6 +497,22 @@ def test_pool_resize_of_bad_rows_and_entries():
     live.check(dk.FLAG_REFS)
 
 
+@pytest.mark.parametrize("offset,pages", [(1, 5000), (0, 8193), (3, 70001), (0, 200003)])
+def test_pool_of_any_size_and_alignment(offset, pages):
+    """Runs of a thread of several loads, pools that no thread's run divides, refs at any address."""
+    live = Live(6, 40, 8, 4, layers=1, H=1)
+    live.ref.refs = [int(x) for x in (torch.rand(pages, generator=gen(pages)) < 0.98)]
+    full = torch.zeros(pages + offset, dtype=torch.int32, device="cuda")
+    live.refs = full[offset:]
+    live.refs.copy_(ints(live.ref.refs))
+    # the caches play no part here: one of a page
+    live.resize([160, 3, 0, 77, 4, 1])
+    assert live.table.tolist() == live.ref.table and live.refs.tolist() == live.ref.refs
+    live.resize([1, 3, 100, 160, 0, 9])
+    assert live.table.tolist() == live.ref.table and live.refs.tolist() == live.ref.refs and live.pages.tolist() == live.ref.pages
+    assert int(live.flags) == 0
+
+
 def test_pool_resize_of_many_rows():
     """More rows than the cluster has threads, more pages than one round of them."""
     n = 9000
@@ -659,6 +675,56 @@ def test_scaled_attention_rows_without_anything_pages_and_lengths_out_of_range(k
     p.d_ctx[1] = 1000
     run_scaled(p, "dense", None)
     assert int(p.d_flags) == dk.FLAG_LENGTH
+
+
+def test_scaled_attention_on_another_stream_and_in_a_graph(kernel):
+    p = ScaledProblem(9, (500, 40), (9, 20), 16, 2, 128, 16).cuda()
+    want = run_scaled(p, "causal", None)
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    out, lse = run_scaled(p, "causal", None, stream=stream)
+    stream.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = run_scaled(p, "causal", None)
+    for k in range(2):
+        p.d_scales[:, :, 1] += 1
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run_scaled(p, "causal", None)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_scaled_attention_expired_waits_report_a_timeout(monkeypatch):
+    """The producers copy nothing: every wait runs out, and the next call is right again."""
+    monkeypatch.setenv("DSPARK_TREE_ATTN_KERNEL", "tc")
+    p = ScaledProblem(10, (500, 40), (9, 20), 16, 2, 128, 16).cuda()
+    monkeypatch.setenv("DSPARK_TEST_HOLD_NS", "2000000")
+    run_scaled(p, "dense", None)
+    torch.cuda.synchronize()
+    assert int(p.d_flags) == dk.FLAG_TIMEOUT
+    monkeypatch.delenv("DSPARK_TEST_HOLD_NS")
+    p.d_flags.zero_()
+    out, lse = run_scaled(p, "dense", None)
+    want, z, to, tl = attention(p, "dense", None)
+    close(out, want, to)
+    assert int(p.d_flags) == 0
+
+
+def test_scaled_attention_tail_behind_a_heavy_token(kernel):
+    """20,000 tokens with 0.1% of the weight between them, behind one that has the rest: their share is not lost."""
+    D, n = 128, 20001
+    p = ScaledProblem(11, (n,), (1,), 4, 1, D, 16, k_exp=(0, 1), v_exp=(0, 1))
+    j = torch.arange(n + 1)
+    page, off = p.table[0].long()[j // 16], j % 16
+    rows = torch.zeros((n + 1, 2 * D))
+    rows[0, 0] = 16.0           # the heavy token's key
+    rows[1:, D:] = 1.0          # the others' values; the heavy one's are 0
+    p.cache[page, 0, off] = rows.to(torch.float8_e4m3fn).view(torch.uint8)
+    p.qkv[:] = 0
+    p.qkv[:, :, 0] = (math.log(n) + math.log(1000.0)) / 16.0 * D ** 0.5
+    check_scaled(p, "dense", None)
 
 
 def test_scaled_attention_nan_codes(kernel):
