@@ -9,12 +9,16 @@
 //
 // Work.  A unit is one (request, page, head, K or V); its tokens are read once: a
 // thread keeps up to kHold 16-byte words while the CTA finds the maximum (64
-// tokens of D 128; more are read again, from L1).  Six CTAs per SM leave registers
-// for that (8,192 tokens of 8 heads 13.9 us; 15.4 with eight and spills, 14.3 with
-// twelve and the words in shared memory, which cost a draft step 2.5 us).  Lengths
+// tokens of D 128; more are read again, from L1).  What bounds it: instructions (half
+// of the issue slots) and one wave of dependent loads (lengths, page, tokens):
+// 8,192 tokens of 8 heads 13.5 us, 50 MB at 55% of the copy rate; 7 tokens of 64
+// requests 6.1 us.  With the words in shared memory twelve CTAs fit an SM, not eight
+// (14.3 and 9.7 us); infinities and NaN left out word by word cost 1.3 us.  Lengths
 // are on the device, so each CTA sums the requests' units itself and takes an
 // equal share of them, as the attention does.  A CTA has 128 threads, so that
 // a draft step's units (7 tokens of 256 bytes) are there all at once.
+#include <type_traits>
+
 #include "draft_step_internal.h"
 #include "page_scale.cuh"
 #include "tree_attn_mma.cuh"
@@ -23,7 +27,7 @@ namespace dspark {
 
 namespace {
 
-constexpr int kThreads = 128, kWarps = kThreads / 32, kHold = 8, kCtas = 6;
+constexpr int kThreads = 128, kWarps = kThreads / 32, kHold = 8, kCtas = 8;
 
 struct Fresh {
     int q0, n, ctx;
@@ -46,11 +50,20 @@ __device__ __forceinline__ int pages_of(const Fresh &r, int bs)
     return r.n ? (r.ctx + r.n - 1) / bs - r.ctx / bs + 1 : 0;
 }
 
-// max of |x| over the finite ones of a bf16 pair, by their bits
+// max of |x| of bf16 pairs, by their bits; FINITE: over the finite ones
+template <bool FINITE>
 __device__ __forceinline__ uint32_t top2(uint32_t top, uint32_t w)
 {
     w &= 0x7fff7fffu;
-    return __vmaxu2(top, w & ~__vcmpgeu2(w, 0x7f807f80u));
+    if (FINITE)
+        w &= ~__vcmpgeu2(w, 0x7f807f80u);
+    return __vmaxu2(top, w);
+}
+
+template <bool FINITE>
+__device__ __forceinline__ uint32_t top8(uint32_t top, const uint4 &v)
+{
+    return top2<FINITE>(top2<FINITE>(top2<FINITE>(top2<FINITE>(top, v.x), v.y), v.z), v.w);
 }
 
 __device__ __forceinline__ int exponent_of(uint32_t bits)  // of the largest |x|, as bf16 bits
@@ -103,32 +116,40 @@ __global__ void __launch_bounds__(kThreads, kCtas) insert_scaled_kernel(const __
             const int64_t ts = part ? p.v_ts : p.k_ts;
             const int row0 = r.q0 + lo - r.ctx, rows = hi - lo;
             uint4 v[kHold];
-            uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < kHold; k++) {
-                const int x = tid / kW + k * kStep;
-                v[k] = x < rows ? __ldg(reinterpret_cast<const uint4 *>(src + (row0 + x) * ts)) : make_uint4(0, 0, 0, 0);
-            }
+            for (int k = 0; k < kHold; k++)
+                if (k * kStep < rows) {  // the same for all
+                    const int x = tid / kW + k * kStep;
+                    v[k] = x < rows ? __ldg(reinterpret_cast<const uint4 *>(src + (row0 + x) * ts)) : make_uint4(0, 0, 0, 0);
+                }
             if (page < 0 || page >= p.num_blocks) {
                 flags |= kFlagBlockRange;
                 continue;
             }
             const int was = held ? page_exponent(p.scales, page, H, h, part) : kScaleMin;
+            // the largest |x| of the CTA's tokens
+            auto largest = [&](auto finite) {
+                constexpr bool kFinite = decltype(finite)::value;
+                uint32_t top = 0;
 #pragma unroll
-            for (int k = 0; k < kHold; k++)
-                top = top2(top2(top2(top2(top, v[k].x), v[k].y), v[k].z), v[k].w);
-            for (int x = tid / kW + kHold * kStep; x < rows; x += kStep) {
-                const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src + (row0 + x) * ts));
-                top = top2(top2(top2(top2(top, y.x), y.y), y.z), y.w);
-            }
-            top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
-            if (lane == 0)
-                tops[turn][warp] = top;
-            __syncthreads();  // everyone has read the old scale too
+                for (int k = 0; k < kHold; k++)
+                    if (k * kStep < rows)
+                        top = top8<kFinite>(top, v[k]);
+                for (int x = tid / kW + kHold * kStep; x < rows; x += kStep)
+                    top = top8<kFinite>(top, __ldg(reinterpret_cast<const uint4 *>(src + (row0 + x) * ts)));
+                top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+                if (lane == 0)
+                    tops[turn][warp] = top;
+                __syncthreads();  // everyone has read the old scale too
 #pragma unroll
-            for (int i = 0; i < kWarps; i++)
-                top = max(top, tops[turn][i]);
-            turn ^= 1;
+                for (int i = 0; i < kWarps; i++)
+                    top = max(top, tops[turn][i]);
+                turn ^= 1;
+                return top;
+            };
+            uint32_t top = largest(std::false_type{});
+            if (top >= 0x7f80u)  // infinities or NaN among them: once more without these
+                top = largest(std::true_type{});
             const int e = max(exponent_of(top), was);
             unsigned char *codes = p.cache + ((page * H + h) * bs) * (int64_t)(2 * D) + part * D;
             // the codes of the context's tokens in the page, where the scale grows
@@ -142,11 +163,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) insert_scaled_kernel(const __
             const float s = __int_as_float((127 - e) << 23);
             unsigned char *dst = codes + (int64_t)(lo - first) * (2 * D) + w * 8;
 #pragma unroll
-            for (int k = 0; k < kHold; k++) {
-                const int x = tid / kW + k * kStep;
-                if (x < rows)
-                    *reinterpret_cast<uint2 *>(dst + (int64_t)x * (2 * D)) = encode8(v[k], s);
-            }
+            for (int k = 0; k < kHold; k++)
+                if (k * kStep < rows) {
+                    const int x = tid / kW + k * kStep;
+                    if (x < rows)
+                        *reinterpret_cast<uint2 *>(dst + (int64_t)x * (2 * D)) = encode8(v[k], s);
+                }
             for (int x = tid / kW + kHold * kStep; x < rows; x += kStep)
                 *reinterpret_cast<uint2 *>(dst + (int64_t)x * (2 * D)) =
                     encode8(__ldg(reinterpret_cast<const uint4 *>(src + (row0 + x) * ts)), s);
