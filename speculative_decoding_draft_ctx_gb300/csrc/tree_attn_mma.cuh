@@ -644,9 +644,39 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&a)[D 
     }
 }
 
+// The same over codes with the A operands in shared memory, as the lanes hold
+// them: at D 256 they would be 64 of the 255 registers.
+template <int D, int NT, int PITCH>
+__device__ __forceinline__ void scores_shared(float (&s)[NT][4], uint32_t queries, uint32_t stage, int key0)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int u = 0; u < D / 64; u++) {
+        uint32_t a[4][4];
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(a[k][0]), "=r"(a[k][1]), "=r"(a[k][2]), "=r"(a[k][3])
+                         : "r"(queries + ((4 * u + k) * 32 + lane) * 16)
+                         : "memory");
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+            const int x = key0 + 8 * i + (lane >> 2);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(stage + x * PITCH + (((4 * u + (lane & 3)) ^ swz(x)) << 4))
+                         : "memory");
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                mma<true>(s[i], a[k], e4m3_to_half2((uint16_t)w[k]), e4m3_to_half2((uint16_t)(w[k] >> 16)));
+        }
+    }
+}
+
 // ------------------------------------------------------------------ the attention kernel
 
-template <int D, bool FP8, int WR>
+template <int D, bool FP8, int WR, bool SCALED = false>
 struct Cfg {
     static constexpr int kWK = kWarps / WR, kRows = 16 * WR, kKeys = kTile / kWK;  // keys of a tile per warp
     static constexpr int kRow = 2 * D * (FP8 ? 1 : 2);                            // bytes of a token's K|V
@@ -657,9 +687,10 @@ struct Cfg {
     static constexpr int kStages = D == 64 ? (FP8 ? 6 : 4) : D == 128 ? (FP8 ? 5 : 2) : (FP8 ? 4 : 2);
     static constexpr int kNT = D / 8;                                            // n-tiles of the output
     static constexpr int kJoin = kWK > 1 ? (kWK / 2) * WR * (kNT * 128 + 64) * 4 : 0;  // bytes to join the key warps
-    static constexpr int kSmem = kStages * kStage + kJoin;
+    static constexpr bool kQShared = SCALED && D == 256;                         // queries in shared memory (scores_shared)
+    static constexpr int kSmem = kStages * kStage + kJoin + (kQShared ? WR * (D / 16) * 512 : 0);
     static constexpr int kPart = WR * (kNT * 128 + 32);                          // floats of one part
-    static_assert(kCtas * (kSmem + 1536) <= 227 * 1024, "shared memory");
+    static_assert(kCtas * (kSmem + 1536 + (SCALED ? kStages * kTile * 16 : 0)) <= 227 * 1024, "shared memory");
 };
 
 // What a CTA tells the join about the item it began and did not finish.
@@ -725,9 +756,9 @@ __device__ __noinline__ void add_nonfinite(const AttnParams &p, int b, Request r
 }
 
 template <int D, bool FP8, int WR, bool SCALED>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) attention_kernel(const __grid_constant__ AttnParams p)
 {
-    using C = Cfg<D, FP8, WR>;
+    using C = Cfg<D, FP8, WR, SCALED>;
     static_assert(FP8 || !SCALED, "page scales are of codes");
     __shared__ float4 page_scales[SCALED ? C::kStages : 1][SCALED ? kTile : 1];
     constexpr int NS = C::kKeys / 8;  // n-tiles of a warp's scores
@@ -802,6 +833,16 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
         uint32_t qa[D / 16][4];
         float rs[2];
         load_q<D, FP8>(p, rq, h, row0 + 16 * wr, qa, rs);
+        const uint32_t queries = stages + C::kStages * C::kStage + C::kJoin + wr * (D / 16) * 512;
+        if constexpr (C::kQShared) {
+            // before the barrier of the item's first tile, behind that of the item before
+            if (wk == 0)
+#pragma unroll
+                for (int k = 0; k < D / 16; k++)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(queries + (k * 32 + lane) * 16), "r"(qa[k][0]), "r"(qa[k][1]),
+                                 "r"(qa[k][2]), "r"(qa[k][3])
+                                 : "memory");
+        }
         const float c0 = base_scale * rs[0], c1 = base_scale * rs[1];
         const int r0 = row0 + 16 * wr + g, i0 = r0 / p.group, i1 = (r0 + 8) / p.group;
         float o[C::kNT][4];
@@ -856,7 +897,10 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_
 #pragma unroll
             for (int n = 0; n < NS; n++)
                 s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-            scores<D, FP8, NS, C::kRow>(s, qa, st, wk * C::kKeys);
+            if constexpr (C::kQShared)
+                scores_shared<D, NS, C::kRow>(s, queries, st, wk * C::kKeys);
+            else
+                scores<D, FP8, NS, C::kRow>(s, qa, st, wk * C::kKeys);
             const uint32_t lv[4] = {live[stage][0], live[stage][1], live[stage][2], live[stage][3]};
             [[maybe_unused]] float back[SCALED ? NS : 1][2];  // 2^-ev of this lane's keys
             const bool masked = drafted || (lv[0] & lv[1] & lv[2] & lv[3]) != 0xffffu;
@@ -1199,7 +1243,7 @@ cudaError_t attention_ctas(int &ctas)
         return cudaErrorInvalidDevice;
     int have = __atomic_load_n(&cached[dev], __ATOMIC_ACQUIRE);
     if (have == 0) {
-        using C = Cfg<D, FP8, WR>;
+        using C = Cfg<D, FP8, WR, SCALED>;
         e = prepare(attention_kernel<D, FP8, WR, SCALED>, C::kSmem, C::kCtas, have);
         if (e != cudaSuccess)
             return e;
@@ -1220,7 +1264,7 @@ int64_t attention_bytes(cudaError_t &e)
 template <int D, bool FP8, int WR, bool SCALED = false>
 cudaError_t attention(const AttnParams &p, cudaStream_t stream)
 {
-    using C = Cfg<D, FP8, WR>;
+    using C = Cfg<D, FP8, WR, SCALED>;
     int ctas = 0;
     cudaError_t e = attention_ctas<D, FP8, WR, SCALED>(ctas);
     if (e != cudaSuccess)
