@@ -69,7 +69,6 @@ struct AttnParams {
     float scale;        // softmax scale
     uint64_t wait_ns;   // limit of every wait of the tensor-core kernels
     bool test_hold;     // test hook (see dspark::test_hold_ns): their producers copy nothing
-    int32_t run;        // page-scaled, tensor cores: tokens that are copied at once (attention_tc_runs_kernel)
     // attention
     uint16_t *out;
     float *parts;       // workspace: partial results, see tree_attn_mma.cuh

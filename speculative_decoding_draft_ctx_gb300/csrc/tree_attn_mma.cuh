@@ -473,9 +473,9 @@ __device__ __forceinline__ uint32_t raw_at(uint32_t tile, int y, int c)
 
 // Rows [row0, row0 + ROWS) of a tile by one warp, after their codes have
 // landed.  Rows from `clean` on have NaN codes zeroed; true if there were any.
-// SCALED: row row0 + i is multiplied by the fp16 number factors[i], a power of two, or zeroed where that is 0.
+// SCALED: row row0 + i is multiplied by the fp16 pair factors[i], a power of two.
 template <int D, int ROWS, bool SCALED = false>
-__device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean, const uint16_t *factors = nullptr)
+__device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean, const uint32_t *factors = nullptr)
 {
     constexpr int kW = D / 16, kR = 32 / kW, kU = kR < 8 ? 8 / kR : 1, kStep = kU * kR;  // whole groups of 8 rows a step
     const int lane = threadIdx.x & 31, c = lane % kW, r = lane / kW;
@@ -484,7 +484,7 @@ __device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean,
 #pragma unroll 1
         for (int y = row0 + r; y < row0 + ROWS; y += kR)
 #pragma unroll 1
-            for (int k = 0; k < 4 && y >= clean && (!SCALED || factors[y - row0] != 0); k++) {
+            for (int k = 0; k < 4 && y >= clean; k++) {
                 const uint32_t at = raw_at<D>(tile, y, c) + 4 * k;
                 uint32_t q;
                 asm volatile("ld.shared.b32 %0, [%1];" : "=r"(q) : "r"(at) : "memory");
@@ -519,7 +519,7 @@ __device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean,
         if constexpr (SCALED)
 #pragma unroll
             for (int u = 0; u < kU; u++)
-                f[u] = factors[d / 128 + u * kR + r] * 0x10001u;
+                f[u] = factors[d / 128 + u * kR + r];
         auto half2_of = [&](uint32_t w, int u) {
             uint32_t h = e4m3_to_half2((uint16_t)w);
             if constexpr (SCALED)
@@ -532,11 +532,6 @@ __device__ __forceinline__ bool convert_rows(uint32_t tile, int row0, int clean,
                          : "=r"(q[u][0]), "=r"(q[u][1]), "=r"(q[u][2]), "=r"(q[u][3])
                          : "r"(from[u] + d)
                          : "memory");
-        if constexpr (SCALED)
-#pragma unroll
-            for (int u = 0; u < kU; u++)
-                if (f[u] == 0)
-                    q[u][0] = q[u][1] = q[u][2] = q[u][3] = 0;
         __syncwarp();  // the rows' codes are read before their bytes are written
 #pragma unroll
         for (int u = 0; u < kU; u++)

@@ -61,19 +61,14 @@
 // memory and returns.
 #pragma once
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include <algorithm>
-#include <mutex>
-
 #include "tc_ptx.cuh"
 #include "tree_attn_mma.cuh"
 
 namespace dspark {
 namespace attn {
 
-constexpr int kKeysTc = 128, kItemCostTc = 6;  // EXTRA of Walk, in tiles of kKeysTc keys
+constexpr int kTcThreads = 448, kKeysTc = 128;  // 8 softmax warps, 4 producers, 2 that issue the products
+constexpr int kProducers = 4, kItemCostTc = 6;   // EXTRA of Walk, in tiles of kKeysTc keys
 // The largest weight 2^(s - m) that waits for a rescale, as an exponent: fp32
 // sums and bf16 weights have room for any; fp16 weights begin at 2^kLift and
 // end below 2^16 (a score is off by 2^-4 at most where kLift is taken off).
@@ -93,11 +88,8 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return d;
 }
 
-template <int D, bool FP8, bool RUNS = false>
+template <int D, bool FP8>
 struct TcCfg {
-    // 8 softmax warps, the producers (four; RUNS: one that copies and four that
-    // convert), the two that issue the products
-    static constexpr int kProducers = RUNS ? 5 : 4, kIssue = 8 + kProducers, kThreads = 32 * (kIssue + 2);
     // Even: where the streams take turns, a stage belongs to one of them within
     // an item, so that neither is ever two phases off a stage's barrier.
     static constexpr int kStagesK = D == 64 ? 4 : 2, kStagesV = D == 64 ? 4 : 2;
@@ -118,13 +110,10 @@ __device__ __forceinline__ int tile_halves(const W &w, int n)
     return 2 * n - (w.finished() && w.rq.ctx + w.rq.nq <= (w.t1 - 1) * kKeysTc + kKeysTc / 2 ? 1 : 0);
 }
 
-// RUNS: `map` is the cache as [rows of one head][2 D bytes], boxes of p.run rows and D bytes.
-template <int D, bool FP8, bool SCALED, bool RUNS>
-__device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused]] const CUtensorMap *map)
+template <int D, bool FP8, bool SCALED = false>
+__global__ void __launch_bounds__(kTcThreads, 1) attention_tc_kernel(const __grid_constant__ AttnParams p)
 {
-    using C = TcCfg<D, FP8, RUNS>;
-    static_assert(!RUNS || (SCALED && D == 128), "raw rows of 128 bytes");
-    constexpr int kIssue = C::kIssue;
+    using C = TcCfg<D, FP8>;
     using namespace tc;
     constexpr int NK = C::kStagesK, NV = C::kStagesV;
     // tensor-memory columns: scores of stream s at 128 s, output at 256 + 128 s
@@ -135,24 +124,22 @@ __device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused
     unsigned char *sq = smem, *sk = smem + 2 * C::kQBytes, *sv = sk + NK * C::kTileBytes;
     __shared__ uint64_t kfull[NK], kempty[NK], vfull[NV], vempty[NV], qfull[2], sfull[2], pfull[4], ofull[2], jfull, jempty, go1, done[2];
     __shared__ uint32_t tmem_slot, live[8][4];
-    // cache rows of each producer's tile and its next, RUNS: of the first of each run, four tiles; ~0: not there
-    __shared__ uint32_t rows[4][RUNS ? 1 : 2][RUNS ? 32 : 64];
-    __shared__ int abort_flag, never_abort, lock;
+    __shared__ uint32_t rows[kProducers][2][64];  // cache rows of each producer's tile and its next; ~0: not there
+    __shared__ int abort_flag, lock;
     __shared__ int bad[16];  // item number + 1 where infinities or NaN came up among an item's drafted V
     __shared__ float join_ml[256];
     // page-scaled: of each 64 keys 2^ek, ev and 2^-ev (x < 0: by key), the keys'
-    // exponents, and the factors of the producers' rows (RUNS: of K's and of V's)
+    // exponents, and the producers' factors of their rows of two tiles
     __shared__ float4 half_scale[SCALED ? 8 : 1][2];
     __shared__ uint16_t key_exps[SCALED ? 8 : 1][SCALED ? kKeysTc : 1];
-    __shared__ uint16_t factors[RUNS ? 2 : SCALED ? 4 : 1][RUNS ? 8 : 2][RUNS ? kKeysTc : SCALED ? 64 : 1];  // fp16; 0: zeros, whatever was copied
-    __shared__ uint64_t landed[2][RUNS ? NK : 1];  // RUNS: a tile's codes are there
-    __shared__ int64_t scratch[C::kThreads / 32 + 4];
+    __shared__ uint32_t factors[SCALED ? kProducers : 1][2][SCALED ? 64 : 1];
+    __shared__ int64_t scratch[kTcThreads / 32 + 4];
     const Patience limit{&abort_flag, p.wait_ns};
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int s = 0; s < NK; s++) {
-            bar_init(kfull + s, RUNS ? 64 : 64 + 2);  // two producer warps' copies, and their live masks
+            bar_init(kfull + s, 64 + 2);  // two producer warps' copies, and their live masks
             bar_init(kempty + s, 2);  // both streams
         }
         for (int s = 0; s < NV; s++) {
@@ -167,18 +154,15 @@ __device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused
             bar_init(pfull + 2 * s + 1, 4);
             bar_init(done + s, 1);
         }
-        if (RUNS)
-            for (int s = 0; s < 2 * NK; s++)
-                bar_init(&landed[0][0] + s, 1);
         bar_init(&jfull, 128);
         bar_init(&jempty, 128);
         bar_init(&go1, 8);
-        abort_flag = 0, never_abort = 0, lock = 0;
+        abort_flag = 0, lock = 0;
         for (int i = 0; i < 16; i++)
             bad[i] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == kIssue) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(tc::saddr(&tmem_slot)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -189,7 +173,7 @@ __device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused
     // ---- this CTA's share of the units
     const int ctas = gridDim.x, cta = blockIdx.x;
     using W = Walk<256, kKeysTc, kItemCostTc>;
-    const Find f = find_request<C::kThreads>(p.num_requests, scratch,
+    const Find f = find_request<kTcThreads>(p.num_requests, scratch,
                                             [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); });
     const Shares shares(f.total, ctas);
     PartDesc *descs = reinterpret_cast<PartDesc *>(p.parts);
@@ -204,7 +188,7 @@ __device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused
     W w;
     w.start(p, f.b >= 0 ? shares.start(cta) : 0, f.b >= 0 ? shares.start(cta + 1) : 0, f.b, f.before, mask_limit);
 
-    if (warp >= kIssue) {
+    if (warp >= 12) {
         // ------------------------------------------------------------ the issuing warps, one per stream
         // The whole warp walks and waits, one lane issues: in a branch of one
         // lane the descriptors went through vector registers and an MMA took
@@ -348,167 +332,10 @@ __device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused
                 mma_commit(done + s);
             __syncwarp();
         };
-        if (warp == kIssue)
+        if (warp == 12)
             stream(std::integral_constant<int, 0>{});
         else
             stream(std::integral_constant<int, 1>{});
-    } else if (RUNS && warp > 8) {
-        // ------------------------------------------------------------ RUNS: the warps that convert (two for K, two for V)
-        const int is_v = (warp - 9) >> 1, sub = (warp - 9) & 1;
-        unsigned char *ring = is_v ? sv : sk;
-        uint64_t *fulls = is_v ? vfull : kfull;
-        bool ok = true;
-        for (int x = 0, item = 0; w.more() && ok; item++) {
-#pragma unroll 1
-            for (int tile = w.t0; tile < w.t1; tile++, x++) {
-                const int st = x % NK;
-                ok = bar_wait(&landed[is_v][RUNS ? st : 0], (uint32_t)(x / NK) & 1u, limit);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok)
-                    break;
-                const bool drafted = is_v && tile * kKeysTc + 64 * (sub + 1) > w.rq.ctx;
-                if (convert_rows<D, 64, SCALED>(tc::saddr(ring) + st * C::kTileBytes, 64 * sub, drafted ? w.rq.ctx - tile * kKeysTc : kKeysTc,
-                                                factors[RUNS ? is_v : 0][RUNS ? x & 7 : 0] + (RUNS ? 64 * sub : 0)))
-                    bad[item & 15] = item + 1;
-                fence_async();
-                bar_arrive(fulls + st);
-            }
-            w.next(p);
-        }
-    } else if (RUNS && warp == 8) {
-        // ------------------------------------------------------------ RUNS: the warp that copies
-        // A tile is kKeysTc / run runs of `run` tokens that lie in one page each, a
-        // lane per run.  Tiles are prepared (rows, masks, exponents; the bytes sent
-        // for into L2) up to two before they are copied; K and V of the next tile are
-        // copied, a box per run, where a stage of theirs is free.
-        const int run = p.run, shift = __ffs(run) - 1, runs = kKeysTc >> shift;
-        int phys = 0, off = -1;            // of the tile looked up last: its run's page, offset of its first token (< 0: past the end)
-        uint32_t exps = 0;                 // of the tile resolved last
-        bool there = false;                // ... whether its page is
-        int left = 0, left_next = 0;       // tokens from the beginning of the tile resolved last, and of the one looked up last
-        int look_tile = w.t0, look_head = 0, looked = 0;  // looked: tiles looked up, two ahead while there are any
-        auto look = [&]() {  // w: the walk of the look-ups
-            off = -1;
-            if (!w.more())
-                return;
-            looked++;
-            left_next = w.rq.ctx + w.rq.nq - look_tile * kKeysTc;
-            look_head = w.head();
-            if (lane < runs && (lane << shift) < left_next) {
-                const int j = look_tile * kKeysTc + (lane << shift), blk = block_of(p, j);
-                off = j - blk * p.block_size;
-                phys = __ldg(p.table + w.b * p.table_stride + blk);
-            }
-            if (++look_tile >= w.t1) {
-                w.next(p);
-                look_tile = w.t0;
-            }
-        };
-        auto resolve = [&](int slot) {
-            uint32_t at = ~0u;
-            there = off >= 0 && phys >= 0 && phys < p.num_blocks;
-            if (there) {
-                const int64_t page = (int64_t)phys * p.num_kv_heads + look_head;
-                at = (uint32_t)(page * p.block_size + off);
-                exps = __ldg(reinterpret_cast<const uint16_t *>(p.block_scales) + page);
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.cache + (int64_t)at * C::kRow), "r"(run * C::kRow) : "memory");
-            } else if (off >= 0) {
-                flags |= kFlagBlockRange;
-            }
-            left = left_next;
-            rows[slot][0][RUNS ? lane : 0] = at;
-            __syncwarp();
-        };
-        // what tile x's keys have in common, and the next one's rows
-        auto prepare = [&](int x) {
-            int ek[4], ev[4], hi[2][2] = {{kScaleMin, kScaleMin}, {kScaleMin, kScaleMin}}, lo[2][2] = {{kScaleMax, kScaleMax}, {kScaleMax, kScaleMax}};
-            uint32_t seen = 0;
-#pragma unroll
-            for (int g = 0; g < 4; g++) {
-                const int key = 32 * g + lane, of = key >> shift;
-                const uint32_t e = __shfl_sync(0xffffffffu, exps, of);
-                const bool is = __shfl_sync(0xffffffffu, there, of) && key < left;
-                ek[g] = min(max((int)(int8_t)(e & 0xffu), kScaleMin), kScaleMax);
-                ev[g] = min(max((int)(int8_t)((e >> 8) & 0xffu), kScaleMin), kScaleMax);
-                const unsigned bits = __ballot_sync(0xffffffffu, is);
-                if (lane == 0)
-                    live[x & 7][g] = bits;
-                seen |= (uint32_t)is << g;
-                if (is) {
-                    hi[g >> 1][0] = max(hi[g >> 1][0], ek[g]), lo[g >> 1][0] = min(lo[g >> 1][0], ek[g]);
-                    hi[g >> 1][1] = max(hi[g >> 1][1], ev[g]), lo[g >> 1][1] = min(lo[g >> 1][1], ev[g]);
-                }
-            }
-#pragma unroll
-            for (int hh = 0; hh < 2; hh++) {
-                const int hk = __reduce_max_sync(0xffffffffu, hi[hh][0]), hv = __reduce_max_sync(0xffffffffu, hi[hh][1]);
-                const bool each = __any_sync(0xffffffffu, hk - lo[hh][0] > kSpread && lo[hh][0] <= hi[hh][0]) ||
-                                  __any_sync(0xffffffffu, hv - lo[hh][1] > kSpread && lo[hh][1] <= hi[hh][1]);
-#pragma unroll
-                for (int g = 2 * hh; g < 2 * hh + 2; g++) {
-                    const int key = 32 * g + lane;
-                    const bool is = (seen >> g) & 1u;
-                    auto factor = [&](int d) { return (uint16_t)(!is ? 0 : each ? 15 << 10 : d < 15 ? (15 - d) << 10 : 1 << 9); };  // 2^-d
-                    factors[0][RUNS ? x & 7 : 0][RUNS ? key : 0] = factor(hk - ek[g]);
-                    factors[RUNS ? 1 : 0][RUNS ? x & 7 : 0][RUNS ? key : 0] = factor(hv - ev[g]);
-                    key_exps[SCALED ? x & 7 : 0][SCALED ? key : 0] = (uint16_t)((ek[g] & 0xff) | (ev[g] & 0xff) << 8);
-                }
-                if (lane == 0)
-                    half_scale[SCALED ? x & 7 : 0][hh] = make_float4(each ? -1.0f : __int_as_float((127 + hk) << 23), (float)hv,
-                                                                     __int_as_float((127 - hv) << 23), 0.0f);
-            }
-            resolve((x + 1) & 3);
-            look();
-        };
-        auto copy = [&](int v, int x) {
-            const uint32_t at = rows[x & 3][0][RUNS ? lane : 0];
-            const int n = __popc(__ballot_sync(0xffffffffu, at != ~0u));
-            uint64_t *bar = &landed[v][RUNS ? x % NK : 0];
-            if (lane == 0)  // (with what prepare() wrote: the ballot came after it)
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(tc::saddr(bar)), "r"(n * run * D) : "memory");
-            __syncwarp();
-            if (at != ~0u)
-                asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                                 raw_at<D>(tc::saddr(v ? sv : sk) + (x % NK) * C::kTileBytes, lane << shift, 0)),
-                             "l"(map), "r"(v * D), "r"((int)at), "r"(tc::saddr(bar))
-                             : "memory");
-            __syncwarp();
-        };
-        look();
-        resolve(0);
-        look();
-        if (p.test_hold)
-            looked = 0;  // test hook: nothing is copied, the other roles' waits run out
-        int prepared = 0, next[2] = {0, 0};  // tiles prepared; the next of K and of V
-        unsigned long long since = 0;        // when the warp began to have nothing to do
-        while (min(next[0], next[1]) < looked) {
-            bool idle = true;
-#pragma unroll
-            for (int v = 0; v < 2; v++)
-                if (next[v] < prepared &&
-                    __all_sync(0xffffffffu, bar_test((v ? vempty : kempty) + next[v] % NK, ((uint32_t)(next[v] / NK) & 1u) ^ 1u))) {
-                    copy(v, next[v]++);
-                    idle = false;
-                }
-            if (prepared < looked && prepared - min(next[0], next[1]) < 3) {
-                prepare(prepared++);
-                idle = false;
-            }
-            if (!idle) {
-                since = 0;
-                continue;
-            }
-            const unsigned long long now = gtimer();
-            since = since ? since : now;
-            if (now - since > limit.ns)
-                *limit.abort = 1;
-            if (__any_sync(0xffffffffu, *limit.abort != 0))
-                break;
-        }
-        // what was sent for has landed before the CTA may end (a copy takes microseconds)
-        for (int v = 0; v < 2; v++)
-            for (int x = max(0, next[v] - NK); x < next[v]; x++)
-                bar_wait(&landed[v][RUNS ? x % NK : 0], (uint32_t)(x / NK) & 1u, Patience{&never_abort, limit.ns});
     } else if (warp >= 8) {
         // ------------------------------------------------------------ producers
         // Two warps copy K, two V, each 64 rows of every tile.  While a warp
@@ -600,7 +427,7 @@ __device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused
 #pragma unroll
                 for (int g = 0; g < 2; g++) {
                     const int d = each || exps[g] >= 0x10000u ? 0 : is_v ? hi[1] - ev[g] : hi[0] - ek[g];
-                    factors[SCALED ? pw : 0][x & 1][SCALED ? 32 * g + lane : 0] = (uint16_t)(d < 15 ? (15 - d) << 10 : 1 << 9);  // 2^-d
+                    factors[pw][x & 1][32 * g + lane] = (uint32_t)(d < 15 ? (15 - d) << 10 : 1 << 9) * 0x10001u;  // 2^-d
                     if (!is_v)
                         key_exps[x & 7][64 * sub + 32 * g + lane] = (uint16_t)((ek[g] & 0xff) | (ev[g] & 0xff) << 8);
                 }
@@ -666,7 +493,7 @@ __device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused
                     cp_wait<0>();
                 __syncwarp();
                 if (convert_rows<D, 64, SCALED>(tc::saddr(ring) + st * C::kTileBytes, 64 * sub, drafted ? w.rq.ctx - tile * kKeysTc : kKeysTc,
-                                                factors[SCALED ? pw : 0][x & 1]))
+                                                SCALED ? factors[pw][x & 1] : nullptr))
                     bad[item & 15] = item + 1;
                 fence_async();
             } else if (drafted) {
@@ -1094,7 +921,7 @@ __device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused
         }
     }
     __syncthreads();
-    if (warp == kIssue) {
+    if (warp == 12) {
         // every product has completed before the tensor memory is freed
         if (lane == 0) {
             const unsigned long long t0 = gtimer();
@@ -1111,19 +938,6 @@ __device__ __forceinline__ void attention_tc(const AttnParams &p, [[maybe_unused
     flags = __reduce_or_sync(0xffffffffu, flags);
     if (lane == 0 && flags && p.error_flags)
         atomicOr(p.error_flags, flags);
-}
-
-template <int D, bool FP8, bool SCALED = false>
-__global__ void __launch_bounds__((TcCfg<D, FP8>::kThreads), 1) attention_tc_kernel(const __grid_constant__ AttnParams p)
-{
-    attention_tc<D, FP8, SCALED, false>(p, nullptr);
-}
-
-template <int D>
-__global__ void __launch_bounds__((TcCfg<D, true, true>::kThreads), 1)
-    attention_tc_runs_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map)
-{
-    attention_tc<D, true, true, true>(p, &map);
 }
 
 constexpr int kJoinDims = 16;
@@ -1207,7 +1021,7 @@ __global__ void __launch_bounds__(128) join_tc_kernel(const __grid_constant__ At
 
 // ------------------------------------------------------------------ launches
 
-template <int D, bool FP8, bool SCALED = false, bool RUNS = false>
+template <int D, bool FP8, bool SCALED = false>
 cudaError_t attention_tc_ctas(int &ctas)
 {
     static int cached[64];
@@ -1221,12 +1035,8 @@ cudaError_t attention_tc_ctas(int &ctas)
     if (have == 0) {
         e = cudaDeviceGetAttribute(&have, cudaDevAttrMultiProcessorCount, dev);
         if (e == cudaSuccess)
-            if constexpr (RUNS)
-                e = cudaFuncSetAttribute(attention_tc_runs_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         TcCfg<D, true, true>::kSmem);
-            else
-                e = cudaFuncSetAttribute(attention_tc_kernel<D, FP8, SCALED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         TcCfg<D, FP8>::kSmem);
+            e = cudaFuncSetAttribute(attention_tc_kernel<D, FP8, SCALED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     TcCfg<D, FP8>::kSmem);
         if (e != cudaSuccess)
             return e;
         __atomic_store_n(&cached[dev], have, __ATOMIC_RELEASE);
@@ -1244,13 +1054,13 @@ int64_t attention_tc_bytes(cudaError_t &e)
 }
 
 template <int D, bool FP8, bool SCALED = false>
-cudaError_t launch_attention_tc(const AttnParams &p, cudaStream_t stream)
+cudaError_t attention_tc(const AttnParams &p, cudaStream_t stream)
 {
     using C = TcCfg<D, FP8>;
     int ctas = 0;
     cudaError_t e = attention_tc_ctas<D, FP8, SCALED>(ctas);
     if (e == cudaSuccess)
-        e = launch_pdl(attention_tc_kernel<D, FP8, SCALED>, ctas, C::kThreads, C::kSmem, stream, p);
+        e = launch_pdl(attention_tc_kernel<D, FP8, SCALED>, ctas, kTcThreads, C::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
     return launch_pdl_grid(join_tc_kernel<D, FP8>, dim3((unsigned)ctas, (unsigned)(2 * (D / kJoinDims))), 128, 0, 0, stream, p, ctas);
@@ -1265,54 +1075,14 @@ int64_t workspace_tc(bool fp8, cudaError_t &e)
 template <int D>
 cudaError_t attention_tc_d(const AttnParams &p, bool fp8, cudaStream_t stream)
 {
-    return fp8 ? launch_attention_tc<D, true>(p, stream) : launch_attention_tc<D, false>(p, stream);
+    return fp8 ? attention_tc<D, true>(p, stream) : attention_tc<D, false>(p, stream);
 }
-
-// The cache as rows of `bytes`, boxes of half a row by `run` rows.
-inline bool encode_runs(CUtensorMap *map, const AttnParams &p, int bytes, int run)
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    if (!fn)
-        return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)(p.num_blocks * p.num_kv_heads * p.block_size)}, strides[1] = {(cuuint64_t)bytes};
-    const cuuint32_t box[2] = {(cuuint32_t)bytes / 2, (cuuint32_t)run}, steps[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<unsigned char *>(p.cache), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Tokens of a tile that surely lie in one page: the largest power of two that divides the block size.
-inline int run_of(int block_size) { return std::min(block_size & -block_size, kKeysTc); }
 
 // (the workspace of an fp8 call: as many CTAs, the same parts)
 template <int D>
 cudaError_t attention_tc_scaled_d(const AttnParams &p, cudaStream_t stream)
 {
-    if constexpr (D == 128) {
-        // Runs of four tokens and more are copied by boxes (a lane names one), from
-        // caches whose rows 31 bits count; shorter ones by the producers that go row by row.
-        const int run = run_of(p.block_size);
-        CUtensorMap map;
-        if (run >= 4 && p.num_blocks * p.num_kv_heads * p.block_size <= INT32_MAX && encode_runs(&map, p, 2 * D, run)) {
-            AttnParams q = p;
-            q.run = run;
-            int ctas = 0;
-            cudaError_t e = attention_tc_ctas<D, true, true, true>(ctas);
-            if (e == cudaSuccess)
-                e = launch_pdl(attention_tc_runs_kernel<D>, ctas, (TcCfg<D, true, true>::kThreads), (TcCfg<D, true, true>::kSmem), stream, q, map);
-            if (e != cudaSuccess)
-                return e;
-            return launch_pdl_grid(join_tc_kernel<D, true>, dim3((unsigned)ctas, (unsigned)(2 * (D / kJoinDims))), 128, 0, 0, stream, p, ctas);
-        }
-    }
-    return launch_attention_tc<D, true, true>(p, stream);
+    return attention_tc<D, true, true>(p, stream);
 }
 
 #define DSPARK_ATTN_TC_SCALED_DECLARE(D) extern template cudaError_t attention_tc_scaled_d<D>(const AttnParams &, cudaStream_t);
