@@ -62,7 +62,7 @@
 // (2^ek, ev, 2^-ev) are read beside its page's number one tile before they are
 // stored, so that no load is waited for.  What bounds it is issue at two warps per
 // scheduler: 64 requests of 1,024 to 8,192 tokens, 64 query and 8 KV heads of 128,
-// take 142 us with a token each (8 rows a KV head; 67 us by their bytes), 271 with
+// take 132 us with a token each (8 rows a KV head; 67 us by their bytes), 271 with
 // seven (56 rows: each of four warps turns all of a tile's codes into fp16 for its
 // 16 rows; 43% of the issue slots, 37% of the tensor pipe).
 //
@@ -687,12 +687,19 @@ struct Cfg {
     static constexpr int kStage = kTile * kRow;
     // CTAs per SM by registers (about 250 a thread at D 128 and 256, 168 at 64),
     // and as many stages as share the SM's shared memory between them
-    static constexpr int kCtas = D == 64 ? 3 : D == 128 ? 2 : 1;
-    static constexpr int kStages = D == 64 ? (FP8 ? 6 : 4) : D == 128 ? (FP8 ? 5 : 2) : (FP8 ? 4 : 2);
+    // Page-scaled at D 128 with up to 32 rows: the queries leave the registers and a
+    // third CTA hides the latencies better than the registers did (8 / 32 rows 142 /
+    // 186 -> 132 / 182 us).  With 64 rows the spills of 168 registers cost more (271 -> 316).
+    static constexpr bool kThree = SCALED && D == 128 && WR <= 2;
+    static constexpr int kCtas = kThree || D == 64 ? 3 : D == 128 ? 2 : 1;
+    static constexpr int kStages = kThree ? 3 : D == 64 ? (FP8 ? 6 : 4) : D == 128 ? (FP8 ? 5 : 2) : (FP8 ? 4 : 2);
     static constexpr int kNT = D / 8;                                            // n-tiles of the output
     static constexpr int kJoin = kWK > 1 ? (kWK / 2) * WR * (kNT * 128 + 64) * 4 : 0;  // bytes to join the key warps
-    static constexpr bool kQShared = SCALED && D == 256;                         // queries in shared memory (scores_shared)
-    static constexpr int kSmem = kStages * kStage + kJoin + (kQShared ? WR * (D / 16) * 512 : 0);
+    // queries in shared memory (scores_shared) where the registers are short: they
+    // spilled at D 256, and at D 64 with 64 rows (196 -> 180 us)
+    static constexpr bool kQShared = SCALED && (D == 256 || kThree || (D == 64 && WR == 4));
+    static constexpr int kQueries = kQShared ? WR * (D / 16) * 512 : 0;  // bytes, in the join's place: an item joins behind its last product
+    static constexpr int kSmem = kStages * kStage + (kJoin > kQueries ? kJoin : kQueries);
     static constexpr int kPart = WR * (kNT * 128 + 32);                          // floats of one part
     static_assert(kCtas * (kSmem + 1536 + (SCALED ? kStages * kTile * 16 : 0)) <= 227 * 1024, "shared memory");
 };
@@ -837,7 +844,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) at
         uint32_t qa[D / 16][4];
         float rs[2];
         load_q<D, FP8>(p, rq, h, row0 + 16 * wr, qa, rs);
-        const uint32_t queries = stages + C::kStages * C::kStage + C::kJoin + wr * (D / 16) * 512;
+        const uint32_t queries = stages + C::kStages * C::kStage + wr * (D / 16) * 512;
         if constexpr (C::kQShared) {
             // before the barrier of the item's first tile, behind that of the item before
             if (wk == 0)
@@ -906,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) at
             else
                 scores<D, FP8, NS, C::kRow>(s, qa, st, wk * C::kKeys);
             const uint32_t lv[4] = {live[stage][0], live[stage][1], live[stage][2], live[stage][3]};
-            [[maybe_unused]] float back[SCALED ? NS : 1][2];  // 2^-ev of this lane's keys
+            [[maybe_unused]] float back[SCALED ? NS : 1][2];  // 2^-ev of this lane's keys (read again instead: 787 -> 909 us at D 256, 64 rows)
             const bool masked = drafted || (lv[0] & lv[1] & lv[2] & lv[3]) != 0xffffu;
 #pragma unroll
             for (int n = 0; n < NS; n++) {
