@@ -43,7 +43,8 @@ STEP_API_SRC = os.path.join(CSRC, "draft_step_api.cpp")
 API_SRCS = (API_SRC, DRAFT_API_SRC, STEP_API_SRC)
 HEADERS = [os.path.join(CSRC, "ctx_kv_internal.h"), os.path.join(CSRC, "ctx_kv_device.cuh"),
            os.path.join(CSRC, "ctx_kv_pipe.cuh"), os.path.join(CSRC, "draft_attn_internal.h"),
-           os.path.join(CSRC, "tree_attn_mma.cuh"), os.path.join(CSRC, "tree_attn_tc.cuh"),
+           os.path.join(CSRC, "tree_attn_mma.cuh"), os.path.join(CSRC, "tree_attn_split.cuh"),
+           os.path.join(CSRC, "tree_attn_tc.cuh"),
            os.path.join(CSRC, "tc_ptx.cuh"), os.path.join(CSRC, "attn_weight.cuh"),
            os.path.join(CSRC, "draft_api_checks.h"), os.path.join(CSRC, "draft_step_internal.h"),
            os.path.join(CSRC, "page_scale.cuh"), os.path.join(INCLUDE, "dspark_ctx_kv.h"),

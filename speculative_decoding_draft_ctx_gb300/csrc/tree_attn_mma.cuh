@@ -60,11 +60,10 @@
 // above, relative to the largest contribution.  The sum of weights takes 2^-ev of
 // it back, exactly but for fp32's own rounding (|ev| <= 32).  A key's three numbers
 // (2^ek, ev, 2^-ev) are read beside its page's number one tile before they are
-// stored, so that no load is waited for.  What bounds it is issue at two warps per
-// scheduler: 64 requests of 1,024 to 8,192 tokens, 64 query and 8 KV heads of 128,
-// take 132 us with a token each (8 rows a KV head; 67 us by their bytes), 271 with
-// seven (56 rows: each of four warps turns all of a tile's codes into fp16 for its
-// 16 rows; 43% of the issue slots, 37% of the tensor pipe).
+// stored, so that no load is waited for.  This kernel takes up to 16 rows at D 128
+// and 32 at D 64: 64 requests of 1,024 to 8,192 tokens, 64 query and 8 KV heads of 128, take
+// 132 us with a token each (67 us by their bytes), bound by issue at three warps per
+// scheduler.  The others: tree_attn_split.cuh.
 //
 // What a row does not see.  Scores of masked keys are replaced by -inf
 // whatever they are; V rows of drafted tokens that hold infinities or NaN are
@@ -375,14 +374,16 @@ struct Walk {
 // through the block table.  A warp takes 16
 // rows; its lanes 0..15 (and 16..31 alike) hold the block of their row, which
 // `fetch` has read for the tile that `load` will copy next.
-template <int ROW>
+// SCALE: what is kept of a row's scales (page-scaled): float4 (2^ek, ev, 2^-ev), or
+// uint32_t, the bf16 bits of 2^ek and of 2^-ev.
+template <int ROW, typename SCALE = float4>
 struct Loader {
     static constexpr int kWords = ROW / 16;
     int64_t phys;
     int off;
     bool live;
     uint32_t exponents;  // page-scaled: of the row that was loaded last, not stored yet, and where they belong
-    float4 *scales_at = nullptr;
+    SCALE *scales_at = nullptr;
 
     __device__ __forceinline__ void fetch(const AttnParams &p, int b, int tile, int len)
     {
@@ -404,11 +405,14 @@ struct Loader {
         if (scales_at) {
             const int ek = min(max((int)(int8_t)(exponents & 0xffu), kScaleMin), kScaleMax);
             const int ev = min(max((int)(int8_t)(exponents >> 8), kScaleMin), kScaleMax);
-            *scales_at = make_float4(__int_as_float((127 + ek) << 23), (float)ev, __int_as_float((127 - ev) << 23), 0.0f);
+            if constexpr (sizeof(SCALE) == 16)
+                *scales_at = make_float4(__int_as_float((127 + ek) << 23), (float)ev, __int_as_float((127 - ev) << 23), 0.0f);
+            else
+                *scales_at = (uint32_t)((127 + ek) << 7 | (127 - ev) << 23);
             scales_at = nullptr;
         }
     }
-    __device__ __forceinline__ void fetch_scales(const AttnParams &p, int h, float4 *stage)
+    __device__ __forceinline__ void fetch_scales(const AttnParams &p, int h, SCALE *stage)
     {
         if ((threadIdx.x & 31) < 16) {
             scales_at = stage + (threadIdx.x >> 5) * 16 + (threadIdx.x & 15);
@@ -648,8 +652,7 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&a)[D 
     }
 }
 
-// The same over codes with the A operands in shared memory, as the lanes hold
-// them: at D 256 they would be 64 of the 255 registers.
+// The same over codes with the A operands in shared memory, as the lanes hold them.
 template <int D, int NT, int PITCH>
 __device__ __forceinline__ void scores_shared(float (&s)[NT][4], uint32_t queries, uint32_t stage, int key0)
 {
@@ -678,6 +681,44 @@ __device__ __forceinline__ void scores_shared(float (&s)[NT][4], uint32_t querie
     }
 }
 
+// Infinities and NaN among the V of a tile's drafted tokens, rows [from, to): zeroed
+// by all threads (and accounted for when the item ends).  Whether this thread met any.
+template <bool FP8, int ROW>
+__device__ __forceinline__ bool zero_nonfinite(unsigned char *stage, int from, int to)
+{
+    bool any = false;
+    for (int x = threadIdx.x; x < kTile * (ROW / 32); x += kThreads) {
+        const int y = x / (ROW / 32), c = ROW / 32 + x % (ROW / 32);
+        if (y < from || y >= to)
+            continue;
+        uint4 *at = reinterpret_cast<uint4 *>(stage + y * ROW + ((c ^ swz(y)) << 4));
+        uint4 v = *at;
+        uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+        bool hit = false;
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            if (nonfinite_word(vw[k], FP8)) {
+                hit = true;
+                if (FP8) {
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        if (((vw[k] >> (8 * e)) & 0x7fu) == 0x7fu)
+                            vw[k] &= ~(0xffu << (8 * e));
+                } else {
+                    if ((vw[k] & 0x7f80u) == 0x7f80u)
+                        vw[k] &= 0xffff0000u;
+                    if ((vw[k] & 0x7f800000u) == 0x7f800000u)
+                        vw[k] &= 0xffffu;
+                }
+            }
+        if (hit) {
+            *at = make_uint4(vw[0], vw[1], vw[2], vw[3]);
+            any = true;
+        }
+    }
+    return any;
+}
+
 // ------------------------------------------------------------------ the attention kernel
 
 template <int D, bool FP8, int WR, bool SCALED = false>
@@ -687,17 +728,13 @@ struct Cfg {
     static constexpr int kStage = kTile * kRow;
     // CTAs per SM by registers (about 250 a thread at D 128 and 256, 168 at 64),
     // and as many stages as share the SM's shared memory between them
-    // Page-scaled at D 128 with up to 32 rows: the queries leave the registers and a
-    // third CTA hides the latencies better than the registers did (8 / 32 rows 142 /
-    // 186 -> 132 / 182 us).  With 64 rows the spills of 168 registers cost more (271 -> 316).
-    static constexpr bool kThree = SCALED && D == 128 && WR <= 2;
-    static constexpr int kCtas = kThree || D == 64 ? 3 : D == 128 ? 2 : 1;
-    static constexpr int kStages = kThree ? 3 : D == 64 ? (FP8 ? 6 : 4) : D == 128 ? (FP8 ? 5 : 2) : (FP8 ? 4 : 2);
+    // Page-scaled at D 128: the queries leave the registers, so that a third CTA hides
+    // the latencies, better than the registers did (142 -> 132 us).
+    static constexpr bool kQShared = SCALED && D == 128;
+    static constexpr int kCtas = kQShared || D == 64 ? 3 : D == 128 ? 2 : 1;
+    static constexpr int kStages = kQShared ? 3 : D == 64 ? (FP8 ? 6 : 4) : D == 128 ? (FP8 ? 5 : 2) : (FP8 ? 4 : 2);
     static constexpr int kNT = D / 8;                                            // n-tiles of the output
     static constexpr int kJoin = kWK > 1 ? (kWK / 2) * WR * (kNT * 128 + 64) * 4 : 0;  // bytes to join the key warps
-    // queries in shared memory (scores_shared) where the registers are short: they
-    // spilled at D 256, and at D 64 with 64 rows (196 -> 180 us)
-    static constexpr bool kQShared = SCALED && (D == 256 || kThree || (D == 64 && WR == 4));
     static constexpr int kQueries = kQShared ? WR * (D / 16) * 512 : 0;  // bytes, in the join's place: an item joins behind its last product
     static constexpr int kSmem = kStages * kStage + (kJoin > kQueries ? kJoin : kQueries);
     static constexpr int kPart = WR * (kNT * 128 + 32);                          // floats of one part
@@ -872,36 +909,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) at
             const int key0 = tile * kTile;
             const bool drafted = key0 + kTile > rq.ctx;  // the tile holds drafted tokens or ends beyond them
             if (drafted) {
-                // infinities and NaN among the drafted V: zeroed here, accounted for at the end
-                for (int x = tid; x < kTile * (C::kRow / 32); x += kThreads) {
-                    const int y = x / (C::kRow / 32), c = C::kRow / 32 + x % (C::kRow / 32);
-                    if (key0 + y < rq.ctx || key0 + y >= len)
-                        continue;
-                    uint4 *at = reinterpret_cast<uint4 *>(smem + stage * C::kStage + y * C::kRow + ((c ^ swz(y)) << 4));
-                    uint4 v = *at;
-                    uint32_t vw[4] = {v.x, v.y, v.z, v.w};
-                    bool hit = false;
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        if (nonfinite_word(vw[k], FP8)) {
-                            hit = true;
-                            if (FP8) {
-#pragma unroll
-                                for (int e = 0; e < 4; e++)
-                                    if (((vw[k] >> (8 * e)) & 0x7fu) == 0x7fu)
-                                        vw[k] &= ~(0xffu << (8 * e));
-                            } else {
-                                if ((vw[k] & 0x7f80u) == 0x7f80u)
-                                    vw[k] &= 0xffff0000u;
-                                if ((vw[k] & 0x7f800000u) == 0x7f800000u)
-                                    vw[k] &= 0xffffu;
-                            }
-                        }
-                    if (hit) {
-                        *at = make_uint4(vw[0], vw[1], vw[2], vw[3]);
-                        any_bad = 1;
-                    }
-                }
+                if (zero_nonfinite<FP8, C::kRow>(smem + stage * C::kStage, rq.ctx - key0, len - key0))
+                    any_bad = 1;
                 __syncthreads();
             }
             float s[NS][4];
@@ -913,7 +922,7 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) at
             else
                 scores<D, FP8, NS, C::kRow>(s, qa, st, wk * C::kKeys);
             const uint32_t lv[4] = {live[stage][0], live[stage][1], live[stage][2], live[stage][3]};
-            [[maybe_unused]] float back[SCALED ? NS : 1][2];  // 2^-ev of this lane's keys (read again instead: 787 -> 909 us at D 256, 64 rows)
+            [[maybe_unused]] float back[SCALED ? NS : 1][2];  // 2^-ev of this lane's keys
             const bool masked = drafted || (lv[0] & lv[1] & lv[2] & lv[3]) != 0xffffu;
 #pragma unroll
             for (int n = 0; n < NS; n++) {
@@ -1316,25 +1325,10 @@ cudaError_t attention_d(const AttnParams &p, int wr, bool fp8, cudaStream_t stre
 }
 
 template <int D>
-int64_t workspace_scaled_d(int wr, cudaError_t &e)
-{
-    int ctas = 0;
-    e = wr == 1 ? attention_ctas<D, true, 1, true>(ctas) : wr == 2 ? attention_ctas<D, true, 2, true>(ctas) : attention_ctas<D, true, 4, true>(ctas);
-    const int64_t part = wr == 1 ? Cfg<D, true, 1>::kPart : wr == 2 ? Cfg<D, true, 2>::kPart : Cfg<D, true, 4>::kPart;
-    return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * part * 4) : 0;
-}
-
+int64_t workspace_scaled_d(int wr, cudaError_t &e);  // tree_attn_split.cuh
 template <int D>
-cudaError_t attention_scaled_d(const AttnParams &p, int wr, cudaStream_t stream)
-{
-    switch (wr) {
-    case 1: return attention<D, true, 1, true>(p, stream);
-    case 2: return attention<D, true, 2, true>(p, stream);
-    default: return attention<D, true, 4, true>(p, stream);
-    }
-}
+cudaError_t attention_scaled_d(const AttnParams &p, int wr, cudaStream_t stream);
 
-// one translation unit per head dim
 #define DSPARK_ATTN_SCALED_DECLARE(D)                              \
     extern template int64_t workspace_scaled_d<D>(int, cudaError_t &); \
     extern template cudaError_t attention_scaled_d<D>(const AttnParams &, int, cudaStream_t);

@@ -1,6 +1,6 @@
 // The drafted tokens' attention (mma.sync) over page-scaled caches for head dim 128
 // (one translation unit per head dim, so that they compile side by side).
-#include "tree_attn_mma.cuh"
+#include "tree_attn_split.cuh"
 
 namespace dspark {
 namespace attn {

@@ -735,6 +735,54 @@ def test_scaled_attention_nan_codes(kernel):
     check_scaled(p, "causal", None)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,nq", [(1, 17), (4, 8), (3, 11), (4, 16), (5, 13)])
+def test_scaled_attention_row_groups(D, G, nq, kernel):
+    """17 to 65 rows a KV head: contexts of no token, of one tile, over several CTAs; requests of fewer rows."""
+    ctx, tokens = (0, 64, 1, 2500, 130), (nq, nq, nq, nq, nq)
+    p = ScaledProblem(G + nq, ctx, tokens, 2 * G, 2, D, 16, packed=True)
+    check_scaled(p, "tree", tree_mask(tokens, 1, D, empty=(0, nq)))
+    tokens = (2 * nq - 1, 0, 1, nq, nq)
+    p = ScaledProblem(G + nq + 1, ctx, tokens, 2 * G, 2, D, 24)
+    check_scaled(p, "causal", None)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq", [5, 12])
+def test_scaled_attention_rising_scores(D, nq, kernel):
+    """A maximum that grows by less and by more than an octave a tile, down to the last token; and one that falls."""
+    n = 1500
+    for k, last in enumerate((1.0, 30.0, -60.0)):
+        p = ScaledProblem(12 + k, (n,), (nq,), 4, 1, D, 16, k_exp=(-4, -3), v_exp=(-2, 3))
+        j = torch.arange(n + nq)
+        page, off = p.table[0].long()[j // 16], j % 16
+        p.cache[page, 0, off, :16] = (j / (n + nq) * 256)[:, None].expand(-1, 16).to(torch.float8_e4m3fn).view(torch.uint8)
+        p.qkv[:, :, :16] = last * D ** 0.5 / 256
+        check_scaled(p, "causal", None)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq", [5, 12])
+def test_scaled_attention_nan_codes_and_a_tail_of_more_rows(D, nq, kernel):
+    """As above for 20 and 48 rows: NaN codes of drafted tokens, and a thin tail behind a heavy token."""
+    p = ScaledProblem(7, (100, 3000), (nq, nq), 8, 2, D, 16)
+    for b, c in enumerate((100, 3000)):
+        for j in (c + 2, c + 4):
+            p.cache[int(p.table[b, j // 16]), :, j % 16, D + j % 7::9] = 0x7f if j % 4 else 0xff
+    check_scaled(p, "causal", None)
+    n = 6001
+    p = ScaledProblem(11, (n,), (nq,), 4, 1, D, 16, k_exp=(0, 1), v_exp=(0, 1))
+    j = torch.arange(n + nq)
+    page, off = p.table[0].long()[j // 16], j % 16
+    rows = torch.zeros((n + nq, 2 * D))
+    rows[0, 0] = 16.0
+    rows[1:, D:] = 1.0
+    p.cache[page, 0, off] = rows.to(torch.float8_e4m3fn).view(torch.uint8)
+    p.qkv[:] = 0
+    p.qkv[:, :, 0] = (math.log(n) + math.log(1000.0)) / 16.0 * D ** 0.5
+    check_scaled(p, "dense", None)
+
+
 # ------------------------------------------------------------------ one step after another
 
 
