@@ -747,6 +747,37 @@ def test_scaled_attention_row_groups(D, G, nq, kernel):
     check_scaled(p, "causal", None)
 
 
+@pytest.mark.parametrize("D,G,nq", [(256, 2, 3), (128, 8, 4), (64, 6, 9), (128, 4, 16), (256, 8, 7)])
+def test_scaled_attention_row_groups_with_empty_rows_bad_pages_and_rows_behind(D, G, nq, kernel):
+    """A row that sees nothing, rows behind the last sequence, then a page out of range: as if its tokens were not there."""
+    tokens = (nq, nq - 1)
+    p = ScaledProblem(D + nq, (0, 150), tokens, 2 * G, 2, D, 16, pad_rows=3).cuda()
+    mask, n = tree_mask(tokens, 1, D, empty=(0, nq)), sum(tokens)
+    mask = torch.cat([mask, torch.full((3, 1), -1, dtype=torch.int64)])
+    out = torch.full((n + 3, 2 * G, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n + 3, 2 * G), 7.0, device="cuda")
+    run_scaled(p, "tree", mask, out=out, lse=lse)
+    assert bool((out[0] == 0).all()) and bool((lse[0] == -math.inf).all()) and bool((out[n:] == 7).all()) and bool((lse[n:] == 7).all())
+    want, z, to, tl = attention(p, "tree", mask)
+    close(out[:n], want, to)
+    assert int(p.d_flags) == 0
+    # the third page of the second request: its 16 tokens are left out
+    p.d_table[1, 2] = -1
+    got = run_scaled(p, "tree", mask)
+    assert int(p.d_flags) == dk.FLAG_BLOCK_RANGE
+    p.d_flags.zero_()
+    fresh = p.d_cache.clone()
+    page = int(p.table[1, 2])
+    p.d_table[1, 2] = page
+    p.d_cache[page] = 0        # V of 0, and scores of 0: they count for the sum only
+    zeros = run_scaled(p, "tree", mask)
+    p.d_cache.copy_(fresh)
+    # e^lse of both, 16 tokens of e^0 apart (lse below 2^4, off by some 2^-20 of it; out twice rounded to bf16, 2^-8 each)
+    a, b = got[1][nq:n].double().exp(), zeros[1][nq:n].double().exp()
+    assert ((b - a - 16).abs() <= 2.0 ** -12 * b).all()
+    assert ((got[0][nq:n].double() * (a / b)[..., None] - zeros[0][nq:n].double()).abs() <= 2.0 ** -6 * got[0][nq:n].double().abs().max()).all()
+
+
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("nq", [5, 12])
 def test_scaled_attention_rising_scores(D, nq, kernel):
