@@ -17,14 +17,14 @@
 // copies issued into the stage that those products have left.
 //
 // What it measured: 64 requests of 1,024 to 8,192 tokens, 64 query and 8 KV heads,
-// against a warp per 16 rows: head dim 256 with 8 / 32 / 56 / 128 rows a KV head 194 /
-// 393 / 583 / 1,160 us (335 / 482 / 787 / 1,560), 128 with 32 / 56 155 / 268 (182 /
-// 272), 64 with 56 178 (180).  What bounds it: some
-// 840 instructions a warp and tile at D 128 at 40% of the issue slots, a third of a
+// against a warp per 16 rows: head dim 256 with 8 / 32 / 56 / 128 rows a KV head 193 /
+// 368 / 543 / 1,088 us (335 / 482 / 787 / 1,560), 128 with 32 / 56 150 / 255 (182 /
+// 272), 64 with 56 166 (180).  What bounds it: some
+// 730 instructions a warp and tile at D 128 at 38% of the issue slots, a third of a
 // warp's time in fixed latencies (products, conversions, shuffles), the barriers
-// behind them; shared memory 55%, the tensor pipe 37%.  A third CTA per SM for 64 rows
-// of 128 (168 registers) spills, and without spills (the tiles planned one by one)
-// took 264.  With the walk in every thread's registers the sums of D 256 spilled: 802.
+// behind them; shared memory 55%, the tensor pipe 40%.  A third CTA per SM for 64 rows
+// of 128 (168 registers) spills (311 where two took 268).  With the walk in every
+// thread's registers the sums of D 256 spilled (802 where 583 was taken).
 #pragma once
 
 #include "tree_attn_mma.cuh"
@@ -33,9 +33,12 @@ namespace dspark {
 namespace attn {
 
 constexpr int kPlans = 8;  // items planned at once
-// A row's m stays until its maximum has grown by more than this (octaves): weights
-// are up to 2^15 then, fp16 goes to 2^16, and the sums are rescaled in few tiles.
-constexpr float kSlack = 1.0f;
+// A row's m stays until its maximum has grown by more than an octave, that is, is more
+// than kLimit above m (a difference, which is exact for scores of any size): weights
+// are up to 2^15 then, fp16 goes to 2^16, and in most tiles no sum is rescaled
+// (267 -> 255 us at 64 rows of D 128).  kNothing: m where nothing has been seen (no
+// infinity, so that -inf - m is one).
+constexpr float kLimit = kLift + 1.0f, kNothing = -3.0e38f;
 
 template <int D, int RT>  // RT: groups of 16 rows
 struct SplitCfg {
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, (SplitCfg<D, RT>::kCtas)) attention_
 #pragma unroll
                 for (int n = 0; n < 2 * C::kWords; n++)
                     o[t][n][0] = o[t][n][1] = o[t][n][2] = o[t][n][3] = 0.0f;
-                m[t][0] = m[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.0f;
+                m[t][0] = m[t][1] = kNothing, l[t][0] = l[t][1] = 0.0f;
             }
             if (tid == 0)
                 any_bad = 0;
@@ -326,37 +329,47 @@ __global__ void __launch_bounds__(kThreads, (SplitCfg<D, RT>::kCtas)) attention_
             add_v(stages + (stage == 0 ? C::kStages - 1 : stage - 1) * C::kStage);
         __syncthreads();  // the maxima and plans are there; the tile before and its weights are done with
         issue(stage == 0 ? C::kStages - 1 : stage - 1);
+        float top[RT][2];
+        bool grown = false;
 #pragma unroll
-        for (int t = 0; t < RT; t++) {
-            float u[2], f[2];
+        for (int t = 0; t < RT; t++)
 #pragma unroll
             for (int x = 0; x < 2; x++) {
                 const float4 v = tops[16 * t + 8 * x + g];
-                float top = reference_of<true>(fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
-                top = top > m[t][x] + kSlack ? top : m[t][x];
-                u[x] = top == -INFINITY ? 0.0f : top;  // nothing seen yet
-                f[x] = ex2(m[t][x] - u[x]);
-                m[t][x] = top;
+                top[t][x] = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+                grown |= top[t][x] - m[t][x] > kLimit;
             }
-            float a0 = 0.0f, a1 = 0.0f;
+        if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+            for (int t = 0; t < RT; t++) {
+                float f[2];
+#pragma unroll
+                for (int x = 0; x < 2; x++) {
+                    const float to = top[t][x] - m[t][x] > kLimit ? reference_of<true>(top[t][x]) : m[t][x];
+                    f[x] = ex2(m[t][x] - to);
+                    m[t][x] = to;
+                    l[t][x] *= f[x];
+                }
+#pragma unroll
+                for (int n = 0; n < 2 * C::kWords; n++)
+                    o[t][n][0] *= f[0], o[t][n][1] *= f[0], o[t][n][2] *= f[1], o[t][n][3] *= f[1];
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < RT; t++) {
 #pragma unroll
             for (int n = 0; n < 2; n++) {
                 float(&x)[4] = s[t][n];
-                x[0] = ex2(x[0] - u[0]), x[1] = ex2(x[1] - u[0]);
-                x[2] = ex2(x[2] - u[1]), x[3] = ex2(x[3] - u[1]);
-                a0 = fmaf(x[1], back[n][1], fmaf(x[0], back[n][0], a0));
-                a1 = fmaf(x[3], back[n][1], fmaf(x[2], back[n][0], a1));
+                x[0] = ex2(x[0] - m[t][0]), x[1] = ex2(x[1] - m[t][0]);
+                x[2] = ex2(x[2] - m[t][1]), x[3] = ex2(x[3] - m[t][1]);
+                // this lane's columns; joined at the end
+                l[t][0] = fmaf(x[1], back[n][1], fmaf(x[0], back[n][0], l[t][0]));
+                l[t][1] = fmaf(x[3], back[n][1], fmaf(x[2], back[n][0], l[t][1]));
             }
             asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(weights + ((t * kWarps + warp) * 32 + lane) * 16),
                          "r"(pack2<true>(s[t][0][0], s[t][0][1])), "r"(pack2<true>(s[t][0][2], s[t][0][3])),
                          "r"(pack2<true>(s[t][1][0], s[t][1][1])), "r"(pack2<true>(s[t][1][2], s[t][1][3]))
                          : "memory");
-            l[t][0] = fmaf(l[t][0], f[0], a0), l[t][1] = fmaf(l[t][1], f[1], a1);  // this lane's columns; joined at the end
-            if (__any_sync(0xffffffffu, f[0] != 1.0f || f[1] != 1.0f)) {
-#pragma unroll
-                for (int n = 0; n < 2 * C::kWords; n++)
-                    o[t][n][0] *= f[0], o[t][n][1] *= f[0], o[t][n][2] *= f[1], o[t][n][3] *= f[1];
-            }
         }
         stage = stage + 1 == C::kStages ? 0 : stage + 1;
         first = false;
@@ -482,8 +495,8 @@ cudaError_t attention_split(const AttnParams &p, cudaStream_t stream)
 }
 
 // Which of the two kernels takes 16 WR rows: measured, a warp per 16 rows / split, us
-// (64 requests as above):  D 64, 16 / 32 / 64 rows  117 / 115, 127 / 141, 180 / 178;
-// D 128  132 / 141, 182 / 155, 272 / 268;  D 256  335 / 194, 482 / 393, 787 / 583.
+// (64 requests as above):  D 64, 16 / 32 / 64 rows  117 / 115, 127 / 141, 180 / 166;
+// D 128  132 / 141, 182 / 150, 272 / 255;  D 256  335 / 193, 482 / 368, 787 / 543.
 template <int D, int WR>
 constexpr bool kSplit = D * WR >= 256;
 

@@ -793,6 +793,27 @@ def test_scaled_attention_rising_scores(D, nq, kernel):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq", [1, 5, 12, 20])
+def test_scaled_attention_of_huge_scores_stays_finite(D, nq, kernel):
+    """Scores (base 2) around 2^20 to 2^26 that grow by 4 to 24 a tile: weights stay in fp16's range, equal values come out."""
+    n, c = 900, D ** -0.5 / math.log(2.0)  # what a product of q and k counts in octaves
+    for size in (2.0 ** 20, 1.3 * 2.0 ** 25, -1.1 * 2.0 ** 26):
+        for step in (4, 12, 16, 24):
+            p = ScaledProblem(13, (n,), (nq,), 4, 1, D, 16, k_exp=(0, 1), v_exp=(0, 1))
+            j = torch.arange(n + nq)
+            page, off = p.table[0].long()[j // 16], j % 16
+            rows = torch.zeros((n + nq, 2 * D))
+            rows[:, 0], rows[:, 1], rows[:, D:] = 256.0, (j // 64).float(), 1.0
+            p.cache[page, 0, off] = rows.to(torch.float8_e4m3fn).view(torch.uint8)
+            p.qkv[:] = 0
+            p.qkv[:, :, 0], p.qkv[:, :, 1] = size / 256 / c, step / c
+            p.cuda()
+            out, lse = run_scaled(p, "dense", None)
+            # weights rounded to fp16 (2^-11 each, one way at most) against their own sum, then out to bf16
+            assert bool(torch.isfinite(lse).all()) and bool(((out.float() - 1).abs() <= 2.0 ** -8 + 2.0 ** -10).all())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("nq", [5, 12])
 def test_scaled_attention_nan_codes_and_a_tail_of_more_rows(D, nq, kernel):
     """As above for 20 and 48 rows: NaN codes of drafted tokens, and a thin tail behind a heavy token."""
