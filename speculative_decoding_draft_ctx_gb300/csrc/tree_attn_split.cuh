@@ -18,12 +18,13 @@
 //
 // What it measured: 64 requests of 1,024 to 8,192 tokens, 64 query and 8 KV heads,
 // against a warp per 16 rows: head dim 256 with 8 / 32 / 56 / 128 rows a KV head 193 /
-// 368 / 543 / 1,088 us (335 / 482 / 787 / 1,560), 128 with 32 / 56 150 / 255 (182 /
+// 368 / 543 / 1,088 us (335 / 482 / 787 / 1,560), 128 with 32 / 56 150 / 237 (182 /
 // 272), 64 with 56 166 (180).  What bounds it: some
-// 730 instructions a warp and tile at D 128 at 38% of the issue slots, a third of a
+// 730 instructions a warp and tile at D 128, a third of a
 // warp's time in fixed latencies (products, conversions, shuffles), the barriers
-// behind them; shared memory 55%, the tensor pipe 40%.  A third CTA per SM for 64 rows
-// of 128 (168 registers) spills (311 where two took 268).  With the walk in every
+// behind them; shared memory 62%, issue 47%,
+// the tensor pipe 44%.  At 56 rows of 128 two CTAs per SM take 255 (a third leaves 168
+// registers, 4 of which spill).  With the walk in every
 // thread's registers the sums of D 256 spilled (802 where 583 was taken).
 #pragma once
 
@@ -36,7 +37,7 @@ constexpr int kPlans = 8;  // items planned at once
 // A row's m stays until its maximum has grown by more than an octave, that is, is more
 // than kLimit above m (a difference, which is exact for scores of any size): weights
 // are up to 2^15 then, fp16 goes to 2^16, and in most tiles no sum is rescaled
-// (267 -> 255 us at 64 rows of D 128).  kNothing: m where nothing has been seen (no
+// (267 -> 255 us at 56 rows of D 128).  kNothing: m where nothing has been seen (no
 // infinity, so that -inf - m is one).
 constexpr float kLimit = kLift + 1.0f, kNothing = -3.0e38f;
 
@@ -44,8 +45,8 @@ template <int D, int RT>  // RT: groups of 16 rows
 struct SplitCfg {
     static constexpr int kRows = 16 * RT, kRow = 2 * D, kStage = kTile * kRow;
     static constexpr int kWords = D / 16 / kWarps;  // 16-byte words of V (16 dims each) per warp
-    static constexpr int kCtas = D == 64 ? 3 : D * RT == 256 ? (D == 256 ? 2 : 3) : D == 256 ? 1 : 2;
-    static constexpr int kStages = D == 64 ? 6 : D * RT == 256 ? 3 : 5;
+    static constexpr int kCtas = D <= 128 ? 3 : RT == 1 ? 2 : 1;  // by registers and, at D 256, shared memory
+    static constexpr int kStages = D == 64 ? 6 : D == 128 || RT == 1 ? 3 : 5;
     static constexpr int kQueries = RT * (D / 16) * 512, kWeights = RT * kWarps * 512;  // bytes
     static constexpr int kSmem = kStages * kStage + kQueries + kWeights;
     static constexpr int kNT = D / 8, kGroup = kNT * 128 + 32;  // floats of 16 rows of a part
@@ -496,7 +497,7 @@ cudaError_t attention_split(const AttnParams &p, cudaStream_t stream)
 
 // Which of the two kernels takes 16 WR rows: measured, a warp per 16 rows / split, us
 // (64 requests as above):  D 64, 16 / 32 / 64 rows  117 / 115, 127 / 141, 180 / 166;
-// D 128  132 / 141, 182 / 150, 272 / 255;  D 256  335 / 193, 482 / 368, 787 / 543.
+// D 128  132 / 141, 182 / 150, 272 / 237;  D 256  335 / 193, 482 / 368, 787 / 543.
 template <int D, int WR>
 constexpr bool kSplit = D * WR >= 256;
 
