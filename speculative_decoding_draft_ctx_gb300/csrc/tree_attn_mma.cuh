@@ -53,18 +53,6 @@
 // 2 before its (then exact, but for what lies 2^-24 below the row's largest)
 // conversion to fp16, and the scores by its inverse.
 //
-// Page-scaled fp8 (SCALED).  A page and head has one power of two for K and one
-// for V, 2^ek and 2^ev.  The products take the codes as above; a score is
-// multiplied by its key's 2^ek, and the weight that the second product takes is
-// 2^(s + ev - m), with m of the running maximum of s + ev: the same rounding as
-// above, relative to the largest contribution.  The sum of weights takes 2^-ev of
-// it back, exactly but for fp32's own rounding (|ev| <= 32).  A key's three numbers
-// (2^ek, ev, 2^-ev) are read beside its page's number one tile before they are
-// stored, so that no load is waited for.  This kernel takes up to 16 rows at D 128
-// and 32 at D 64: 64 requests of 1,024 to 8,192 tokens, 64 query and 8 KV heads of 128, take
-// 132 us with a token each (67 us by their bytes), bound by issue at three warps per
-// scheduler.  The others: tree_attn_split.cuh.
-//
 // What a row does not see.  Scores of masked keys are replaced by -inf
 // whatever they are; V rows of drafted tokens that hold infinities or NaN are
 // zeroed in the tile, and the results of the rows that do see them are set
@@ -374,16 +362,15 @@ struct Walk {
 // through the block table.  A warp takes 16
 // rows; its lanes 0..15 (and 16..31 alike) hold the block of their row, which
 // `fetch` has read for the tile that `load` will copy next.
-// SCALE: what is kept of a row's scales (page-scaled): float4 (2^ek, ev, 2^-ev), or
-// uint32_t, the bf16 bits of 2^ek and of 2^-ev.
-template <int ROW, typename SCALE = float4>
+// Page-scaled caches: a row's scales are kept as the bf16 bits of 2^ek and of 2^-ev.
+template <int ROW>
 struct Loader {
     static constexpr int kWords = ROW / 16;
     int64_t phys;
     int off;
     bool live;
     uint32_t exponents;  // page-scaled: of the row that was loaded last, not stored yet, and where they belong
-    SCALE *scales_at = nullptr;
+    uint32_t *scales_at = nullptr;
 
     __device__ __forceinline__ void fetch(const AttnParams &p, int b, int tile, int len)
     {
@@ -405,14 +392,11 @@ struct Loader {
         if (scales_at) {
             const int ek = min(max((int)(int8_t)(exponents & 0xffu), kScaleMin), kScaleMax);
             const int ev = min(max((int)(int8_t)(exponents >> 8), kScaleMin), kScaleMax);
-            if constexpr (sizeof(SCALE) == 16)
-                *scales_at = make_float4(__int_as_float((127 + ek) << 23), (float)ev, __int_as_float((127 - ev) << 23), 0.0f);
-            else
-                *scales_at = (uint32_t)((127 + ek) << 7 | (127 - ev) << 23);
+            *scales_at = (uint32_t)((127 + ek) << 7 | (127 - ev) << 23);
             scales_at = nullptr;
         }
     }
-    __device__ __forceinline__ void fetch_scales(const AttnParams &p, int h, SCALE *stage)
+    __device__ __forceinline__ void fetch_scales(const AttnParams &p, int h, uint32_t *stage)
     {
         if ((threadIdx.x & 31) < 16) {
             scales_at = stage + (threadIdx.x >> 5) * 16 + (threadIdx.x & 15);
@@ -652,35 +636,6 @@ __device__ __forceinline__ void scores(float (&s)[NT][4], const uint32_t (&a)[D 
     }
 }
 
-// The same over codes with the A operands in shared memory, as the lanes hold them.
-template <int D, int NT, int PITCH>
-__device__ __forceinline__ void scores_shared(float (&s)[NT][4], uint32_t queries, uint32_t stage, int key0)
-{
-    const int lane = threadIdx.x & 31;
-#pragma unroll 1
-    for (int u = 0; u < D / 64; u++) {
-        uint32_t a[4][4];
-#pragma unroll
-        for (int k = 0; k < 4; k++)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(a[k][0]), "=r"(a[k][1]), "=r"(a[k][2]), "=r"(a[k][3])
-                         : "r"(queries + ((4 * u + k) * 32 + lane) * 16)
-                         : "memory");
-#pragma unroll
-        for (int i = 0; i < NT; i++) {
-            const int x = key0 + 8 * i + (lane >> 2);
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(stage + x * PITCH + (((4 * u + (lane & 3)) ^ swz(x)) << 4))
-                         : "memory");
-#pragma unroll
-            for (int k = 0; k < 4; k++)
-                mma<true>(s[i], a[k], e4m3_to_half2((uint16_t)w[k]), e4m3_to_half2((uint16_t)(w[k] >> 16)));
-        }
-    }
-}
-
 // Infinities and NaN among the V of a tile's drafted tokens, rows [from, to): zeroed
 // by all threads (and accounted for when the item ends).  Whether this thread met any.
 template <bool FP8, int ROW>
@@ -721,24 +676,20 @@ __device__ __forceinline__ bool zero_nonfinite(unsigned char *stage, int from, i
 
 // ------------------------------------------------------------------ the attention kernel
 
-template <int D, bool FP8, int WR, bool SCALED = false>
+template <int D, bool FP8, int WR>
 struct Cfg {
     static constexpr int kWK = kWarps / WR, kRows = 16 * WR, kKeys = kTile / kWK;  // keys of a tile per warp
     static constexpr int kRow = 2 * D * (FP8 ? 1 : 2);                            // bytes of a token's K|V
     static constexpr int kStage = kTile * kRow;
     // CTAs per SM by registers (about 250 a thread at D 128 and 256, 168 at 64),
     // and as many stages as share the SM's shared memory between them
-    // Page-scaled at D 128: the queries leave the registers, so that a third CTA hides
-    // the latencies, better than the registers did (142 -> 132 us).
-    static constexpr bool kQShared = SCALED && D == 128;
-    static constexpr int kCtas = kQShared || D == 64 ? 3 : D == 128 ? 2 : 1;
-    static constexpr int kStages = kQShared ? 3 : D == 64 ? (FP8 ? 6 : 4) : D == 128 ? (FP8 ? 5 : 2) : (FP8 ? 4 : 2);
+    static constexpr int kCtas = D == 64 ? 3 : D == 128 ? 2 : 1;
+    static constexpr int kStages = D == 64 ? (FP8 ? 6 : 4) : D == 128 ? (FP8 ? 5 : 2) : (FP8 ? 4 : 2);
     static constexpr int kNT = D / 8;                                            // n-tiles of the output
     static constexpr int kJoin = kWK > 1 ? (kWK / 2) * WR * (kNT * 128 + 64) * 4 : 0;  // bytes to join the key warps
-    static constexpr int kQueries = kQShared ? WR * (D / 16) * 512 : 0;  // bytes, in the join's place: an item joins behind its last product
-    static constexpr int kSmem = kStages * kStage + (kJoin > kQueries ? kJoin : kQueries);
+    static constexpr int kSmem = kStages * kStage + kJoin;
     static constexpr int kPart = WR * (kNT * 128 + 32);                          // floats of one part
-    static_assert(kCtas * (kSmem + 1536 + (SCALED ? kStages * kTile * 16 : 0)) <= 227 * 1024, "shared memory");
+    static_assert(kCtas * (kSmem + 1536) <= 227 * 1024, "shared memory");
 };
 
 // What a CTA tells the join about the item it began and did not finish.
@@ -803,12 +754,10 @@ __device__ __noinline__ void add_nonfinite(const AttnParams &p, int b, Request r
     }
 }
 
-template <int D, bool FP8, int WR, bool SCALED>
-__global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) attention_kernel(const __grid_constant__ AttnParams p)
+template <int D, bool FP8, int WR>
+__global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR>::kCtas)) attention_kernel(const __grid_constant__ AttnParams p)
 {
-    using C = Cfg<D, FP8, WR, SCALED>;
-    static_assert(FP8 || !SCALED, "page scales are of codes");
-    __shared__ float4 page_scales[SCALED ? C::kStages : 1][SCALED ? kTile : 1];
+    using C = Cfg<D, FP8, WR>;
     constexpr int NS = C::kKeys / 8;  // n-tiles of a warp's scores
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int64_t scratch[kWarps + 4];
@@ -852,12 +801,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) at
     if (cp.more())
         ld.fetch(p, cp.b, cp_tile, cp.rq.ctx + cp.rq.nq);
     auto issue = [&](int stage) {
-        if constexpr (SCALED)
-            ld.store_scales();
         if (cp.more()) {
             ld.load(p, cp.head(), stages + stage * C::kStage, live[stage], flags);
-            if constexpr (SCALED)
-                ld.fetch_scales(p, cp.head(), page_scales[stage]);
             if (++cp_tile >= cp.t1) {
                 cp.next(p);
                 cp_tile = cp.t0;
@@ -881,16 +826,6 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) at
         uint32_t qa[D / 16][4];
         float rs[2];
         load_q<D, FP8>(p, rq, h, row0 + 16 * wr, qa, rs);
-        const uint32_t queries = stages + C::kStages * C::kStage + wr * (D / 16) * 512;
-        if constexpr (C::kQShared) {
-            // before the barrier of the item's first tile, behind that of the item before
-            if (wk == 0)
-#pragma unroll
-                for (int k = 0; k < D / 16; k++)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(queries + (k * 32 + lane) * 16), "r"(qa[k][0]), "r"(qa[k][1]),
-                                 "r"(qa[k][2]), "r"(qa[k][3])
-                                 : "memory");
-        }
         const float c0 = base_scale * rs[0], c1 = base_scale * rs[1];
         const int r0 = row0 + 16 * wr + g, i0 = r0 / p.group, i1 = (r0 + 8) / p.group;
         float o[C::kNT][4];
@@ -917,26 +852,13 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) at
 #pragma unroll
             for (int n = 0; n < NS; n++)
                 s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
-            if constexpr (C::kQShared)
-                scores_shared<D, NS, C::kRow>(s, queries, st, wk * C::kKeys);
-            else
-                scores<D, FP8, NS, C::kRow>(s, qa, st, wk * C::kKeys);
+            scores<D, FP8, NS, C::kRow>(s, qa, st, wk * C::kKeys);
             const uint32_t lv[4] = {live[stage][0], live[stage][1], live[stage][2], live[stage][3]};
-            [[maybe_unused]] float back[SCALED ? NS : 1][2];  // 2^-ev of this lane's keys
             const bool masked = drafted || (lv[0] & lv[1] & lv[2] & lv[3]) != 0xffffu;
 #pragma unroll
             for (int n = 0; n < NS; n++) {
-                float4 x0 = make_float4(1.0f, 0.0f, 1.0f, 0.0f), x1 = x0;
-                if constexpr (SCALED) {
-                    x0 = page_scales[stage][wk * C::kKeys + 8 * n + 2 * (lane & 3)];
-                    x1 = page_scales[stage][wk * C::kKeys + 8 * n + 2 * (lane & 3) + 1];
-                }
-                s[n][0] = __fmul_rn(s[n][0], c0 * x0.x), s[n][1] = __fmul_rn(s[n][1], c0 * x1.x);  // rounded apart from the
-                s[n][2] = __fmul_rn(s[n][2], c1 * x0.x), s[n][3] = __fmul_rn(s[n][3], c1 * x1.x);  // subtraction of m: exactly 0 at the maximum
-                if constexpr (SCALED) {
-                    s[n][0] += x0.y, s[n][1] += x1.y, s[n][2] += x0.y, s[n][3] += x1.y;
-                    back[n][0] = x0.z, back[n][1] = x1.z;
-                }
+                s[n][0] = __fmul_rn(s[n][0], c0), s[n][1] = __fmul_rn(s[n][1], c0);  // rounded apart from the
+                s[n][2] = __fmul_rn(s[n][2], c1), s[n][3] = __fmul_rn(s[n][3], c1);  // subtraction of m: exactly 0 at the maximum
                 if (masked) {
 #pragma unroll
                     for (int e = 0; e < 2; e++) {
@@ -970,13 +892,8 @@ __global__ void __launch_bounds__(kThreads, (Cfg<D, FP8, WR, SCALED>::kCtas)) at
             for (int n = 0; n < NS; n++) {
                 s[n][0] = ex2(s[n][0] - u0), s[n][1] = ex2(s[n][1] - u0);
                 s[n][2] = ex2(s[n][2] - u1), s[n][3] = ex2(s[n][3] - u1);
-                if constexpr (SCALED) {
-                    a0 = fmaf(s[n][1], back[n][1], fmaf(s[n][0], back[n][0], a0));
-                    a1 = fmaf(s[n][3], back[n][1], fmaf(s[n][2], back[n][0], a1));
-                } else {
-                    a0 += s[n][0] + s[n][1];
-                    a1 += s[n][2] + s[n][3];
-                }
+                a0 += s[n][0] + s[n][1];
+                a1 += s[n][2] + s[n][3];
             }
             l0 = fmaf(l0, f0, a0), l1 = fmaf(l1, f1, a1);  // this lane's columns; joined over the quad at the end
             if (__any_sync(0xffffffffu, f0 != 1.0f || f1 != 1.0f)) {
@@ -1251,7 +1168,7 @@ cudaError_t prepare(K kernel, int smem, int per_sm_most, int &ctas)
 }
 
 // The attention's CTAs for this variant on the current device (cached).
-template <int D, bool FP8, int WR, bool SCALED = false>
+template <int D, bool FP8, int WR>
 cudaError_t attention_ctas(int &ctas)
 {
     static int cached[64];  // written with the same value by whoever comes first
@@ -1263,8 +1180,8 @@ cudaError_t attention_ctas(int &ctas)
         return cudaErrorInvalidDevice;
     int have = __atomic_load_n(&cached[dev], __ATOMIC_ACQUIRE);
     if (have == 0) {
-        using C = Cfg<D, FP8, WR, SCALED>;
-        e = prepare(attention_kernel<D, FP8, WR, SCALED>, C::kSmem, C::kCtas, have);
+        using C = Cfg<D, FP8, WR>;
+        e = prepare(attention_kernel<D, FP8, WR>, C::kSmem, C::kCtas, have);
         if (e != cudaSuccess)
             return e;
         __atomic_store_n(&cached[dev], have, __ATOMIC_RELEASE);
@@ -1281,15 +1198,15 @@ int64_t attention_bytes(cudaError_t &e)
     return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * (int64_t)Cfg<D, FP8, WR>::kPart * 4) : 0;
 }
 
-template <int D, bool FP8, int WR, bool SCALED = false>
+template <int D, bool FP8, int WR>
 cudaError_t attention(const AttnParams &p, cudaStream_t stream)
 {
-    using C = Cfg<D, FP8, WR, SCALED>;
+    using C = Cfg<D, FP8, WR>;
     int ctas = 0;
-    cudaError_t e = attention_ctas<D, FP8, WR, SCALED>(ctas);
+    cudaError_t e = attention_ctas<D, FP8, WR>(ctas);
     if (e != cudaSuccess)
         return e;
-    e = launch_pdl(attention_kernel<D, FP8, WR, SCALED>, ctas, kThreads, C::kSmem, stream, p);
+    e = launch_pdl(attention_kernel<D, FP8, WR>, ctas, kThreads, C::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
     return launch_pdl_grid(join_kernel<D, FP8, WR>, dim3((unsigned)ctas, (unsigned)WR), kThreads, 0, 0, stream, p, ctas);
@@ -1323,6 +1240,8 @@ cudaError_t attention_d(const AttnParams &p, int wr, bool fp8, cudaStream_t stre
     default: return fp8 ? attention<D, true, 4>(p, stream) : attention<D, false, 4>(p, stream);
     }
 }
+
+// one translation unit per head dim
 
 template <int D>
 int64_t workspace_scaled_d(int wr, cudaError_t &e);  // tree_attn_split.cuh

@@ -1,14 +1,21 @@
-// Page-scaled attention for up to 64 query rows at a time: keys split over the
-// warps for the scores, dims for the output (mma.sync, sm_103a).
+// Attention over page-scaled caches for up to 64 query rows at a time: keys split over
+// the warps for the scores, dims for the output (mma.sync, sm_103a).
 //
-// The mathematics, items, shares, tiles and the join are those of
-// tree_attn_mma.cuh.  There each warp has 16 rows and all dims of its own, so all four
-// of a 64-row item turn all of a tile's codes into fp16, and at D 256 the sums of
-// few rows already are 128 registers of a thread.  Here a warp takes 16 of a
-// tile's 64 keys for all rows, and a quarter of the dims of V over all keys:
-// every code is converted once.  The queries lie in shared memory as the lanes
-// take them; so do the weights, written by the warp that has their keys as the
-// operands of one product of depth 16, and read by all.
+// Mathematics.  A page and head has one power of two for K and one for V, 2^ek and
+// 2^ev.  The products take the codes, exact in fp16, as in tree_attn_mma.cuh; a score
+// is multiplied by its key's 2^ek, and the weight that the second product takes is
+// 2^(s + ev - m), with m of the running maximum of s + ev: rounded as there, relative
+// to the largest contribution.  The sum of weights takes 2^-ev of it back, exactly but
+// for fp32's own rounding (|ev| <= 32).  A key's scales are read beside its page's
+// number one tile before they are stored, so that no load is waited for.
+//
+// Split.  Items, shares, tiles and the join are those of tree_attn_mma.cuh.  There each
+// warp has 16 rows and all dims of its own, so all four of a 64-row item turn all of a
+// tile's codes into fp16, and at D 256 the sums of few rows already are 128 registers
+// of a thread.  Here a warp takes 16 of a tile's 64 keys for all rows, and a quarter of
+// the dims of V over all keys: every code is converted once.  The queries lie in
+// shared memory as the lanes take them; so do the weights, written by the warp that has
+// their keys as the operands of one product of depth 16, and read by all.
 //
 // A tile has two barriers.  Behind the first its codes, and the weights of the
 // tile before, are there: its scores are taken, the warps' row maxima written,
@@ -16,16 +23,16 @@
 // all know the common maximum; sums are rescaled, the weights written and the next
 // copies issued into the stage that those products have left.
 //
-// What it measured: 64 requests of 1,024 to 8,192 tokens, 64 query and 8 KV heads,
-// against a warp per 16 rows: head dim 256 with 8 / 32 / 56 / 128 rows a KV head 193 /
-// 368 / 543 / 1,088 us (335 / 482 / 787 / 1,560), 128 with 32 / 56 150 / 237 (182 /
-// 272), 64 with 56 166 (180).  What bounds it: some
-// 730 instructions a warp and tile at D 128, a third of a
-// warp's time in fixed latencies (products, conversions, shuffles), the barriers
-// behind them; shared memory 62%, issue 47%,
-// the tensor pipe 44%.  At 56 rows of 128 two CTAs per SM take 255 (a third leaves 168
-// registers, 4 of which spill).  With the walk in every
-// thread's registers the sums of D 256 spilled (802 where 583 was taken).
+// What it measured: 64 requests of 1,024 to 8,192 tokens, 64 query and 8 KV heads, with
+// 8 / 32 / 56 rows a KV head, us, and with a warp per 16 rows:
+//   D 64   115 / 121 / 166    117 / 127 / 180
+//   D 128  117 / 150 / 236    132 / 182 / 272
+//   D 256  193 / 368 / 541    335 / 482 / 787
+// What bounds it: at 56 rows of D 128 some 830 instructions a warp and tile, a third of
+// a warp's time in fixed latencies (products, conversions, shuffles), the barriers
+// behind them; shared memory 62%, issue 47%, the tensor pipe 44%.  Few rows: the copies
+// in flight (below).  With the walk over the requests in every thread's registers the
+// sums of D 256 spilled (802 where 583 was taken).
 #pragma once
 
 #include "tree_attn_mma.cuh"
@@ -33,7 +40,6 @@
 namespace dspark {
 namespace attn {
 
-constexpr int kPlans = 8;  // items planned at once
 // A row's m stays until its maximum has grown by more than an octave, that is, is more
 // than kLimit above m (a difference, which is exact for scores of any size): weights
 // are up to 2^15 then, fp16 goes to 2^16, and in most tiles no sum is rescaled
@@ -45,12 +51,17 @@ template <int D, int RT>  // RT: groups of 16 rows
 struct SplitCfg {
     static constexpr int kRows = 16 * RT, kRow = 2 * D, kStage = kTile * kRow;
     static constexpr int kWords = D / 16 / kWarps;  // 16-byte words of V (16 dims each) per warp
-    static constexpr int kCtas = D <= 128 ? 3 : RT == 1 ? 2 : 1;  // by registers and, at D 256, shared memory
-    static constexpr int kStages = D == 64 ? 6 : D == 128 || RT == 1 ? 3 : 5;
+    // CTAs per SM by registers and shared memory, stages by what these leave.  Few rows
+    // wait for copies: 8 rows of D 128 take 117 us with 3 CTAs of 4 stages, 141 with 4 of
+    // 3 and 150 with 2 of 6; of D 64 115 with 4 of 5 or 6, 125 with 2 of 10, 148 with 3
+    // of 6; 32 rows of D 64 121 with 3 of 7, 130 with 4 of 5 or 3 of 6, 149 with 2 of 10.
+    static constexpr int kCtas = D == 64 ? (RT == 1 ? 4 : 3) : D == 128 ? 3 : RT == 1 ? 2 : 1;
+    static constexpr int kStages = D == 64 ? (RT == 2 ? 7 : 6) : D == 128 ? (RT == 1 ? 4 : 3) : RT == 1 ? 3 : 5;
+    static constexpr int kPlans = kStages <= 6 ? 8 : 16;  // items planned at once
     static constexpr int kQueries = RT * (D / 16) * 512, kWeights = RT * kWarps * 512;  // bytes
     static constexpr int kSmem = kStages * kStage + kQueries + kWeights;
     static constexpr int kNT = D / 8, kGroup = kNT * 128 + 32;  // floats of 16 rows of a part
-    static_assert(kCtas * (kSmem + 1024 + 640 + 20 * kRows + kStages * (kTile * 4 + 16)) <= 228 * 1024, "shared memory");
+    static_assert(kCtas * (kSmem + 1024 + 288 + 44 * kPlans + 20 * kRows + kStages * (kTile * 4 + 16)) <= 228 * 1024, "shared memory");
 };
 
 // One item of a CTA's share, as thread 0 plans it for all: the walk over the
@@ -98,9 +109,9 @@ __global__ void __launch_bounds__(kThreads, (SplitCfg<D, RT>::kCtas)) attention_
     // ---- thread 0 plans the items
     __shared__ W walk;
     __shared__ int64_t units;
-    __shared__ ItemPlan plan[kPlans];
+    __shared__ ItemPlan plan[C::kPlans];
     auto plan_next = [&](int item) {
-        ItemPlan &to = plan[item & (kPlans - 1)];
+        ItemPlan &to = plan[item & (C::kPlans - 1)];
         to.there = walk.more();
         if (!to.there)
             return;
@@ -110,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, (SplitCfg<D, RT>::kCtas)) attention_
         walk.next(p);
     };
     // copies run kStages - 1 tiles ahead, the block table's entries a tile more, plans an item more
-    static_assert(C::kStages + 2 <= kPlans, "plans in use");
+    static_assert(C::kStages + 2 <= C::kPlans, "plans in use");
     int planned = C::kStages;  // the last item planned
     if (tid == 0) {
         const Shares shares(f.total, ctas);
@@ -121,13 +132,13 @@ __global__ void __launch_bounds__(kThreads, (SplitCfg<D, RT>::kCtas)) attention_
     }
     __syncthreads();
 
-    Loader<C::kRow, uint32_t> ld;
+    Loader<C::kRow> ld;
     // the tile that is copied next: `of` of its item (end: no more)
     struct {
         int item, tile, end, b, h, len;
     } to;
     auto enter = [&](int item) {
-        const ItemPlan &i = plan[item & (kPlans - 1)];
+        const ItemPlan &i = plan[item & (C::kPlans - 1)];
         to.item = item, to.tile = i.t0, to.end = i.there ? i.t1 : -1, to.b = i.b, to.h = i.h, to.len = i.rq.ctx + i.rq.nq;
     };
     enter(0);
@@ -203,8 +214,8 @@ __global__ void __launch_bounds__(kThreads, (SplitCfg<D, RT>::kCtas)) attention_
 
     int stage = 0, item = 0, tile = plan[0].t0, end = plan[0].t1, ctx = plan[0].rq.ctx, len = ctx + plan[0].rq.nq;
     bool first = true;
-    while (plan[item & (kPlans - 1)].there) {
-        const ItemPlan &now = plan[item & (kPlans - 1)];
+    while (plan[item & (C::kPlans - 1)].there) {
+        const ItemPlan &now = plan[item & (C::kPlans - 1)];
         if (first) {
             if (warp < RT) {  // behind the barrier that ends the item before
                 uint32_t qa[D / 16][4];
@@ -449,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, (SplitCfg<D, RT>::kCtas)) attention_
         if (bad && !(begun && done) && tid == 0)
             descs[cta].bad[begun ? 1 : 0] = 1;
         {
-            const ItemPlan &next = plan[++item & (kPlans - 1)];
+            const ItemPlan &next = plan[++item & (C::kPlans - 1)];
             tile = next.t0, end = next.t1, ctx = next.rq.ctx, len = ctx + next.rq.nq;
             first = true;
         }
@@ -495,42 +506,18 @@ cudaError_t attention_split(const AttnParams &p, cudaStream_t stream)
     return launch_pdl_grid(join_kernel<D, true, RT>, dim3((unsigned)ctas, (unsigned)RT), kThreads, 0, 0, stream, p, ctas);
 }
 
-// Which of the two kernels takes 16 WR rows: measured, a warp per 16 rows / split, us
-// (64 requests as above):  D 64, 16 / 32 / 64 rows  117 / 115, 127 / 141, 180 / 166;
-// D 128  132 / 141, 182 / 150, 272 / 237;  D 256  335 / 193, 482 / 368, 787 / 543.
-template <int D, int WR>
-constexpr bool kSplit = D * WR >= 256;
-
-template <int D, int WR>
-cudaError_t scaled_ctas(int &ctas)
-{
-    if constexpr (kSplit<D, WR>)
-        return split_ctas<D, WR>(ctas);
-    else
-        return attention_ctas<D, true, WR, true>(ctas);
-}
-
-template <int D, int WR>
-cudaError_t attention_scaled(const AttnParams &p, cudaStream_t stream)
-{
-    if constexpr (kSplit<D, WR>)
-        return attention_split<D, WR>(p, stream);
-    else
-        return attention<D, true, WR, true>(p, stream);
-}
-
 template <int D>
 int64_t workspace_scaled_d(int wr, cudaError_t &e)
 {
     int ctas = 0;
-    e = wr == 1 ? scaled_ctas<D, 1>(ctas) : wr == 2 ? scaled_ctas<D, 2>(ctas) : scaled_ctas<D, 4>(ctas);
+    e = wr == 1 ? split_ctas<D, 1>(ctas) : wr == 2 ? split_ctas<D, 2>(ctas) : split_ctas<D, 4>(ctas);
     return e == cudaSuccess ? (int64_t)ctas * ((int64_t)sizeof(PartDesc) + 2 * (int64_t)wr * Cfg<D, true, 1>::kPart * 4) : 0;
 }
 
 template <int D>
 cudaError_t attention_scaled_d(const AttnParams &p, int wr, cudaStream_t stream)
 {
-    return wr == 1 ? attention_scaled<D, 1>(p, stream) : wr == 2 ? attention_scaled<D, 2>(p, stream) : attention_scaled<D, 4>(p, stream);
+    return wr == 1 ? attention_split<D, 1>(p, stream) : wr == 2 ? attention_split<D, 2>(p, stream) : attention_split<D, 4>(p, stream);
 }
 
 }  // namespace attn
