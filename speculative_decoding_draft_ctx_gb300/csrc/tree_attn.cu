@@ -43,11 +43,11 @@ constexpr int64_t kTcRows = 32;
 // Page-scaled caches: an item of mma.sync has up to 64 rows, and beyond these reads
 // the cache again, while the tensor-core kernel is bound by its producers, whose
 // time does not depend on the rows.  Measured, mma.sync / tensor cores, us:
-//   rows 56, 64 requests x 8 heads over 4,000   D 128 264 / 324, D 64 185 / 274
-//   rows 72, the same                           D 128 496 / 328, D 64 347 / 272
-//   rows 56, 1 x 8 over 2,000                   D 128 21.7 / 21.4, D 64 20.4 / 19.8
-//   rows 72, the same                           D 128 24.7 / 21.9, D 64 22.7 / 19.8
-//   rows 504, 1 x 4 over 16,000                 D 128 76 / 45, D 64 55 / 38
+//   rows 56, 64 requests x 8 heads over 4,000   D 128 263 / 323, D 64 186 / 274
+//   rows 72, the same                           D 128 495 / 327, D 64 349 / 269
+//   rows 56, 1 x 8 over 2,000                   D 128 19.9 / 21.6, D 64 18.6 / 19.8
+//   rows 72, the same                           D 128 23.5 / 21.9, D 64 19.7 / 19.9
+//   rows 504, 1 x 4 over 16,000                 D 128 76 / 45, D 64 56 / 38
 constexpr int64_t kTcRowsScaled = 64;
 
 enum Pin { kNone, kMma, kTc };

@@ -216,13 +216,14 @@ struct Shares {
 
 // Block-wide search (THREADS threads, scratch of THREADS / 32 + 4 words) of the
 // request that holds this CTA's first unit: `units(b)` is evaluated by one thread.
+// `sharing(total)` CTAs share the units.
 struct Find {
     int64_t total, before;  // all units; those of the requests before `b`
     int b;                  // < 0: the CTA has no share
 };
 
-template <int THREADS, typename F>
-__device__ __forceinline__ Find find_request(int requests, int64_t *scratch, F units)
+template <int THREADS, typename F, typename G>
+__device__ __forceinline__ Find find_request(int requests, int64_t *scratch, F units, G sharing)
 {
     constexpr int W = THREADS / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -257,8 +258,9 @@ __device__ __forceinline__ Find find_request(int requests, int64_t *scratch, F u
     for (int b0 = 0; b0 < requests; b0 += THREADS)
         scan(b0);
     f.total = base;
-    const int64_t target = Shares(base, gridDim.x).start(blockIdx.x);
-    if ((int64_t)blockIdx.x >= base)  // fewer units than CTAs
+    const Shares shares(base, sharing(base));
+    const int64_t target = shares.start(blockIdx.x);
+    if ((int)blockIdx.x >= shares.n)  // no share for this CTA
         return f;
     auto hit = [&](int b0) {
         if (target >= end - mine && target < end) {
@@ -280,6 +282,12 @@ __device__ __forceinline__ Find find_request(int requests, int64_t *scratch, F u
     f.b = (int)scratch[W];
     f.before = scratch[W + 1];
     return f;
+}
+
+template <int THREADS, typename F>
+__device__ __forceinline__ Find find_request(int requests, int64_t *scratch, F units)
+{
+    return find_request<THREADS>(requests, scratch, units, [](int64_t) { return (int)gridDim.x; });
 }
 
 // The flattened sequence of work: for every request, for every item (a row

@@ -47,6 +47,12 @@ namespace attn {
 // infinity, so that -inf - m is one).
 constexpr float kLimit = kLift + 1.0f, kNothing = -3.0e38f;
 
+// Units per CTA at least, where that leaves a CTA per SM: every CTA of a long request
+// leaves a part to join.  One request of 16,000 tokens, 4 KV heads, 8 / 56 rows, us: D 64
+// 56 / 46 with a unit each, 26 / 34 with 4, 24 / 31 with 8; D 128 36 / 46, 26 / 37, 24 / 35;
+// but 4 requests of 3,000, 8 KV heads, 56 rows of D 128 take 29, 29 and 35.
+constexpr int kGrain = 4;
+
 template <int D, int RT>  // RT: groups of 16 rows
 struct SplitCfg {
     static constexpr int kRows = 16 * RT, kRow = 2 * D, kStage = kTile * kRow;
@@ -94,8 +100,9 @@ __global__ void __launch_bounds__(kThreads, (SplitCfg<D, RT>::kCtas)) attention_
     // ---- this CTA's share of the units
     const int ctas = gridDim.x, cta = blockIdx.x;
     using W = Walk<C::kRows, kTile, kItemCost>;
-    const Find f = find_request<kThreads>(p.num_requests, scratch,
-                                          [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); });
+    auto sharing = [&](int64_t total) { return (int)min((int64_t)ctas, max((int64_t)(ctas / C::kCtas), total / kGrain)); };
+    const Find f = find_request<kThreads>(p.num_requests, scratch, [&](int b) { return W::units(p, request(p, b, mask_limit, flags)); },
+                                          sharing);
     PartDesc *descs = reinterpret_cast<PartDesc *>(p.parts);
     float *parts = p.parts + (int64_t)ctas * (sizeof(PartDesc) / 4);
     if (tid == 0)
@@ -117,14 +124,14 @@ __global__ void __launch_bounds__(kThreads, (SplitCfg<D, RT>::kCtas)) attention_
             return;
         to.rq = walk.rq, to.b = walk.b, to.h = walk.head(), to.row0 = walk.row0(), to.t0 = walk.t0, to.t1 = walk.t1;
         to.begun = walk.begun(), to.done = walk.finished();
-        to.last = to.begun && !to.done ? walk.last_cta(Shares(units, gridDim.x)) : 0;
+        to.last = to.begun && !to.done ? walk.last_cta(Shares(units, sharing(units))) : 0;
         walk.next(p);
     };
     // copies run kStages - 1 tiles ahead, the block table's entries a tile more, plans an item more
     static_assert(C::kStages + 2 <= C::kPlans, "plans in use");
     int planned = C::kStages;  // the last item planned
     if (tid == 0) {
-        const Shares shares(f.total, ctas);
+        const Shares shares(f.total, sharing(f.total));
         units = f.total;
         walk.start(p, shares.start(cta), shares.start(cta + 1), f.b, f.before, mask_limit);
         for (int i = 0; i <= planned; i++)
