@@ -146,11 +146,16 @@ __device__ __forceinline__ void add_left(float p, float q, const Share &s, int &
         if (x > y)
             hi += xh - yh, lo += xl - yl;
     } else {
-        // S q as y + rest, rest below half a unit of y; a y above 1 leaves nothing
-        const float z = clean(q), y = z * s.hi, rest = fmaf(z, s.lo, fmaf(z, s.hi, -y));
+        // S q as y + rest; a y above 1 leaves nothing.  rest0 is up to one and a half steps of
+        // y0: with y0 from 1/2 on more than r can count, with y0 of 2^-24 to 2^-23, whose steps
+        // are half units, enough to take a unit from a p that rounds to the same whole one.
+        // Summed once more (exactly: |rest0| < y0), rest is at most half a step of y: r counts
+        // it, it rounds to 0 below 2^-23, and an entry is never below 0.
+        const float z = clean(q), y0 = __fmul_rn(z, s.hi), rest0 = fmaf(z, s.lo, fmaf(z, s.hi, -y0));
+        const float y = __fadd_rn(y0, rest0), rest = __fsub_rn(rest0, __fsub_rn(y, y0));
         split(y, yh, yl);
         const int r = __float_as_int(fmaf(rest, 70368744177664.0f, 12582912.0f)) - kLo;  // rest 2^46 to the nearest integer
-        if (y <= 1.0f && x - y > rest)
+        if (y <= 1.0f && __fsub_rn(x, y) > rest)
             hi += xh - yh, lo += xl - yl - r;
     }
 }

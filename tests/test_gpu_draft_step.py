@@ -935,3 +935,33 @@ def test_a_step_in_a_graph():
         assert all(torch.equal(x, y) for x, y in zip(got, want))
         assert all(torch.equal(a[x], b[x]) for x in a)
     assert int(a["lens"].min()) >= 4
+
+
+# ------------------------------------------------------------------ verification: residuals to the unit, long pieces, shares
+
+
+def test_verify_residuals_to_the_unit():
+    """After two rejections S = 1 + Z lies between two fp32 numbers, so S q has a rest of more than half a step of its
+    fp32 part: what is left of an entry is the whole number of 2^-46 next to p - S q all the same, never below 0."""
+    def one(p, q, u, want):
+        P, Q = torch.zeros((3, 16)), torch.zeros((3, 16))
+        for i, x in p.items():
+            P[0, i] = float.fromhex(x)
+        for i, x in q.items():
+            Q[0, i] = float.fromhex(x)
+        # token 9, which the target never has, is drafted twice and rejected twice
+        got = check_verify(P, Q, torch.tensor([0, 9, 9]), torch.tensor([0, 3], dtype=torch.int32), torch.zeros(3, dtype=torch.int32),
+                           torch.tensor([u, 0.5, 0.5]), 2)
+        assert got[0].tolist() == [[want, -1, -1]]
+
+    # entry 0 keeps 0.021 of 0.92, 5 and 13 the rest: the border between 0 and 5 lies just below these numbers
+    p = {0: "0x1.d7e1cap-1", 5: "0x1.e6502ep-5", 13: "0x1.e2697p-11"}
+    q = {0: "0x1.7f3488p-1", 5: "0x1.eb851ep-6", 9: "0x1.99999ap-3"}
+    for u in ("0x1.dac448p-2", "0x1.dac44ap-2"):
+        one(p, q, float.fromhex(u), 5)
+    # entry 0 keeps less than half a unit: no number draws it
+    p = {0: "0x1.f034b2p-24", 5: "0x1.6p-1", 13: "0x1.000928p-12"}
+    q = {0: "0x1.8ce31ap-24", 5: "0x1.cp-2", 9: "0x1p-1"}
+    for u in (0.125, 0.5, 0.875):
+        one(p, q, u, 5)
+    one(p, q, 1 - 2.0 ** -12, 13)
