@@ -75,8 +75,8 @@ extern "C" {
  * A request without rows gets -1 and 0; one of more than 1024 rows too
  * (DSPARK_FLAG_LENGTH).  A drafted token outside [0, vocab) is rejected, one
  * whose parent is not a row before it is not tested (DSPARK_FLAG_ROW); a last row
- * without any probability gives token -1 (DSPARK_FLAG_ROW).  The outputs must not overlap the
- * inputs.  A row's entries sum to less than 65,536 (they are probabilities).
+ * without any probability gives token -1 (DSPARK_FLAG_ROW).  Outputs that overlap
+ * one another or an input are refused.  A row's entries sum to less than 65,536 (they are probabilities).
  */
 typedef enum { DSPARK_PROB_FP32 = 0, DSPARK_PROB_BF16 = 1 } dspark_prob_dtype;
 

@@ -49,6 +49,21 @@ bool overlap(const void *a, int64_t an, const void *b, int64_t bn)  // of an and
     return x < y + (uint64_t)bn && y < x + (uint64_t)an;
 }
 
+// Whether `bytes` bytes from `out` on share any with `rows` rows of `width` bytes, `stride` bytes apart (either way).
+bool overlap_rows(const void *out, int64_t bytes, const void *at, int64_t rows, int64_t width, int64_t stride)
+{
+    if (bytes < 1 || rows < 1 || width < 1)
+        return false;
+    __int128 x = (__int128)reinterpret_cast<uintptr_t>(at) - (__int128)reinterpret_cast<uintptr_t>(out), s = stride;
+    if (s < 0) {
+        x += (rows - 1) * s;
+        s = -s;
+    }
+    // row r is [x + r s, x + r s + width) there: the first that ends behind 0 begins before `bytes`
+    const __int128 r = x + width > 0 ? 0 : s == 0 ? rows : -(x + width) / s + 1;
+    return r < rows && x + r * s < bytes;
+}
+
 // Rows of the block table that a call changes.
 int check_pool(const int32_t *table, int64_t stride, int64_t blocks, int rows, const int32_t *pages, const int32_t *refs,
                int64_t num_blocks, int block_size)
@@ -101,6 +116,20 @@ int dspark_verify_drafts(const void *target, int target_dtype, int64_t target_st
         !aligned(tokens, 8) || !aligned(out_tokens, 8) || !aligned(parents, 4) || !aligned(uniforms, 4) ||
         !aligned(row_start, 4) || !aligned(out_rows, 4) || !aligned(counts, 4) || !aligned(error_flags, 4))
         return fail(DSPARK_ERR_ALIGNMENT, "buffers must be aligned to their element's size");
+    const int64_t T = num_rows, B = num_requests, t_size = target_dtype == DSPARK_PROB_BF16 ? 2 : 4, d_size = draft_dtype == DSPARK_PROB_BF16 ? 2 : 4;
+    const struct {
+        const void *at;
+        int64_t bytes;
+    } used[] = {{out_tokens, B * (max_accepted + 1) * 8}, {out_rows, B * max_accepted * 4}, {counts, B * 4}, {row_start, (B + 1) * 4},
+                {tokens, T * 8}, {uniforms, T * 4}, {parents, parents ? T * 4 : 0}};
+    for (int i = 0; i < 3; i++) {
+        bool shared = overlap_rows(used[i].at, used[i].bytes, target, T, vocab * t_size, target_stride * t_size) ||
+                      overlap_rows(used[i].at, used[i].bytes, draft, draft ? T : 0, vocab * d_size, draft_stride * d_size);
+        for (int k = i + 1; k < 7; k++)
+            shared |= used[k].bytes > 0 && overlap(used[i].at, used[i].bytes, used[k].at, used[k].bytes);
+        if (shared)
+            return fail(DSPARK_ERR_INVALID_ARG, "out_tokens, out_rows or counts overlap one another or an input");
+    }
     VerifyParams p{};
     p.target = target;
     p.draft = draft;

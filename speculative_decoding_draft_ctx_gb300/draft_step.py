@@ -102,8 +102,8 @@ def verify_drafts(target_probs, draft_tokens, row_start, uniforms, max_accepted,
     ``tokens``: int64 ``[B, max_accepted + 1]``, the accepted tokens, the last
     one, then -1; ``rows``: int32 ``[B, max_accepted]``, the accepted tokens' rows
     (what ``compact_kv`` takes), then -1; ``counts``: int32 ``[B]``, how many
-    stand.  Made by the call if not given; they must not overlap the inputs.  A request has up to 1024 rows; one
-    without rows gets -1 and 0.  FLAG_ROW: a token outside the vocabulary
+    stand.  Made by the call if not given; refused where they overlap one another or
+    an input.  A request has up to 1024 rows; one without rows gets -1 and 0.  FLAG_ROW: a token outside the vocabulary
     (rejected), a parent that is not a row before it (never tested), or a last row
     without any probability (token -1).
     """

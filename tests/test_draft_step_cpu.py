@@ -49,6 +49,21 @@ def test_verify_status(L, over, want):
     assert status(L, "dspark_verify_drafts", VERIFY, VERIFY_BASE, over) == want
 
 
+VERIFY_APART = dict(VERIFY_BASE, t=FAKE, d=FAKE + 8192, tok=FAKE + 16384, up=FAKE + 16640, u=FAKE + 16896, start=FAKE + 17152, ot=FAKE + 17408,
+                    orow=FAKE + 17664, oc=FAKE + 17920)
+
+
+@pytest.mark.parametrize("over", [
+    dict(ot=FAKE + 3192), dict(ot=FAKE + 8192 + 1592), dict(oc=FAKE + 8192 - 4), dict(ot=FAKE + 16384 - 72), dict(ot=FAKE + 16384 + 56),
+    dict(orow=FAKE + 16640), dict(oc=FAKE + 16640 + 28), dict(orow=FAKE + 16896 + 28), dict(oc=FAKE + 17152 + 8), dict(ot=FAKE + 17152),
+    dict(orow=FAKE + 17408 + 76), dict(oc=FAKE + 17408 + 76), dict(oc=FAKE + 17664 + 28), dict(d=0, t=FAKE + 4096, ts=-100, ot=FAKE + 4096 - 2872),
+    dict(ts=0, oc=FAKE + 396), dict(ts=1024, oc=FAKE + 4096 + 396), dict(ts=1 << 40, oc=FAKE + (7 << 42)), dict(ds=-(1 << 40), d=8 << 41, oc=1 << 41)])
+def test_verify_refuses_outputs_over_inputs_or_one_another(L, over):
+    """The first or last bytes of a buffer or row."""
+    assert status(L, "dspark_verify_drafts", VERIFY, VERIFY_APART, over) == BAD
+    assert b"overlap" in L.dspark_ctx_kv_last_error()
+
+
 COMPACT = "caches scales L blocks nkv bs D dt table stride cols ctx B rows rstride width counts first lens flags stream"
 COMPACT_BASE = dict(caches=layers(FAKE, FAKE + 4096), scales=None, L=2, blocks=4, nkv=2, bs=16, D=128, dt=0, table=FAKE, stride=4, cols=4, ctx=FAKE, B=3,
                     rows=FAKE + 256, rstride=4, width=4, counts=FAKE + 512, first=1, lens=FAKE + 1024, flags=0, stream=0)

@@ -965,3 +965,19 @@ def test_verify_residuals_to_the_unit():
     for u in (0.125, 0.5, 0.875):
         one(p, q, u, 5)
     one(p, q, 1 - 2.0 ** -12, 13)
+
+
+def test_verify_outputs_between_rows_and_over_inputs():
+    """Outputs may lie in the gaps between rows of probabilities; over an input they are refused."""
+    g = gen(21)
+    t, d, tok, start, _, u = draws(100, [3, 2], g)
+    wide = torch.full((t.shape[0], 120), float("nan"), device="cuda")
+    wide[:, :100] = t.cuda()
+    flat, base = wide.view(torch.int32).flatten(), (wide[:, :100], tok.cuda(), start.cuda(), u.cuda(), 3, d.cuda())
+    counts, rows = flat[2 * 120 + 100:2 * 120 + 102], flat[3 * 120 + 114:4 * 120].view(2, 3)
+    got = dk.verify_drafts(*base, counts=counts, rows=rows)
+    assert all(torch.equal(x.cpu(), y) for x, y in zip(got, verify(t, d, tok, start, None, u, 3, True))) and got[2] is counts
+    for over in (dict(counts=flat[2 * 120 + 99:2 * 120 + 101]), dict(rows=flat[3 * 120 + 115:4 * 120 + 1].view(2, 3)), dict(counts=base[2][1:]),
+                 dict(counts=base[3].view(torch.int32)[:2]), dict(rows=rows, counts=rows[1, 1:])):
+        with pytest.raises(dk.DSparkError, match="overlap"):
+            dk.verify_drafts(*base, **over)
