@@ -981,3 +981,22 @@ def test_verify_outputs_between_rows_and_over_inputs():
                  dict(counts=base[3].view(torch.int32)[:2]), dict(rows=rows, counts=rows[1, 1:])):
         with pytest.raises(dk.DSparkError, match="overlap"):
             dk.verify_drafts(*base, **over)
+
+
+@pytest.mark.parametrize("replacement", [True, False])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,V,n", [(20, 131073, 5), (200, 9001, 5), (24, 70000, 7)])
+def test_verify_trees_of_long_pieces(B, V, n, dtype, replacement):
+    """More entries per warp than are kept in shared memory: every round reads its rows again."""
+    g = gen(B + n)
+    t, d, tok, start, up, u = draws(V, [n] * B, g, arity=4, distinct=not replacement, target_dtype=dtype, draft_dtype=dtype)
+    u = 1 - (1 - u) * 0.4  # more rejections
+    u[start[:-1].long()] = torch.rand(B, generator=g)
+    got = check_verify(t, d, tok, start, up, u, 3, replacement)
+    # requests whose last row has rejected two children and more: S is neither 0 nor 1 there
+    lost = 0
+    for b in range(B):
+        k = int(got[2][b])
+        at = int(got[1][b, k - 1]) if k else 0
+        lost += k < 3 and int((up[start[b] + 1:start[b + 1]] == at).sum()) >= 2
+    assert lost >= B // 4
