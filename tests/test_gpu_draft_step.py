@@ -1000,3 +1000,33 @@ def test_verify_trees_of_long_pieces(B, V, n, dtype, replacement):
         at = int(got[1][b, k - 1]) if k else 0
         lost += k < 3 and int((up[start[b] + 1:start[b + 1]] == at).sum()) >= 2
     assert lost >= B // 4
+
+
+SHARES = [  # p, q, their denominator, the fewest equal steps of u_0, u_1 and u_2 with all borders of tests and draws on a step
+    ("replacement", (5, 2, 4, 5), (4, 8, 1, 3), 16, (4, 4, 3)), ("replacement", (3, 10, 1, 2), (2, 1, 12, 1), 16, (138, 12, 11)),
+    ("distinct", (3, 2, 4, 3), (2, 8, 1, 1), 12, (4, 4, 3)), ("distinct", (10, 3, 1, 2), (2, 11, 2, 1), 16, (99, 22, 9)),
+    ("taken", (3, 3, 3, 1), None, 10, (84, 10, 21)), ("taken", (1, 1, 1, 1), None, 4, (6, 4, 3))]
+
+
+@pytest.mark.parametrize("kind,p,q,n,steps", SHARES)
+def test_verify_shares_are_the_target_s(kind, p, q, n, steps):
+    """Two children of one row: over the middles of all steps the first token comes exactly as often as the target has it, summed
+    over the drafts by how often these are drawn; for drafts taken without drawing, whatever they are."""
+    V = len(p)
+    u = torch.cartesian_prod(*[(torch.arange(k) + 0.5) / k for k in steps])
+    B, total = u.shape[0], torch.zeros(V, dtype=torch.float64)
+    P = (torch.tensor(p) / n).expand(3 * B, V).contiguous().cuda()
+    Q = None if q is None else (torch.tensor(q) / n).expand(3 * B, V).contiguous().cuda()
+    up, start = torch.zeros(3 * B, dtype=torch.int32, device="cuda"), torch.arange(0, 3 * B + 1, 3, dtype=torch.int32, device="cuda")
+    for x in range(V):
+        for y in range(V):
+            if kind == "distinct" and x == y:
+                continue
+            tok = torch.tensor([0, x, y]).repeat(B).cuda()
+            tokens, _, _ = dk.verify_drafts(P, tok, start, u.flatten().cuda(), 1, Q, up, replacement=kind != "distinct")
+            share = torch.bincount(tokens[:, 0].cpu(), minlength=V).double() / B
+            if kind == "taken":
+                assert (share - torch.tensor(p).double() / n).abs().max() < 1e-12, (x, y, share)
+            else:
+                total += share * q[x] / n * (q[y] / n if kind == "replacement" else q[y] / (n - q[x]))
+    assert kind == "taken" or (total - torch.tensor(p).double() / n).abs().max() < 1e-12, total
