@@ -1030,3 +1030,18 @@ def test_verify_shares_are_the_target_s(kind, p, q, n, steps):
             else:
                 total += share * q[x] / n * (q[y] / n if kind == "replacement" else q[y] / (n - q[x]))
     assert kind == "taken" or (total - torch.tensor(p).double() / n).abs().max() < 1e-12, total
+
+
+# ------------------------------------------------------------------ compaction and the pool at more than one turn of the threads
+
+
+@pytest.mark.parametrize("bs,D,H", [(16, 256, 9), (3, 128, 33), (16, 64, 40)])
+def test_compact_scaled_columns_in_turns(bs, D, H):
+    """More 16-byte columns than a CTA has threads, of page-scaled caches: each turn has exponents of its own."""
+    assert H * D // 8 > 256
+    check_compact("scaled", [0, 5, 9, 14, 15, 16, 200], PATHS, H, D, bs)
+
+
+def test_compact_scaled_columns_in_turns_of_a_long_path():
+    """The same with more moves into one page than are looked up at once."""
+    check_compact("scaled", [3, 70], [list(range(2, 1202, 2)), list(range(300, 900))], 17, 128, 400, layers=1)
