@@ -1045,3 +1045,28 @@ def test_compact_scaled_columns_in_turns(bs, D, H):
 def test_compact_scaled_columns_in_turns_of_a_long_path():
     """The same with more moves into one page than are looked up at once."""
     check_compact("scaled", [3, 70], [list(range(2, 1202, 2)), list(range(300, 900))], 17, 128, 400, layers=1)
+
+
+@pytest.mark.parametrize("pages,n,free", [(8193, 1025, 8193), (70001, 4096, 70001), (8193, 4096, 2000), (70001, 4096, 1200), (5000, 1500, 800)])
+def test_pool_fork_over_several_ctas(pages, n, free):
+    """Pools of one, two and eight CTAs, more pairs than a CTA has threads, some of them in need of a page; pages that run
+    out behind pair 1,024."""
+    src = 5
+    live = Live(n + src, 40, pages, 2, layers=1, H=1)
+    lens = [79, 1, 16, 33, 0]
+    live.resize([2 * 40, 2, 16, 40, 3] + [0] * n)
+    live.check()
+    if free < pages:  # the others are held by somebody else
+        r = random.Random(n)
+        left = [p for p, x in enumerate(live.ref.refs) if x == 0]
+        for p in r.sample(left, len(left) - free):
+            live.ref.refs[p] = 1
+        live.refs.copy_(ints(live.ref.refs))
+    live.set_lens(lens + [0] * n)
+    order = list(range(src, n + src))
+    random.Random(pages).shuffle(order)
+    live.fork([((i * 7 + i // 5) % src, d) for i, d in enumerate(order)])
+    need = sum(lens[(i * 7 + i // 5) % src] % 2 for i in range(n))
+    assert need > 512 and (free >= need or free > 1024 * need // n)
+    live.check(0 if free >= need else dk.FLAG_PAGES)
+    assert sum(live.ref.pages[d] > 0 for d in order) > 0
