@@ -43,9 +43,10 @@ namespace attn {
 // A row's m stays until its maximum has grown by more than an octave, that is, is more
 // than kLimit above m (a difference, which is exact for scores of any size): weights
 // are up to 2^15 then, fp16 goes to 2^16, and in most tiles no sum is rescaled
-// (267 -> 255 us at 56 rows of D 128).  kNothing: m where nothing has been seen (no
-// infinity, so that -inf - m is one).
-constexpr float kLimit = kLift + 1.0f, kNothing = -3.0e38f;
+// (267 -> 255 us at 56 rows of D 128).  kNothing: m where nothing has been seen, the
+// lowest number (no infinity, so that -inf - m is one; no score lies below it, and one
+// that equals it weighs 1).
+constexpr float kLimit = kLift + 1.0f, kNothing = -3.402823466e38f;
 
 // Units per CTA at least, where that leaves a CTA per SM: every CTA of a long request
 // leaves a part to join.  One request of 16,000 tokens, 4 KV heads, 8 / 56 rows, us: D 64

@@ -1070,3 +1070,26 @@ def test_pool_fork_over_several_ctas(pages, n, free):
     assert need > 512 and (free >= need or free > 1024 * need // n)
     live.check(0 if free >= need else dk.FLAG_PAGES)
     assert sum(live.ref.pages[d] > 0 for d in order) > 0
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("nq", [1, 5, 12, 20])
+def test_scaled_attention_of_the_lowest_scores(D, nq, kernel):
+    """Every score (base 2) within a few percent of fp32's lowest number, all alike: the mean of the values comes out."""
+    n, c = 200, D ** -0.5 / math.log(2.0)  # what a product of q and k counts in octaves
+    p = ScaledProblem(14, (n,), (nq,), 4, 1, D, 16, k_exp=(0, 1), v_exp=(0, 1))
+    j = torch.arange(n + nq)
+    page, off = p.table[0].long()[j // 16], j % 16
+    rows = torch.zeros((n + nq, 2 * D))
+    rows[:, 0] = 256.0
+    rows[:, D:] = (j % 8)[:, None].float()
+    p.cache[page, 0, off] = rows.to(torch.float8_e4m3fn).view(torch.uint8)
+    p.qkv[:] = 0
+    p.qkv[:, :, 0] = -3.2e38 / 256 / c
+    assert 3.1e38 < abs(float(p.qkv[0, 0, 0])) * 256 * c < 3.3e38
+    p.cuda()
+    out, lse = run_scaled(p, "dense", None)
+    # weights are alike (1 each) and the values whole: their sums are exact, the quotient rounded in fp32 and to bf16
+    mean = float((j % 8).double().mean())
+    assert bool(((out.double() - mean).abs() <= (2.0 ** -8 + 2.0 ** -21) * mean).all())
+    assert bool(((lse / (float(p.qkv[0, 0, 0]) * 256 * D ** -0.5) - 1).abs() <= 2.0 ** -20).all())
