@@ -1093,3 +1093,98 @@ def test_scaled_attention_of_the_lowest_scores(D, nq, kernel):
     mean = float((j % 8).double().mean())
     assert bool(((out.double() - mean).abs() <= (2.0 ** -8 + 2.0 ** -21) * mean).all())
     assert bool(((lse / (float(p.qkv[0, 0, 0]) * 256 * D ** -0.5) - 1).abs() <= 2.0 ** -20).all())
+
+
+# ------------------------------------------------------------------ far offsets, calls side by side
+
+
+def test_scaled_cache_beyond_32_bits(kernel):
+    """Insert, attention, compaction and fork in pages beyond 2^32 bytes of a cache do what they do in a small one."""
+    g = gen(31)
+    D, bs, H, nq = 128, 16, 8, 20
+    small = ScaledProblem(15, (100, 30, 45), (nq, 3, 0), 2 * H, H, D, bs).cuda()
+    pages = (1 << 32) // (H * bs * 2 * D) * 9 // 8
+    shift = pages - small.blocks
+    big, scales = torch.empty((pages, H, bs, 2 * D), dtype=torch.uint8, device="cuda"), torch.zeros((pages, H, 2), dtype=torch.int8, device="cuda")
+    big[shift:], scales[shift:] = small.d_cache, small.d_scales
+    near, far = (small.d_cache, small.d_scales, small.d_table), (big, scales, torch.where(small.d_table >= 0, small.d_table + shift, -1).to(torch.int32))
+    assert int(far[2][0].max()) * H * bs * 2 * D > 1 << 32
+    kv, f = torch.randn((nq + 3, 2, H, D), generator=g).bfloat16().cuda(), flag()
+    rows, counts = ints([[2, 5, 9, 17], [2, -1, -1, -1], [-1] * 4]), ints([4, 1, 0])
+    got = []
+    for cache, sc, table in (near, far):
+        dk.insert_kv_scaled(kv[:, 0], kv[:, 1], cache, sc, table, small.d_start, small.d_ctx, error_flags=f)
+        out = dk.tree_attention(small.d_q, cache, table, small.d_start, small.d_ctx, causal=True, block_scales=sc, error_flags=f)
+        lens = dk.compact_kv(cache, table, small.d_ctx, rows, counts, block_scales=sc, error_flags=f)
+        got.append((*out, lens, cache[-small.blocks:], sc[-small.blocks:]))
+    assert int(f) == 0 and all(torch.equal(a, b) for a, b in zip(*got))
+    # request 0 continued as a fourth: the one free page, beyond 2^32 bytes, takes its last tokens
+    free = max(set(range(shift, pages)) - set(far[2].flatten().tolist()))
+    assert free * H * bs * 2 * D > 1 << 32
+    table, refs = torch.full((4, far[2].shape[1]), -1, dtype=torch.int32, device="cuda"), torch.ones(pages, dtype=torch.int32, device="cuda")
+    table[:3], refs[free] = far[2], 0
+    lens = torch.cat([lens, ints([0])])
+    full, tail = divmod(int(lens[0]), bs)
+    old = int(table[0, full])
+    dk.fork_kv(big, table, -(-lens // bs), lens, ints([0]), ints([3]), refs, block_scales=scales, error_flags=f)
+    assert tail and int(table[3, full]) == free and int(refs[free]) == 1 and int(lens[3]) == int(lens[0]) and int(f) == 0
+    assert torch.equal(big[free, :, :tail], big[old, :, :tail]) and torch.equal(scales[free], scales[old])
+
+
+def test_verify_rows_beyond_32_bits():
+    """Requests whose rows of probabilities lie beyond 2^32 bytes."""
+    g = gen(32)
+    t, d, tok, start, up, u = draws(131072, [3, 4, 2], g, arity=2)
+    T, far = t.shape[0], 9000
+    wide = [torch.empty((far + T, 131072), device="cuda") for _ in range(2)]
+    tokens, parents, numbers = torch.zeros(far + T, dtype=torch.int64), torch.zeros(far + T, dtype=torch.int32), torch.zeros(far + T)
+    for x, y in zip((*wide, tokens, parents, numbers), (t, d, tok, up, u)):
+        x[far:] = y
+    assert far * 131072 * 4 > 1 << 32
+    got = dk.verify_drafts(wide[0], tokens.cuda(), (start + far).cuda(), numbers.cuda(), 4, wide[1], parents.cuda())
+    assert all(torch.equal(x.cpu(), y) for x, y in zip(got, verify(t, d, tok, start, up, u, 4, True)))
+
+
+def test_calls_side_by_side_on_two_streams():
+    """Each operator in two graphs replayed at once on different streams, between calls on a third: no call shares anything with another."""
+    g = gen(33)
+    p = ScaledProblem(16, (900, 33, 400), (7, 20, 3), 16, 2, 128, 16).cuda()
+    t, d, tok, start, up, u = [x.cuda() for x in draws(5000, [9, 20, 5], g, arity=3)]
+    kv = torch.randn((30, 2, 2, 128), generator=g).bfloat16().cuda()
+
+    def state():
+        return dict(cache=p.d_cache.clone(), scales=p.d_scales.clone(), table=torch.full((6, 70), -1, dtype=torch.int32, device="cuda"),
+                    pages=ints([0] * 6), refs=ints([0] * p.blocks), lens=ints([40, 7, 0, 0, 0, 0]))
+
+    def work(s):
+        a = dk.tree_attention(p.d_q, s["cache"], p.d_table, p.d_start, p.d_ctx, causal=True, block_scales=s["scales"])
+        b = dk.verify_drafts(t, tok, start, u, 8, d, up)
+        dk.resize_kv(s["table"], s["pages"], s["lens"], s["refs"], 16)
+        dk.fork_kv([s["cache"]], s["table"], s["pages"], s["lens"], ints_src, ints_dst, s["refs"], block_scales=[s["scales"]])
+        dk.insert_kv_scaled(kv[:, 0], kv[:, 1], s["cache"], s["scales"], p.d_table, p.d_start, p.d_ctx)
+        return *a, *b
+
+    ints_src, ints_dst = ints([0, 1, 0, 1]), ints([2, 3, 4, 5])
+    first = state()
+    want = work(first)
+    torch.cuda.synchronize()
+    streams, states, graphs, outs = [torch.cuda.Stream() for _ in range(3)], [state() for _ in range(2)], [], []
+    for s in states:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(work(s))
+        graphs.append(graph)
+    for turn in range(3):
+        fresh = state()
+        for s in states:
+            for k, x in state().items():
+                s[k].copy_(x)
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        with torch.cuda.stream(streams[2]):
+            third = work(fresh)
+        torch.cuda.synchronize()
+        for out, s in zip((*outs, third), (*states, fresh)):
+            assert all(torch.equal(a, b) for a, b in zip(out, want)) and all(torch.equal(s[k], first[k]) for k in first)
