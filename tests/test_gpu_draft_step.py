@@ -1188,3 +1188,17 @@ def test_calls_side_by_side_on_two_streams():
         torch.cuda.synchronize()
         for out, s in zip((*outs, third), (*states, fresh)):
             assert all(torch.equal(a, b) for a, b in zip(out, want)) and all(torch.equal(s[k], first[k]) for k in first)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30, 1.5])
+def test_scaled_attention_takes_any_scale(D, scale, kernel):
+    """Scales of none, of either sign, so small that products underflow, and large, over exponents far apart and near."""
+    for nq, k_exp in ((3, (-6, -3)), (20, (-32, 3))):
+        p = ScaledProblem(17 + nq, (150, 0, 70), (nq, 2, nq), 8, 2, D, 16, k_exp=k_exp)
+        p.cuda()
+        out, lse = run_scaled(p, "causal", None, scale=scale)
+        want, z, to, tl = attention(p, "causal", None, scale=scale)
+        close(lse, z, tl)
+        close(out, want, to)
+        assert int(p.d_flags) == 0
