@@ -55,6 +55,19 @@ cudaError_t launch_pdl(void (*kernel)(Params...), int blocks, int threads, size_
     return launch_pdl_grid(kernel, dim3((unsigned)blocks), threads, smem, 0, stream, std::forward<Args>(args)...);
 }
 
+// Launches `kernel` once the stream's earlier work is done, its dependents early all
+// the same: for a grid of long-running CTAs that needs every slot of the GPU.
+template <typename... Params, typename... Args>
+cudaError_t launch_whole(void (*kernel)(Params...), int blocks, int threads, size_t smem, cudaStream_t stream, Args &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // The kernel side of launch_pdl, before any global load or store (L2
 // prefetch hints may precede it: they hand no data to the program): wait for
 // the stream's previous kernel to finish and its writes to be visible, then

@@ -505,10 +505,16 @@ cudaError_t split_ctas(int &ctas)
 template <int D, int RT>
 cudaError_t attention_split(const AttnParams &p, cudaStream_t stream)
 {
+    using C = SplitCfg<D, RT>;
     int ctas = 0;
     cudaError_t e = split_ctas<D, RT>(ctas);
+    // Four CTAs that take every register of an SM are not launched early: placed between those
+    // that the kernel before still has there, some find no slot (of 608 eight began when others
+    // had ended).  64 requests, us, early / not: D 64, 8 rows 118 / 84 (94 / 85 behind an insert).
+    // With fewer CTAs early is as good or better: 56 rows of D 128 235 / 238.
     if (e == cudaSuccess)
-        e = launch_pdl(attention_split_kernel<D, RT>, ctas, kThreads, SplitCfg<D, RT>::kSmem, stream, p);
+        e = C::kCtas == 4 ? launch_whole(attention_split_kernel<D, RT>, ctas, kThreads, C::kSmem, stream, p)
+                          : launch_pdl(attention_split_kernel<D, RT>, ctas, kThreads, C::kSmem, stream, p);
     if (e != cudaSuccess)
         return e;
     return launch_pdl_grid(join_kernel<D, true, RT>, dim3((unsigned)ctas, (unsigned)RT), kThreads, 0, 0, stream, p, ctas);

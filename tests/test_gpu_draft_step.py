@@ -1202,3 +1202,43 @@ def test_scaled_attention_takes_any_scale(D, scale, kernel):
         close(lse, z, tl)
         close(out, want, to)
         assert int(p.d_flags) == 0
+
+
+@pytest.mark.parametrize("D,nq", [(64, 1), (64, 4), (128, 1)])
+def test_scaled_attention_calls_behind_one_another_lose_nothing(D, nq, monkeypatch):
+    """Grids that fill the GPU, one call behind another: as fast, to a fifth, as launched without any overlap (a tenth of the CTAs that
+    had to wait for a slot would cost a half), and the same bits."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    B, H, bs = 64, 8, 16
+    ctx = [1024 + 7168 * i // (B - 1) for i in range(B)]
+    need = [-(-(c + nq) // bs) for c in ctx]
+    table, order, at = torch.zeros((B, max(need)), dtype=torch.int32, device="cuda"), torch.randperm(sum(need), generator=g, device="cuda").int(), 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    cache = torch.randint(0, 0x70, (at, H, bs, 2 * D), generator=g, device="cuda", dtype=torch.uint8)
+    scales = torch.randint(-9, -6, (at, H, 2), generator=g, device="cuda").to(torch.int8)
+    q = torch.randn((B * nq, 8 * H, D), generator=g, device="cuda").bfloat16()
+    start, lens = torch.arange(0, B * nq + 1, nq, dtype=torch.int32, device="cuda"), ints(ctx)
+    graphs, outs = [], []
+    for early in ("1", "0"):
+        monkeypatch.setenv("DSPARK_PDL", early)
+        dk.tree_attention(q, cache, table, start, lens, causal=True, block_scales=scales)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(8):
+                out = dk.tree_attention(q, cache, table, start, lens, causal=True, block_scales=scales)
+        graphs.append(graph)
+        outs.append(out)
+    times = [[], []]
+    for _ in range(12):
+        for graph, t in zip(graphs, times):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            graph.replay()
+            b.record()
+            torch.cuda.synchronize()
+            t.append(a.elapsed_time(b))
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+    assert min(times[0]) < 1.2 * min(times[1]), (min(times[0]), min(times[1]))
