@@ -25,14 +25,19 @@
 //
 // What it measured: 64 requests of 1,024 to 8,192 tokens, 64 query and 8 KV heads, with
 // 8 / 32 / 56 rows a KV head, us, and with a warp per 16 rows:
-//   D 64   115 / 121 / 166    117 / 127 / 180
-//   D 128  117 / 150 / 236    132 / 182 / 272
-//   D 256  193 / 368 / 541    335 / 482 / 787
+//   D 64    83 / 107 / 168     92 / 122 / 181
+//   D 128  107 / 151 / 235    132 / 182 / 272
+//   D 256  193 / 367 / 543    335 / 482 / 787
 // What bounds it: at 56 rows of D 128 some 830 instructions a warp and tile, a third of
 // a warp's time in fixed latencies (products, conversions, shuffles), the barriers
-// behind them; shared memory 62%, issue 47%, the tensor pipe 44%.  Few rows: the copies
-// in flight (below).  With the walk over the requests in every thread's registers the
-// sums of D 256 spilled (802 where 583 was taken).
+// behind them; shared memory 62%, issue 47%, the tensor pipe 44%.  Few rows are bound by
+// the path through a tile, not by bytes: at 8 rows a scheduler's 3.8 warps issue 55% of
+// the time, an instruction takes a warp 7 cycles (1.7 fixed latencies, 0.9 barriers, 0.9
+// shared memory, 0.7 loads), DRAM is at 36% (D 64) and 56% (D 128).  In a copy with clocks
+// read between its steps (D 64 and D 128 alike) the copies had landed but for 50 of some
+// 3,000 cycles a tile; issuing the next ones, 16 bytes of a key each, took 1,150, the scores 700.
+// With the walk over the requests in every thread's registers the sums of D 256 spilled
+// (802 where 583 was taken).
 #pragma once
 
 #include "tree_attn_mma.cuh"
@@ -49,22 +54,23 @@ namespace attn {
 constexpr float kLimit = kLift + 1.0f, kNothing = -3.402823466e38f;
 
 // Units per CTA at least, where that leaves a CTA per SM: every CTA of a long request
-// leaves a part to join.  One request of 16,000 tokens, 4 KV heads, 8 / 56 rows, us: D 64
-// 56 / 46 with a unit each, 26 / 34 with 4, 24 / 31 with 8; D 128 36 / 46, 26 / 37, 24 / 35;
-// but 4 requests of 3,000, 8 KV heads, 56 rows of D 128 take 29, 29 and 35.
+// leaves a part to join.  One request of 16,000 tokens, 4 KV heads, us: 8 / 56 rows of D 64
+// 57 / 46 with a unit each, 26 / 33 with 4, 24 / 30 with 8; 56 rows of D 128 46, 36, 35;
+// but 4 requests of 3,000, 8 KV heads, 56 rows of D 128 take 30, 30 and 33, of D 64 23, 23, 26.
 constexpr int kGrain = 4;
 
 template <int D, int RT>  // RT: groups of 16 rows
 struct SplitCfg {
     static constexpr int kRows = 16 * RT, kRow = 2 * D, kStage = kTile * kRow;
     static constexpr int kWords = D / 16 / kWarps;  // 16-byte words of V (16 dims each) per warp
-    // CTAs per SM by registers and shared memory, stages by what these leave.  Few rows
-    // wait for copies: 8 rows of D 128 take 117 us with 3 CTAs of 4 stages, 141 with 4 of
-    // 3 and 150 with 2 of 6; of D 64 115 with 4 of 5 or 6, 125 with 2 of 10, 148 with 3
-    // of 6; 32 rows of D 64 121 with 3 of 7, 130 with 4 of 5 or 3 of 6, 149 with 2 of 10.
-    static constexpr int kCtas = D == 64 ? (RT == 1 ? 4 : 3) : D == 128 ? 3 : RT == 1 ? 2 : 1;
-    static constexpr int kStages = D == 64 ? (RT == 2 ? 7 : 6) : D == 128 ? (RT == 1 ? 4 : 3) : RT == 1 ? 3 : 5;
-    static constexpr int kPlans = kStages <= 6 ? 8 : 16;  // items planned at once
+    // CTAs per SM by registers and shared memory, stages by what these leave: more warps
+    // cover a tile's latencies, more stages gain nothing.  64 requests, us: 8 rows of D 128
+    // 107 with 4 CTAs of 3 stages, 117 with 3 of 4, 150 with 2 of 6; of D 64 83 with 4 of
+    // 5 or 6, 95 with 3 of 6, 126 with 2 of 10; 32 rows of D 64 107 with 4 of 5, 117 with 3 of
+    // 6 or 7, 149 with 2 of 10.
+    static constexpr int kCtas = D == 64 ? (RT <= 2 ? 4 : 3) : D == 128 ? (RT == 1 ? 4 : 3) : RT == 1 ? 2 : 1;
+    static constexpr int kStages = D == 64 ? (RT == 2 ? 5 : 6) : D == 128 ? 3 : RT == 1 ? 3 : 5;
+    static constexpr int kPlans = 8;  // items planned at once
     static constexpr int kQueries = RT * (D / 16) * 512, kWeights = RT * kWarps * 512;  // bytes
     static constexpr int kSmem = kStages * kStage + kQueries + kWeights;
     static constexpr int kNT = D / 8, kGroup = kNT * 128 + 32;  // floats of 16 rows of a part
@@ -510,8 +516,9 @@ cudaError_t attention_split(const AttnParams &p, cudaStream_t stream)
     cudaError_t e = split_ctas<D, RT>(ctas);
     // Four CTAs that take every register of an SM are not launched early: placed between those
     // that the kernel before still has there, some find no slot (of 608 eight began when others
-    // had ended).  64 requests, us, early / not: D 64, 8 rows 118 / 84 (94 / 85 behind an insert).
-    // With fewer CTAs early is as good or better: 56 rows of D 128 235 / 238.
+    // had ended).  64 requests, us, early / not: D 64, 8 rows 118 / 83 (95 / 85 behind an insert),
+    // 32 rows 130 / 107, D 128, 8 rows 144 / 107.  With fewer CTAs early is as good or better (56
+    // rows of D 128 235 / 238); what it costs four is 0.2 us of a request over 300 tokens (9.5).
     if (e == cudaSuccess)
         e = C::kCtas == 4 ? launch_whole(attention_split_kernel<D, RT>, ctas, kThreads, C::kSmem, stream, p)
                           : launch_pdl(attention_split_kernel<D, RT>, ctas, kThreads, C::kSmem, stream, p);
