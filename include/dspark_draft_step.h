@@ -101,6 +101,8 @@ int dspark_verify_drafts(const void *target, int target_dtype, int64_t target_st
  *  new_lens       device, int32 [num_requests], or NULL: receives
  *                 context_lens[b] + first + counts[b]; must not overlap
  *                 context_lens, rows or counts.
+ * A request that had no rows in the step (a count of 0) grows by `first` like the others;
+ * whoever keeps such a request in the batch keeps its old length too.
  * Requests must not share the pages that rows move into.  In a page-scaled cache
  * such a page's scale grows to the largest scale that comes in, and what it
  * holds is encoded anew.  A request whose counts, rows or places are out of range

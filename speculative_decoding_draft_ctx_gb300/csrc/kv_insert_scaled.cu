@@ -9,10 +9,12 @@
 //
 // Work.  A unit is one (request, page, head, K or V); its tokens are read once: a
 // thread keeps up to kHold 16-byte words while the CTA finds the maximum (64
-// tokens of D 128; more are read again, from L1).  What bounds it: instructions (half
-// of the issue slots) and one wave of dependent loads (lengths, page, tokens):
-// 8,192 tokens of 8 heads 13.5 us, 50 MB at 55% of the copy rate; 7 tokens of 64
-// requests 6.1 us.  With the words in shared memory twelve CTAs fit an SM, not eight
+// tokens of D 128; more are read again, from L1).  8,192 tokens of 8 heads take 13.5 us,
+// 50 MB at 55% of the copy rate, 7 tokens of 64 requests 6.0 us.  What bounds them: the
+// first no unit alone, issue slots 60%, DRAM 27%: of a warp's 11.8 cycles an instruction
+// 2.7 go into waiting for loads (a unit's page and tokens are loaded when the one
+// before is stored), 2.5 into fixed latencies, 1.5 into waiting for a slot, 1.1 into
+// barriers; the second one wave of dependent loads (lengths, page, tokens).  With the words in shared memory twelve CTAs fit an SM, not eight
 // (14.3 and 9.7 us); infinities and NaN left out word by word cost 1.3 us.  Lengths
 // are on the device, so each CTA sums the requests' units itself and takes an
 // equal share of them, as the attention does.  A CTA has 128 threads, so that

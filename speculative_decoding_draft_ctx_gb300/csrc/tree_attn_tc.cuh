@@ -75,9 +75,11 @@ constexpr int kProducers = 4, kItemCostTc = 6;   // EXTRA of Walk, in tiles of k
 constexpr float kMost = 8.0f, kMostFp8 = kLift + 1.0f;
 // Page-scaled: weights begin at 2^kLiftScaled, so that the maximum of s + ev, which
 // the pages' exponents move too, may grow by seven octaves before a rescale of the
-// output (with kLift, by one: 35 of 50 tiles rescaled in a draft step of 64
-// requests, 1,500 cycles each).  A weight keeps its 2^-11 down to 2^-22 of the
-// largest; below it is off by at most 2^-33 of that.
+// output.  A weight keeps its 2^-11 down to 2^-22 of the largest; below it is off by
+// at most 2^-33 of that.  With kLift in its place, one octave, six more bits of a thin
+// tail and, us at D 128 / 64: two trees over 65,537 and 131,072 tokens 267 / 276, not
+// 261 / 273; 64 requests x 9 tokens 367 / 323, not 359 / 317; 8 x 256 over 2,000 tokens
+// 165 / 153, not 160 / 152.
 constexpr float kLiftScaled = 8.0f, kMostScaled = 15.0f;
 constexpr int kSpread = 15;  // of the exponents of 64 keys of a page-scaled cache
 

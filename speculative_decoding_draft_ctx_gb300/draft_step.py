@@ -192,7 +192,8 @@ def compact_kv(kv_caches, block_table, context_lens, rows, counts, first=1, bloc
 
     ``rows`` (int32 ``[B, width]``) and ``counts`` (int32 ``[B]``) are what
     ``verify_drafts`` returned: rows ascend and lie at or behind ``first + j``.
-    ``first=1``: row 0 is the last accepted token, whose K/V stays.  Requests must
+    ``first=1``: row 0 is the last accepted token, whose K/V stays.  (A request that
+    had no rows in the step grows by ``first`` too: keep its old length.)  Requests must
     not share the pages that rows move into.  ``block_scales`` (int8 ``[num_blocks,
     num_kv_heads, 2]`` per layer): page-scaled caches; a page's scale grows to the
     largest that comes in, and what the page holds is encoded anew.
